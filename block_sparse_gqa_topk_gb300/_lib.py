@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmsa.so")
@@ -32,7 +33,8 @@ EXPORTS = ("msa_workspace_size", "msa_index_topk", "msa_fwd", "msa_bwd",
            "msa_index_topk_varlen", "msa_fwd_varlen", "msa_bwd_varlen",
            "msa_decode_workspace_size", "msa_decode", "msa_quantize_kv_fp8",
            "msa_decode_fp8", "msa_quantize_fwd_fp8", "msa_fwd_fp8", "msa_plan_size",
-           "msa_index_topk_plan", "msa_fwd_plan", "msa_bwd_plan")
+           "msa_index_topk_plan", "msa_fwd_plan", "msa_bwd_plan", "msa_rope", "msa_cache_write",
+           "msa_cache_read")
 
 MSA_KERNEL_INDEX = 0
 MSA_KERNEL_FWD = 1
@@ -41,12 +43,31 @@ MSA_KERNEL_INDEX_LSE = 3
 
 MSA_DEBUG_WITHHOLD_LOAD = 1
 
+MSA_DTYPE_BF16 = 0
+MSA_DTYPE_F16 = 1
+MSA_DTYPE_F32 = 2
+
+MSA_CACHE_BF16 = 0
+MSA_CACHE_E4M3 = 1
+
 
 class Problem(ctypes.Structure):
     """msa_problem_t"""
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("B", "N", "H_q", "H_kv", "d", "d_idx", "Bk", "topk", "causal")] + \
                [("scale", ctypes.c_float), ("scale_idx", ctypes.c_float)]
+
+
+# msa_rope_t: B, N, rot_dim, interleaved, inverse, dtype, positions_bits, mscale, and the
+# batch and token strides of positions; msa_rope_tensor_t: x, y, their strides, H, d.
+# Packed to bytes: a decode step's host time is mostly marshalling.
+ROPE = struct.Struct("=7if2q")
+ROPE_TENSOR = struct.Struct("=QQ6qii")
+CACHE_STRIDES = struct.Struct("=5q")
+# msa_paged_cache_t: num_pages, page_size, H_kv, d, d_idx, kind, k, v, k_idx, k_scale, v_scale
+PAGED_CACHE = struct.Struct("=6i5Q")
+# msa_page_table_t: ids, B, max_pages, stride
+PAGE_TABLE = struct.Struct("=Qiiq")
 
 
 class MSAError(RuntimeError):
@@ -123,6 +144,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.msa_quantize_fwd_fp8.restype = i32
     lib.msa_fwd_fp8.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.msa_fwd_fp8.restype = i32
+    buf = ctypes.c_char_p  # a packed structure
+    lib.msa_rope.argtypes = [buf, vp, vp, buf, i32, vp]
+    lib.msa_rope.restype = i32
+    lib.msa_cache_write.argtypes = [buf, buf, vp, vp, i32, vp, vp, vp, buf, vp]
+    lib.msa_cache_write.restype = i32
+    lib.msa_cache_read.argtypes = [buf, buf, vp, vp, i32, vp, vp, vp, vp]
+    lib.msa_cache_read.restype = i32
     _lib = lib
     return lib
 
@@ -260,6 +288,24 @@ def msa_fwd_fp8(prob, q8, q_scale, k8, k_scale, v8t, v_scale, block_idx, o, lse,
                 stream) -> int:
     return load().msa_fwd_fp8(ctypes.byref(prob), q8, q_scale, k8, k_scale, v8t, v_scale, block_idx,
                               o, lse, ws, ws_bytes, stream)
+
+
+def msa_rope(rope: bytes, turns, positions, tensors: bytes, num_tensors: int, stream) -> int:
+    """rope: a packed ROPE, tensors: packed ROPE_TENSORs."""
+    return load().msa_rope(rope, turns, positions, tensors, num_tensors, stream)
+
+
+def msa_cache_write(cache: bytes, pages: bytes, lens, cu_seqlens, total_tokens, k, v, k_idx, strides,
+                    stream) -> int:
+    """cache: a packed PAGED_CACHE, pages: a packed PAGE_TABLE, strides: packed CACHE_STRIDES
+    or None."""
+    return load().msa_cache_write(cache, pages, lens, cu_seqlens, total_tokens, k, v, k_idx, strides,
+                                  stream)
+
+
+def msa_cache_read(cache: bytes, pages: bytes, lens, cu_seqlens, total_tokens, k, v, k_idx,
+                   stream) -> int:
+    return load().msa_cache_read(cache, pages, lens, cu_seqlens, total_tokens, k, v, k_idx, stream)
 
 
 def msa_version() -> int:

@@ -1,0 +1,301 @@
+// cache.cu -- tokens into a paged cache and back (see include/msa.h).
+//
+// A row is one head's key or value of a token (d values), or the token's index key; it
+// moves through the lanes of a part of a warp, 8 values a lane.  An E4M3 cache stores
+//   s = amax |x| / 448 (1 for an all-zero row),  code = E4M3 nearest to x / s,
+// the rule of msa_quantize_kv_fp8 bit for bit (IEEE divisions), and reads back
+// decode(code) * s rounded once to bf16.  Both directions are bound by HBM: every row is
+// read once and written once.
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include "kernels.h"
+#include "paged.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kSteps = 4;  // rows a lane group of a warp moves at once
+
+struct CacheParams {
+  PageView pages;
+  const int32_t* lens;
+  const int32_t* cu;  // null: one token a sequence
+  int B, T, H;
+  void* k;  // pool
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  __nv_bfloat16* k_idx;
+  __nv_bfloat16* xk;  // packed rows: read by the write, written by the read
+  __nv_bfloat16* xv;
+  __nv_bfloat16* xi;
+  int64_t sk[2], sv[2], si;  // their strides: token, head; token
+  int rows;                  // of a token: 2 H, and the index key's where there is one
+  int d_idx;
+  int* status;
+};
+
+constexpr int64_t kNoToken = -1;   // the packed row belongs to no sequence: left as it is
+constexpr int64_t kNoPlace = -2;   // its place does not exist: recorded in the status word
+
+__device__ __forceinline__ int64_t token_row(const CacheParams& p, int t) {
+  int b = t, after = 1;
+  if (p.cu) {
+    int lo = 0, hi = p.B - 1;  // last sequence that starts at or before t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldg(&p.cu[mid]) <= t) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    const int first = __ldg(&p.cu[b]), end = __ldg(&p.cu[b + 1]);
+    if (t < first || t >= end) {
+      // behind the last sequence is no error; anything else is a broken cu_seqlens
+      return t >= first && b == p.B - 1 && end >= first ? kNoToken : kNoPlace;
+    }
+    after = end - t;
+  }
+  const int len = __ldg(&p.lens[b]);
+  if (!p.cu && len == 0) return kNoToken;  // an empty slot of a padded decode batch
+  const int64_t pos = (int64_t)len - after;
+  if (pos < 0 || len > (int64_t)p.pages.max_pages * p.pages.page_size) return kNoPlace;
+  const int64_t row = pool_row(p.pages, b, (int)pos);
+  return row < 0 ? kNoPlace : row;
+}
+
+__device__ __forceinline__ void widen(uint4 w, float (&f)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f[2 * e] = __uint_as_float(u[e] << 16);
+    f[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+  }
+}
+
+// One warp per (token, chunk of rows): it finds the token's place once and moves kSteps
+// rows a lane group with all their loads in flight.  Rows of a token: the keys of its H
+// heads, the values, then the index key.
+template <int D, bool F8, bool WRITE>
+__global__ void __launch_bounds__(kThreads) cache_kernel(const CacheParams p) {
+  constexpr int LPR = D / 8;      // lanes of a row, 8 values each
+  constexpr int RPS = 32 / LPR;   // rows of a step
+  constexpr int CHUNK = RPS * kSteps;
+  const int lane = threadIdx.x & 31, sub = lane % LPR;
+  const int chunks = (p.rows + CHUNK - 1) / CHUNK;
+  const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+  if (unit >= (int64_t)p.T * chunks) return;
+  const int t = (int)(unit / chunks);
+  const int r0 = (int)(unit - (int64_t)t * chunks) * CHUNK + lane / LPR;
+  int64_t row = token_row(p, t);
+  if (row == kNoToken) return;
+  const bool bad = row == kNoPlace;
+  if (bad) {
+    if (lane == 0) set_status(p.status, MSA_ERR_ARG);
+    if (WRITE) return;
+    row = 0;  // not read: the read's rows of a missing place are zeros
+  }
+  uint4* packed[kSteps];
+  void* pool[kSteps];
+  float* scale[kSteps];
+  int kind[kSteps];  // 0: nothing, 1: key or value, 2: index key
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int r = r0 + i * RPS;
+    kind[i] = r < 2 * p.H ? 1 : r < p.rows && sub * 8 < p.d_idx ? 2 : 0;
+    const bool v = r >= p.H;
+    const int h = v ? r - p.H : r;
+    const int64_t cell = row * p.H + h;
+    if (kind[i] == 2) {
+      packed[i] = reinterpret_cast<uint4*>(p.xi + t * p.si + sub * 8);
+      pool[i] = p.k_idx + row * p.d_idx + sub * 8;
+    } else {
+      packed[i] = reinterpret_cast<uint4*>((v ? p.xv + t * p.sv[0] + h * p.sv[1]
+                                              : p.xk + t * p.sk[0] + h * p.sk[1]) + sub * 8);
+      pool[i] = static_cast<uint8_t*>(v ? p.v : p.k) + (cell * D + sub * 8) * (F8 ? 1 : 2);
+      scale[i] = F8 ? (v ? p.v_scale : p.k_scale) + cell : nullptr;
+    }
+  }
+  uint4 w[kSteps];
+  float s[kSteps];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    w[i] = make_uint4(0, 0, 0, 0);
+    s[i] = 0.f;
+    if (kind[i] == 0 || bad) continue;
+    if (WRITE) {
+      w[i] = __ldg(packed[i]);
+    } else if (F8 && kind[i] == 1) {
+      const uint2 c = *static_cast<const uint2*>(pool[i]);
+      w[i].x = c.x;
+      w[i].y = c.y;
+      s[i] = *scale[i];
+    } else {
+      w[i] = *static_cast<const uint4*>(pool[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    if constexpr (F8 && WRITE) {
+      float f[8];
+      widen(w[i], f);
+      float amax = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      if (kind[i] == 1) {
+        const float sc = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+        uint32_t c[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float2 q = make_float2(__fdiv_rn(f[e], sc), __fdiv_rn(f[e + 1], sc));
+          const uint32_t two = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+          c[e >> 2] |= (two & 0xffffu) << (8 * (e & 3));
+        }
+        *static_cast<uint2*>(pool[i]) = make_uint2(c[0], c[1]);
+        if (sub == 0) *scale[i] = sc;
+        continue;
+      }
+    }
+    if (kind[i] == 0) continue;
+    if (WRITE) {
+      *static_cast<uint4*>(pool[i]) = w[i];
+    } else if (F8 && kind[i] == 1) {
+      uint32_t y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)((e < 2 ? w[i].x : w[i].y) >> (16 * (e & 1)));
+        const float2 v2 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
+        y[e] = pack_bf16(v2.x * s[i], v2.y * s[i]);
+      }
+      *packed[i] = make_uint4(y[0], y[1], y[2], y[3]);
+    } else {
+      *packed[i] = w[i];
+    }
+  }
+}
+
+template <int D, bool F8, bool WRITE>
+cudaError_t launch_cache(const CacheParams& p, cudaStream_t st) {
+  constexpr int CHUNK = 32 / (D / 8) * kSteps;
+  const int64_t warps = (int64_t)p.T * ((p.rows + CHUNK - 1) / CHUNK);
+  const int64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
+  cache_kernel<D, F8, WRITE><<<(unsigned)grid, kThreads, 0, st>>>(p);
+  note_launch();
+  return cudaGetLastError();
+}
+
+template <bool WRITE>
+int run_cache(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int32_t* lens,
+              const int32_t* cu, int total_tokens, void* k, void* v, void* k_idx,
+              const int64_t* strides, cudaStream_t stream) {
+  int rc = check_cache(c);
+  if (rc) return rc;
+  PageView pages;
+  if ((rc = check_pages(c, pt, &pages))) return rc;
+  if (total_tokens < 0) return MSA_ERR_SHAPE;
+  if (!cu && total_tokens != pt->B) return MSA_ERR_SHAPE;
+  if (pt->B == 0 || total_tokens == 0) return MSA_OK;
+  if (!lens || !k || !v) return MSA_ERR_ARG;
+  if (k_idx && c->d_idx == 0) return MSA_ERR_SHAPE;
+  const void* ptrs[] = {k, v, k_idx};
+  for (const void* x : ptrs)
+    if (reinterpret_cast<uintptr_t>(x) & 15) return MSA_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(cu)) & 3) return MSA_ERR_ARG;
+  CacheParams p = {};
+  const int64_t dense[5] = {(int64_t)c->H_kv * c->d, c->d, (int64_t)c->H_kv * c->d, c->d, c->d_idx};
+  if (!strides) strides = dense;
+  for (int i = 0; i < 5; ++i)
+    if ((i < 4 || k_idx) && strides[i] % 8) return MSA_ERR_ARG;  // rows start on 16 bytes
+  p.rows = 2 * c->H_kv + (k_idx ? 1 : 0);
+  if ((int64_t)total_tokens * p.rows >= (int64_t)1 << 33) return MSA_ERR_UNSUPPORTED;
+  Ctx cx;
+  if ((rc = device_ctx(&cx))) return rc;
+  p.pages = pages;
+  p.lens = lens;
+  p.cu = cu;
+  p.B = pt->B;
+  p.T = total_tokens;
+  p.H = c->H_kv;
+  p.k = c->k;
+  p.v = c->v;
+  p.k_scale = c->k_scale;
+  p.v_scale = c->v_scale;
+  p.k_idx = static_cast<__nv_bfloat16*>(c->k_idx);
+  p.xk = static_cast<__nv_bfloat16*>(k);
+  p.xv = static_cast<__nv_bfloat16*>(v);
+  p.xi = static_cast<__nv_bfloat16*>(k_idx);
+  p.sk[0] = strides[0];
+  p.sk[1] = strides[1];
+  p.sv[0] = strides[2];
+  p.sv[1] = strides[3];
+  p.si = strides[4];
+  p.d_idx = c->d_idx;
+  p.status = cx.status;
+  const bool f8 = c->kind == MSA_CACHE_E4M3;
+  cudaError_t e;
+  if (c->d == 128)
+    e = f8 ? launch_cache<128, true, WRITE>(p, stream) : launch_cache<128, false, WRITE>(p, stream);
+  else
+    e = f8 ? launch_cache<64, true, WRITE>(p, stream) : launch_cache<64, false, WRITE>(p, stream);
+  return finish(e);
+}
+
+}  // namespace
+
+int check_cache(const msa_paged_cache_t* c) {
+  if (!c) return MSA_ERR_ARG;
+  if (c->num_pages < 0 || c->page_size <= 0 || c->H_kv <= 0 || c->d <= 0 || c->d_idx < 0)
+    return MSA_ERR_SHAPE;
+  if (c->kind != MSA_CACHE_BF16 && c->kind != MSA_CACHE_E4M3) return MSA_ERR_ARG;
+  if (c->page_size % 16 != 0 || c->page_size > 65536) return MSA_ERR_UNSUPPORTED;
+  if (c->d != 64 && c->d != 128) return MSA_ERR_UNSUPPORTED;
+  if (c->d_idx != 0 && c->d_idx != 32 && c->d_idx != 64) return MSA_ERR_UNSUPPORTED;
+  if (c->H_kv > 1024) return MSA_ERR_UNSUPPORTED;
+  if (c->num_pages == 0) return MSA_OK;  // no page to address
+  const bool f8 = c->kind == MSA_CACHE_E4M3;
+  const void* need[] = {c->k, c->v, f8 ? c->k_scale : c->k, f8 ? c->v_scale : c->v,
+                        c->d_idx ? c->k_idx : c->k};
+  for (const void* x : need)
+    if (!x || (reinterpret_cast<uintptr_t>(x) & 15)) return MSA_ERR_ARG;
+  return MSA_OK;
+}
+
+int check_pages(const msa_paged_cache_t* c, const msa_page_table_t* pt, PageView* out) {
+  if (!pt) return MSA_ERR_ARG;
+  if (pt->B < 0 || pt->max_pages < 0 || pt->stride < 0) return MSA_ERR_SHAPE;
+  if ((int64_t)pt->max_pages * c->page_size > 0x7fffffffLL) return MSA_ERR_UNSUPPORTED;
+  if (pt->B > 0 && pt->max_pages > 0 &&
+      (!pt->ids || (reinterpret_cast<uintptr_t>(pt->ids) & 3)))
+    return MSA_ERR_ARG;
+  out->table = pt->ids;
+  out->table_stride = pt->stride;
+  out->num_pages = c->num_pages;
+  out->page_size = c->page_size;
+  out->max_pages = pt->max_pages;
+  out->shift = page_shift(c->page_size);
+  return MSA_OK;
+}
+
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" {
+
+int msa_cache_write(const msa_paged_cache_t* c, const msa_page_table_t* pages, const int32_t* lens,
+                    const int32_t* cu_seqlens, int total_tokens, const void* k, const void* v,
+                    const void* k_idx, const int64_t* strides, cudaStream_t stream) {
+  return run_cache<true>(c, pages, lens, cu_seqlens, total_tokens, const_cast<void*>(k),
+                         const_cast<void*>(v), const_cast<void*>(k_idx), strides, stream);
+}
+
+int msa_cache_read(const msa_paged_cache_t* c, const msa_page_table_t* pages, const int32_t* lens,
+                   const int32_t* cu_seqlens, int total_tokens, void* k, void* v, void* k_idx,
+                   cudaStream_t stream) {
+  if (pages && pages->B > 0 && total_tokens > 0 && !cu_seqlens) return MSA_ERR_ARG;
+  return run_cache<false>(c, pages, lens, cu_seqlens, total_tokens, k, v, k_idx, nullptr, stream);
+}
+
+}  // extern "C"

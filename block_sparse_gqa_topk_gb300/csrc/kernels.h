@@ -178,6 +178,11 @@ int validate_problem(const msa_problem_t* p, Shape* s);
 int device_ctx(Ctx* cx);
 int finish(cudaError_t e);  // MSA_OK or MSA_ERR_CUDA
 
+// Checks of a paged cache and of a page table (cache.cu), shared by the calls that use them.
+struct PageView;
+int check_cache(const msa_paged_cache_t* c);
+int check_pages(const msa_paged_cache_t* c, const msa_page_table_t* pt, PageView* out);
+
 // Argument checks and call sequences of the three training calls, shared by the fixed
 // and the packed variable-length entry points (msa_api.cu, attn_bwd.cu).  ws is the
 // call's workspace of ws_*_bytes(s) bytes, 256-byte aligned.

@@ -10,6 +10,9 @@ block_idx [B,H_kv,N,topk] int32.
 """
 from __future__ import annotations
 
+import contextlib
+import dataclasses
+import fractions
 import math
 
 import torch
@@ -212,10 +215,16 @@ class MSAFunction(torch.autograd.Function):
 
 
 def attention(q, k, v, q_idx, k_idx, topk: int = 16, Bk: int = 128, scale=None, scale_idx=None,
-              kl_coef: float = 1.0):
+              kl_coef: float = 1.0, *, rope=None, positions=None):
     """MSA attention for training: returns o; backward also trains the index heads.
     Stopping the gradient at the index-branch input is the caller's job (feed the
-    projections a detached hidden state)."""
+    projections a detached hidden state).  With `rope` (from new_rope, rot_dim <= d_idx) the
+    four operands of the scores get rotary positions first: each token's index in its
+    sequence, or positions [B, N]."""
+    if rope is not None:
+        q, k, q_idx, k_idx = _rotated((q, k, q_idx, k_idx), rope, positions)
+    elif positions is not None:
+        raise ValueError("positions are those of rope, which is not given")
     o, _ = MSAFunction.apply(q, k, v, q_idx, k_idx, topk, Bk, scale, scale_idx, kl_coef)
     return o
 
@@ -473,3 +482,363 @@ def msa_fwd_fp8(q8, q_scale, k8, k_scale, v8t, v_scale, block_idx, *, scale=None
                           _stream(dev))
     _lib.check(rc, "msa_fwd_fp8")
     return o, lse
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions (see include/msa.h).
+# ---------------------------------------------------------------------------
+_ROPE_DTYPES = {torch.bfloat16: _lib.MSA_DTYPE_BF16, torch.float16: _lib.MSA_DTYPE_F16,
+                torch.float32: _lib.MSA_DTYPE_F32}
+_TWO_PI = fractions.Fraction(2 * 31415926535897932384626433832795028841971693993751, 10 ** 49)
+
+
+def _on(device):
+    """Makes `device` current for the calls inside, where it is not already."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+@dataclasses.dataclass(frozen=True, eq=False)
+class Rope:
+    """Rotary frequencies on a device (from new_rope)."""
+    turns: torch.Tensor  # int64 [rot_dim / 2]: turns a position, in units of 2^-64
+    rot_dim: int
+    interleaved: bool
+    mscale: float
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling=None):
+    """Radians a position of the rot_dim / 2 pairs (list of float) and the factor mscale on the
+    rotated values.  scaling, to reach past the trained context:
+      None                               f_i = base^(-2i / rot_dim)
+      {"type": "linear", "factor": s}    f_i / s
+      {"type": "ntk", "factor": s}       base s^(rot_dim / (rot_dim - 2)) in place of base
+      {"type": "yarn", "factor": s, "original_len": L, "beta_fast": 32, "beta_slow": 1}
+          pairs that turn beta_fast times or more over L keep f_i, those that turn beta_slow
+          times or fewer take f_i / s, the ones between a linear mix by their turns;
+          mscale = 0.1 ln s + 1 (or "mscale") -- YaRN, Peng et al. 2023."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError(f"rot_dim must be even and at least 2, got {rot_dim}")
+    if not (math.isfinite(base) and base > 0):
+        raise ValueError(f"base must be positive, got {base}")
+    half = rot_dim // 2
+    if scaling is None:
+        return [base ** (-2.0 * i / rot_dim) for i in range(half)], 1.0
+    known = {"linear": {"factor"}, "ntk": {"factor"},
+             "yarn": {"factor", "original_len", "beta_fast", "beta_slow", "mscale"}}
+    kind = scaling.get("type")
+    if kind not in known:
+        raise ValueError(f"unknown scaling type {kind!r}: one of {sorted(known)}")
+    extra = set(scaling) - known[kind] - {"type"}
+    if extra or "factor" not in scaling:
+        raise ValueError(f"scaling {kind!r} takes {sorted(known[kind])}, got {sorted(scaling)}")
+    s = float(scaling["factor"])
+    if not (math.isfinite(s) and s > 0):
+        raise ValueError(f"factor must be positive, got {s}")
+    if kind == "ntk":
+        if rot_dim == 2:
+            raise ValueError("ntk scaling needs rot_dim > 2")
+        base *= s ** (rot_dim / (rot_dim - 2))
+    f = [base ** (-2.0 * i / rot_dim) for i in range(half)]
+    if kind == "ntk":
+        return f, 1.0
+    if kind == "linear":
+        return [x / s for x in f], 1.0
+    if "original_len" not in scaling:
+        raise ValueError("scaling 'yarn' needs original_len")
+    L = float(scaling["original_len"])
+    fast, slow = float(scaling.get("beta_fast", 32.0)), float(scaling.get("beta_slow", 1.0))
+    if not (L > 0 and fast > slow >= 0):
+        raise ValueError("yarn needs original_len > 0 and beta_fast > beta_slow >= 0")
+    keep = [min(1.0, max(0.0, (L * x / (2 * math.pi) - slow) / (fast - slow))) for x in f]
+    return ([x * g + x / s * (1.0 - g) for x, g in zip(f, keep)],
+            float(scaling.get("mscale", 0.1 * math.log(s) + 1.0)))
+
+
+def new_rope(rot_dim: int, *, base: float = 10000.0, interleaved: bool = False, scaling=None,
+             inv_freq=None, mscale=None, device="cuda") -> Rope:
+    """Rotary positions over the first rot_dim values of a head: pairs (i, i + rot_dim / 2), or
+    (2i, 2i + 1) with interleaved.  Frequencies from base and scaling (rope_frequencies), or
+    given as inv_freq (rot_dim / 2 radians a position); mscale overrides the factor on the
+    rotated values.  One handle serves every layer and position."""
+    if inv_freq is None:
+        freq, m = rope_frequencies(rot_dim, base, scaling)
+    else:
+        if scaling is not None:
+            raise ValueError("inv_freq and scaling exclude one another")
+        if rot_dim < 2 or rot_dim % 2:
+            raise ValueError(f"rot_dim must be even and at least 2, got {rot_dim}")
+        freq, m = [float(x) for x in inv_freq], 1.0
+        if len(freq) != rot_dim // 2 or not all(map(math.isfinite, freq)):
+            raise ValueError(f"inv_freq must be {rot_dim // 2} finite numbers")
+    if rot_dim > 512:
+        raise ValueError(f"rot_dim is at most 512, got {rot_dim}")
+    m = float(m if mscale is None else mscale)
+    if not math.isfinite(m):
+        raise ValueError("mscale must be finite")
+    one = 1 << 64
+    turns = [int(round(fractions.Fraction(x) / _TWO_PI * one)) % one for x in freq]
+    turns = torch.tensor([t - one if t >= one // 2 else t for t in turns], dtype=torch.int64)
+    return Rope(turns.to(device), rot_dim, bool(interleaved), m)
+
+
+def msa_rope(xs, rope: Rope, positions=None, *, inverse: bool = False, inplace: bool = False):
+    """Rotary positions of one to four tensors in one launch; returns them as a tuple (new
+    contiguous tensors, or xs themselves with inplace).  inverse turns back (the gradient).
+
+    positions None: tokens [B, N, H, d] or [B, N, d] (one head), each at its index in its
+    sequence.  positions int32 or int64 [T]: packed tokens [T, H, d] or [T, d];  [B, N] (a
+    broadcast row is fine): tokens [B, N, H, d] or [B, N, d].  bf16, fp16 or float32 (all the
+    same), d >= rot_dim; any strides (views of a fused projection), the last axis contiguous
+    or else copied once."""
+    xs = (xs,) if isinstance(xs, torch.Tensor) else tuple(xs)
+    if not 1 <= len(xs) <= 4:
+        raise ValueError(f"one to four tensors, got {len(xs)}")
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must come from new_rope")
+    x0 = xs[0]
+    bits, ps = 32, (0, 0)
+    if positions is None:
+        if not isinstance(x0, torch.Tensor) or x0.dim() < 3:
+            raise ValueError("without positions the tensors are [B, N, H, d] or [B, N, d]")
+        lead = tuple(x0.shape[:2])
+    else:
+        if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
+            raise TypeError("positions must be an int32 or int64 tensor")
+        if positions.dim() not in (1, 2):
+            raise ValueError(f"positions must be [T] or [B, N], got {tuple(positions.shape)}")
+        if positions.dtype == torch.int64:
+            bits = 64
+        ps = positions.stride() if positions.dim() == 2 else (0, positions.stride(0))
+        lead = tuple(positions.shape)
+    dev, dtype = rope.turns.device, x0.dtype
+    if dtype not in _ROPE_DTYPES:
+        raise TypeError(f"tensors must be bf16, fp16 or float32, got {dtype}")
+    if dev.type != "cuda" or (positions is not None and positions.device != dev):
+        raise ValueError("rope, positions and the tensors must be on one CUDA device (no CPU path exists)")
+    n = len(lead)
+    ys, packed, keep = [], [], []
+    for i, x in enumerate(xs):
+        if not isinstance(x, torch.Tensor):
+            raise TypeError(f"tensor {i} must be a tensor")
+        if x.device != dev:
+            raise ValueError("rope, positions and the tensors must be on one CUDA device (no CPU path exists)")
+        if x.dtype != dtype:
+            raise TypeError(f"all tensors must be {dtype}, got {x.dtype}")
+        if x.dim() not in (n + 1, n + 2) or tuple(x.shape[:n]) != lead:
+            raise ValueError(f"tensor {i} must be {lead} + ([H,] d), got {tuple(x.shape)}")
+        if x.shape[-1] < rope.rot_dim:
+            raise ValueError(f"tensor {i} has d = {x.shape[-1]} < rot_dim = {rope.rot_dim}")
+        if inplace:
+            if any(s == 0 and k > 1 for s, k in zip(x.stride(), x.shape)) or x.stride(-1) != 1:
+                raise ValueError(f"tensor {i} cannot be turned in place: its values overlap or its "
+                                 "last axis is strided")
+            if x.requires_grad and torch.is_grad_enabled():
+                raise ValueError(f"tensor {i} requires a gradient: use rope, which is differentiable")
+            y = x
+            torch.autograd.graph.increment_version(x)
+        else:
+            if x.stride(-1) != 1:
+                x = x.contiguous()
+                keep.append(x)
+            y = torch.empty(x.shape, dtype=dtype, device=dev)
+        ys.append(y)
+        if x.numel() == 0:
+            continue
+        sx, sy = x.stride(), y.stride()
+        hx, hy = (sx[n], sy[n]) if x.dim() == n + 2 else (0, 0)
+        packed.append(_lib.ROPE_TENSOR.pack(
+            x.data_ptr(), y.data_ptr(), sx[0] if n == 2 else 0, sx[n - 1], hx, sy[0] if n == 2 else 0,
+            sy[n - 1], hy, x.shape[n] if x.dim() == n + 2 else 1, x.shape[-1]))
+    if packed:
+        B, N = lead if n == 2 else (1, lead[0])
+        r = _lib.ROPE.pack(B, N, rope.rot_dim, rope.interleaved, inverse, _ROPE_DTYPES[dtype], bits,
+                           rope.mscale, ps[0], ps[1])
+        with _on(dev):
+            rc = _lib.msa_rope(r, rope.turns.data_ptr(), _ptr(positions), b"".join(packed), len(packed),
+                               _stream(dev))
+        _lib.check(rc, "msa_rope")
+    return tuple(ys)
+
+
+class RopeFunction(torch.autograd.Function):
+    """msa_rope with its gradient, the inverse turn (linear in x: differentiable again)."""
+
+    @staticmethod
+    def forward(ctx, rope, positions, inverse, *xs):
+        ctx.rope, ctx.inverse = rope, inverse
+        ctx.save_for_backward(positions)
+        ctx.set_materialize_grads(False)
+        return msa_rope(xs, rope, positions, inverse=inverse)
+
+    @staticmethod
+    def backward(ctx, *dys):
+        (positions,) = ctx.saved_tensors
+        got = [i for i, g in enumerate(dys) if g is not None and ctx.needs_input_grad[3 + i]]
+        out = [None] * len(dys)
+        if got:
+            dxs = RopeFunction.apply(ctx.rope, positions, not ctx.inverse, *(dys[i] for i in got))
+            for i, g in zip(got, dxs):
+                out[i] = g
+        return (None, None, None, *out)
+
+
+def rope(xs, rope: Rope, positions=None):
+    """msa_rope for training: the rotated tensors as a tuple, differentiable in xs."""
+    xs = (xs,) if isinstance(xs, torch.Tensor) else tuple(xs)
+    if torch.is_grad_enabled() and any(isinstance(x, torch.Tensor) and x.requires_grad for x in xs):
+        return RopeFunction.apply(rope, positions, False, *xs)
+    return msa_rope(xs, rope, positions)
+
+
+_rotated = rope  # for attention, whose argument is named rope too
+
+
+# ---------------------------------------------------------------------------
+# Paged cache (see include/msa.h).
+# ---------------------------------------------------------------------------
+class PagedCache:
+    """A pool of pages: k, v [num_pages, page_size, H_kv, d] bf16, or uint8 E4M3 codes with
+    k_scale, v_scale [num_pages, page_size, H_kv] float32; k_idx [num_pages, page_size, d_idx]
+    bf16, or None for a cache without index keys.  Page tables (int32 [B, max_pages]) and
+    lengths (int32 [B]) belong to the calls."""
+
+    def __init__(self, k, v, k_idx=None, k_scale=None, v_scale=None):
+        fp8 = isinstance(k, torch.Tensor) and k.dtype == torch.uint8
+        kind = torch.uint8 if fp8 else torch.bfloat16
+        _need(k, "k", kind, ndim=4)
+        _need(v, "v", kind, ndim=4)
+        P, page, H_kv, d = k.shape
+        if v.shape != k.shape:
+            raise ValueError(f"v must be {tuple(k.shape)}, got {tuple(v.shape)}")
+        if (k_scale is not None or v_scale is not None) != fp8 or (k_scale is None) != (v_scale is None):
+            raise ValueError("E4M3 codes (uint8) have k_scale and v_scale; bf16 pages have none")
+        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is not None:
+                _need(t, n, torch.float32, ndim=3)
+                if tuple(t.shape) != (P, page, H_kv):
+                    raise ValueError(f"{n} must be {(P, page, H_kv)}, got {tuple(t.shape)}")
+        d_idx = 0
+        if k_idx is not None:
+            _need(k_idx, "k_idx", ndim=3)
+            d_idx = k_idx.shape[2]
+            if tuple(k_idx.shape[:2]) != (P, page):
+                raise ValueError(f"k_idx must be {(P, page)} + (d_idx,), got {tuple(k_idx.shape)}")
+        if any(t is not None and t.device != k.device for t in (v, k_idx, k_scale, v_scale)):
+            raise ValueError("the pages of a cache must be on one device")
+        if page < 16 or page % 16:
+            raise ValueError(f"page_size must be a multiple of 16, got {page}")
+        if d not in (64, 128) or d_idx not in (0, 32, 64):
+            raise ValueError(f"d must be 64 or 128 and d_idx 32 or 64, got {d} and {d_idx}")
+        self.k, self.v, self.k_idx, self.k_scale, self.v_scale = k, v, k_idx, k_scale, v_scale
+        self.num_pages, self.page_size, self.H_kv, self.d, self.d_idx, self.fp8 = P, page, H_kv, d, d_idx, fp8
+        self.device = k.device
+        self._c = _lib.PAGED_CACHE.pack(
+            P, page, H_kv, d, d_idx, _lib.MSA_CACHE_E4M3 if fp8 else _lib.MSA_CACHE_BF16,
+            *(0 if t is None else t.data_ptr() for t in (k, v, k_idx, k_scale, v_scale)))
+
+
+def new_paged_cache(num_pages: int, H_kv: int, *, page_size: int = 128, d: int = 128, d_idx: int = 64,
+                    fp8: bool = False, device="cuda") -> PagedCache:
+    """An empty PagedCache (d_idx 0: without index keys)."""
+    def pages(*tail, dtype):
+        return torch.zeros((num_pages, page_size, *tail), dtype=dtype, device=device)
+
+    kv = torch.uint8 if fp8 else torch.bfloat16
+    return PagedCache(pages(H_kv, d, dtype=kv), pages(H_kv, d, dtype=kv),
+                      pages(d_idx, dtype=torch.bfloat16) if d_idx else None,
+                      pages(H_kv, dtype=torch.float32) if fp8 else None,
+                      pages(H_kv, dtype=torch.float32) if fp8 else None)
+
+
+def _pages_arg(cache, page_table, lens):
+    """The packed page table after the checks that a paged call's arguments share."""
+    if not isinstance(cache, PagedCache):
+        raise TypeError("cache must be a PagedCache")
+    for t, n, nd in ((page_table, "page_table", 2), (lens, "lens", 1)):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+            raise TypeError(f"{n} must be an int32 tensor")
+        if t.device != cache.device:
+            raise ValueError(f"{n} must be on the cache's device")
+        if t.dim() != nd or (t.numel() > 1 and t.stride(-1) != 1 and t.shape[-1] > 1):
+            raise ValueError(f"{n} must have {nd} dims, the last contiguous")
+    B, max_pages = page_table.shape
+    if lens.shape[0] != B:
+        raise ValueError(f"lens must be [{B}], got {tuple(lens.shape)}")
+    return _lib.PAGE_TABLE.pack(page_table.data_ptr(), B, max_pages, page_table.stride(0)), B, max_pages
+
+
+def _cu_arg(cu_seqlens, cache, B):
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dtype != torch.int32:
+        raise TypeError("cu_seqlens must be an int32 tensor")
+    if cu_seqlens.device != cache.device or cu_seqlens.shape != (B + 1,) or not cu_seqlens.is_contiguous():
+        raise ValueError(f"cu_seqlens must be a contiguous [{B + 1}] on the cache's device")
+
+
+def _cache_rows(t, name, cache, shape):
+    """A packed input of msa_cache_write, copied where its rows do not start on 16 bytes."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bf16 tensor")
+    if t.device != cache.device:
+        raise ValueError(f"{name} must be on the cache's device (no CPU path exists)")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1 or t.data_ptr() % 16 or any(s % 8 for s in t.stride()[:-1]):
+        t = t.contiguous()
+        if t.data_ptr() % 16:  # contiguous already, but off a 16-byte boundary
+            t = t.clone()
+    return t
+
+
+def msa_cache_write(cache: PagedCache, page_table, lens, k, v, k_idx=None, *, cu_seqlens=None) -> None:
+    """Writes new tokens into the cache's pages, as E4M3 codes and row scales where it holds
+    those: k, v [T, H_kv, d], k_idx [T, d_idx] (given exactly if the cache has index keys), bf16,
+    any strides.  lens (int32 [B]): lengths after the call; sequence b's n new tokens go to
+    positions lens[b] - n .. lens[b] - 1.  cu_seqlens (int32 [B + 1]) splits the T packed tokens;
+    without it there is one token a sequence (T = B), and lens[b] = 0 skips the slot.  A token
+    whose place does not exist is dropped and sets the device status."""
+    pages, B, _ = _pages_arg(cache, page_table, lens)
+    T = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else -1
+    k = _cache_rows(k, "k", cache, (max(T, 0), cache.H_kv, cache.d))
+    v = _cache_rows(v, "v", cache, (T, cache.H_kv, cache.d))
+    if (k_idx is None) != (cache.k_idx is None):
+        raise ValueError("k_idx must be given exactly if the cache has index keys")
+    if k_idx is not None:
+        k_idx = _cache_rows(k_idx, "k_idx", cache, (T, cache.d_idx))
+    if cu_seqlens is not None:
+        _cu_arg(cu_seqlens, cache, B)
+    elif T != B:
+        raise ValueError(f"without cu_seqlens there is one token a sequence: {B}, got {T}")
+    if T == 0 or B == 0:
+        return
+    strides = _lib.CACHE_STRIDES.pack(k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                                      0 if k_idx is None else k_idx.stride(0))
+    with _on(cache.device):
+        rc = _lib.msa_cache_write(cache._c, pages, lens.data_ptr(), _ptr(cu_seqlens), T, k.data_ptr(),
+                                  v.data_ptr(), _ptr(k_idx), strides, _stream(cache.device))
+    _lib.check(rc, "msa_cache_write")
+
+
+def msa_cache_read(cache: PagedCache, page_table, lens, cu_seqlens, total_tokens: int):
+    """The last cu_seqlens[b + 1] - cu_seqlens[b] tokens of every sequence (up to position
+    lens[b] - 1) in packed order: k, v [total_tokens, H_kv, d] and k_idx [total_tokens, d_idx]
+    (None without index keys), bf16.  With lens[b] tokens of each it is the whole context, as
+    msa_fwd_varlen and its companions take it.  Rows behind cu_seqlens[B] are not written."""
+    pages, B, _ = _pages_arg(cache, page_table, lens)
+    _cu_arg(cu_seqlens, cache, B)
+    T = int(total_tokens)
+    if T < 0:
+        raise ValueError("total_tokens must not be negative")
+    dev = cache.device
+    k = torch.empty((T, cache.H_kv, cache.d), dtype=torch.bfloat16, device=dev)
+    v = torch.empty((T, cache.H_kv, cache.d), dtype=torch.bfloat16, device=dev)
+    k_idx = None
+    if cache.k_idx is not None:
+        k_idx = torch.empty((T, cache.d_idx), dtype=torch.bfloat16, device=dev)
+    if T and B:
+        with _on(dev):
+            rc = _lib.msa_cache_read(cache._c, pages, lens.data_ptr(), cu_seqlens.data_ptr(), T, k.data_ptr(),
+                                     v.data_ptr(), _ptr(k_idx), _stream(dev))
+        _lib.check(rc, "msa_cache_read")
+    return k, v, k_idx

@@ -295,6 +295,95 @@ int msa_fwd_fp8(const msa_problem_t* p, const uint8_t* q8, const float* q_scale,
                 const int32_t* block_idx, void* o, float* lse, void* workspace,
                 size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * Rotary positions of up to four tensors in one call (q, k, q_idx, k_idx of a layer).
+ *   The first rot_dim of a head's d values are rot_dim / 2 pairs: values (i, i + rot_dim/2)
+ *   (interleaved = 0) or (2i, 2i + 1) (interleaved = 1).  With a = position * f_i,
+ *     y1 = mscale (x1 cos a - x2 sin a),  y2 = mscale (x2 cos a + x1 sin a),
+ *   or with inverse = 1 the transposed turn (the gradient: dx from dy).  Values past
+ *   rot_dim are copied.  turns: device uint64 [rot_dim / 2], turns[i] = the fraction of
+ *   f_i / (2 pi) as a multiple of 2^-64, so that position * turns[i] modulo 2^64 is the
+ *   angle's fraction of a turn, exactly, at any distance; the sine and cosine are taken of
+ *   that fraction in float32.  The pages have no rotary form: this is an operator of the
+ *   projections in front of the method.
+ * Tokens form B x N rows (a packed axis is B = 1); strides in elements, the values of a
+ *   head contiguous.  positions: device int32 or int64 (positions_bits 32 or 64) with
+ *   positions_stride {batch, token}; NULL takes each token's index 0 .. N-1.  x and y of a
+ *   tensor are the same memory (in place, same strides) or do not overlap.  All tensors
+ *   have the type dtype; arithmetic is float32, rounded once.  rot_dim even, at most 512
+ *   and at most every d; d <= 512, H <= 1024.  Any alignment of whole elements; 16-byte
+ *   aligned rows are moved 16 bytes at a time.
+ */
+#define MSA_DTYPE_BF16 0
+#define MSA_DTYPE_F16 1
+#define MSA_DTYPE_F32 2
+typedef struct msa_rope {
+  int32_t B, N, rot_dim;
+  int32_t interleaved, inverse, dtype;
+  int32_t positions_bits;
+  float mscale;
+  int64_t positions_stride[2]; /* batch, token */
+} msa_rope_t;
+typedef struct msa_rope_tensor {
+  const void* x;
+  void* y;
+  int64_t x_stride[3], y_stride[3]; /* batch, token, head */
+  int32_t H, d;
+} msa_rope_tensor_t;
+int msa_rope(const msa_rope_t* r, const uint64_t* turns, const void* positions,
+             const msa_rope_tensor_t* tensors, int num_tensors, cudaStream_t stream);
+
+/*
+ * Paged cache.  A pool of num_pages pages of page_size token rows:
+ *   k, v   [num_pages][page_size][H_kv][d]   bf16, or E4M3 codes (kind MSA_CACHE_E4M3) with
+ *   k_scale, v_scale [num_pages][page_size][H_kv] float32 (the rule of msa_quantize_kv_fp8);
+ *   k_idx  [num_pages][page_size][d_idx]     bf16 (d_idx = 0: a cache without index keys).
+ * A page table row per sequence names its pages in order (device int32, `stride` elements
+ * from row to row): the token at position pos lives in row pos % page_size of page
+ * ids[b * stride + pos / page_size].  Entries past a sequence's length are not read.  A
+ * contiguous cache [B][Lmax] is the same memory with pages 0, 1, 2, ...
+ * page_size: a multiple of 16; d in {64, 128}; d_idx in {0, 32, 64}; max_pages * page_size
+ * below 2^31.  Pool pointers 16-byte aligned.  num_pages and the table are checked on the
+ * device: an id outside the pool, like a length that is negative or past the table, is
+ * recorded as MSA_ERR_ARG in the status word, and no memory outside the pool is touched.
+ *
+ * msa_cache_write: the calls' new tokens into the pool.  k, v [total_tokens][H_kv][d] and
+ *   k_idx [total_tokens][d_idx] (may be NULL) in bf16.  cu_seqlens (device int32 [B + 1],
+ *   cu_seqlens[0] = 0, non-decreasing) gives each sequence's packed tokens; NULL means one
+ *   token a sequence (total_tokens = B).  lens (device int32 [B]) are the lengths after the
+ *   call: sequence b's n tokens land at positions lens[b] - n .. lens[b] - 1.  With
+ *   cu_seqlens NULL, lens[b] = 0 marks an empty slot, which is skipped.  Tokens behind
+ *   cu_seqlens[B] are skipped.  A token without a place (position below 0, length past the
+ *   table, page outside the pool, cu_seqlens broken around it) is not written and sets
+ *   MSA_ERR_ARG.  Two tokens must not share a place.  strides: NULL for contiguous inputs,
+ *   or five element counts (k token, k head, v token, v head, k_idx token), multiples of 8.
+ * msa_cache_read: the same rows back, in bf16, to contiguous k, v, k_idx (NULL: not read);
+ *   cu_seqlens says how many of each sequence's last tokens (up to position lens[b] - 1)
+ *   are wanted.  E4M3 rows are decode(code) * scale rounded once.  Rows behind
+ *   cu_seqlens[B] are left as they are; rows without a place are zeros and set MSA_ERR_ARG.
+ */
+#define MSA_CACHE_BF16 0
+#define MSA_CACHE_E4M3 1
+typedef struct msa_paged_cache {
+  int32_t num_pages, page_size, H_kv, d, d_idx, kind;
+  void* k;
+  void* v;
+  void* k_idx;
+  float* k_scale;
+  float* v_scale;
+} msa_paged_cache_t;
+typedef struct msa_page_table {
+  const int32_t* ids;
+  int32_t B, max_pages;
+  int64_t stride;
+} msa_page_table_t;
+int msa_cache_write(const msa_paged_cache_t* c, const msa_page_table_t* pages, const int32_t* lens,
+                    const int32_t* cu_seqlens, int total_tokens, const void* k, const void* v,
+                    const void* k_idx, const int64_t* strides, cudaStream_t stream);
+int msa_cache_read(const msa_paged_cache_t* c, const msa_page_table_t* pages, const int32_t* lens,
+                   const int32_t* cu_seqlens, int total_tokens, void* k, void* v, void* k_idx,
+                   cudaStream_t stream);
+
 /* Synchronises `stream`, then reads and clears the current device's status word
  * (MSA_OK or the first MSA_ERR_* a kernel recorded since the last read). */
 int msa_get_device_status(cudaStream_t stream, int* status);

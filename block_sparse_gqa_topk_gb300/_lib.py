@@ -34,7 +34,8 @@ EXPORTS = ("msa_workspace_size", "msa_index_topk", "msa_fwd", "msa_bwd",
            "msa_decode_workspace_size", "msa_decode", "msa_quantize_kv_fp8",
            "msa_decode_fp8", "msa_quantize_fwd_fp8", "msa_fwd_fp8", "msa_plan_size",
            "msa_index_topk_plan", "msa_fwd_plan", "msa_bwd_plan", "msa_rope", "msa_cache_write",
-           "msa_cache_read")
+           "msa_cache_read", "msa_decode_paged_workspace_size", "msa_decode_paged",
+           "msa_decode_paged_dense")
 
 MSA_KERNEL_INDEX = 0
 MSA_KERNEL_FWD = 1
@@ -151,6 +152,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.msa_cache_write.restype = i32
     lib.msa_cache_read.argtypes = [buf, buf, vp, vp, i32, vp, vp, vp, vp]
     lib.msa_cache_read.restype = i32
+    lib.msa_decode_paged_workspace_size.argtypes = [buf, buf, i32, i32]
+    lib.msa_decode_paged_workspace_size.restype = sz
+    lib.msa_decode_paged.argtypes = [buf, buf, vp, i32, i32, f32, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.msa_decode_paged.restype = i32
+    lib.msa_decode_paged_dense.argtypes = [buf, buf, vp, i32, f32, vp, vp, vp, vp, sz, vp]
+    lib.msa_decode_paged_dense.restype = i32
     _lib = lib
     return lib
 
@@ -306,6 +313,21 @@ def msa_cache_write(cache: bytes, pages: bytes, lens, cu_seqlens, total_tokens, 
 def msa_cache_read(cache: bytes, pages: bytes, lens, cu_seqlens, total_tokens, k, v, k_idx,
                    stream) -> int:
     return load().msa_cache_read(cache, pages, lens, cu_seqlens, total_tokens, k, v, k_idx, stream)
+
+
+def msa_decode_paged_workspace_size(cache: bytes, pages: bytes, H_q: int, topk: int) -> int:
+    return int(load().msa_decode_paged_workspace_size(cache, pages, H_q, topk))
+
+
+def msa_decode_paged(cache: bytes, pages: bytes, lens, H_q, topk, scale, q, q_idx, block_idx, o, lse, ws,
+                     ws_bytes, stream) -> int:
+    return load().msa_decode_paged(cache, pages, lens, H_q, topk, scale, q, q_idx, block_idx, o, lse, ws,
+                                   ws_bytes, stream)
+
+
+def msa_decode_paged_dense(cache: bytes, pages: bytes, lens, H_q, scale, q, o, lse, ws, ws_bytes,
+                           stream) -> int:
+    return load().msa_decode_paged_dense(cache, pages, lens, H_q, scale, q, o, lse, ws, ws_bytes, stream)
 
 
 def msa_version() -> int:

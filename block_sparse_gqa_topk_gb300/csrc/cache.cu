@@ -244,7 +244,7 @@ int run_cache(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
 
 }  // namespace
 
-int check_cache(const msa_paged_cache_t* c) {
+int check_cache_sizes(const msa_paged_cache_t* c) {
   if (!c) return MSA_ERR_ARG;
   if (c->num_pages < 0 || c->page_size <= 0 || c->H_kv <= 0 || c->d <= 0 || c->d_idx < 0)
     return MSA_ERR_SHAPE;
@@ -253,6 +253,12 @@ int check_cache(const msa_paged_cache_t* c) {
   if (c->d != 64 && c->d != 128) return MSA_ERR_UNSUPPORTED;
   if (c->d_idx != 0 && c->d_idx != 32 && c->d_idx != 64) return MSA_ERR_UNSUPPORTED;
   if (c->H_kv > 1024) return MSA_ERR_UNSUPPORTED;
+  return MSA_OK;
+}
+
+int check_cache(const msa_paged_cache_t* c) {
+  const int rc = check_cache_sizes(c);
+  if (rc) return rc;
   if (c->num_pages == 0) return MSA_OK;  // no page to address
   const bool f8 = c->kind == MSA_CACHE_E4M3;
   const void* need[] = {c->k, c->v, f8 ? c->k_scale : c->k, f8 ? c->v_scale : c->v,

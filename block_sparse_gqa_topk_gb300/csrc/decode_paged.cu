@@ -1,0 +1,826 @@
+// decode_paged.cu -- attention of one new token a sequence over a paged cache (see
+// include/msa.h): over the whole cache (msa_decode_paged_dense), or over the blocks that the
+// index branch selects (msa_decode_paged).
+//
+// For head h of group g, over the tokens T of the sequence (or of its selected blocks):
+//   s_j = scale q_h . k_j,  o = sum_j e^(s_j - m) v_j / l,  l = sum_j e^(s_j - m),
+//   lse = m + ln l,  m = max_j s_j,
+// in one pass with a running m, l and o, and joined over the parts of a split by
+//   lse = ln sum_i e^lse_i,  o = sum_i e^(lse_i - lse) o_i.
+//
+// The cache is read once and each byte meets 2 G multiply-adds, so HBM sets the pace and the
+// products run on mma.sync with the group's heads as the 16 rows.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include "decode_select.cuh"
+#include "kernels.h"
+#include "paged.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kUnit = 16 * kWarps;  // tokens of a unit of work: 16 a warp
+// CTAs over which a call's units are spread: three on each of the 152 SMs.  Each leaves at
+// most two partial results (its first and its last (sequence, group)), whatever the batch.
+constexpr int kCtas = 152 * 3;
+
+struct PagedDecode {
+  PageView pages;
+  const __nv_bfloat16* q;      // [B][H G][d]
+  const __nv_bfloat16* q_idx;  // [B][H][d_idx]
+  const void* k;
+  const void* v;
+  const float* k_scale;
+  const float* v_scale;
+  const __nv_bfloat16* k_idx;
+  const int32_t* lens;  // [B]
+  int32_t* block_idx;   // [B][H][topk]; null: the whole cache
+  float* pooled;        // [B][H][nb]
+  float* part_o;        // [2 kCtas][G][d]
+  float* part_lse;      // [2 kCtas][G], in bits (log2)
+  __nv_bfloat16* o;
+  float* lse;
+  int B, H, G, topk, nb;
+  float scale_log2;  // scale * log2 e: scores in bits
+  int* status;
+};
+
+// Length of sequence b; 0 (an empty slot) where it does not fit the table.
+__device__ __forceinline__ int seq_len(const PagedDecode& p, int b) {
+  const int n = __ldg(&p.lens[b]);
+  if (n < 0 || n > (int64_t)p.pages.max_pages * p.pages.page_size) {
+    set_status(p.status, MSA_ERR_ARG);
+    return 0;
+  }
+  return n;
+}
+
+__device__ __forceinline__ int seq_units(const PagedDecode& p, int len) {
+  if (p.block_idx) {  // the own block, cut at the length, comes last of the selected ones
+    const int blocks = (len + 127) / 128;
+    len -= max(0, blocks - p.topk) * 128;
+  }
+  return (len + kUnit - 1) / kUnit;
+}
+
+// The units of all (sequence, group) pairs in order, cut into equal runs.
+struct Schedule {
+  int64_t total;  // units
+  int64_t run;    // units of a CTA
+};
+
+// Every thread of the CTA gets the schedule and a sequence with its first unit: the one that
+// holds the first unit of run x (BY_RUN; any sequence where the run is empty), or sequence x.
+template <bool BY_RUN>
+__device__ __forceinline__ Schedule find_unit(const PagedDecode& p, int x, int* b_out, int64_t* base_out) {
+  __shared__ int64_t s_sum[kWarps];
+  __shared__ int s_b;
+  __shared__ int64_t s_base;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += (int64_t)seq_units(p, seq_len(p, b)) * p.H;
+  int64_t scan = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += y;
+  }
+  if (lane == 31) s_sum[warp] = scan;
+  if (tid == 0) {
+    s_b = 0;
+    s_base = 0;
+  }
+  __syncthreads();
+  Schedule sc;
+  sc.total = 0;
+  int64_t base = scan - mine;  // first unit of this thread's sequences
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) base += s_sum[w];
+    sc.total += s_sum[w];
+  }
+  sc.run = max((int64_t)1, (sc.total + kCtas - 1) / kCtas);
+  const int64_t want = sc.run * x;
+  if (BY_RUN ? want >= base && want < base + mine : x >= b0 && x < b1) {
+    int b = b0;
+    for (; BY_RUN || b < x; ++b) {
+      const int64_t n = (int64_t)seq_units(p, seq_len(p, b)) * p.H;
+      if (BY_RUN && want < base + n) break;
+      base += n;
+    }
+    s_b = b;
+    s_base = base;
+  }
+  __syncthreads();
+  *b_out = s_b;
+  *base_out = s_base;
+  return sc;
+}
+
+// D(16x8) += A(16x16, row) * B(16x8, col), fp16
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The two E4M3 codes in the low 16 bits as a pair of fp16 (exact).
+__device__ __forceinline__ uint32_t widen_f16(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+
+// 2^(a - b), 0 for a = -inf whatever b.
+__device__ __forceinline__ float weight(float a, float b) { return a == -INFINITY ? 0.f : exp2f(a - b); }
+
+// Shared memory of one warp's stage: 16 key rows and 16 value rows (and their scales).
+//   bf16: rows of 2 D bytes, 16-byte chunks XOR-swizzled for ldmatrix;
+//   E4M3: rows padded so that the 8-byte fragment loads fall in distinct banks.
+template <int D, bool F8>
+struct Stage {
+  static constexpr int ROW = F8 ? D : 2 * D;
+  static constexpr int KROW = F8 ? D + 32 : 2 * D;
+  static constexpr int VROW = F8 ? D + 16 : 2 * D;
+  static constexpr int V0 = 16 * KROW;
+  static constexpr int S0 = V0 + 16 * VROW;  // [2][16] scales
+  static constexpr int BYTES = S0 + (F8 ? 128 : 0);
+  static constexpr int COUNT = F8 ? 3 : 2;
+};
+
+// One warp's running softmax over its keys, for rows gq and gq + 8 of the fragments (heads;
+// with at most 8 heads the rows gq + 8 carry the low part of P instead, see step()).
+template <int D, bool F8, bool WIDE>
+struct WarpState {
+  static constexpr int R = WIDE ? 2 : 1;
+  static constexpr int NT = D / 8;
+  uint32_t qa[D / 16][4];  // query fragments (E4M3: fp16, scaled to [1, 2) by a power of two)
+  float o[NT][4];
+  float m[R], mv[R], l[R];  // max, max with the value scale (E4M3), this lane's part of the sum
+  float fac[R];             // accumulator -> score in bits
+
+  __device__ __forceinline__ void load_q(const PagedDecode& p, int64_t head0, int gq, int tq) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int h = gq + 8 * r;
+      const bool ok = h < p.G;
+      const __nv_bfloat16* row = p.q + (head0 + (ok ? h : 0)) * D;
+      if constexpr (!F8) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            qa[ks][r + 2 * half] =
+                ok ? __ldg(reinterpret_cast<const uint32_t*>(row + ks * 16 + half * 8 + 2 * tq)) : 0u;
+      } else {
+        // lane tq holds values 32 j + 8 tq + 0..7 of the row, in the order in which step()
+        // reads the codes of a key
+        float f[D / 32][8], amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          const uint4 w = ok ? __ldg(reinterpret_cast<const uint4*>(row + 32 * j + 8 * tq)) : make_uint4(0, 0, 0, 0);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[j][2 * e] = __uint_as_float(u[e] << 16);
+            f[j][2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+            amax = fmaxf(amax, fmaxf(fabsf(f[j][2 * e]), fabsf(f[j][2 * e + 1])));
+          }
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // 2^-e with 2^e <= amax: bf16 values keep all their bits in fp16, except those
+        // 2^-14 and more below the row's largest, which move by at most 2^-25 of it
+        const int e = min((int)(__float_as_uint(amax) >> 23), 253);
+        const float down = __uint_as_float((uint32_t)(254 - e) << 23);
+        if (r < R) fac[r] = p.scale_log2 / down;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            qa[2 * j + s][r] = pack_f16(f[j][4 * s] * down, f[j][4 * s + 1] * down);
+            qa[2 * j + s][r + 2] = pack_f16(f[j][4 * s + 2] * down, f[j][4 * s + 3] * down);
+          }
+      }
+    }
+    if constexpr (!F8) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) fac[r] = p.scale_log2;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = mv[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+  }
+
+  // The 16 keys of a landed stage, of which the first n are the sequence's.
+  __device__ __forceinline__ void step(const uint8_t* st, int n, int lane) {
+    using St = Stage<D, F8>;
+    const int gq = lane >> 2, tq = lane & 3;
+    float sc[2][4] = {};
+    if constexpr (!F8) {
+      const int mi = lane >> 3, row = (lane & 7) + (mi >> 1) * 8;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t kb[4];
+        ldmatrix_x4(kb, st + swz<St::ROW>(row, 2 * ks + (mi & 1)));
+        mma_bf16_16816(sc[0], qa[ks], kb[0], kb[1]);
+        mma_bf16_16816(sc[1], qa[ks], kb[2], kb[3]);
+      }
+    } else {
+      // the order of a product's terms is free: lane tq takes values 32 j + 8 tq + 0..7 of
+      // key gq as the k slots of steps 2 j and 2 j + 1, and so do the query fragments
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          const uint2 c = *reinterpret_cast<const uint2*>(st + (half * 8 + gq) * St::KROW + 32 * j + 8 * tq);
+          mma_f16_16816(sc[half], qa[2 * j], widen_f16(c.x & 0xffffu), widen_f16(c.x >> 16));
+          mma_f16_16816(sc[half], qa[2 * j + 1], widen_f16(c.y & 0xffffu), widen_f16(c.y >> 16));
+        }
+    }
+    // scores in bits; this lane's keys: 2 tq, 2 tq + 1, and those + 8
+    float lv[4];  // log2 of the value scales
+    if constexpr (F8) {
+      const float* scale = reinterpret_cast<const float*>(st + St::S0);
+      float kscale[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = (i >> 1) * 8 + 2 * tq + (i & 1);
+        kscale[i] = scale[key];
+        lv[i] = log2f(scale[16 + key]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < R; ++r) sc[i >> 1][2 * r + (i & 1)] *= kscale[i];
+    }
+    float pr[2][4], alpha[R];  // what multiplies the values
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float top = -INFINITY, topv = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float& s = sc[i >> 1][2 * r + (i & 1)];
+        const int key = (i >> 1) * 8 + 2 * tq + (i & 1);
+        s = key < n ? s * fac[r] : -INFINITY;
+        top = fmaxf(top, s);
+        if constexpr (F8) topv = fmaxf(topv, s + lv[i]);
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float m_new = fmaxf(m[r], top);
+      const float m_use = m_new == -INFINITY ? 0.f : m_new;
+      const float beta = ex2_fast(m[r] - m_use);
+      m[r] = m_new;
+      l[r] *= beta;
+      if constexpr (F8) {
+        // o is kept in units of 2^mv, mv the running max of score + log2(value scale): the
+        // weights of the codes then fit fp16 whatever the scales are
+        topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, 1));
+        topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, 2));
+        const float v_new = fmaxf(mv[r], topv);
+        const float v_use = v_new == -INFINITY ? 0.f : v_new;
+        alpha[r] = ex2_fast(mv[r] - v_use);
+        mv[r] = v_new;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float s = sc[i >> 1][2 * r + (i & 1)];
+          l[r] += ex2_fast(s - m_use);
+          pr[i >> 1][2 * r + (i & 1)] = s == -INFINITY ? 0.f : ex2_fast(s + lv[i] - v_use);
+        }
+      } else {
+        alpha[r] = beta;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float e = ex2_fast(sc[i >> 1][2 * r + (i & 1)] - m_use);
+          l[r] += e;
+          pr[i >> 1][2 * r + (i & 1)] = e;
+        }
+      }
+    }
+    bool same = alpha[0] == 1.f;
+    if constexpr (WIDE) same = same && alpha[R - 1] == 1.f;
+    if (!__all_sync(0xffffffffu, same)) {
+      const float a0 = alpha[0], a1 = alpha[R - 1];  // rows gq + 8: the same heads' low part
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        o[i][0] *= a0;
+        o[i][1] *= a0;
+        o[i][2] *= a1;
+        o[i][3] *= a1;
+      }
+    }
+    if constexpr (!F8) {
+      // P enters in two bf16 parts (together 2^-17 of its value): the output's own rounding
+      // stays its largest error.  With at most 8 heads the low parts ride in the rows that no
+      // head uses; with more they take a product of their own.
+      uint32_t hi[4] = {}, lo[4] = {};
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float e0 = pr[half][2 * r], e1 = pr[half][2 * r + 1];
+          const uint32_t h = pack_bf16(e0, e1);
+          hi[2 * half + r] = h;
+          lo[2 * half + r] = pack_bf16(e0 - __uint_as_float(h << 16), e1 - __uint_as_float(h & 0xffff0000u));
+        }
+      if constexpr (!WIDE) {
+        hi[1] = lo[0];
+        hi[3] = lo[2];
+      }
+      const int mi = lane >> 3, row = (lane & 7) + (mi & 1) * 8;
+#pragma unroll
+      for (int dt = 0; dt < D / 16; ++dt) {
+        uint32_t vb[4];
+        ldmatrix_x4_trans(vb, st + St::V0 + swz<St::ROW>(row, 2 * dt + (mi >> 1)));
+        mma_bf16_16816(o[2 * dt], hi, vb[0], vb[1]);
+        mma_bf16_16816(o[2 * dt + 1], hi, vb[2], vb[3]);
+        if constexpr (WIDE) {
+          mma_bf16_16816(o[2 * dt], lo, vb[0], vb[1]);
+          mma_bf16_16816(o[2 * dt + 1], lo, vb[2], vb[3]);
+        }
+      }
+    } else {
+      uint32_t a[4] = {};  // weights in fp16: 2^-12 of their value
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int r = 0; r < R; ++r) a[2 * half + r] = pack_f16(pr[half][2 * r], pr[half][2 * r + 1]);
+      // column gq of tile t (of 8) is value 64 c + 8 gq + t: a lane's 8 codes of each of its
+      // four keys serve the 8 tiles, two keys side by side in a fragment register
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint2 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = *reinterpret_cast<const uint2*>(st + St::V0 + ((i >> 1) * 8 + 2 * tq + (i & 1)) * St::VROW + 64 * c + 8 * gq);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          // codes t of two keys into the low 16 bits
+          const uint32_t sel = (t & 3) | ((4 + (t & 3)) << 4);
+          const uint32_t b0 = __byte_perm(t < 4 ? w[0].x : w[0].y, t < 4 ? w[1].x : w[1].y, sel);
+          const uint32_t b1 = __byte_perm(t < 4 ? w[2].x : w[2].y, t < 4 ? w[3].x : w[3].y, sel);
+          mma_f16_16816(o[8 * c + t], a, widen_f16(b0 & 0xffffu), widen_f16(b1 & 0xffffu));
+        }
+      }
+    }
+  }
+
+  // Column of the head's values that o[i][e] holds.
+  __device__ __forceinline__ static int column(int i, int e, int tq) {
+    return F8 ? (i >> 3) * 64 + 8 * (2 * tq + (e & 1)) + (i & 7) : 8 * i + 2 * tq + (e & 1);
+  }
+};
+
+// One CTA works through its run of units: span after span of one (sequence, group), each
+// warp on 16 of a unit's 64 tokens with its own stages in shared memory and its own running
+// softmax; the warps join when a span ends.  A whole (sequence, group) is written out, a
+// part of one goes to the CTA's slot 0 (its first span) or 1.
+template <int D, bool F8, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDecode p) {
+  using St = Stage<D, F8>;
+  constexpr int ROWS = WIDE ? 16 : 8;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float s_m[kWarps][16], s_mv[kWarps][16], s_l[kWarps][16];
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gq = lane >> 2, tq = lane & 3;
+  int b;
+  int64_t base;
+  const Schedule sc = find_unit<true>(p, blockIdx.x, &b, &base);
+  griddep_wait();  // the selected blocks
+  int64_t u = sc.run * blockIdx.x;
+  const int64_t u_end = min(sc.total, u + sc.run);
+  uint8_t* ring = smem + warp * St::COUNT * St::BYTES;
+  WarpState<D, F8, WIDE> ws;
+  for (int slot = 0; u < u_end; slot = 1) {
+    int len = seq_len(p, b);
+    int units = seq_units(p, len);
+    while (base + (int64_t)units * p.H <= u) {  // next sequence that has any
+      base += (int64_t)units * p.H;
+      ++b;
+      len = seq_len(p, b);
+      units = seq_units(p, len);
+    }
+    const int g = (int)((u - base) / units);
+    const int u0 = (int)(u - base - (int64_t)g * units);
+    const int n = (int)min((int64_t)(units - u0), u_end - u);
+    const int64_t head0 = ((int64_t)b * p.H + g) * p.G;
+    ws.load_q(p, head0, gq, tq);
+    const int32_t* blocks = p.block_idx ? p.block_idx + ((int64_t)b * p.H + g) * p.topk : nullptr;
+    // first token of this warp in unit i
+    auto first_token = [&](int i) {
+      const int x = u0 + i;
+      if (!blocks) return x * kUnit + warp * 16;
+      constexpr int PER = 128 / kUnit;
+      return __ldg(&blocks[x / PER]) * 128 + (x % PER) * kUnit + warp * 16;
+    };
+    auto load = [&](int i) {
+      if (i < n) {
+        uint8_t* st = ring + (i % St::COUNT) * St::BYTES;
+        const int pos = first_token(i);
+        const int have = min(16, len - pos);  // tokens of the sequence; none: nothing to load
+        if (have > 0) {
+          const int64_t row0 = pool_row(p.pages, b, pos);  // 16 tokens never straddle a page
+          if (row0 < 0) set_status(p.status, MSA_ERR_ARG);
+          constexpr int CH = St::ROW / 16;  // 16-byte chunks of a row
+          constexpr int RPI = 32 / CH;      // rows of one copy instruction
+          const int r0 = lane / CH, ch = lane % CH;
+          const int64_t step = (int64_t)p.H * St::ROW;
+          const int64_t at = row0 < 0 ? 0 : ((row0 + r0) * p.H + g) * St::ROW + ch * 16;
+          const uint8_t* kp = static_cast<const uint8_t*>(p.k) + at;
+          const uint8_t* vp = static_cast<const uint8_t*>(p.v) + at;
+#pragma unroll
+          for (int j = 0; j < 16 / RPI; ++j) {
+            const int r = r0 + j * RPI;
+            const bool ok = row0 >= 0 && r < have;  // else zeros: no stale NaN meets a weight of 0
+            const int64_t off = ok ? (int64_t)j * RPI * step : -(row0 < 0 ? 0 : (int64_t)r0 * step);
+            const uint32_t ko = F8 ? r * St::KROW + ch * 16 : swz<(F8 ? 128 : St::ROW)>(r, ch);
+            const uint32_t vo = F8 ? r * St::VROW + ch * 16 : ko;
+            cp_async_16(st + ko, kp + off, ok);
+            cp_async_16(st + St::V0 + vo, vp + off, ok);
+          }
+          if constexpr (F8) {
+            const int r = lane & 15;
+            const bool ok = row0 >= 0 && r < have;
+            const float* src = (lane < 16 ? p.k_scale : p.v_scale) + (ok ? (row0 + r) * p.H + g : 0);
+            cp_async_4(st + St::S0 + lane * 4, src, ok);
+          }
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < St::COUNT - 1; ++i) load(i);
+    for (int i = 0; i < n; ++i) {
+      cp_async_wait<St::COUNT - 2>();
+      __syncwarp();  // unit i has landed for all lanes, and all are done with unit i - 1
+      load(i + St::COUNT - 1);
+      const int have = len - first_token(i);
+      if (have > 0) ws.step(ring + (i % St::COUNT) * St::BYTES, have, lane);
+    }
+    cp_async_wait<0>();
+    // join the warps
+#pragma unroll
+    for (int r = 0; r < (WIDE ? 2 : 1); ++r) {
+      float l = ws.l[r];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (tq == 0) {
+        s_m[warp][gq + 8 * r] = ws.m[r];
+        s_mv[warp][gq + 8 * r] = F8 ? ws.mv[r] : ws.m[r];
+        s_l[warp][gq + 8 * r] = l;
+      }
+    }
+    __syncthreads();  // every warp is done with its stages
+    float* s_o = reinterpret_cast<float*>(smem);  // [kWarps][ROWS][D]
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int col = ws.column(i, e, tq);
+        float* row = s_o + (warp * ROWS + gq) * D + col;
+        if constexpr (WIDE) {
+          row[0] = ws.o[i][e];
+          row[8 * D] = ws.o[i][2 + e];
+        } else {
+          row[0] = ws.o[i][e] + ws.o[i][2 + e];
+        }
+      }
+    __syncthreads();
+    const bool whole = u0 == 0 && n == units;
+    const int64_t part = (int64_t)(2 * blockIdx.x + slot) * p.G;
+    for (int x = tid; x < p.G * (D / 2); x += kThreads) {
+      const int h = x / (D / 2), c = 2 * (x % (D / 2));
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][h]);
+      float l = 0.f;
+      float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        l += s_l[w][h] * weight(s_m[w][h], top);
+        const float f = weight(s_mv[w][h], top);
+        const float2 y = *reinterpret_cast<const float2*>(s_o + (w * ROWS + h) * D + c);
+        acc.x += f * y.x;
+        acc.y += f * y.y;
+      }
+      if (whole || l > 0.f) {  // a part whose scores are all -inf weighs nothing in the join
+        acc.x /= l;
+        acc.y /= l;
+      }
+      const float lse2 = top + log2f(l);
+      if (whole) {
+        *reinterpret_cast<uint32_t*>(p.o + (head0 + h) * D + c) = pack_bf16(acc.x, acc.y);
+        if (c == 0) p.lse[head0 + h] = lse2 * 0.6931471805599453f;
+      } else {
+        *reinterpret_cast<float2*>(p.part_o + (part + h) * D + c) = acc;
+        if (c == 0) p.part_lse[part + h] = lse2;
+      }
+    }
+    __syncthreads();  // the stages are free for the next span
+    u += n;
+  }
+}
+
+// One CTA per (sequence, group): joins its parts, if the split cut it; an empty sequence
+// gets o = 0 and lse = -inf.
+template <int D>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedDecode p) {
+  const int b = blockIdx.x / p.H, g = blockIdx.x - b * p.H;
+  int bb;
+  int64_t base;
+  const Schedule sc = find_unit<false>(p, b, &bb, &base);
+  const int units = seq_units(p, seq_len(p, b));
+  const int64_t head0 = ((int64_t)b * p.H + g) * p.G;
+  griddep_wait();
+  if (units == 0) {
+    for (int x = threadIdx.x; x < p.G * D; x += kThreads) p.o[head0 * D + x] = __float2bfloat16(0.f);
+    for (int h = threadIdx.x; h < p.G; h += kThreads) p.lse[head0 + h] = -INFINITY;
+    return;
+  }
+  const int64_t u0 = base + (int64_t)g * units, u1 = u0 + units;
+  const int c0 = (int)(u0 / sc.run), c1 = (int)((u1 - 1) / sc.run);
+  if (c0 == c1) return;
+  // the part of CTA c: its slot 1 where it began with another (sequence, group)
+  auto part_of = [&](int c) { return (int64_t)(2 * c + (c == c0 && u0 != sc.run * c0)) * p.G; };
+  for (int x = threadIdx.x; x < p.G * (D / 2); x += kThreads) {
+    const int h = x / (D / 2), col = 2 * (x % (D / 2));
+    float top = -INFINITY;
+    for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(&p.part_lse[part_of(c) + h]));
+    float l = 0.f;
+    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+      const int64_t at = part_of(c) + h;
+      const float w = weight(__ldcg(&p.part_lse[at]), top);
+      const float2 y = __ldcg(reinterpret_cast<const float2*>(p.part_o + at * D + col));
+      l += w;
+      acc.x = fmaf(w, y.x, acc.x);
+      acc.y = fmaf(w, y.y, acc.y);
+    }
+    *reinterpret_cast<uint32_t*>(p.o + (head0 + h) * D + col) = pack_bf16(acc.x / l, acc.y / l);
+    if (col == 0) p.lse[head0 + h] = (top + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+// pooled[b][g][c] = max over the 128 keys j of block c of q_idx[b, g] . k_idx[j], for every
+// block wholly before the new token's, as decode_pool_kernel computes it, over pages: one
+// warp per block, 8 NT groups per CTA, the index keys straight into mma.sync fragments (each
+// lane 16 contiguous bytes of a key row, the k slots permuted alike in the query fragments).
+// Bound by HBM: four tiles of 16 keys are in flight per warp.
+template <int DI, int NT>
+__global__ void __launch_bounds__(256) paged_pool_kernel(const PagedDecode p) {
+  griddep_launch_dependents();
+  const int b = blockIdx.y;
+  const int len = seq_len(p, b);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x * 8 + warp;
+  if (c >= (len - 1) / 128) return;  // also for an empty slot: (0 - 1) / 128 = 0
+  const int gq = lane >> 2, tq = lane & 3;
+  constexpr int NP = DI / 32;  // 32-wide d chunks: two k steps each
+  constexpr int U = 4;         // tiles in flight
+  // the pool row of each of the block's 8 tiles (a tile of 16 keys lies within one page)
+  int64_t row = lane < 8 ? pool_row(p.pages, b, c * 128 + lane * 16) : 0;
+  if (row < 0) set_status(p.status, MSA_ERR_ARG);
+  uint4 bq[NT][NP];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int grp = blockIdx.z * 8 * NT + nt * 8 + gq;
+    const uint4* qrow = reinterpret_cast<const uint4*>(p.q_idx + ((int64_t)b * p.H + grp) * DI);
+#pragma unroll
+    for (int j = 0; j < NP; ++j) bq[nt][j] = grp < p.H ? __ldg(&qrow[j * 4 + tq]) : make_uint4(0, 0, 0, 0);
+  }
+  float mx[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
+#pragma unroll
+  for (int m0 = 0; m0 < 8; m0 += U) {
+    uint4 w0[U][NP], w1[U][NP];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = __shfl_sync(0xffffffffu, row, m0 + u);
+      const uint4* kb = reinterpret_cast<const uint4*>(p.k_idx + (r < 0 ? 0 : r) * DI);
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        w0[u][j] = r < 0 ? make_uint4(0, 0, 0, 0) : __ldg(&kb[gq * (DI / 8) + j * 4 + tq]);
+        w1[u][j] = r < 0 ? make_uint4(0, 0, 0, 0) : __ldg(&kb[(gq + 8) * (DI / 8) + j * 4 + tq]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          const uint32_t a0[4] = {w0[u][j].x, w1[u][j].x, w0[u][j].y, w1[u][j].y};
+          const uint32_t a1[4] = {w0[u][j].z, w1[u][j].z, w0[u][j].w, w1[u][j].w};
+          mma_bf16_16816(acc, a0, bq[nt][j].x, bq[nt][j].y);
+          mma_bf16_16816(acc, a1, bq[nt][j].z, bq[nt][j].w);
+        }
+        mx[nt][0] = fmax3(mx[nt][0], acc[0], acc[2]);
+        mx[nt][1] = fmax3(mx[nt][1], acc[1], acc[3]);
+      }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float m = mx[nt][e];
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+      const int grp = blockIdx.z * 8 * NT + nt * 8 + 2 * tq + e;
+      if (gq == 0 && grp < p.H) p.pooled[((int64_t)b * p.H + grp) * p.nb + c] = m;
+    }
+}
+
+// One CTA per (group, sequence): the new token's blocks; none for an empty slot.
+template <int KM>
+__global__ void __launch_bounds__(256) paged_select_kernel(const PagedDecode p) {
+  griddep_launch_dependents();
+  const int64_t bg = (int64_t)blockIdx.y * p.H + blockIdx.x;
+  const int len = seq_len(p, blockIdx.y);
+  int32_t* dst = p.block_idx + bg * p.topk;
+  griddep_wait();
+  if (len == 0) {
+    for (int s = threadIdx.x; s < p.topk; s += blockDim.x) dst[s] = -1;
+    return;
+  }
+  select_blocks<KM>(p.pooled + bg * p.nb, (len - 1) / 128, p.topk, dst);
+}
+
+// Launches with programmatic stream serialization: the kernel may be scheduled while its
+// predecessor drains, and waits for it (griddep_wait) before it touches what that wrote.
+template <typename Kern>
+cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, bool after, cudaStream_t stream,
+                   const PagedDecode& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = after ? 1 : 0;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int D, bool F8, bool WIDE>
+cudaError_t launch_attn(const PagedDecode& p, cudaStream_t stream) {
+  constexpr int smem = kWarps * Stage<D, F8>::COUNT * Stage<D, F8>::BYTES;
+  static_assert(smem >= kWarps * (WIDE ? 16 : 8) * D * 4, "the join reuses the stages");
+  auto* kern = paged_attn_kernel<D, F8, WIDE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  if ((e = launch(kern, dim3(kCtas), kThreads, smem, p.block_idx != nullptr, stream, p)) != cudaSuccess)
+    return e;
+  return launch(paged_join_kernel<D>, dim3((unsigned)(p.B * p.H)), kThreads, 0, true, stream, p);
+}
+
+struct Layout {
+  size_t part_o, part_lse, pooled, bytes;
+};
+
+// Sizes of a call; MSA_OK and the workspace's layout.  topk = 0: the whole cache.
+int check_sizes(const msa_paged_cache_t* c, const msa_page_table_t* pt, int H_q, int topk, Layout* lay) {
+  int rc = check_cache_sizes(c);
+  if (rc) return rc;
+  if (!pt) return MSA_ERR_ARG;
+  if (pt->B < 0 || pt->max_pages < 0 || pt->stride < 0) return MSA_ERR_SHAPE;
+  const int64_t cap = (int64_t)pt->max_pages * c->page_size;
+  if (cap > 0x7fffffffLL) return MSA_ERR_UNSUPPORTED;
+  if (H_q <= 0 || H_q % c->H_kv != 0) return MSA_ERR_SHAPE;
+  const int G = H_q / c->H_kv;
+  if (G > 16 || topk > kMaxSelect) return MSA_ERR_UNSUPPORTED;
+  if ((int64_t)pt->B * c->H_kv > (1 << 24) || pt->B > 65535) return MSA_ERR_UNSUPPORTED;
+  if (topk > 0 && c->d_idx == 0) return MSA_ERR_SHAPE;
+  lay->part_o = 0;
+  lay->part_lse = align256((size_t)2 * kCtas * G * c->d * 4);
+  lay->pooled = lay->part_lse + align256((size_t)2 * kCtas * G * 4);
+  lay->bytes = lay->pooled + (topk > 0 ? align256((size_t)pt->B * c->H_kv * ((cap + 127) / 128) * 4) : 0);
+  return MSA_OK;
+}
+
+int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int32_t* lens, int H_q,
+              int topk, float scale, const void* q, const void* q_idx, int32_t* block_idx, void* o,
+              float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  Layout lay;
+  int rc = check_sizes(c, pt, H_q, topk, &lay);
+  if (rc) return rc;
+  if (!(scale > 0.f) || !isfinite(scale)) return MSA_ERR_ARG;
+  PagedDecode p = {};
+  if ((rc = check_cache(c))) return rc;
+  if ((rc = check_pages(c, pt, &p.pages))) return rc;
+  if (pt->B == 0) return MSA_OK;
+  const void* ptrs[] = {q, o, lse, topk > 0 ? q_idx : q, topk > 0 ? (const void*)block_idx : q};
+  for (const void* x : ptrs)
+    if (!x || (reinterpret_cast<uintptr_t>(x) & 15) != 0) return MSA_ERR_ARG;
+  if (!lens || (reinterpret_cast<uintptr_t>(lens) & 3)) return MSA_ERR_ARG;
+  if (!workspace || workspace_bytes < lay.bytes) return MSA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return MSA_ERR_ARG;
+  Ctx cx;
+  if ((rc = device_ctx(&cx))) return rc;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_idx = static_cast<const __nv_bfloat16*>(q_idx);
+  p.k = c->k;
+  p.v = c->v;
+  p.k_scale = c->k_scale;
+  p.v_scale = c->v_scale;
+  p.k_idx = static_cast<const __nv_bfloat16*>(c->k_idx);
+  p.lens = lens;
+  p.block_idx = topk > 0 ? block_idx : nullptr;
+  p.pooled = reinterpret_cast<float*>(w + lay.pooled);
+  p.part_o = reinterpret_cast<float*>(w + lay.part_o);
+  p.part_lse = reinterpret_cast<float*>(w + lay.part_lse);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.B = pt->B;
+  p.H = c->H_kv;
+  p.G = H_q / c->H_kv;
+  p.topk = topk;
+  p.nb = (int)(((int64_t)pt->max_pages * c->page_size + 127) / 128);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.status = cx.status;
+  cudaError_t e = cudaSuccess;
+  if (topk > 0) {
+    const int nt = p.H > 8 ? 2 : 1;
+    const dim3 grid((unsigned)((p.nb + 7) / 8), (unsigned)p.B, (unsigned)((p.H + 8 * nt - 1) / (8 * nt)));
+    if (grid.x > 0) {
+      if (c->d_idx == 64)
+        e = nt == 1 ? launch(paged_pool_kernel<64, 1>, grid, 256, 0, false, stream, p)
+                    : launch(paged_pool_kernel<64, 2>, grid, 256, 0, false, stream, p);
+      else
+        e = nt == 1 ? launch(paged_pool_kernel<32, 1>, grid, 256, 0, false, stream, p)
+                    : launch(paged_pool_kernel<32, 2>, grid, 256, 0, false, stream, p);
+      if (e != cudaSuccess) return MSA_ERR_CUDA;
+    }
+    const dim3 gsel((unsigned)p.H, (unsigned)p.B);
+    e = topk <= 16 ? launch(paged_select_kernel<15>, gsel, 256, 0, true, stream, p)
+                   : launch(paged_select_kernel<31>, gsel, 256, 0, true, stream, p);
+    if (e != cudaSuccess) return MSA_ERR_CUDA;
+  }
+  const bool wide = p.G > 8, f8 = c->kind == MSA_CACHE_E4M3;
+  if (c->d == 128) {
+    if (f8) e = wide ? launch_attn<128, true, true>(p, stream) : launch_attn<128, true, false>(p, stream);
+    else e = wide ? launch_attn<128, false, true>(p, stream) : launch_attn<128, false, false>(p, stream);
+  } else {
+    if (f8) e = wide ? launch_attn<64, true, true>(p, stream) : launch_attn<64, true, false>(p, stream);
+    else e = wide ? launch_attn<64, false, true>(p, stream) : launch_attn<64, false, false>(p, stream);
+  }
+  return finish(e);
+}
+
+}  // namespace
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" {
+
+size_t msa_decode_paged_workspace_size(const msa_paged_cache_t* c, const msa_page_table_t* pages, int H_q,
+                                       int topk) {
+  Layout lay;
+  return topk >= 0 && check_sizes(c, pages, H_q, topk, &lay) == MSA_OK ? lay.bytes : 0;
+}
+
+int msa_decode_paged(const msa_paged_cache_t* c, const msa_page_table_t* pages, const int32_t* lens,
+                     int H_q, int topk, float scale, const void* q, const void* q_idx,
+                     int32_t* block_idx, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                     cudaStream_t stream) {
+  if (topk <= 0) return MSA_ERR_SHAPE;
+  return run_paged(c, pages, lens, H_q, topk, scale, q, q_idx, block_idx, o, lse, workspace,
+                   workspace_bytes, stream);
+}
+
+int msa_decode_paged_dense(const msa_paged_cache_t* c, const msa_page_table_t* pages,
+                           const int32_t* lens, int H_q, float scale, const void* q, void* o, float* lse,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return run_paged(c, pages, lens, H_q, 0, scale, q, nullptr, nullptr, o, lse, workspace, workspace_bytes,
+                   stream);
+}
+
+}  // extern "C"

@@ -180,7 +180,8 @@ int finish(cudaError_t e);  // MSA_OK or MSA_ERR_CUDA
 
 // Checks of a paged cache and of a page table (cache.cu), shared by the calls that use them.
 struct PageView;
-int check_cache(const msa_paged_cache_t* c);
+int check_cache_sizes(const msa_paged_cache_t* c);
+int check_cache(const msa_paged_cache_t* c);  // sizes and pool pointers
 int check_pages(const msa_paged_cache_t* c, const msa_page_table_t* pt, PageView* out);
 
 // Argument checks and call sequences of the three training calls, shared by the fixed

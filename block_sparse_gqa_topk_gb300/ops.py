@@ -842,3 +842,63 @@ def msa_cache_read(cache: PagedCache, page_table, lens, cu_seqlens, total_tokens
                                      v.data_ptr(), _ptr(k_idx), _stream(dev))
         _lib.check(rc, "msa_cache_read")
     return k, v, k_idx
+
+
+# ---------------------------------------------------------------------------
+# Decode over a paged cache (see include/msa.h).  The workspace is allocated on the calling
+# stream: calls on other streams and other captured graphs never share it.
+# ---------------------------------------------------------------------------
+def _paged_args(q, cache, page_table, lens, topk, scale):
+    pages, B, _ = _pages_arg(cache, page_table, lens)
+    _need(q, "q", ndim=3)
+    H_q, d = q.shape[1:]
+    if q.device != cache.device or q.shape[0] != B or d != cache.d or H_q == 0 or H_q % cache.H_kv:
+        raise ValueError(f"q must be [{B}, a multiple of {cache.H_kv}, {cache.d}] on the cache's device, "
+                         f"got {tuple(q.shape)}")
+    if H_q // cache.H_kv > 16:
+        raise ValueError(f"at most 16 query heads a group, got {H_q // cache.H_kv}")
+    dev = cache.device
+    nws = _lib.msa_decode_paged_workspace_size(cache._c, pages, H_q, topk)
+    if nws == 0:
+        raise ValueError("the sizes of this call are outside the supported set")
+    return (pages, H_q, float(1.0 / math.sqrt(d) if scale is None else scale), torch.empty_like(q),
+            torch.empty((B, H_q), dtype=torch.float32, device=dev),
+            torch.empty(nws, dtype=torch.uint8, device=dev), nws)
+
+
+def msa_decode_paged(q, q_idx, cache: PagedCache, page_table, lens, topk: int = 16, *, scale=None):
+    """msa_decode over pages: q [B,H_q,d], q_idx [B,H_kv,d_idx] (new token); page_table int32
+    [B,max_pages], lens int32 [B] (lengths including the new token; 0: an empty slot).
+    Returns (block_idx [B,H_kv,topk] int32, o [B,H_q,d] bf16, lse [B,H_q] f32)."""
+    if not 1 <= topk <= 32:
+        raise ValueError(f"topk must be 1 .. 32, got {topk}")
+    if not isinstance(cache, PagedCache):
+        raise TypeError("cache must be a PagedCache")
+    if cache.k_idx is None:
+        raise ValueError("the cache has no index keys")
+    pages, H_q, scale, o, lse, ws, nws = _paged_args(q, cache, page_table, lens, topk, scale)
+    _need(q_idx, "q_idx", ndim=3)
+    B, H_kv = q.shape[0], cache.H_kv
+    if tuple(q_idx.shape) != (B, H_kv, cache.d_idx) or q_idx.device != cache.device:
+        raise ValueError(f"q_idx must be {(B, H_kv, cache.d_idx)} on the cache's device, got {tuple(q_idx.shape)}")
+    block_idx = torch.empty((B, H_kv, topk), dtype=torch.int32, device=cache.device)
+    if B:
+        with _on(cache.device):
+            rc = _lib.msa_decode_paged(cache._c, pages, lens.data_ptr(), H_q, topk, scale, q.data_ptr(),
+                                       q_idx.data_ptr(), block_idx.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                       ws.data_ptr(), nws, _stream(cache.device))
+        _lib.check(rc, "msa_decode_paged")
+    return block_idx, o, lse
+
+
+def msa_decode_paged_dense(q, cache: PagedCache, page_table, lens, *, scale=None):
+    """Attention of one new token a sequence over its whole paged cache: arguments as in
+    msa_decode_paged.  Returns (o [B,H_q,d] bf16, lse [B,H_q] f32)."""
+    pages, H_q, scale, o, lse, ws, nws = _paged_args(q, cache, page_table, lens, 0, scale)
+    if q.shape[0]:
+        with _on(cache.device):
+            rc = _lib.msa_decode_paged_dense(cache._c, pages, lens.data_ptr(), H_q, scale, q.data_ptr(),
+                                             o.data_ptr(), lse.data_ptr(), ws.data_ptr(), nws,
+                                             _stream(cache.device))
+        _lib.check(rc, "msa_decode_paged_dense")
+    return o, lse

@@ -384,6 +384,33 @@ int msa_cache_read(const msa_paged_cache_t* c, const msa_page_table_t* pages, co
                    const int32_t* cu_seqlens, int total_tokens, void* k, void* v, void* k_idx,
                    cudaStream_t stream);
 
+/*
+ * Decode over a paged cache: one new query token per sequence, its own k, v and k_idx
+ * already in the cache (msa_cache_write), lens[b] the length with it.
+ *   msa_decode_paged: msa_decode's computation (block selection over the index keys, ties to
+ *     the lower block, then attention over the selected blocks) on pages.  topk <= 32.
+ *   msa_decode_paged_dense: attention over all lens[b] tokens (the dense set of the indexer
+ *     warm-up, and layers without an index branch).
+ * lens[b] = 0 is an empty slot of a padded batch: o = 0, lse = -inf, block_idx all -1.  A
+ *   length that is negative or past the table sets MSA_ERR_ARG in the status word and counts
+ *   as 0; a page id outside the pool sets it too and reads as zero rows.
+ * H_q a multiple of the cache's H_kv with G = H_q / H_kv <= 16 (any G); B <= 65535.
+ * In:  q [B][H_q][d], q_idx [B][H_kv][d_idx] (bf16), pages, lens (device int32 [B]).
+ * Out: block_idx [B][H_kv][topk] (int32), o [B][H_q][d] (bf16), lse [B][H_q] (float32).
+ * Workspace: msa_decode_paged_workspace_size (topk 0 for the dense call; 0 if the sizes are
+ *   invalid), 256-byte aligned.  The result does not depend on what it held, nor on the order
+ *   in which the GPU runs the parts: no atomics take part.
+ */
+size_t msa_decode_paged_workspace_size(const msa_paged_cache_t* c, const msa_page_table_t* pages, int H_q,
+                                       int topk);
+int msa_decode_paged(const msa_paged_cache_t* c, const msa_page_table_t* pages, const int32_t* lens,
+                     int H_q, int topk, float scale, const void* q, const void* q_idx,
+                     int32_t* block_idx, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                     cudaStream_t stream);
+int msa_decode_paged_dense(const msa_paged_cache_t* c, const msa_page_table_t* pages,
+                           const int32_t* lens, int H_q, float scale, const void* q, void* o, float* lse,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Synchronises `stream`, then reads and clears the current device's status word
  * (MSA_OK or the first MSA_ERR_* a kernel recorded since the last read). */
 int msa_get_device_status(cudaStream_t stream, int* status);

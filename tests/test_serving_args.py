@@ -111,3 +111,34 @@ def test_cache_calls_check_their_arguments():
     assert write(cu=258) == ARG
     assert write(s=_lib.CACHE_STRIDES.pack(128, 64, 128, 60, 32)) == ARG
     assert read(cu=None) == ARG
+
+
+def test_decode_calls_check_their_arguments():
+    need = _lib.msa_decode_paged_workspace_size(cache(), table(), 4, 0)
+    more = _lib.msa_decode_paged_workspace_size(cache(), table(n=1 << 20), 4, 4)
+    assert 0 < need < more
+    big = 1 << 40
+
+    def dense(c=cache(), t=table(), lens=256, H_q=4, scale=1.0, q=256, o=256, lse=256, ws=256, n=big):
+        return _lib.msa_decode_paged_dense(c, t, lens, H_q, scale, q, o, lse, ws, n, None)
+
+    def sparse(c=cache(), t=table(), lens=256, H_q=4, topk=4, scale=1.0, q=256, qi=256, bi=256, o=256, lse=256,
+               ws=256, n=big):
+        return _lib.msa_decode_paged(c, t, lens, H_q, topk, scale, q, qi, bi, o, lse, ws, n, None)
+
+    for f in (dense, sparse):
+        for kw, code in [(dict(c=None), ARG), (dict(t=None), ARG), (dict(c=cache(d=96)), UNSUP),
+                         (dict(c=cache(page=8)), UNSUP), (dict(c=cache(k=0)), ARG), (dict(t=table(ids=0)), ARG),
+                         (dict(t=table(B=-1)), SHAPE), (dict(t=table(B=65536)), UNSUP),
+                         (dict(t=table(n=1 << 28)), UNSUP), (dict(H_q=3), SHAPE), (dict(H_q=0), SHAPE),
+                         (dict(H_q=34), UNSUP), (dict(scale=0.0), ARG), (dict(scale=float("nan")), ARG),
+                         (dict(q=None), ARG), (dict(o=264), ARG), (dict(lse=None), ARG), (dict(lens=None), ARG),
+                         (dict(lens=258), ARG), (dict(ws=None), WS), (dict(n=need - 1), WS), (dict(ws=128), ARG),
+                         (dict(t=table(B=0)), OK)]:
+            assert f(**kw) == code, (f, kw)
+    for kw, code in [(dict(topk=0), SHAPE), (dict(topk=33), UNSUP), (dict(c=cache(di=0)), SHAPE),
+                     (dict(qi=None), ARG), (dict(bi=264), ARG)]:
+        assert sparse(**kw) == code, kw
+    size = _lib.msa_decode_paged_workspace_size
+    assert size(cache(), table(), 4, -1) == 0 and size(cache(), table(), 3, 0) == 0
+    assert size(cache(di=0), table(), 4, 4) == 0 and size(cache(k=0), table(ids=0), 4, 4) > 0

@@ -33,6 +33,8 @@ struct CacheParams {
   __nv_bfloat16* xi;
   int64_t sk[2], sv[2], si;  // their strides: token, head; token
   int rows;                  // of a token: 2 H, and the index key's where there is one
+  float inv_rows;
+  int steps;                 // chunks of a warp
   int d_idx;
   int* status;
 };
@@ -73,114 +75,150 @@ __device__ __forceinline__ void widen(uint4 w, float (&f)[8]) {
   }
 }
 
-// One warp per (token, chunk of rows): it finds the token's place once and moves kSteps
-// rows a lane group with all their loads in flight.  Rows of a token: the keys of its H
-// heads, the values, then the index key.
+// E4M3 codes of a row's 8 values at scale sc (amax / 448): the code nearest to the float32
+// quotient x / sc.  With r the rounded reciprocal, q0 = x r and the remainder x - q0 sc, which
+// one fma gives exactly, q0 + r (x - q0 sc) is the rounded quotient (Markstein 1990); that it
+// gives every code that division gives is checked over all pairs of bf16 significands.  Rows
+// whose amax leaves the range in which nothing underflows are divided.
+__device__ __forceinline__ uint2 quantize8(const float (&f)[8], float amax, float sc) {
+  float q[8];
+  if (amax > 1e-18f && amax < 1e18f) {
+    const float r = __frcp_rn(sc);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float q0 = f[e] * r;
+      q[e] = copysignf(fmaf(fmaf(-q0, sc, f[e]), r, q0), f[e]);  // a zero keeps its sign
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = __fdiv_rn(f[e], sc);
+  }
+  uint32_t c[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(q[e], q[e + 1]), __NV_SATFINITE, __NV_E4M3);
+    c[e >> 2] |= (two & 0xffffu) << (8 * (e & 3));
+  }
+  return make_uint2(c[0], c[1]);
+}
+
+// Items are the rows of the packed tokens in order: the keys of a token's H heads, the
+// values, the index key.  A warp takes `steps` chunks of CHUNK consecutive items; its lanes
+// find the places of the (at most 32) tokens among them together, so the chain of lookups
+// (sequence, length, page) is paid once, and then move kSteps rows at a time with all their
+// loads in flight.
 template <int D, bool F8, bool WRITE>
-__global__ void __launch_bounds__(kThreads) cache_kernel(const CacheParams p) {
+__global__ void __launch_bounds__(kThreads) cache_kernel(const __grid_constant__ CacheParams p) {
   constexpr int LPR = D / 8;      // lanes of a row, 8 values each
   constexpr int RPS = 32 / LPR;   // rows of a step
   constexpr int CHUNK = RPS * kSteps;
   const int lane = threadIdx.x & 31, sub = lane % LPR;
-  const int chunks = (p.rows + CHUNK - 1) / CHUNK;
-  const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
-  if (unit >= (int64_t)p.T * chunks) return;
-  const int t = (int)(unit / chunks);
-  const int r0 = (int)(unit - (int64_t)t * chunks) * CHUNK + lane / LPR;
-  int64_t row = token_row(p, t);
-  if (row == kNoToken) return;
-  const bool bad = row == kNoPlace;
-  if (bad) {
-    if (lane == 0) set_status(p.status, MSA_ERR_ARG);
-    if (WRITE) return;
-    row = 0;  // not read: the read's rows of a missing place are zeros
+  const int64_t items = (int64_t)p.T * p.rows;
+  const int64_t i0 = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5) * (CHUNK * p.steps);
+  if (i0 >= items) return;
+  const int n = (int)min((int64_t)CHUNK * p.steps, items - i0);
+  const int t0 = (int)(i0 / p.rows);
+  const int skip = (int)(i0 - (int64_t)t0 * p.rows);
+  int64_t place = kNoToken;
+  if (lane * p.rows < skip + n) {
+    place = token_row(p, t0 + lane);
+    if (place == kNoPlace) set_status(p.status, MSA_ERR_ARG);
   }
-  uint4* packed[kSteps];
-  void* pool[kSteps];
-  float* scale[kSteps];
-  int kind[kSteps];  // 0: nothing, 1: key or value, 2: index key
+  for (int c = 0; c < n; c += CHUNK) {
+    uint4* packed[kSteps];
+    void* pool[kSteps];
+    float* scale[kSteps];
+    int kind[kSteps];  // 0: nothing, 1: key or value, 2: index key; negative: its place is missing
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int r = r0 + i * RPS;
-    kind[i] = r < 2 * p.H ? 1 : r < p.rows && sub * 8 < p.d_idx ? 2 : 0;
-    const bool v = r >= p.H;
-    const int h = v ? r - p.H : r;
-    const int64_t cell = row * p.H + h;
-    if (kind[i] == 2) {
-      packed[i] = reinterpret_cast<uint4*>(p.xi + t * p.si + sub * 8);
-      pool[i] = p.k_idx + row * p.d_idx + sub * 8;
-    } else {
-      packed[i] = reinterpret_cast<uint4*>((v ? p.xv + t * p.sv[0] + h * p.sv[1]
-                                              : p.xk + t * p.sk[0] + h * p.sk[1]) + sub * 8);
-      pool[i] = static_cast<uint8_t*>(v ? p.v : p.k) + (cell * D + sub * 8) * (F8 ? 1 : 2);
-      scale[i] = F8 ? (v ? p.v_scale : p.k_scale) + cell : nullptr;
+    for (int i = 0; i < kSteps; ++i) {
+      const int x = c + i * RPS + lane / LPR;
+      const int y = x + skip;
+      const int tok = (int)(((float)y + 0.5f) * p.inv_rows);  // exact: y < 2^12
+      const int r = y - tok * p.rows;
+      int64_t row = __shfl_sync(0xffffffffu, place, tok);
+      kind[i] = x >= n || row == kNoToken ? 0 : r < 2 * p.H ? 1 : sub * 8 < p.d_idx ? 2 : 0;
+      if (row < 0) {
+        kind[i] = -kind[i];
+        row = 0;
+      }
+      const int64_t t = t0 + tok;
+      const bool v = r >= p.H;
+      const int h = v ? r - p.H : r;
+      if (r == 2 * p.H) {
+        packed[i] = reinterpret_cast<uint4*>(p.xi + t * p.si + sub * 8);
+        pool[i] = p.k_idx + row * p.d_idx + sub * 8;
+      } else {
+        const int64_t cell = row * p.H + h;
+        packed[i] = reinterpret_cast<uint4*>((v ? p.xv + t * p.sv[0] + h * p.sv[1]
+                                                : p.xk + t * p.sk[0] + h * p.sk[1]) + sub * 8);
+        pool[i] = static_cast<uint8_t*>(v ? p.v : p.k) + (cell * D + sub * 8) * (F8 ? 1 : 2);
+        scale[i] = F8 ? (v ? p.v_scale : p.k_scale) + cell : nullptr;
+      }
     }
-  }
-  uint4 w[kSteps];
-  float s[kSteps];
+    uint4 w[kSteps];
+    float s[kSteps];
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    w[i] = make_uint4(0, 0, 0, 0);
-    s[i] = 0.f;
-    if (kind[i] == 0 || bad) continue;
-    if (WRITE) {
-      w[i] = __ldg(packed[i]);
-    } else if (F8 && kind[i] == 1) {
-      const uint2 c = *static_cast<const uint2*>(pool[i]);
-      w[i].x = c.x;
-      w[i].y = c.y;
-      s[i] = *scale[i];
-    } else {
-      w[i] = *static_cast<const uint4*>(pool[i]);
+    for (int i = 0; i < kSteps; ++i) {
+      w[i] = make_uint4(0, 0, 0, 0);  // what a missing place reads as
+      s[i] = 0.f;
+      if (kind[i] <= 0) continue;
+      if (WRITE) {
+        w[i] = __ldg(packed[i]);
+      } else if (F8 && kind[i] == 1) {
+        const uint2 x = *static_cast<const uint2*>(pool[i]);
+        w[i].x = x.x;
+        w[i].y = x.y;
+        s[i] = *scale[i];
+      } else {
+        w[i] = *static_cast<const uint4*>(pool[i]);
+      }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    if constexpr (F8 && WRITE) {
-      float f[8];
-      widen(w[i], f);
-      float amax = 0.f;
+    for (int i = 0; i < kSteps; ++i) {
+      if constexpr (F8 && WRITE) {
+        float f[8];
+        widen(w[i], f);
+        float amax = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      if (kind[i] == 1) {
-        const float sc = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-        uint32_t c[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float2 q = make_float2(__fdiv_rn(f[e], sc), __fdiv_rn(f[e + 1], sc));
-          const uint32_t two = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
-          c[e >> 2] |= (two & 0xffffu) << (8 * (e & 3));
+        for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (kind[i] == 1) {
+          const float sc = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+          *static_cast<uint2*>(pool[i]) = quantize8(f, amax, sc);
+          if (sub == 0) *scale[i] = sc;
+          continue;
         }
-        *static_cast<uint2*>(pool[i]) = make_uint2(c[0], c[1]);
-        if (sub == 0) *scale[i] = sc;
-        continue;
       }
-    }
-    if (kind[i] == 0) continue;
-    if (WRITE) {
-      *static_cast<uint4*>(pool[i]) = w[i];
-    } else if (F8 && kind[i] == 1) {
-      uint32_t y[4];
+      if (WRITE ? kind[i] <= 0 : kind[i] == 0) continue;
+      if (WRITE) {
+        *static_cast<uint4*>(pool[i]) = w[i];
+      } else if (F8 && kind[i] == 1) {
+        uint32_t y[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)((e < 2 ? w[i].x : w[i].y) >> (16 * (e & 1)));
-        const float2 v2 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
-        y[e] = pack_bf16(v2.x * s[i], v2.y * s[i]);
+        for (int e = 0; e < 4; ++e) {
+          const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)((e < 2 ? w[i].x : w[i].y) >> (16 * (e & 1)));
+          const float2 v2 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
+          y[e] = pack_bf16(v2.x * s[i], v2.y * s[i]);
+        }
+        *packed[i] = make_uint4(y[0], y[1], y[2], y[3]);
+      } else {
+        *packed[i] = w[i];
       }
-      *packed[i] = make_uint4(y[0], y[1], y[2], y[3]);
-    } else {
-      *packed[i] = w[i];
     }
   }
 }
 
 template <int D, bool F8, bool WRITE>
-cudaError_t launch_cache(const CacheParams& p, cudaStream_t st) {
+cudaError_t launch_cache(CacheParams& p, int num_sms, cudaStream_t st) {
   constexpr int CHUNK = 32 / (D / 8) * kSteps;
-  const int64_t warps = (int64_t)p.T * ((p.rows + CHUNK - 1) / CHUNK);
+  const int64_t items = (int64_t)p.T * p.rows;
+  // chunks of a warp: up to 8, while 16 warps a SM remain and 32 lanes find all its tokens
+  p.steps = 8;
+  while (p.steps > 1 && (items / (CHUNK * p.steps) < 16 * num_sms || CHUNK * p.steps > 30 * p.rows)) p.steps >>= 1;
+  const int64_t warps = (items + CHUNK * p.steps - 1) / (CHUNK * p.steps);
   const int64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cache_kernel<D, F8, WRITE><<<(unsigned)grid, kThreads, 0, st>>>(p);
   note_launch();
   return cudaGetLastError();
@@ -209,6 +247,7 @@ int run_cache(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   for (int i = 0; i < 5; ++i)
     if ((i < 4 || k_idx) && strides[i] % 8) return MSA_ERR_ARG;  // rows start on 16 bytes
   p.rows = 2 * c->H_kv + (k_idx ? 1 : 0);
+  p.inv_rows = 1.f / (float)p.rows;
   if ((int64_t)total_tokens * p.rows >= (int64_t)1 << 33) return MSA_ERR_UNSUPPORTED;
   Ctx cx;
   if ((rc = device_ctx(&cx))) return rc;
@@ -236,9 +275,11 @@ int run_cache(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   const bool f8 = c->kind == MSA_CACHE_E4M3;
   cudaError_t e;
   if (c->d == 128)
-    e = f8 ? launch_cache<128, true, WRITE>(p, stream) : launch_cache<128, false, WRITE>(p, stream);
+    e = f8 ? launch_cache<128, true, WRITE>(p, cx.num_sms, stream)
+           : launch_cache<128, false, WRITE>(p, cx.num_sms, stream);
   else
-    e = f8 ? launch_cache<64, true, WRITE>(p, stream) : launch_cache<64, false, WRITE>(p, stream);
+    e = f8 ? launch_cache<64, true, WRITE>(p, cx.num_sms, stream)
+           : launch_cache<64, false, WRITE>(p, cx.num_sms, stream);
   return finish(e);
 }
 

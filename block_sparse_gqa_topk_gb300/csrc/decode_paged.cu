@@ -42,6 +42,7 @@ struct PagedDecode {
   float* pooled;        // [B][H][nb]
   float* part_o;        // [2 kCtas][G][d]
   float* part_lse;      // [2 kCtas][G], in bits (log2)
+  int64_t* starts;      // [B + 1] first unit of each sequence, written for the join
   __nv_bfloat16* o;
   float* lse;
   int B, H, G, topk, nb;
@@ -72,11 +73,14 @@ struct Schedule {
   int64_t total;  // units
   int64_t run;    // units of a CTA
 };
+__device__ __forceinline__ int64_t run_units(int64_t total) {
+  return max((int64_t)1, (total + kCtas - 1) / kCtas);
+}
 
-// Every thread of the CTA gets the schedule and a sequence with its first unit: the one that
-// holds the first unit of run x (BY_RUN; any sequence where the run is empty), or sequence x.
-template <bool BY_RUN>
-__device__ __forceinline__ Schedule find_unit(const PagedDecode& p, int x, int* b_out, int64_t* base_out) {
+// Every thread of the CTA gets the schedule, and a sequence with its first unit: the one that
+// holds the first unit of the CTA's run (any sequence where the run is empty).  CTA 0 leaves
+// the sequences' first units for the join.
+__device__ __forceinline__ Schedule find_run(const PagedDecode& p, int* b_out, int64_t* base_out) {
   __shared__ int64_t s_sum[kWarps];
   __shared__ int s_b;
   __shared__ int64_t s_base;
@@ -105,18 +109,21 @@ __device__ __forceinline__ Schedule find_unit(const PagedDecode& p, int x, int* 
     if (w < warp) base += s_sum[w];
     sc.total += s_sum[w];
   }
-  sc.run = max((int64_t)1, (sc.total + kCtas - 1) / kCtas);
-  const int64_t want = sc.run * x;
-  if (BY_RUN ? want >= base && want < base + mine : x >= b0 && x < b1) {
-    int b = b0;
-    for (; BY_RUN || b < x; ++b) {
+  sc.run = run_units(sc.total);
+  const int64_t want = sc.run * blockIdx.x;
+  const bool here = want >= base && want < base + mine;
+  if (here || blockIdx.x == 0) {
+    for (int b = b0; b < b1; ++b) {
       const int64_t n = (int64_t)seq_units(p, seq_len(p, b)) * p.H;
-      if (BY_RUN && want < base + n) break;
+      if (blockIdx.x == 0) p.starts[b] = base;
+      if (here && want >= base && want < base + n) {
+        s_b = b;
+        s_base = base;
+      }
       base += n;
     }
-    s_b = b;
-    s_base = base;
   }
+  if (blockIdx.x == 0 && tid == 0) p.starts[p.B] = sc.total;
   __syncthreads();
   *b_out = s_b;
   *base_out = s_base;
@@ -405,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
   const int gq = lane >> 2, tq = lane & 3;
   int b;
   int64_t base;
-  const Schedule sc = find_unit<true>(p, blockIdx.x, &b, &base);
+  const Schedule sc = find_run(p, &b, &base);
   griddep_wait();  // the selected blocks
   int64_t u = sc.run * blockIdx.x;
   const int64_t u_end = min(sc.total, u + sc.run);
@@ -425,34 +432,59 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
     const int n = (int)min((int64_t)(units - u0), u_end - u);
     const int64_t head0 = ((int64_t)b * p.H + g) * p.G;
     ws.load_q(p, head0, gq, tq);
-    const int32_t* blocks = p.block_idx ? p.block_idx + ((int64_t)b * p.H + g) * p.topk : nullptr;
-    // first token of this warp in unit i
+    // Page ids of the next 32 units sit in the lanes of a register (and those of the 32 after
+    // them are on their way), so that no lookup stands in front of a copy.  Selected blocks,
+    // at most 32, sit in another.
+    int blk = 0;
+    if (p.block_idx && lane < p.topk) blk = __ldg(&p.block_idx[((int64_t)b * p.H + g) * p.topk + lane]);
+    // first token of this warp in unit u0 + i
     auto first_token = [&](int i) {
       const int x = u0 + i;
-      if (!blocks) return x * kUnit + warp * 16;
+      if (!p.block_idx) return x * kUnit + warp * 16;
       constexpr int PER = 128 / kUnit;
-      return __ldg(&blocks[x / PER]) * 128 + (x % PER) * kUnit + warp * 16;
+      return __shfl_sync(0xffffffffu, blk, (x / PER) & 31) * 128 + (x % PER) * kUnit + warp * 16;
     };
+    const int32_t* table = p.pages.table + (int64_t)b * p.pages.table_stride;
+    auto page_ids = [&](int i) {  // of units i .. i + 31, one a lane; -1 where there is none
+      int x = u0 + i + lane, tok;
+      if (!p.block_idx) {
+        tok = x * kUnit + warp * 16;
+      } else {
+        constexpr int PER = 128 / kUnit;
+        const int c = __shfl_sync(0xffffffffu, blk, (x / PER) & 31);
+        tok = c * 128 + (x % PER) * kUnit + warp * 16;
+      }
+      return i + lane < n && tok < len ? __ldg(&table[page_of(p.pages, tok)]) : -1;
+    };
+    int ids = page_ids(0), ids_next = page_ids(32);
     auto load = [&](int i) {
       if (i < n) {
+        if (i > 0 && (i & 31) == 0) {
+          ids = ids_next;
+          ids_next = page_ids(i + 32);
+        }
         uint8_t* st = ring + (i % St::COUNT) * St::BYTES;
         const int pos = first_token(i);
+        const int id = __shfl_sync(0xffffffffu, ids, i & 31);
         const int have = min(16, len - pos);  // tokens of the sequence; none: nothing to load
         if (have > 0) {
-          const int64_t row0 = pool_row(p.pages, b, pos);  // 16 tokens never straddle a page
-          if (row0 < 0) set_status(p.status, MSA_ERR_ARG);
+          // 16 tokens never straddle a page
+          const bool good = (unsigned)id < (unsigned)p.pages.num_pages;
+          if (!good) set_status(p.status, MSA_ERR_ARG);
+          const int64_t row0 =
+              good ? (int64_t)id * p.pages.page_size + (pos - page_of(p.pages, pos) * p.pages.page_size) : 0;
           constexpr int CH = St::ROW / 16;  // 16-byte chunks of a row
           constexpr int RPI = 32 / CH;      // rows of one copy instruction
           const int r0 = lane / CH, ch = lane % CH;
           const int64_t step = (int64_t)p.H * St::ROW;
-          const int64_t at = row0 < 0 ? 0 : ((row0 + r0) * p.H + g) * St::ROW + ch * 16;
+          const int64_t at = (row0 * p.H + g) * St::ROW + ch * 16;
           const uint8_t* kp = static_cast<const uint8_t*>(p.k) + at;
           const uint8_t* vp = static_cast<const uint8_t*>(p.v) + at;
 #pragma unroll
           for (int j = 0; j < 16 / RPI; ++j) {
             const int r = r0 + j * RPI;
-            const bool ok = row0 >= 0 && r < have;  // else zeros: no stale NaN meets a weight of 0
-            const int64_t off = ok ? (int64_t)j * RPI * step : -(row0 < 0 ? 0 : (int64_t)r0 * step);
+            const bool ok = good && r < have;  // else zeros: no stale NaN meets a weight of 0
+            const int64_t off = ok ? r * step : 0;
             const uint32_t ko = F8 ? r * St::KROW + ch * 16 : swz<(F8 ? 128 : St::ROW)>(r, ch);
             const uint32_t vo = F8 ? r * St::VROW + ch * 16 : ko;
             cp_async_16(st + ko, kp + off, ok);
@@ -460,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
           }
           if constexpr (F8) {
             const int r = lane & 15;
-            const bool ok = row0 >= 0 && r < have;
+            const bool ok = good && r < have;
             const float* src = (lane < 16 ? p.k_scale : p.v_scale) + (ok ? (row0 + r) * p.H + g : 0);
             cp_async_4(st + St::S0 + lane * 4, src, ok);
           }
@@ -541,44 +573,89 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
   }
 }
 
-// One CTA per (sequence, group): joins its parts, if the split cut it; an empty sequence
-// gets o = 0 and lse = -inf.
+// Joins the parts of every (sequence, group) that the split cut; an empty sequence gets
+// o = 0 and lse = -inf.  Grid (B H, head splits): a CTA takes heads blockIdx.y, + gridDim.y,
+// ...; its warps take parts in turn, a lane 4 columns (8 warps x 32 lanes x 4 = 8 parts of 128
+// columns at once; 16 of 64).
+constexpr int kJoinThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedDecode p) {
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedDecode p) {
+  constexpr int LANES = D / 4;                    // threads of a part
+  constexpr int PARTS = kJoinThreads / LANES;     // parts at once
+  __shared__ float s_w[kCtas + 1], s_red[8], s_sum[8];
+  __shared__ float4 s_acc[PARTS][LANES];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / p.H, g = blockIdx.x - b * p.H;
-  int bb;
-  int64_t base;
-  const Schedule sc = find_unit<false>(p, b, &bb, &base);
-  const int units = seq_units(p, seq_len(p, b));
   const int64_t head0 = ((int64_t)b * p.H + g) * p.G;
   griddep_wait();
-  if (units == 0) {
-    for (int x = threadIdx.x; x < p.G * D; x += kThreads) p.o[head0 * D + x] = __float2bfloat16(0.f);
-    for (int h = threadIdx.x; h < p.G; h += kThreads) p.lse[head0 + h] = -INFINITY;
+  const int64_t first = __ldcg(&p.starts[b]), end = __ldcg(&p.starts[b + 1]);
+  const int64_t run = run_units(__ldcg(&p.starts[p.B]));
+  if (first == end) {
+    for (int h = blockIdx.y; h < p.G; h += gridDim.y) {
+      for (int x = tid; x < D; x += kJoinThreads) p.o[(head0 + h) * D + x] = __float2bfloat16(0.f);
+      if (tid == 0) p.lse[head0 + h] = -INFINITY;
+    }
     return;
   }
-  const int64_t u0 = base + (int64_t)g * units, u1 = u0 + units;
-  const int c0 = (int)(u0 / sc.run), c1 = (int)((u1 - 1) / sc.run);
-  if (c0 == c1) return;
-  // the part of CTA c: its slot 1 where it began with another (sequence, group)
-  auto part_of = [&](int c) { return (int64_t)(2 * c + (c == c0 && u0 != sc.run * c0)) * p.G; };
-  for (int x = threadIdx.x; x < p.G * (D / 2); x += kThreads) {
-    const int h = x / (D / 2), col = 2 * (x % (D / 2));
+  const int64_t units = (end - first) / p.H, u0 = first + g * units;
+  const int c0 = (int)(u0 / run), n = (int)((u0 + units - 1) / run) - c0 + 1;
+  if (n == 1) return;
+  // part i is slot 0 of CTA c0 + i, except where CTA c0 began with another (sequence, group)
+  const int late = u0 != run * c0;
+  auto part_of = [&](int i) { return (int64_t)(2 * (c0 + i) + (i == 0 ? late : 0)) * p.G; };
+  for (int h = blockIdx.y; h < p.G; h += gridDim.y) {
     float top = -INFINITY;
-    for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(&p.part_lse[part_of(c) + h]));
+    for (int i = tid; i < n; i += kJoinThreads) {
+      const float x = __ldcg(&p.part_lse[part_of(i) + h]);
+      s_w[i] = x;
+      top = fmaxf(top, x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) s_red[warp] = top;
+    __syncthreads();
+    top = s_red[0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) top = fmaxf(top, s_red[w]);
+    float sum = 0.f;
+    for (int i = tid; i < n; i += kJoinThreads) {
+      const float x = weight(s_w[i], top);
+      s_w[i] = x;
+      sum += x;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
     float l = 0.f;
-    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) l += s_sum[w];
+    const int col = tid % LANES;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const int64_t at = part_of(c) + h;
-      const float w = weight(__ldcg(&p.part_lse[at]), top);
-      const float2 y = __ldcg(reinterpret_cast<const float2*>(p.part_o + at * D + col));
-      l += w;
+    for (int i = tid / LANES; i < n; i += PARTS) {
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + (part_of(i) + h) * D) + col);
+      const float w = s_w[i];
       acc.x = fmaf(w, y.x, acc.x);
       acc.y = fmaf(w, y.y, acc.y);
+      acc.z = fmaf(w, y.z, acc.z);
+      acc.w = fmaf(w, y.w, acc.w);
     }
-    *reinterpret_cast<uint32_t*>(p.o + (head0 + h) * D + col) = pack_bf16(acc.x / l, acc.y / l);
-    if (col == 0) p.lse[head0 + h] = (top + log2f(l)) * 0.6931471805599453f;
+    s_acc[tid / LANES][col] = acc;
+    __syncthreads();
+    if (tid < LANES) {
+      for (int i = 1; i < PARTS; ++i) {
+        const float4 y = s_acc[i][tid];
+        acc.x += y.x;
+        acc.y += y.y;
+        acc.z += y.z;
+        acc.w += y.w;
+      }
+      *reinterpret_cast<uint2*>(p.o + (head0 + h) * D + 4 * tid) =
+          make_uint2(pack_bf16(acc.x / l, acc.y / l), pack_bf16(acc.z / l, acc.w / l));
+      if (tid == 0) p.lse[head0 + h] = (top + log2f(l)) * 0.6931471805599453f;
+    }
+    __syncthreads();
   }
 }
 
@@ -697,11 +774,14 @@ cudaError_t launch_attn(const PagedDecode& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if ((e = launch(kern, dim3(kCtas), kThreads, smem, p.block_idx != nullptr, stream, p)) != cudaSuccess)
     return e;
-  return launch(paged_join_kernel<D>, dim3((unsigned)(p.B * p.H)), kThreads, 0, true, stream, p);
+  // one CTA a head while they are few: the join is a chain of loads, shorter the fewer heads
+  const int64_t rows = (int64_t)p.B * p.H;
+  const unsigned split = rows * p.G <= 1024 ? (unsigned)p.G : 1u;
+  return launch(paged_join_kernel<D>, dim3((unsigned)rows, split), kJoinThreads, 0, true, stream, p);
 }
 
 struct Layout {
-  size_t part_o, part_lse, pooled, bytes;
+  size_t part_o, part_lse, starts, pooled, bytes;
 };
 
 // Sizes of a call; MSA_OK and the workspace's layout.  topk = 0: the whole cache.
@@ -719,7 +799,8 @@ int check_sizes(const msa_paged_cache_t* c, const msa_page_table_t* pt, int H_q,
   if (topk > 0 && c->d_idx == 0) return MSA_ERR_SHAPE;
   lay->part_o = 0;
   lay->part_lse = align256((size_t)2 * kCtas * G * c->d * 4);
-  lay->pooled = lay->part_lse + align256((size_t)2 * kCtas * G * 4);
+  lay->starts = lay->part_lse + align256((size_t)2 * kCtas * G * 4);
+  lay->pooled = lay->starts + align256(((size_t)pt->B + 1) * 8);
   lay->bytes = lay->pooled + (topk > 0 ? align256((size_t)pt->B * c->H_kv * ((cap + 127) / 128) * 4) : 0);
   return MSA_OK;
 }
@@ -756,6 +837,7 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   p.pooled = reinterpret_cast<float*>(w + lay.pooled);
   p.part_o = reinterpret_cast<float*>(w + lay.part_o);
   p.part_lse = reinterpret_cast<float*>(w + lay.part_lse);
+  p.starts = reinterpret_cast<int64_t*>(w + lay.starts);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.B = pt->B;

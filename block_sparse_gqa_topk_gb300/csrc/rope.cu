@@ -28,6 +28,7 @@ struct RopeTensor {
   const void* x;
   void* y;
   int H, parts, rot_parts, d;  // items per head, of them rotated
+  int last;                    // items of a token in this tensor and those before it
   float inv_parts, inv_H;
   int64_t xs[3], ys[3];  // strides of batch, token, head
 };
@@ -39,7 +40,7 @@ struct RopeParams {
   int64_t ps[2];  // strides of positions: batch, token
   int64_t tokens;
   int N, half, tpb, n;
-  float mscale, sign;
+  float mscale, sign, inv_half;
   RopeTensor t[kMaxRopeTensors];
 };
 
@@ -63,17 +64,19 @@ struct alignas(V * sizeof(T)) Pack {
 // an integer, and the product's two roundings move it by less than 2^18 / q * 2^-23.
 __device__ __forceinline__ int small_div(int x, float inv) { return (int)(((float)x + 0.5f) * inv); }
 
-// One CTA serves tpb tokens: their sines and cosines go to shared memory once, then the
-// items (V pairs of one head, or 2 V values to copy) of every tensor are spread over the
-// threads, four in flight each.  Bound by HBM: every value is read and written once.
+// One CTA serves tpb tokens: their sines and cosines, and where their rows start, go to
+// shared memory once; then the items (V pairs of one head, or 2 V values to copy) of all the
+// tensors together are spread over the threads, four in flight each.  Bound by HBM: every
+// value is read and written once.
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float2 s_cs[kMaxTokens * kMaxHalf];
+  __shared__ longlong2 s_off[kMaxRopeTensors][kMaxTokens];  // of x and y
   const int64_t t0 = (int64_t)blockIdx.x * p.tpb;
   const int nt = (int)min((int64_t)p.tpb, p.tokens - t0);
   for (int i = threadIdx.x; i < nt * p.half; i += kThreads) {
-    const int tok = i / p.half, pair = i - tok * p.half;
-    const int64_t t = t0 + tok, b = t / p.N, n = t - b * p.N;
+    const int tok = small_div(i, p.inv_half), pair = i - tok * p.half;
+    const int64_t t = t0 + tok, b = p.N == p.tokens ? 0 : t / p.N, n = t - b * p.N;
     int64_t pos = n;
     if (p.positions) {
       const int64_t at = b * p.ps[0] + n * p.ps[1];
@@ -85,61 +88,63 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
     sincospif((float)frac * 1.0842021724855044e-19f /* 2^-63: half turns */, &s, &c);
     s_cs[i] = make_float2(c * p.mscale, s * p.mscale * p.sign);
   }
+  if (threadIdx.x < p.n * kMaxTokens) {
+    const int ti = threadIdx.x / kMaxTokens, tok = threadIdx.x % kMaxTokens;
+    const int64_t t = t0 + tok, b = t / p.N, n = t - b * p.N;
+    s_off[ti][tok] = make_longlong2(b * p.t[ti].xs[0] + n * p.t[ti].xs[1], b * p.t[ti].ys[0] + n * p.t[ti].ys[1]);
+  }
   __syncthreads();
-  for (int ti = 0; ti < p.n; ++ti) {
-    const RopeTensor& a = p.t[ti];
-    const int items = nt * a.H * a.parts;
-    constexpr int U = 4;
-    for (int base = threadIdx.x; base < items; base += U * kThreads) {
-      Pack<T, V> lo[U], hi[U];
-      int64_t yo[U];
-      int cs[U], step[U];  // angle index (-1: copied), distance of the second vector
+  const int items = nt * p.t[p.n - 1].last;
+  constexpr int U = 4;
+  for (int base = threadIdx.x; base < items; base += U * kThreads) {
+    Pack<T, V> lo[U], hi[U];
+    T* dst[U];
+    int cs[U], step[U];  // angle index (-1: copied), distance of the second vector (0: no item)
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int x = base + u * kThreads;
-        step[u] = 0;
-        if (x >= items) continue;
-        const int row = small_div(x, a.inv_parts), part = x - row * a.parts;
-        const int tok = small_div(row, a.inv_H), h = row - tok * a.H;
-        const int64_t t = t0 + tok, b = t / p.N, n = t - b * p.N;
-        int64_t xo = b * a.xs[0] + n * a.xs[1] + h * a.xs[2];
-        yo[u] = b * a.ys[0] + n * a.ys[1] + h * a.ys[2];
-        int at;
-        if (part < a.rot_parts) {
-          cs[u] = tok * p.half + part * V;
-          at = INTER ? part * 2 * V : part * V;
-          step[u] = INTER ? V : p.half;
-        } else {
-          cs[u] = -1;
-          at = 2 * p.half + (part - a.rot_parts) * 2 * V;
-          step[u] = at + V < a.d ? V : -1;  // the last copied item may hold one vector
-        }
-        xo += at;
-        yo[u] += at;
-        const T* src = static_cast<const T*>(a.x) + xo;
-        lo[u] = *reinterpret_cast<const Pack<T, V>*>(src);
-        if (step[u] > 0) hi[u] = *reinterpret_cast<const Pack<T, V>*>(src + step[u]);
+    for (int u = 0; u < U; ++u) {
+      int x = base + u * kThreads;
+      step[u] = 0;
+      if (x >= items) continue;
+      int ti = 0;
+      while (x >= nt * p.t[ti].last) ++ti;
+      const RopeTensor& a = p.t[ti];
+      if (ti > 0) x -= nt * p.t[ti - 1].last;
+      const int row = small_div(x, a.inv_parts), part = x - row * a.parts;
+      const int tok = small_div(row, a.inv_H), h = row - tok * a.H;
+      int at;
+      if (part < a.rot_parts) {
+        cs[u] = tok * p.half + part * V;
+        at = INTER ? part * 2 * V : part * V;
+        step[u] = INTER ? V : p.half;
+      } else {
+        cs[u] = -1;
+        at = 2 * p.half + (part - a.rot_parts) * 2 * V;
+        step[u] = at + V < a.d ? V : -1;  // the last copied item may hold one vector
       }
+      const longlong2 off = s_off[ti][tok];
+      const T* src = static_cast<const T*>(a.x) + (off.x + h * a.xs[2] + at);
+      dst[u] = static_cast<T*>(a.y) + (off.y + h * a.ys[2] + at);
+      lo[u] = *reinterpret_cast<const Pack<T, V>*>(src);
+      if (step[u] > 0) hi[u] = *reinterpret_cast<const Pack<T, V>*>(src + step[u]);
+    }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (step[u] == 0) continue;
-        if (cs[u] >= 0) {
+    for (int u = 0; u < U; ++u) {
+      if (step[u] == 0) continue;
+      if (cs[u] >= 0) {
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float2 w = s_cs[cs[u] + e];
-            // the pair's two values: the vectors side by side, or neighbours in them
-            T* p1 = INTER ? (2 * e < V ? &lo[u].v[(2 * e) % V] : &hi[u].v[(2 * e) % V]) : &lo[u].v[e];
-            T* p2 = INTER ? (2 * e + 1 < V ? &lo[u].v[(2 * e + 1) % V] : &hi[u].v[(2 * e + 1) % V])
-                          : &hi[u].v[e];
-            const float x1 = to_f(*p1), x2 = to_f(*p2);
-            *p1 = from_f<T>(x1 * w.x - x2 * w.y);
-            *p2 = from_f<T>(x2 * w.x + x1 * w.y);
-          }
+        for (int e = 0; e < V; ++e) {
+          const float2 w = s_cs[cs[u] + e];
+          // the pair's two values: the vectors side by side, or neighbours in them
+          T* p1 = INTER ? (2 * e < V ? &lo[u].v[(2 * e) % V] : &hi[u].v[(2 * e) % V]) : &lo[u].v[e];
+          T* p2 = INTER ? (2 * e + 1 < V ? &lo[u].v[(2 * e + 1) % V] : &hi[u].v[(2 * e + 1) % V])
+                        : &hi[u].v[e];
+          const float x1 = to_f(*p1), x2 = to_f(*p2);
+          *p1 = from_f<T>(x1 * w.x - x2 * w.y);
+          *p2 = from_f<T>(x2 * w.x + x1 * w.y);
         }
-        T* dst = static_cast<T*>(a.y) + yo[u];
-        *reinterpret_cast<Pack<T, V>*>(dst) = lo[u];
-        if (step[u] > 0) *reinterpret_cast<Pack<T, V>*>(dst + step[u]) = hi[u];
       }
+      *reinterpret_cast<Pack<T, V>*>(dst[u]) = lo[u];
+      if (step[u] > 0) *reinterpret_cast<Pack<T, V>*>(dst[u] + step[u]) = hi[u];
     }
   }
 }
@@ -202,11 +207,12 @@ extern "C" int msa_rope(const msa_rope_t* r, const uint64_t* turns, const void* 
   p.ps[1] = r->positions_stride[1];
   p.N = r->N;
   p.half = r->rot_dim / 2;
+  p.inv_half = 1.f / (float)p.half;
   p.mscale = r->mscale;
   p.sign = r->inverse ? -1.f : 1.f;
   p.n = num_tensors;
   const int w = vec ? V : 1;
-  int most = 1;  // items of a token in the largest tensor
+  int all = 0;  // items of a token
   for (int i = 0; i < num_tensors; ++i) {
     const msa_rope_tensor_t& t = tensors[i];
     RopeTensor& a = p.t[i];
@@ -223,12 +229,13 @@ extern "C" int msa_rope(const msa_rope_t* r, const uint64_t* turns, const void* 
       a.xs[k] = t.x_stride[k];
       a.ys[k] = t.y_stride[k];
     }
-    most = most > a.H * a.parts ? most : a.H * a.parts;
+    all += a.H * a.parts;
+    a.last = all;
   }
   // tokens a CTA: up to kMaxTokens while the grid still fills the GPU and an item index
   // stays below 2^18
   p.tpb = kMaxTokens;
-  while (p.tpb > 1 && ((p.tokens + p.tpb - 1) / p.tpb < 8 * cx.num_sms || (int64_t)p.tpb * most > (1 << 18)))
+  while (p.tpb > 1 && ((p.tokens + p.tpb - 1) / p.tpb < 8 * cx.num_sms || (int64_t)p.tpb * all > (1 << 18)))
     p.tpb >>= 1;
   if ((p.tokens + p.tpb - 1) / p.tpb > 0x7fffffffLL) return MSA_ERR_UNSUPPORTED;
   const bool inter = r->interleaved != 0;

@@ -10,7 +10,6 @@ block_idx [B,H_kv,N,topk] int32.
 """
 from __future__ import annotations
 
-import contextlib
 import dataclasses
 import fractions
 import math
@@ -38,6 +37,15 @@ def release_workspace() -> None:
 
 def _stream(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
+
+
+# The same handle without a Stream object: a decode step's calls are host-bound (0.1 us for
+# 2.0 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(index: int) -> int:
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 def _ptr(t):
@@ -492,11 +500,16 @@ _ROPE_DTYPES = {torch.bfloat16: _lib.MSA_DTYPE_BF16, torch.float16: _lib.MSA_DTY
 _TWO_PI = fractions.Fraction(2 * 31415926535897932384626433832795028841971693993751, 10 ** 49)
 
 
-def _on(device):
-    """Makes `device` current for the calls inside, where it is not already."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _call(dev, name, f, *args):
+    """f(*args, stream) on `dev`'s current stream, with `dev` current; raises on an error."""
+    index = dev.index
+    if index == torch.cuda.current_device():
+        rc = f(*args, _stream_of(index))
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, _stream_of(index))
+    if rc:
+        _lib.check(rc, name)
 
 
 @dataclasses.dataclass(frozen=True, eq=False)
@@ -655,10 +668,8 @@ def msa_rope(xs, rope: Rope, positions=None, *, inverse: bool = False, inplace: 
         B, N = lead if n == 2 else (1, lead[0])
         r = _lib.ROPE.pack(B, N, rope.rot_dim, rope.interleaved, inverse, _ROPE_DTYPES[dtype], bits,
                            rope.mscale, ps[0], ps[1])
-        with _on(dev):
-            rc = _lib.msa_rope(r, rope.turns.data_ptr(), _ptr(positions), b"".join(packed), len(packed),
-                               _stream(dev))
-        _lib.check(rc, "msa_rope")
+        _call(dev, "msa_rope", _lib.msa_rope, r, rope.turns.data_ptr(), _ptr(positions), b"".join(packed),
+              len(packed))
     return tuple(ys)
 
 
@@ -678,7 +689,11 @@ class RopeFunction(torch.autograd.Function):
         got = [i for i, g in enumerate(dys) if g is not None and ctx.needs_input_grad[3 + i]]
         out = [None] * len(dys)
         if got:
-            dxs = RopeFunction.apply(ctx.rope, positions, not ctx.inverse, *(dys[i] for i in got))
+            turn = [dys[i] for i in got]
+            if torch.is_grad_enabled():  # a second derivative is wanted
+                dxs = RopeFunction.apply(ctx.rope, positions, not ctx.inverse, *turn)
+            else:
+                dxs = msa_rope(turn, ctx.rope, positions, inverse=not ctx.inverse)
             for i, g in zip(got, dxs):
                 out[i] = g
         return (None, None, None, *out)
@@ -814,10 +829,8 @@ def msa_cache_write(cache: PagedCache, page_table, lens, k, v, k_idx=None, *, cu
         return
     strides = _lib.CACHE_STRIDES.pack(k.stride(0), k.stride(1), v.stride(0), v.stride(1),
                                       0 if k_idx is None else k_idx.stride(0))
-    with _on(cache.device):
-        rc = _lib.msa_cache_write(cache._c, pages, lens.data_ptr(), _ptr(cu_seqlens), T, k.data_ptr(),
-                                  v.data_ptr(), _ptr(k_idx), strides, _stream(cache.device))
-    _lib.check(rc, "msa_cache_write")
+    _call(cache.device, "msa_cache_write", _lib.msa_cache_write, cache._c, pages, lens.data_ptr(),
+          _ptr(cu_seqlens), T, k.data_ptr(), v.data_ptr(), _ptr(k_idx), strides)
 
 
 def msa_cache_read(cache: PagedCache, page_table, lens, cu_seqlens, total_tokens: int):
@@ -837,10 +850,8 @@ def msa_cache_read(cache: PagedCache, page_table, lens, cu_seqlens, total_tokens
     if cache.k_idx is not None:
         k_idx = torch.empty((T, cache.d_idx), dtype=torch.bfloat16, device=dev)
     if T and B:
-        with _on(dev):
-            rc = _lib.msa_cache_read(cache._c, pages, lens.data_ptr(), cu_seqlens.data_ptr(), T, k.data_ptr(),
-                                     v.data_ptr(), _ptr(k_idx), _stream(dev))
-        _lib.check(rc, "msa_cache_read")
+        _call(dev, "msa_cache_read", _lib.msa_cache_read, cache._c, pages, lens.data_ptr(),
+              cu_seqlens.data_ptr(), T, k.data_ptr(), v.data_ptr(), _ptr(k_idx))
     return k, v, k_idx
 
 
@@ -883,11 +894,9 @@ def msa_decode_paged(q, q_idx, cache: PagedCache, page_table, lens, topk: int = 
         raise ValueError(f"q_idx must be {(B, H_kv, cache.d_idx)} on the cache's device, got {tuple(q_idx.shape)}")
     block_idx = torch.empty((B, H_kv, topk), dtype=torch.int32, device=cache.device)
     if B:
-        with _on(cache.device):
-            rc = _lib.msa_decode_paged(cache._c, pages, lens.data_ptr(), H_q, topk, scale, q.data_ptr(),
-                                       q_idx.data_ptr(), block_idx.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                       ws.data_ptr(), nws, _stream(cache.device))
-        _lib.check(rc, "msa_decode_paged")
+        _call(cache.device, "msa_decode_paged", _lib.msa_decode_paged, cache._c, pages, lens.data_ptr(), H_q,
+              topk, scale, q.data_ptr(), q_idx.data_ptr(), block_idx.data_ptr(), o.data_ptr(), lse.data_ptr(),
+              ws.data_ptr(), nws)
     return block_idx, o, lse
 
 
@@ -896,9 +905,6 @@ def msa_decode_paged_dense(q, cache: PagedCache, page_table, lens, *, scale=None
     msa_decode_paged.  Returns (o [B,H_q,d] bf16, lse [B,H_q] f32)."""
     pages, H_q, scale, o, lse, ws, nws = _paged_args(q, cache, page_table, lens, 0, scale)
     if q.shape[0]:
-        with _on(cache.device):
-            rc = _lib.msa_decode_paged_dense(cache._c, pages, lens.data_ptr(), H_q, scale, q.data_ptr(),
-                                             o.data_ptr(), lse.data_ptr(), ws.data_ptr(), nws,
-                                             _stream(cache.device))
-        _lib.check(rc, "msa_decode_paged_dense")
+        _call(cache.device, "msa_decode_paged_dense", _lib.msa_decode_paged_dense, cache._c, pages,
+              lens.data_ptr(), H_q, scale, q.data_ptr(), o.data_ptr(), lse.data_ptr(), ws.data_ptr(), nws)
     return o, lse

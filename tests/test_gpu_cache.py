@@ -121,6 +121,39 @@ def test_write_then_read(case, fp8):
         assert torch.equal(gi[:T], ki)
 
 
+def test_quantised_codes_over_all_significands():
+    """Every pair of bf16 significands (a value's and its row's amax) over 24 exponents, both
+    signs, and rows far below and above the usual range: the codes and scales of the oracle."""
+    sig = np.arange(128, dtype=np.uint32)
+    rows = []
+    for shift in range(24):  # one value per significand of 2^-shift times the amax's binade
+        for top in sig:
+            x = ((127 - shift) << 7 | sig).astype(np.uint16)
+            x[1::2] |= 0x8000
+            row = np.concatenate([x, [(127 << 7) | top | (0x8000 if top % 3 == 0 else 0)]])
+            rows.append(np.where((row & 0x7FFF) > ((127 << 7) | top), 0x8000, row))  # none above amax
+    a = np.stack(rows)
+    # rows of 128: the amax takes the place of a value in turn, so none is left out
+    x = np.concatenate([np.where(np.arange(128) == k, a[:, 128:], a[:, :128]) for k in (0, 127)])
+    extra = []
+    for e in (1, 30, 66, 67, 186, 187, 240, 254):  # amax binades, tiny to huge
+        extra.append(np.where(x[:256] & 0x7F80, np.clip((x[:256] & 0x7F80).astype(np.int64) + ((e - 127) << 7), 0,
+                                                        e << 7) | (x[:256] & 0x807F), x[:256]).astype(np.uint16))
+    x = np.concatenate([x] + extra).astype(np.uint16)
+    T = len(x)
+    page = 128
+    c = ops.new_paged_cache((T + page - 1) // page, 1, page_size=page, d=128, d_idx=0, fp8=True)
+    k = torch.from_numpy(x.view(np.int16)).cuda().view(torch.bfloat16).view(T, 1, 128)
+    t = dev(np.arange(c.num_pages)[None])
+    ops.msa_cache_write(c, t, dev([T]), k, k, cu_seqlens=dev([0, T]))
+    codes, scale = oracle_fp8.quantize_rows(x)
+    for n in "kv":
+        assert np.array_equal(getattr(c, n).flatten(0, 2)[:T].cpu().numpy(), codes)
+        got = getattr(c, n + "_scale").flatten()[:T].cpu().numpy()
+        assert np.array_equal(got.view(np.uint32), scale.view(np.uint32))
+    assert ops.device_status() == 0
+
+
 def test_one_token_a_sequence_and_empty_slots():
     """The decode step's write: no cu_seqlens, empty slots skipped, growing page by page."""
     page, H, d, di = 16, 2, 128, 64

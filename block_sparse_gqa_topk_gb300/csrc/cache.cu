@@ -1,7 +1,7 @@
 // cache.cu -- tokens into a paged cache and back (see include/msa.h).
 //
 // A row is one head's key or value of a token (d values), or the token's index key; it
-// moves through the lanes of a part of a warp, 8 values a lane.  An E4M3 cache stores
+// moves through the lanes of a part of a warp.  An E4M3 cache stores
 //   s = amax |x| / 448 (1 for an all-zero row),  code = E4M3 nearest to x / s,
 // the rule of msa_quantize_kv_fp8 bit for bit (IEEE divisions), and reads back
 // decode(code) * s rounded once to bf16.  Both directions are bound by HBM: every row is
@@ -16,7 +16,6 @@ namespace msa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSteps = 4;  // rows a lane group of a warp moves at once
 
 struct CacheParams {
   PageView pages;
@@ -66,57 +65,72 @@ __device__ __forceinline__ int64_t token_row(const CacheParams& p, int t) {
   return row < 0 ? kNoPlace : row;
 }
 
-__device__ __forceinline__ void widen(uint4 w, float (&f)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f[2 * e] = __uint_as_float(u[e] << 16);
-    f[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-  }
+__device__ __forceinline__ float2 widen(uint32_t w) {  // two bf16
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// E4M3 codes of a row's 8 values at scale sc (amax / 448): the code nearest to the float32
+// E4M3 codes of eight values at scale sc (amax / 448): the code nearest to the float32
 // quotient x / sc.  With r the rounded reciprocal, q0 = x r and the remainder x - q0 sc, which
 // one fma gives exactly, q0 + r (x - q0 sc) is the rounded quotient (Markstein 1990); that it
 // gives every code that division gives is checked over all pairs of bf16 significands.  Rows
 // whose amax leaves the range in which nothing underflows are divided.
-__device__ __forceinline__ uint2 quantize8(const float (&f)[8], float amax, float sc) {
-  float q[8];
-  if (amax > 1e-18f && amax < 1e18f) {
-    const float r = __frcp_rn(sc);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float q0 = f[e] * r;
-      q[e] = copysignf(fmaf(fmaf(-q0, sc, f[e]), r, q0), f[e]);  // a zero keeps its sign
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = __fdiv_rn(f[e], sc);
-  }
+__device__ __forceinline__ uint2 quantize8(uint4 w, float sc, float r, bool divide) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   uint32_t c[2] = {0, 0};
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) {
-    const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(q[e], q[e + 1]), __NV_SATFINITE, __NV_E4M3);
-    c[e >> 2] |= (two & 0xffffu) << (8 * (e & 3));
+  for (int e = 0; e < 4; ++e) {
+    const float2 x = widen(u[e]);
+    float2 q;
+    if (divide) {
+      q = make_float2(__fdiv_rn(x.x, sc), __fdiv_rn(x.y, sc));
+    } else {
+      const float2 rr = make_float2(r, r), q0 = fmul2(x, rr);
+      q = ffma2(ffma2(q0, make_float2(-sc, -sc), x), rr, q0);
+      q = make_float2(copysignf(q.x, x.x), copysignf(q.y, x.y));  // a zero keeps its sign
+    }
+    const uint32_t two = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+    c[e >> 1] |= (two & 0xffffu) << (16 * (e & 1));
   }
   return make_uint2(c[0], c[1]);
+}
+
+// decode(code) * s of eight codes, rounded to bf16.
+__device__ __forceinline__ uint4 dequantize8(uint2 c, float s) {
+  uint32_t y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)((e < 2 ? c.x : c.y) >> (16 * (e & 1)));
+    const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
+    y[e] = pack_bf16(v.x * s, v.y * s);
+  }
+  return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
 // Items are the rows of the packed tokens in order: the keys of a token's H heads, the
 // values, the index key.  A warp takes `steps` chunks of CHUNK consecutive items; its lanes
 // find the places of the (at most 32) tokens among them together, so the chain of lookups
-// (sequence, length, page) is paid once, and then move kSteps rows at a time with all their
+// (sequence, length, page) is paid once, and then move STEPS rows at a time with all their
 // loads in flight.
+// A lane moves 16 bytes of the pool a row: 8 bf16 values, or 16 codes.
+template <int D, bool F8>
+struct Lanes {
+  static constexpr int VALUES = F8 ? 16 : 8;       // of a lane
+  static constexpr int LPR = D / VALUES;           // lanes of a row
+  static constexpr int RPS = 32 / LPR;             // rows of a step
+  static constexpr int STEPS = F8 ? 2 : 4;         // rows a lane has in flight
+  static constexpr int CHUNK = RPS * STEPS;
+};
+
 template <int D, bool F8, bool WRITE>
 __global__ void __launch_bounds__(kThreads) cache_kernel(const __grid_constant__ CacheParams p) {
-  constexpr int LPR = D / 8;      // lanes of a row, 8 values each
-  constexpr int RPS = 32 / LPR;   // rows of a step
-  constexpr int CHUNK = RPS * kSteps;
-  const int lane = threadIdx.x & 31, sub = lane % LPR;
+  using L = Lanes<D, F8>;
+  constexpr int STEPS = L::STEPS;
+  constexpr int W = L::VALUES / 8;  // 16-byte vectors of a lane in the packed rows
+  const int lane = threadIdx.x & 31, sub = lane % L::LPR;
   const int64_t items = (int64_t)p.T * p.rows;
-  const int64_t i0 = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5) * (CHUNK * p.steps);
+  const int64_t i0 = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5) * (L::CHUNK * p.steps);
   if (i0 >= items) return;
-  const int n = (int)min((int64_t)CHUNK * p.steps, items - i0);
+  const int n = (int)min((int64_t)L::CHUNK * p.steps, items - i0);
   const int t0 = (int)(i0 / p.rows);
   const int skip = (int)(i0 - (int64_t)t0 * p.rows);
   int64_t place = kNoToken;
@@ -124,19 +138,19 @@ __global__ void __launch_bounds__(kThreads) cache_kernel(const __grid_constant__
     place = token_row(p, t0 + lane);
     if (place == kNoPlace) set_status(p.status, MSA_ERR_ARG);
   }
-  for (int c = 0; c < n; c += CHUNK) {
-    uint4* packed[kSteps];
-    void* pool[kSteps];
-    float* scale[kSteps];
-    int kind[kSteps];  // 0: nothing, 1: key or value, 2: index key; negative: its place is missing
+  for (int c = 0; c < n; c += L::CHUNK) {
+    uint4* packed[STEPS];
+    uint4* pool[STEPS];
+    float* scale[STEPS];
+    int kind[STEPS];   // 0: nothing, 1: key or value, 2: index key; negative: its place is missing
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int x = c + i * RPS + lane / LPR;
+    for (int i = 0; i < STEPS; ++i) {
+      const int x = c + i * L::RPS + lane / L::LPR;
       const int y = x + skip;
       const int tok = (int)(((float)y + 0.5f) * p.inv_rows);  // exact: y < 2^12
       const int r = y - tok * p.rows;
       int64_t row = __shfl_sync(0xffffffffu, place, tok);
-      kind[i] = x >= n || row == kNoToken ? 0 : r < 2 * p.H ? 1 : sub * 8 < p.d_idx ? 2 : 0;
+      kind[i] = x >= n || row == kNoToken ? 0 : r < 2 * p.H ? 1 : sub * L::VALUES < p.d_idx ? 2 : 0;
       if (row < 0) {
         kind[i] = -kind[i];
         row = 0;
@@ -144,74 +158,77 @@ __global__ void __launch_bounds__(kThreads) cache_kernel(const __grid_constant__
       const int64_t t = t0 + tok;
       const bool v = r >= p.H;
       const int h = v ? r - p.H : r;
+      scale[i] = nullptr;
       if (r == 2 * p.H) {
-        packed[i] = reinterpret_cast<uint4*>(p.xi + t * p.si + sub * 8);
-        pool[i] = p.k_idx + row * p.d_idx + sub * 8;
+        packed[i] = reinterpret_cast<uint4*>(p.xi + t * p.si + sub * L::VALUES);
+        pool[i] = reinterpret_cast<uint4*>(p.k_idx + row * p.d_idx + sub * L::VALUES);
       } else {
         const int64_t cell = row * p.H + h;
         packed[i] = reinterpret_cast<uint4*>((v ? p.xv + t * p.sv[0] + h * p.sv[1]
-                                                : p.xk + t * p.sk[0] + h * p.sk[1]) + sub * 8);
-        pool[i] = static_cast<uint8_t*>(v ? p.v : p.k) + (cell * D + sub * 8) * (F8 ? 1 : 2);
-        scale[i] = F8 ? (v ? p.v_scale : p.k_scale) + cell : nullptr;
+                                                : p.xk + t * p.sk[0] + h * p.sk[1]) + sub * L::VALUES);
+        pool[i] = reinterpret_cast<uint4*>(static_cast<uint8_t*>(v ? p.v : p.k) +
+                                           (cell * D + sub * L::VALUES) * (F8 ? 1 : 2));
+        if (F8) scale[i] = (v ? p.v_scale : p.k_scale) + cell;
       }
     }
-    uint4 w[kSteps];
-    float s[kSteps];
+    uint4 w[STEPS][W];
+    float s[STEPS];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      w[i] = make_uint4(0, 0, 0, 0);  // what a missing place reads as
+    for (int i = 0; i < STEPS; ++i) {
+#pragma unroll
+      for (int k = 0; k < W; ++k) w[i][k] = make_uint4(0, 0, 0, 0);  // what a missing place reads as
       s[i] = 0.f;
       if (kind[i] <= 0) continue;
-      if (WRITE) {
-        w[i] = __ldg(packed[i]);
-      } else if (F8 && kind[i] == 1) {
-        const uint2 x = *static_cast<const uint2*>(pool[i]);
-        w[i].x = x.x;
-        w[i].y = x.y;
+      if (!WRITE && F8 && kind[i] == 1) {
+        w[i][0] = *pool[i];
         s[i] = *scale[i];
       } else {
-        w[i] = *static_cast<const uint4*>(pool[i]);
+#pragma unroll
+        for (int k = 0; k < W; ++k) w[i][k] = WRITE ? __ldg(packed[i] + k) : pool[i][k];
       }
     }
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
+    for (int i = 0; i < STEPS; ++i) {
       if constexpr (F8 && WRITE) {
-        float f[8];
-        widen(w[i], f);
         float amax = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+        for (int k = 0; k < W; ++k) {
+          const uint32_t u[4] = {w[i][k].x, w[i][k].y, w[i][k].z, w[i][k].w};
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          for (int e = 0; e < 4; ++e) {
+            const float2 x = widen(u[e]);
+            amax = fmax3(amax, fabsf(x.x), fabsf(x.y));
+          }
+        }
+#pragma unroll
+        for (int o = L::LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         if (kind[i] == 1) {
           const float sc = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-          *static_cast<uint2*>(pool[i]) = quantize8(f, amax, sc);
+          const float r = __frcp_rn(sc);
+          const bool divide = !(amax > 1e-18f && amax < 1e18f);
+          const uint2 a = quantize8(w[i][0], sc, r, divide), b = quantize8(w[i][W - 1], sc, r, divide);
+          *pool[i] = make_uint4(a.x, a.y, b.x, b.y);
           if (sub == 0) *scale[i] = sc;
           continue;
         }
       }
       if (WRITE ? kind[i] <= 0 : kind[i] == 0) continue;
-      if (WRITE) {
-        *static_cast<uint4*>(pool[i]) = w[i];
-      } else if (F8 && kind[i] == 1) {
-        uint32_t y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)((e < 2 ? w[i].x : w[i].y) >> (16 * (e & 1)));
-          const float2 v2 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
-          y[e] = pack_bf16(v2.x * s[i], v2.y * s[i]);
+      if constexpr (F8 && !WRITE) {
+        if (kind[i] == 1 || kind[i] == -1) {
+          packed[i][0] = dequantize8(make_uint2(w[i][0].x, w[i][0].y), s[i]);
+          packed[i][W - 1] = dequantize8(make_uint2(w[i][0].z, w[i][0].w), s[i]);
+          continue;
         }
-        *packed[i] = make_uint4(y[0], y[1], y[2], y[3]);
-      } else {
-        *packed[i] = w[i];
       }
+#pragma unroll
+      for (int k = 0; k < W; ++k) (WRITE ? pool[i] : packed[i])[k] = w[i][k];
     }
   }
 }
 
 template <int D, bool F8, bool WRITE>
 cudaError_t launch_cache(CacheParams& p, int num_sms, cudaStream_t st) {
-  constexpr int CHUNK = 32 / (D / 8) * kSteps;
+  constexpr int CHUNK = Lanes<D, F8>::CHUNK;
   const int64_t items = (int64_t)p.T * p.rows;
   // chunks of a warp: up to 8, while 16 warps a SM remain and 32 lanes find all its tokens
   p.steps = 8;

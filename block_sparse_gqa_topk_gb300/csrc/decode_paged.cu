@@ -144,10 +144,11 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// The two E4M3 codes in the low 16 bits as a pair of fp16 (exact).
+// Two E4M3 codes as a pair of fp16 (exact).
 __device__ __forceinline__ uint32_t widen_f16(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+  return h;
 }
 
 // 2^(a - b), 0 for a = -inf whatever b.
@@ -272,7 +273,7 @@ struct WarpState {
       for (int i = 0; i < 4; ++i) {
         const int key = (i >> 1) * 8 + 2 * tq + (i & 1);
         kscale[i] = scale[key];
-        lv[i] = log2f(scale[16 + key]);
+        lv[i] = __log2f(scale[16 + key]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -286,8 +287,8 @@ struct WarpState {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float& s = sc[i >> 1][2 * r + (i & 1)];
-        const int key = (i >> 1) * 8 + 2 * tq + (i & 1);
-        s = key < n ? s * fac[r] : -INFINITY;
+        s *= fac[r];
+        if (n < 16) s = (i >> 1) * 8 + 2 * tq + (i & 1) < n ? s : -INFINITY;
         top = fmaxf(top, s);
         if constexpr (F8) topv = fmaxf(topv, s + lv[i]);
       }
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
   using St = Stage<D, F8>;
   constexpr int ROWS = WIDE ? 16 : 8;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[kWarps][16], s_mv[kWarps][16], s_l[kWarps][16];
+  __shared__ float s_m[kWarps][16], s_mv[kWarps][16], s_l[kWarps][16], s_w[kWarps][16], s_lse[16];
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gq = lane >> 2, tq = lane & 3;
@@ -417,6 +418,11 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
   int64_t u = sc.run * blockIdx.x;
   const int64_t u_end = min(sc.total, u + sc.run);
   uint8_t* ring = smem + warp * St::COUNT * St::BYTES;
+  constexpr int CH = St::ROW / 16;  // 16-byte chunks of a row
+  constexpr int RPI = 32 / CH;      // rows of one copy instruction
+  const int r0 = lane / CH, ch = lane % CH;
+  const int64_t row_step = (int64_t)p.H * St::ROW;
+  const int64_t lane_off = r0 * row_step + ch * 16;
   WarpState<D, F8, WIDE> ws;
   for (int slot = 0; u < u_end; slot = 1) {
     int len = seq_len(p, b);
@@ -431,7 +437,6 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
     const int u0 = (int)(u - base - (int64_t)g * units);
     const int n = (int)min((int64_t)(units - u0), u_end - u);
     const int64_t head0 = ((int64_t)b * p.H + g) * p.G;
-    ws.load_q(p, head0, gq, tq);
     // Page ids of the next 32 units sit in the lanes of a register (and those of the 32 after
     // them are on their way), so that no lookup stands in front of a copy.  Selected blocks,
     // at most 32, sit in another.
@@ -473,22 +478,24 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
           if (!good) set_status(p.status, MSA_ERR_ARG);
           const int64_t row0 =
               good ? (int64_t)id * p.pages.page_size + (pos - page_of(p.pages, pos) * p.pages.page_size) : 0;
-          constexpr int CH = St::ROW / 16;  // 16-byte chunks of a row
-          constexpr int RPI = 32 / CH;      // rows of one copy instruction
-          const int r0 = lane / CH, ch = lane % CH;
-          const int64_t step = (int64_t)p.H * St::ROW;
-          const int64_t at = (row0 * p.H + g) * St::ROW + ch * 16;
+          const int64_t at = (row0 * p.H + g) * St::ROW + lane_off;
           const uint8_t* kp = static_cast<const uint8_t*>(p.k) + at;
           const uint8_t* vp = static_cast<const uint8_t*>(p.v) + at;
+          const bool full = good && have == 16;
 #pragma unroll
           for (int j = 0; j < 16 / RPI; ++j) {
             const int r = r0 + j * RPI;
-            const bool ok = good && r < have;  // else zeros: no stale NaN meets a weight of 0
-            const int64_t off = ok ? r * step : 0;
             const uint32_t ko = F8 ? r * St::KROW + ch * 16 : swz<(F8 ? 128 : St::ROW)>(r, ch);
             const uint32_t vo = F8 ? r * St::VROW + ch * 16 : ko;
-            cp_async_16(st + ko, kp + off, ok);
-            cp_async_16(st + St::V0 + vo, vp + off, ok);
+            if (full) {
+              cp_async_16(st + ko, kp + j * RPI * row_step);
+              cp_async_16(st + St::V0 + vo, vp + j * RPI * row_step);
+            } else {  // else zeros: no stale NaN meets a weight of 0
+              const bool ok = good && r < have;
+              const int64_t off = ok ? j * RPI * row_step : -lane_off;
+              cp_async_16(st + ko, kp + off, ok);
+              cp_async_16(st + St::V0 + vo, vp + off, ok);
+            }
           }
           if constexpr (F8) {
             const int r = lane & 15;
@@ -502,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
     };
 #pragma unroll
     for (int i = 0; i < St::COUNT - 1; ++i) load(i);
+    ws.load_q(p, head0, gq, tq);
     for (int i = 0; i < n; ++i) {
       cp_async_wait<St::COUNT - 2>();
       __syncwarp();  // unit i has landed for all lanes, and all are done with unit i - 1
@@ -537,34 +545,41 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
           row[0] = ws.o[i][e] + ws.o[i][2 + e];
         }
       }
+    // weights of the warps in each head's joined value, and its lse in bits
+    if (tid < p.G) {
+      float top = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][tid]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) l += s_l[w][tid] * weight(s_m[w][tid], top);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s_w[w][tid] = weight(s_mv[w][tid], top) / l;
+      s_lse[tid] = top + log2f(l);
+    }
     __syncthreads();
     const bool whole = u0 == 0 && n == units;
     const int64_t part = (int64_t)(2 * blockIdx.x + slot) * p.G;
-    for (int x = tid; x < p.G * (D / 2); x += kThreads) {
-      const int h = x / (D / 2), c = 2 * (x % (D / 2));
-      float top = -INFINITY;
+    for (int x = tid; x < p.G * (D / 4); x += kThreads) {
+      const int h = x / (D / 4), c = 4 * (x % (D / 4));
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float lse2 = s_lse[h];
+      if (whole || lse2 > -INFINITY) {  // a part whose scores are all -inf weighs nothing in the join
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][h]);
-      float l = 0.f;
-      float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        l += s_l[w][h] * weight(s_m[w][h], top);
-        const float f = weight(s_mv[w][h], top);
-        const float2 y = *reinterpret_cast<const float2*>(s_o + (w * ROWS + h) * D + c);
-        acc.x += f * y.x;
-        acc.y += f * y.y;
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = s_w[w][h];
+          const float4 y = *reinterpret_cast<const float4*>(s_o + (w * ROWS + h) * D + c);
+          acc.x = fmaf(f, y.x, acc.x);
+          acc.y = fmaf(f, y.y, acc.y);
+          acc.z = fmaf(f, y.z, acc.z);
+          acc.w = fmaf(f, y.w, acc.w);
+        }
       }
-      if (whole || l > 0.f) {  // a part whose scores are all -inf weighs nothing in the join
-        acc.x /= l;
-        acc.y /= l;
-      }
-      const float lse2 = top + log2f(l);
       if (whole) {
-        *reinterpret_cast<uint32_t*>(p.o + (head0 + h) * D + c) = pack_bf16(acc.x, acc.y);
+        *reinterpret_cast<uint2*>(p.o + (head0 + h) * D + c) =
+            make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
         if (c == 0) p.lse[head0 + h] = lse2 * 0.6931471805599453f;
       } else {
-        *reinterpret_cast<float2*>(p.part_o + (part + h) * D + c) = acc;
+        *reinterpret_cast<float4*>(p.part_o + (part + h) * D + c) = acc;
         if (c == 0) p.part_lse[part + h] = lse2;
       }
     }
@@ -663,7 +678,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedDec
 // block wholly before the new token's, as decode_pool_kernel computes it, over pages: one
 // warp per block, 8 NT groups per CTA, the index keys straight into mma.sync fragments (each
 // lane 16 contiguous bytes of a key row, the k slots permuted alike in the query fragments).
-// Bound by HBM: four tiles of 16 keys are in flight per warp.
+// Bound by HBM: all 8 tiles of a block are in flight at once.
 template <int DI, int NT>
 __global__ void __launch_bounds__(256) paged_pool_kernel(const PagedDecode p) {
   griddep_launch_dependents();
@@ -674,7 +689,7 @@ __global__ void __launch_bounds__(256) paged_pool_kernel(const PagedDecode p) {
   if (c >= (len - 1) / 128) return;  // also for an empty slot: (0 - 1) / 128 = 0
   const int gq = lane >> 2, tq = lane & 3;
   constexpr int NP = DI / 32;  // 32-wide d chunks: two k steps each
-  constexpr int U = 4;         // tiles in flight
+  constexpr int U = 8;         // tiles in flight
   // the pool row of each of the block's 8 tiles (a tile of 16 keys lies within one page)
   int64_t row = lane < 8 ? pool_row(p.pages, b, c * 128 + lane * 16) : 0;
   if (row < 0) set_status(p.status, MSA_ERR_ARG);
@@ -743,7 +758,12 @@ __global__ void __launch_bounds__(256) paged_select_kernel(const PagedDecode p) 
     for (int s = threadIdx.x; s < p.topk; s += blockDim.x) dst[s] = -1;
     return;
   }
-  select_blocks<KM>(p.pooled + bg * p.nb, (len - 1) / 128, p.topk, dst);
+  const float* src = p.pooled + bg * p.nb;
+  const int c_own = (len - 1) / 128;
+  // a threshold over registers while a thread's share of the blocks fits them, else lists
+  if (c_own <= 4 * 256) select_blocks_by_threshold<4>(src, c_own, p.topk, dst);
+  else if (c_own <= 16 * 256) select_blocks_by_threshold<16>(src, c_own, p.topk, dst);
+  else select_blocks<KM>(src, c_own, p.topk, dst);
 }
 
 // Launches with programmatic stream serialization: the kernel may be scheduled while its

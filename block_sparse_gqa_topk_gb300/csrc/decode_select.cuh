@@ -87,4 +87,91 @@ __device__ __forceinline__ void select_blocks(const float* __restrict__ src, int
   for (int s = M + 1 + t; s < topk; s += blockDim.x) dst[s] = -1;
 }
 
+// The same result for c_own <= PER * 256, by threshold: thread t holds blocks t PER ..
+// t PER + PER - 1 as order-preserving integers; the M-th largest value T is built bit by bit
+// (the largest T that at least M values reach: one block-wide count a bit), and a scan over
+// the threads, whose order is the blocks', places the values above T and the first of those
+// equal to it.  Distinct scores are told apart after about 18 counts, which replace the
+// lists' insertions and rounds.
+template <int PER>
+__device__ __forceinline__ void select_blocks_by_threshold(const float* __restrict__ src, int c_own, int topk,
+                                                           int32_t* __restrict__ dst) {
+  __shared__ int s_count[2][8], s_above[8], s_equal[8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int M = min(topk - 1, c_own);
+  uint32_t key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int c = tid * PER + i;
+    const uint32_t u = c < c_own ? __float_as_uint(__ldg(&src[c])) : 0xffffffffu;
+    key[i] = (u & 0x80000000u) ? ~u : (u | 0x80000000u);  // past the end: 0, below every score
+  }
+  if (M > 0) {
+    uint32_t T = 0;
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t want = T | (1u << bit);
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) n += key[i] >= want;
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0) s_count[bit & 1][warp] = n;
+      __syncthreads();
+      n = 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) n += s_count[bit & 1][w];
+      if (n >= M) T = want;
+      if (n == M) {  // exactly the values from T up: no bit below matters
+        --T;
+        break;
+      }
+    }
+    // places: values above T all count, those equal to T in block order while room is left
+    int above = 0, equal = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      above += key[i] > T;
+      equal += key[i] == T && tid * PER + i < c_own;
+    }
+    int sa = above, se = equal;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, sa, o), e = __shfl_up_sync(0xffffffffu, se, o);
+      if (lane >= o) {
+        sa += a;
+        se += e;
+      }
+    }
+    if (lane == 31) {
+      s_above[warp] = sa;
+      s_equal[warp] = se;
+    }
+    __syncthreads();
+    int total = 0;
+    sa -= above;
+    se -= equal;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      total += s_above[w];
+      if (w < warp) {
+        sa += s_above[w];
+        se += s_equal[w];
+      }
+    }
+    const int room = M - total;  // equal values that are taken
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = tid * PER + i;
+      if (key[i] > T) {
+        dst[sa + min(se, room)] = c;
+        ++sa;
+      } else if (key[i] == T && c < c_own) {
+        if (se < room) dst[sa + se] = c;
+        ++se;
+      }
+    }
+  }
+  if (tid == 0) dst[M] = c_own;
+  for (int s = M + 1 + tid; s < topk; s += blockDim.x) dst[s] = -1;
+}
+
 }  // namespace msa

@@ -31,14 +31,21 @@ int status_ptr(int** out) {
 int make_ctx(Ctx* cx) {
   int rc = status_ptr(&cx->status);
   if (rc) return rc;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MSA_ERR_CUDA;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return MSA_ERR_CUDA;
-  int major = 0, minor = 0;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  if (major != 10 || minor != 3) return MSA_ERR_UNSUPPORTED;  // built for sm_103a only
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MSA_ERR_CUDA;
+  // a device's SM count and kind do not change: asked for once (-1: not an sm_103)
+  static std::atomic<int> sm_count[64];
+  int sms = sm_count[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return MSA_ERR_CUDA;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    if (major != 10 || minor != 3) sms = -1;
+    sm_count[dev].store(sms, std::memory_order_relaxed);
+  }
+  if (sms < 0) return MSA_ERR_UNSUPPORTED;  // built for sm_103a only
   {
     std::lock_guard<std::mutex> lk(g_mu);
     cx->wait_ns = g_wait_ns;

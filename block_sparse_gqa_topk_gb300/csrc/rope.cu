@@ -29,7 +29,7 @@ struct RopeTensor {
   void* y;
   int H, parts, rot_parts, d;  // items per head, of them rotated
   int last;                    // items of a token in this tensor and those before it
-  float inv_parts, inv_H;
+  uint32_t div_parts, div_H;
   int64_t xs[3], ys[3];  // strides of batch, token, head
 };
 
@@ -40,7 +40,8 @@ struct RopeParams {
   int64_t ps[2];  // strides of positions: batch, token
   int64_t tokens;
   int N, half, tpb, n;
-  float mscale, sign, inv_half;
+  float mscale, sign;
+  uint32_t div_half;
   RopeTensor t[kMaxRopeTensors];
 };
 
@@ -60,22 +61,23 @@ struct alignas(V * sizeof(T)) Pack {
   T v[V];
 };
 
-// x / q for 0 <= x < 2^18 with inv = 1 / q in float: (x + 0.5) / q is at least 0.5 / q from
-// an integer, and the product's two roundings move it by less than 2^18 / q * 2^-23.
-__device__ __forceinline__ int small_div(int x, float inv) { return (int)(((float)x + 0.5f) * inv); }
+// x / q for 0 <= x < 2^18 and q < 2^14 with m = ceil(2^32 / q): x m / 2^32 exceeds x / q by less
+// than 2^18 / 2^32 < 1 / q.  (q = 1 has m = 2^32, which does not fit: m = 0 stands for it.)
+__device__ __forceinline__ int small_div(int x, uint32_t m) { return m ? (int)__umulhi((uint32_t)x, m) : x; }
+uint32_t magic(int q) { return q == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + q - 1) / q); }
 
 // One CTA serves tpb tokens: their sines and cosines, and where their rows start, go to
 // shared memory once; then the items (V pairs of one head, or 2 V values to copy) of all the
-// tensors together are spread over the threads, four in flight each.  Bound by HBM: every
+// tensors together are spread over the threads, two in flight each.  Bound by HBM: every
 // value is read and written once.
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float2 s_cs[kMaxTokens * kMaxHalf];
   __shared__ longlong2 s_off[kMaxRopeTensors][kMaxTokens];  // of x and y
   const int64_t t0 = (int64_t)blockIdx.x * p.tpb;
   const int nt = (int)min((int64_t)p.tpb, p.tokens - t0);
   for (int i = threadIdx.x; i < nt * p.half; i += kThreads) {
-    const int tok = small_div(i, p.inv_half), pair = i - tok * p.half;
+    const int tok = small_div(i, p.div_half), pair = i - tok * p.half;
     const int64_t t = t0 + tok, b = p.N == p.tokens ? 0 : t / p.N, n = t - b * p.N;
     int64_t pos = n;
     if (p.positions) {
@@ -95,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   }
   __syncthreads();
   const int items = nt * p.t[p.n - 1].last;
-  constexpr int U = 4;
+  constexpr int U = 2;
   for (int base = threadIdx.x; base < items; base += U * kThreads) {
     Pack<T, V> lo[U], hi[U];
     T* dst[U];
@@ -109,8 +111,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       while (x >= nt * p.t[ti].last) ++ti;
       const RopeTensor& a = p.t[ti];
       if (ti > 0) x -= nt * p.t[ti - 1].last;
-      const int row = small_div(x, a.inv_parts), part = x - row * a.parts;
-      const int tok = small_div(row, a.inv_H), h = row - tok * a.H;
+      const int row = small_div(x, a.div_parts), part = x - row * a.parts;
+      const int tok = small_div(row, a.div_H), h = row - tok * a.H;
       int at;
       if (part < a.rot_parts) {
         cs[u] = tok * p.half + part * V;
@@ -207,7 +209,7 @@ extern "C" int msa_rope(const msa_rope_t* r, const uint64_t* turns, const void* 
   p.ps[1] = r->positions_stride[1];
   p.N = r->N;
   p.half = r->rot_dim / 2;
-  p.inv_half = 1.f / (float)p.half;
+  p.div_half = magic(p.half);
   p.mscale = r->mscale;
   p.sign = r->inverse ? -1.f : 1.f;
   p.n = num_tensors;
@@ -223,8 +225,8 @@ extern "C" int msa_rope(const msa_rope_t* r, const uint64_t* turns, const void* 
     a.rot_parts = p.half / w;
     const int tail = t.x == t.y ? 0 : t.d - r->rot_dim;  // in place: already there
     a.parts = a.rot_parts + (tail + 2 * w - 1) / (2 * w);
-    a.inv_parts = 1.f / (float)a.parts;
-    a.inv_H = 1.f / (float)a.H;
+    a.div_parts = magic(a.parts);
+    a.div_H = magic(a.H);
     for (int k = 0; k < 3; ++k) {
       a.xs[k] = t.x_stride[k];
       a.ys[k] = t.y_stride[k];

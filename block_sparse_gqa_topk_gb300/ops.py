@@ -625,51 +625,60 @@ def msa_rope(xs, rope: Rope, positions=None, *, inverse: bool = False, inplace: 
             bits = 64
         ps = positions.stride() if positions.dim() == 2 else (0, positions.stride(0))
         lead = tuple(positions.shape)
-    dev, dtype = rope.turns.device, x0.dtype
-    if dtype not in _ROPE_DTYPES:
+    turns = rope.turns
+    dev, dtype, rot = turns.device, x0.dtype, rope.rot_dim
+    code = _ROPE_DTYPES.get(dtype)
+    if code is None:
         raise TypeError(f"tensors must be bf16, fp16 or float32, got {dtype}")
     if dev.type != "cuda" or (positions is not None and positions.device != dev):
         raise ValueError("rope, positions and the tensors must be on one CUDA device (no CPU path exists)")
     n = len(lead)
+    tokens = lead[0] * lead[1] if n == 2 else lead[0]
     ys, packed, keep = [], [], []
-    for i, x in enumerate(xs):
+    pack, empty = _lib.ROPE_TENSOR.pack, torch.empty  # a decode step is host-bound: see each lookup once
+    for x in xs:
         if not isinstance(x, torch.Tensor):
-            raise TypeError(f"tensor {i} must be a tensor")
+            raise TypeError("every operand must be a tensor")
         if x.device != dev:
             raise ValueError("rope, positions and the tensors must be on one CUDA device (no CPU path exists)")
         if x.dtype != dtype:
             raise TypeError(f"all tensors must be {dtype}, got {x.dtype}")
-        if x.dim() not in (n + 1, n + 2) or tuple(x.shape[:n]) != lead:
-            raise ValueError(f"tensor {i} must be {lead} + ([H,] d), got {tuple(x.shape)}")
-        if x.shape[-1] < rope.rot_dim:
-            raise ValueError(f"tensor {i} has d = {x.shape[-1]} < rot_dim = {rope.rot_dim}")
+        shape = x.shape
+        more = len(shape) - n
+        if shape[:n] != lead or not 1 <= more <= 2:
+            raise ValueError(f"every tensor must be {lead} + ([H,] d), got {tuple(shape)}")
+        d, H = shape[-1], shape[n] if more == 2 else 1
+        if d < rot:
+            raise ValueError(f"d = {d} < rot_dim = {rot}")
+        sx = x.stride()
         if inplace:
-            if any(s == 0 and k > 1 for s, k in zip(x.stride(), x.shape)) or x.stride(-1) != 1:
-                raise ValueError(f"tensor {i} cannot be turned in place: its values overlap or its "
-                                 "last axis is strided")
+            if sx[-1] != 1 or any(s == 0 and k > 1 for s, k in zip(sx, shape)):
+                raise ValueError("a tensor whose values overlap, or whose last axis is strided, cannot be "
+                                 "turned in place")
             if x.requires_grad and torch.is_grad_enabled():
-                raise ValueError(f"tensor {i} requires a gradient: use rope, which is differentiable")
+                raise ValueError("a tensor that requires a gradient cannot be turned in place: use rope")
             y = x
             torch.autograd.graph.increment_version(x)
         else:
-            if x.stride(-1) != 1:
+            if sx[-1] != 1:
                 x = x.contiguous()
                 keep.append(x)
-            y = torch.empty(x.shape, dtype=dtype, device=dev)
+                sx = x.stride()
+            y = empty(shape, dtype=dtype, device=dev)
         ys.append(y)
-        if x.numel() == 0:
+        if tokens == 0 or H == 0:
             continue
-        sx, sy = x.stride(), y.stride()
-        hx, hy = (sx[n], sy[n]) if x.dim() == n + 2 else (0, 0)
-        packed.append(_lib.ROPE_TENSOR.pack(
-            x.data_ptr(), y.data_ptr(), sx[0] if n == 2 else 0, sx[n - 1], hx, sy[0] if n == 2 else 0,
-            sy[n - 1], hy, x.shape[n] if x.dim() == n + 2 else 1, x.shape[-1]))
+        # strides of batch, token and head; a new y is contiguous
+        b, t, h = sx[0] if n == 2 else 0, sx[n - 1], sx[n] if more == 2 else 0
+        if inplace:
+            packed.append(pack(x.data_ptr(), x.data_ptr(), b, t, h, b, t, h, H, d))
+        else:
+            packed.append(pack(x.data_ptr(), y.data_ptr(), b, t, h, lead[-1] * H * d, H * d, d, H, d))
     if packed:
-        B, N = lead if n == 2 else (1, lead[0])
-        r = _lib.ROPE.pack(B, N, rope.rot_dim, rope.interleaved, inverse, _ROPE_DTYPES[dtype], bits,
-                           rope.mscale, ps[0], ps[1])
-        _call(dev, "msa_rope", _lib.msa_rope, r, rope.turns.data_ptr(), _ptr(positions), b"".join(packed),
-              len(packed))
+        B, N = lead if n == 2 else (1, tokens)
+        r = _lib.ROPE.pack(B, N, rot, rope.interleaved, inverse, code, bits, rope.mscale, ps[0], ps[1])
+        _call(dev, "msa_rope", _lib.msa_rope, r, turns.data_ptr(),
+              None if positions is None else positions.data_ptr(), b"".join(packed), len(packed))
     return tuple(ys)
 
 

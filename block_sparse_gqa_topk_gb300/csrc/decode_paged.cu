@@ -23,7 +23,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kUnit = 16 * kWarps;  // tokens of a unit of work: 16 a warp
 // CTAs over which a call's units are spread: three on each of the 152 SMs.  Each leaves at
 // most two partial results (its first and its last (sequence, group)), whatever the batch.
 constexpr int kCtas = 152 * 3;
@@ -46,6 +45,7 @@ struct PagedDecode {
   __nv_bfloat16* o;
   float* lse;
   int B, H, G, topk, nb;
+  int unit_shift;    // log2 of a unit's tokens
   float scale_log2;  // scale * log2 e: scores in bits
   int* status;
 };
@@ -65,22 +65,24 @@ __device__ __forceinline__ int seq_units(const PagedDecode& p, int len) {
     const int blocks = (len + 127) / 128;
     len -= max(0, blocks - p.topk) * 128;
   }
-  return (len + kUnit - 1) / kUnit;
+  return (int)(((int64_t)len + (1 << p.unit_shift) - 1) >> p.unit_shift);
 }
 
-// The units of all (sequence, group) pairs in order, cut into equal runs.
-struct Schedule {
-  int64_t total;  // units
-  int64_t run;    // units of a CTA
-};
-__device__ __forceinline__ int64_t run_units(int64_t total) {
-  return max((int64_t)1, (total + kCtas - 1) / kCtas);
+// The units of all (sequence, group) pairs, in order, are cut into n = min(kCtas, total) runs
+// whose lengths differ by at most one: CTA c < n takes units total c / n .. total (c + 1) / n - 1
+// (none is empty, so that every part between a pair's first and last CTA is written).
+__device__ __forceinline__ int64_t run_start(int64_t total, int cta) {
+  const int n = (int)min((int64_t)kCtas, total);
+  return cta < n ? total * cta / n : total;
+}
+__device__ __forceinline__ int cta_of(int64_t total, int64_t unit) {
+  return (int)(((unit + 1) * min((int64_t)kCtas, total) - 1) / total);
 }
 
-// Every thread of the CTA gets the schedule, and a sequence with its first unit: the one that
-// holds the first unit of the CTA's run (any sequence where the run is empty).  CTA 0 leaves
-// the sequences' first units for the join.
-__device__ __forceinline__ Schedule find_run(const PagedDecode& p, int* b_out, int64_t* base_out) {
+// Every thread of the CTA gets the number of units, and a sequence with its first unit: the
+// one that holds the first unit of the CTA's run (any sequence where the run is empty).  CTA 0
+// leaves the sequences' first units for the join.
+__device__ __forceinline__ int64_t find_run(const PagedDecode& p, int* b_out, int64_t* base_out) {
   __shared__ int64_t s_sum[kWarps];
   __shared__ int s_b;
   __shared__ int64_t s_base;
@@ -101,16 +103,13 @@ __device__ __forceinline__ Schedule find_run(const PagedDecode& p, int* b_out, i
     s_base = 0;
   }
   __syncthreads();
-  Schedule sc;
-  sc.total = 0;
-  int64_t base = scan - mine;  // first unit of this thread's sequences
+  int64_t total = 0, base = scan - mine;  // first unit of this thread's sequences
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) base += s_sum[w];
-    sc.total += s_sum[w];
+    total += s_sum[w];
   }
-  sc.run = run_units(sc.total);
-  const int64_t want = sc.run * blockIdx.x;
+  const int64_t want = run_start(total, blockIdx.x);
   const bool here = want >= base && want < base + mine;
   if (here || blockIdx.x == 0) {
     for (int b = b0; b < b1; ++b) {
@@ -123,17 +122,25 @@ __device__ __forceinline__ Schedule find_run(const PagedDecode& p, int* b_out, i
       base += n;
     }
   }
-  if (blockIdx.x == 0 && tid == 0) p.starts[p.B] = sc.total;
+  if (blockIdx.x == 0 && tid == 0) p.starts[p.B] = total;
   __syncthreads();
   *b_out = s_b;
   *base_out = s_base;
-  return sc;
+  return total;
 }
 
 // D(16x8) += A(16x16, row) * B(16x8, col), fp16
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// D(16x8) += A(16x32, row) * B(32x8, col), E4M3
+__device__ __forceinline__ void mma_e4m3_16832(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -154,27 +161,43 @@ __device__ __forceinline__ uint32_t widen_f16(uint32_t two) {
 // 2^(a - b), 0 for a = -inf whatever b.
 __device__ __forceinline__ float weight(float a, float b) { return a == -INFINITY ? 0.f : exp2f(a - b); }
 
-// Shared memory of one warp's stage: 16 key rows and 16 value rows (and their scales).
-//   bf16: rows of 2 D bytes, 16-byte chunks XOR-swizzled for ldmatrix;
-//   E4M3: rows padded so that the 8-byte fragment loads fall in distinct banks.
+// Shared memory of one warp's stage: KEYS key rows and as many value rows (and their scales).
+//   bf16: 16 rows of 2 D bytes, 16-byte chunks XOR-swizzled for ldmatrix;
+//   E4M3: 32 rows (the same bytes); key rows of D bytes whose 64-byte halves are swapped in odd
+//   rows, value rows padded by 16 bytes: the fragment loads then fall in distinct banks.
 template <int D, bool F8>
 struct Stage {
+  static constexpr int KEYS = F8 ? 32 : 16;
   static constexpr int ROW = F8 ? D : 2 * D;
-  static constexpr int KROW = F8 ? D + 32 : 2 * D;
   static constexpr int VROW = F8 ? D + 16 : 2 * D;
-  static constexpr int V0 = 16 * KROW;
-  static constexpr int S0 = V0 + 16 * VROW;  // [2][16] scales
-  static constexpr int BYTES = S0 + (F8 ? 128 : 0);
-  static constexpr int COUNT = F8 ? 3 : 2;
+  static constexpr int V0 = KEYS * ROW;
+  static constexpr int S0 = V0 + KEYS * VROW;  // [2][KEYS] scales
+  static constexpr int BYTES = S0 + (F8 ? 2 * KEYS * 4 : 0);
+  static constexpr int COUNT = 2;
+  static constexpr int UNIT = KEYS * kWarps;  // tokens of a unit of work
+  static constexpr int PER = 128 / UNIT;      // units of a block
+  static constexpr int HALVES = KEYS / 16;    // runs of 16 tokens, which never straddle a page
+  __device__ __forceinline__ static uint32_t key_at(int r, int ch) {
+    if constexpr (!F8) return swz<ROW>(r, ch);
+    else return r * ROW + ((D == 128 ? ch ^ ((r & 1) << 2) : ch) << 4);
+  }
+  __device__ __forceinline__ static uint32_t value_at(int r, int ch) {
+    if constexpr (!F8) return V0 + swz<ROW>(r, ch);
+    else return V0 + r * VROW + (ch << 4);
+  }
 };
 
-// One warp's running softmax over its keys, for rows gq and gq + 8 of the fragments (heads;
-// with at most 8 heads the rows gq + 8 carry the low part of P instead, see step()).
+// One warp's running softmax over its keys, for rows gq and gq + 8 of the fragments: heads gq
+// and gq + 8 (WIDE), or with at most 8 heads the low parts of head gq's operands.
 template <int D, bool F8, bool WIDE>
 struct WarpState {
+  using St = Stage<D, F8>;
   static constexpr int R = WIDE ? 2 : 1;
-  static constexpr int NT = D / 8;
-  uint32_t qa[D / 16][4];  // query fragments (E4M3: fp16, scaled to [1, 2) by a power of two)
+  static constexpr int NT = D / 8;           // tiles of 8 value columns
+  static constexpr int KT = St::KEYS / 8;    // tiles of 8 keys
+  static constexpr int QS = F8 ? D / 32 : D / 16;
+  uint32_t qa[QS][4];                        // query fragments
+  uint32_t ql[F8 && WIDE ? QS : 1][4];       // their low parts
   float o[NT][4];
   float m[R], mv[R], l[R];  // max, max with the value scale (E4M3), this lane's part of the sum
   float fac[R];             // accumulator -> score in bits
@@ -187,39 +210,61 @@ struct WarpState {
       const __nv_bfloat16* row = p.q + (head0 + (ok ? h : 0)) * D;
       if constexpr (!F8) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
+        for (int ks = 0; ks < QS; ++ks)
 #pragma unroll
           for (int half = 0; half < 2; ++half)
             qa[ks][r + 2 * half] =
                 ok ? __ldg(reinterpret_cast<const uint32_t*>(row + ks * 16 + half * 8 + 2 * tq)) : 0u;
-      } else {
-        // lane tq holds values 32 j + 8 tq + 0..7 of the row, in the order in which step()
-        // reads the codes of a key
-        float f[D / 32][8], amax = 0.f;
+      } else if (r < R) {
+        // lane tq holds values 64 j + 16 tq + 0..15 of the row, in the order in which step()
+        // reads the codes of a key: words 4 (2 j + s) + {0, 1} are k slots 4 tq.. and
+        // 16 + 4 tq.. of k step 2 j + s
+        float f[D / 64][16], amax = 0.f;
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          const uint4 w = ok ? __ldg(reinterpret_cast<const uint4*>(row + 32 * j + 8 * tq)) : make_uint4(0, 0, 0, 0);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        for (int j = 0; j < D / 64; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[j][2 * e] = __uint_as_float(u[e] << 16);
-            f[j][2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-            amax = fmaxf(amax, fmaxf(fabsf(f[j][2 * e]), fabsf(f[j][2 * e + 1])));
+          for (int half = 0; half < 2; ++half) {
+            const uint4 w = ok ? __ldg(reinterpret_cast<const uint4*>(row + 64 * j + 16 * tq + 8 * half))
+                               : make_uint4(0, 0, 0, 0);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float a = __uint_as_float(u[e] << 16), b = __uint_as_float(u[e] & 0xffff0000u);
+              f[j][8 * half + 2 * e] = a;
+              f[j][8 * half + 2 * e + 1] = b;
+              amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(b)));
+            }
           }
-        }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // 2^-e with 2^e <= amax: bf16 values keep all their bits in fp16, except those
-        // 2^-14 and more below the row's largest, which move by at most 2^-25 of it
+        // The row scaled by a power of two to a largest value in [128, 256), as the sum of two
+        // E4M3 values: 4 significant bits each hold all 8 of a bf16 value, except that values
+        // 2^-10 and more below the largest keep only multiples of 2^-9 (2^-18 of the largest).
         const int e = min((int)(__float_as_uint(amax) >> 23), 253);
-        const float down = __uint_as_float((uint32_t)(254 - e) << 23);
-        if (r < R) fac[r] = p.scale_log2 / down;
+        const float down = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e)
+        fac[r] = p.scale_log2 / down * 0.0078125f;
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j)
+        for (int j = 0; j < D / 64; ++j)
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            qa[2 * j + s][r] = pack_f16(f[j][4 * s] * down, f[j][4 * s + 1] * down);
-            qa[2 * j + s][r + 2] = pack_f16(f[j][4 * s + 2] * down, f[j][4 * s + 3] * down);
+          for (int w = 0; w < 4; ++w) {
+            uint32_t hi = 0, lo = 0;
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              const float a = f[j][4 * w + k] * down * 128.f, b = f[j][4 * w + k + 1] * down * 128.f;
+              const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+              const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2, __NV_E4M3)));
+              const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, b - back.y), __NV_SATFINITE, __NV_E4M3);
+              hi |= (h2 & 0xffffu) << (8 * k);
+              lo |= (l2 & 0xffffu) << (8 * k);
+            }
+            uint32_t* frag = qa[2 * j + (w >> 1)];
+            if constexpr (WIDE) {
+              frag[r + 2 * (w & 1)] = hi;
+              ql[2 * j + (w >> 1)][r + 2 * (w & 1)] = lo;
+            } else {
+              frag[2 * (w & 1)] = hi;
+              frag[1 + 2 * (w & 1)] = lo;
+            }
           }
       }
     }
@@ -238,60 +283,87 @@ struct WarpState {
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
   }
 
-  // The 16 keys of a landed stage, of which the first n are the sequence's.
+  // o rows gq times a0, rows gq + 8 times a1
+  __device__ __forceinline__ void rescale(float a0, float a1) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const float2 x = fmul2(make_float2(o[i][0], o[i][1]), make_float2(a0, a0));
+      o[i][0] = x.x;
+      o[i][1] = x.y;
+      if constexpr (WIDE || !F8) {  // E4M3 with at most 8 heads leaves those rows zero
+        const float2 y = fmul2(make_float2(o[i][2], o[i][3]), make_float2(a1, a1));
+        o[i][2] = y.x;
+        o[i][3] = y.y;
+      }
+    }
+  }
+
+  // The keys of a landed stage, of which the first n are the sequence's.
   __device__ __forceinline__ void step(const uint8_t* st, int n, int lane) {
-    using St = Stage<D, F8>;
     const int gq = lane >> 2, tq = lane & 3;
-    float sc[2][4] = {};
+    float sc[KT][4] = {};
     if constexpr (!F8) {
       const int mi = lane >> 3, row = (lane & 7) + (mi >> 1) * 8;
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
+      for (int ks = 0; ks < QS; ++ks) {
         uint32_t kb[4];
-        ldmatrix_x4(kb, st + swz<St::ROW>(row, 2 * ks + (mi & 1)));
+        ldmatrix_x4(kb, st + St::key_at(row, 2 * ks + (mi & 1)));
         mma_bf16_16816(sc[0], qa[ks], kb[0], kb[1]);
         mma_bf16_16816(sc[1], qa[ks], kb[2], kb[3]);
       }
     } else {
-      // the order of a product's terms is free: lane tq takes values 32 j + 8 tq + 0..7 of
+      // the order of a product's terms is free: lane tq takes values 64 j + 16 tq + 0..15 of
       // key gq as the k slots of steps 2 j and 2 j + 1, and so do the query fragments
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
+      for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          const uint2 c = *reinterpret_cast<const uint2*>(st + (half * 8 + gq) * St::KROW + 32 * j + 8 * tq);
-          mma_f16_16816(sc[half], qa[2 * j], widen_f16(c.x & 0xffffu), widen_f16(c.x >> 16));
-          mma_f16_16816(sc[half], qa[2 * j + 1], widen_f16(c.y & 0xffffu), widen_f16(c.y >> 16));
+        for (int j = 0; j < D / 64; ++j) {
+          const uint4 c = *reinterpret_cast<const uint4*>(st + St::key_at(8 * t + gq, 4 * j + tq));
+          mma_e4m3_16832(sc[t], qa[2 * j], c.x, c.y);
+          mma_e4m3_16832(sc[t], qa[2 * j + 1], c.z, c.w);
+          if constexpr (WIDE) {
+            mma_e4m3_16832(sc[t], ql[2 * j], c.x, c.y);
+            mma_e4m3_16832(sc[t], ql[2 * j + 1], c.z, c.w);
+          }
         }
+      if constexpr (!WIDE) {
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+          sc[t][0] += sc[t][2];
+          sc[t][1] += sc[t][3];
+        }
+      }
     }
-    // scores in bits; this lane's keys: 2 tq, 2 tq + 1, and those + 8
-    float lv[4];  // log2 of the value scales
+    // scores in bits; this lane's keys: 8 t + 2 tq + e
+    float2 lv[F8 ? KT : 1];  // log2 of the value scales
     if constexpr (F8) {
       const float* scale = reinterpret_cast<const float*>(st + St::S0);
-      float kscale[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = (i >> 1) * 8 + 2 * tq + (i & 1);
-        kscale[i] = scale[key];
-        lv[i] = __log2f(scale[16 + key]);
+      for (int t = 0; t < KT; ++t) {
+        const float2 ks = *reinterpret_cast<const float2*>(scale + 8 * t + 2 * tq);
+        const float2 vs = *reinterpret_cast<const float2*>(scale + St::KEYS + 8 * t + 2 * tq);
+        lv[t] = make_float2(__log2f(vs.x), __log2f(vs.y));
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          sc[t][2 * r] *= ks.x;
+          sc[t][2 * r + 1] *= ks.y;
+        }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int r = 0; r < R; ++r) sc[i >> 1][2 * r + (i & 1)] *= kscale[i];
     }
-    float pr[2][4], alpha[R];  // what multiplies the values
+    float pr[KT][2 * R], alpha[R];  // what multiplies the values
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float top = -INFINITY, topv = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float& s = sc[i >> 1][2 * r + (i & 1)];
-        s *= fac[r];
-        if (n < 16) s = (i >> 1) * 8 + 2 * tq + (i & 1) < n ? s : -INFINITY;
-        top = fmaxf(top, s);
-        if constexpr (F8) topv = fmaxf(topv, s + lv[i]);
-      }
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float& s = sc[t][2 * r + e];
+          s *= fac[r];
+          if (n < St::KEYS) s = 8 * t + 2 * tq + e < n ? s : -INFINITY;
+          top = fmaxf(top, s);
+          if constexpr (F8) topv = fmaxf(topv, s + (e ? lv[t].y : lv[t].x));
+        }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const float m_new = fmaxf(m[r], top);
@@ -309,46 +381,41 @@ struct WarpState {
         alpha[r] = ex2_fast(mv[r] - v_use);
         mv[r] = v_new;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float s = sc[i >> 1][2 * r + (i & 1)];
-          l[r] += ex2_fast(s - m_use);
-          pr[i >> 1][2 * r + (i & 1)] = s == -INFINITY ? 0.f : ex2_fast(s + lv[i] - v_use);
-        }
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float s = sc[t][2 * r + e];
+            l[r] += ex2_fast(s - m_use);
+            pr[t][2 * r + e] = ex2_fast(s + (e ? lv[t].y : lv[t].x) - v_use);
+          }
       } else {
         alpha[r] = beta;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float e = ex2_fast(sc[i >> 1][2 * r + (i & 1)] - m_use);
-          l[r] += e;
-          pr[i >> 1][2 * r + (i & 1)] = e;
-        }
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x = ex2_fast(sc[t][2 * r + e] - m_use);
+            l[r] += x;
+            pr[t][2 * r + e] = x;
+          }
       }
     }
     bool same = alpha[0] == 1.f;
     if constexpr (WIDE) same = same && alpha[R - 1] == 1.f;
-    if (!__all_sync(0xffffffffu, same)) {
-      const float a0 = alpha[0], a1 = alpha[R - 1];  // rows gq + 8: the same heads' low part
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        o[i][0] *= a0;
-        o[i][1] *= a0;
-        o[i][2] *= a1;
-        o[i][3] *= a1;
-      }
-    }
+    if (!__all_sync(0xffffffffu, same)) rescale(alpha[0], alpha[R - 1]);
     if constexpr (!F8) {
       // P enters in two bf16 parts (together 2^-17 of its value): the output's own rounding
       // stays its largest error.  With at most 8 heads the low parts ride in the rows that no
       // head uses; with more they take a product of their own.
       uint32_t hi[4] = {}, lo[4] = {};
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
+      for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          const float e0 = pr[half][2 * r], e1 = pr[half][2 * r + 1];
+          const float e0 = pr[t][2 * r], e1 = pr[t][2 * r + 1];
           const uint32_t h = pack_bf16(e0, e1);
-          hi[2 * half + r] = h;
-          lo[2 * half + r] = pack_bf16(e0 - __uint_as_float(h << 16), e1 - __uint_as_float(h & 0xffff0000u));
+          hi[2 * t + r] = h;
+          lo[2 * t + r] = pack_bf16(e0 - __uint_as_float(h << 16), e1 - __uint_as_float(h & 0xffff0000u));
         }
       if constexpr (!WIDE) {
         hi[1] = lo[0];
@@ -358,7 +425,7 @@ struct WarpState {
 #pragma unroll
       for (int dt = 0; dt < D / 16; ++dt) {
         uint32_t vb[4];
-        ldmatrix_x4_trans(vb, st + St::V0 + swz<St::ROW>(row, 2 * dt + (mi >> 1)));
+        ldmatrix_x4_trans(vb, st + St::value_at(row, 2 * dt + (mi >> 1)));
         mma_bf16_16816(o[2 * dt], hi, vb[0], vb[1]);
         mma_bf16_16816(o[2 * dt + 1], hi, vb[2], vb[3]);
         if constexpr (WIDE) {
@@ -367,26 +434,31 @@ struct WarpState {
         }
       }
     } else {
-      uint32_t a[4] = {};  // weights in fp16: 2^-12 of their value
+      // weights in fp16 (2^-12 of their value), two k steps of 16 keys.  Column gq of tile t
+      // (of 8) is value 64 c + 8 gq + t: a lane's 8 codes of each of its four keys serve the
+      // 8 tiles, two keys side by side in a fragment register.
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
+      for (int hs = 0; hs < St::HALVES; ++hs) {
+        uint32_t a[4] = {};
 #pragma unroll
-        for (int r = 0; r < R; ++r) a[2 * half + r] = pack_f16(pr[half][2 * r], pr[half][2 * r + 1]);
-      // column gq of tile t (of 8) is value 64 c + 8 gq + t: a lane's 8 codes of each of its
-      // four keys serve the 8 tiles, two keys side by side in a fragment register
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint2 w[4];
+          for (int r = 0; r < R; ++r) a[2 * t + r] = pack_f16(pr[2 * hs + t][2 * r], pr[2 * hs + t][2 * r + 1]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = *reinterpret_cast<const uint2*>(st + St::V0 + ((i >> 1) * 8 + 2 * tq + (i & 1)) * St::VROW + 64 * c + 8 * gq);
+        for (int c = 0; c < D / 64; ++c) {
+          uint2 w[4];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          // codes t of two keys into the low 16 bits
-          const uint32_t sel = (t & 3) | ((4 + (t & 3)) << 4);
-          const uint32_t b0 = __byte_perm(t < 4 ? w[0].x : w[0].y, t < 4 ? w[1].x : w[1].y, sel);
-          const uint32_t b1 = __byte_perm(t < 4 ? w[2].x : w[2].y, t < 4 ? w[3].x : w[3].y, sel);
-          mma_f16_16816(o[8 * c + t], a, widen_f16(b0 & 0xffffu), widen_f16(b1 & 0xffffu));
+          for (int i = 0; i < 4; ++i)
+            w[i] = *reinterpret_cast<const uint2*>(
+                st + St::V0 + (16 * hs + (i >> 1) * 8 + 2 * tq + (i & 1)) * St::VROW + 64 * c + 8 * gq);
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            // codes t of two keys into the low 16 bits
+            const uint32_t sel = (t & 3) | ((4 + (t & 3)) << 4);
+            const uint32_t b0 = __byte_perm(t < 4 ? w[0].x : w[0].y, t < 4 ? w[1].x : w[1].y, sel);
+            const uint32_t b1 = __byte_perm(t < 4 ? w[2].x : w[2].y, t < 4 ? w[3].x : w[3].y, sel);
+            mma_f16_16816(o[8 * c + t], a, widen_f16(b0), widen_f16(b1));
+          }
         }
       }
     }
@@ -399,8 +471,8 @@ struct WarpState {
 };
 
 // One CTA works through its run of units: span after span of one (sequence, group), each
-// warp on 16 of a unit's 64 tokens with its own stages in shared memory and its own running
-// softmax; the warps join when a span ends.  A whole (sequence, group) is written out, a
+// warp on its quarter of a unit's tokens with its own stages in shared memory and its own
+// running softmax; the warps join when a span ends.  A whole (sequence, group) is written out, a
 // part of one goes to the CTA's slot 0 (its first span) or 1.
 template <int D, bool F8, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDecode p) {
@@ -413,10 +485,10 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
   const int gq = lane >> 2, tq = lane & 3;
   int b;
   int64_t base;
-  const Schedule sc = find_run(p, &b, &base);
+  const int64_t total = find_run(p, &b, &base);
   griddep_wait();  // the selected blocks
-  int64_t u = sc.run * blockIdx.x;
-  const int64_t u_end = min(sc.total, u + sc.run);
+  int64_t u = run_start(total, blockIdx.x);
+  const int64_t u_end = run_start(total, blockIdx.x + 1);
   uint8_t* ring = smem + warp * St::COUNT * St::BYTES;
   constexpr int CH = St::ROW / 16;  // 16-byte chunks of a row
   constexpr int RPI = 32 / CH;      // rows of one copy instruction
@@ -445,63 +517,61 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
     // first token of this warp in unit u0 + i
     auto first_token = [&](int i) {
       const int x = u0 + i;
-      if (!p.block_idx) return x * kUnit + warp * 16;
-      constexpr int PER = 128 / kUnit;
-      return __shfl_sync(0xffffffffu, blk, (x / PER) & 31) * 128 + (x % PER) * kUnit + warp * 16;
+      if (!p.block_idx) return x * St::UNIT + warp * St::KEYS;
+      return __shfl_sync(0xffffffffu, blk, (x / St::PER) & 31) * 128 + (x % St::PER) * St::UNIT + warp * St::KEYS;
     };
     const int32_t* table = p.pages.table + (int64_t)b * p.pages.table_stride;
-    auto page_ids = [&](int i) {  // of units i .. i + 31, one a lane; -1 where there is none
-      int x = u0 + i + lane, tok;
-      if (!p.block_idx) {
-        tok = x * kUnit + warp * 16;
-      } else {
-        constexpr int PER = 128 / kUnit;
-        const int c = __shfl_sync(0xffffffffu, blk, (x / PER) & 31);
-        tok = c * 128 + (x % PER) * kUnit + warp * 16;
-      }
-      return i + lane < n && tok < len ? __ldg(&table[page_of(p.pages, tok)]) : -1;
+    constexpr int AHEAD = 32 / St::HALVES;  // units whose page ids a register holds
+    auto page_ids = [&](int i) {  // of the halves of units i .. i + AHEAD - 1, one a lane
+      const int x = u0 + i + lane / St::HALVES;
+      int tok = (lane % St::HALVES) * 16 + warp * St::KEYS;
+      if (!p.block_idx) tok += x * St::UNIT;
+      else tok += __shfl_sync(0xffffffffu, blk, (x / St::PER) & 31) * 128 + (x % St::PER) * St::UNIT;
+      return i + lane / St::HALVES < n && tok < len ? __ldg(&table[page_of(p.pages, tok)]) : -1;
     };
-    int ids = page_ids(0), ids_next = page_ids(32);
+    int ids = page_ids(0), ids_next = page_ids(AHEAD);
     auto load = [&](int i) {
       if (i < n) {
-        if (i > 0 && (i & 31) == 0) {
+        if (i > 0 && i % AHEAD == 0) {
           ids = ids_next;
-          ids_next = page_ids(i + 32);
+          ids_next = page_ids(i + AHEAD);
         }
         uint8_t* st = ring + (i % St::COUNT) * St::BYTES;
-        const int pos = first_token(i);
-        const int id = __shfl_sync(0xffffffffu, ids, i & 31);
-        const int have = min(16, len - pos);  // tokens of the sequence; none: nothing to load
-        if (have > 0) {
-          // 16 tokens never straddle a page
+        const int pos0 = first_token(i);
+#pragma unroll
+        for (int hs = 0; hs < St::HALVES; ++hs) {
+          const int pos = pos0 + 16 * hs;
+          const int id = __shfl_sync(0xffffffffu, ids, (i % AHEAD) * St::HALVES + hs);
+          const int have = len - pos;  // tokens of the sequence from here on
+          if (hs == 0 && have <= 0) break;  // step() will not look at this stage
           const bool good = (unsigned)id < (unsigned)p.pages.num_pages;
-          if (!good) set_status(p.status, MSA_ERR_ARG);
+          if (!good && have > 0) set_status(p.status, MSA_ERR_ARG);
           const int64_t row0 =
               good ? (int64_t)id * p.pages.page_size + (pos - page_of(p.pages, pos) * p.pages.page_size) : 0;
           const int64_t at = (row0 * p.H + g) * St::ROW + lane_off;
           const uint8_t* kp = static_cast<const uint8_t*>(p.k) + at;
           const uint8_t* vp = static_cast<const uint8_t*>(p.v) + at;
-          const bool full = good && have == 16;
+          const bool full = good && have >= 16;
 #pragma unroll
           for (int j = 0; j < 16 / RPI; ++j) {
             const int r = r0 + j * RPI;
-            const uint32_t ko = F8 ? r * St::KROW + ch * 16 : swz<(F8 ? 128 : St::ROW)>(r, ch);
-            const uint32_t vo = F8 ? r * St::VROW + ch * 16 : ko;
+            uint8_t* kd = st + St::key_at(16 * hs + r, ch);
+            uint8_t* vd = st + St::value_at(16 * hs + r, ch);
             if (full) {
-              cp_async_16(st + ko, kp + j * RPI * row_step);
-              cp_async_16(st + St::V0 + vo, vp + j * RPI * row_step);
+              cp_async_16(kd, kp + j * RPI * row_step);
+              cp_async_16(vd, vp + j * RPI * row_step);
             } else {  // else zeros: no stale NaN meets a weight of 0
               const bool ok = good && r < have;
               const int64_t off = ok ? j * RPI * row_step : -lane_off;
-              cp_async_16(st + ko, kp + off, ok);
-              cp_async_16(st + St::V0 + vo, vp + off, ok);
+              cp_async_16(kd, kp + off, ok);
+              cp_async_16(vd, vp + off, ok);
             }
           }
-          if constexpr (F8) {
+          if constexpr (F8) {  // lanes 0..15 the keys' scales, the others the values'
             const int r = lane & 15;
             const bool ok = good && r < have;
             const float* src = (lane < 16 ? p.k_scale : p.v_scale) + (ok ? (row0 + r) * p.H + g : 0);
-            cp_async_4(st + St::S0 + lane * 4, src, ok);
+            cp_async_4(st + St::S0 + ((lane < 16 ? 0 : St::KEYS) + 16 * hs + r) * 4, src, ok);
           }
         }
       }
@@ -604,7 +674,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedDec
   const int64_t head0 = ((int64_t)b * p.H + g) * p.G;
   griddep_wait();
   const int64_t first = __ldcg(&p.starts[b]), end = __ldcg(&p.starts[b + 1]);
-  const int64_t run = run_units(__ldcg(&p.starts[p.B]));
+  const int64_t total = __ldcg(&p.starts[p.B]);
   if (first == end) {
     for (int h = blockIdx.y; h < p.G; h += gridDim.y) {
       for (int x = tid; x < D; x += kJoinThreads) p.o[(head0 + h) * D + x] = __float2bfloat16(0.f);
@@ -613,10 +683,10 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedDec
     return;
   }
   const int64_t units = (end - first) / p.H, u0 = first + g * units;
-  const int c0 = (int)(u0 / run), n = (int)((u0 + units - 1) / run) - c0 + 1;
+  const int c0 = cta_of(total, u0), n = cta_of(total, u0 + units - 1) - c0 + 1;
   if (n == 1) return;
   // part i is slot 0 of CTA c0 + i, except where CTA c0 began with another (sequence, group)
-  const int late = u0 != run * c0;
+  const int late = u0 != run_start(total, c0);
   auto part_of = [&](int i) { return (int64_t)(2 * (c0 + i) + (i == 0 ? late : 0)) * p.G; };
   for (int h = blockIdx.y; h < p.G; h += gridDim.y) {
     float top = -INFINITY;
@@ -789,6 +859,7 @@ template <int D, bool F8, bool WIDE>
 cudaError_t launch_attn(const PagedDecode& p, cudaStream_t stream) {
   constexpr int smem = kWarps * Stage<D, F8>::COUNT * Stage<D, F8>::BYTES;
   static_assert(smem >= kWarps * (WIDE ? 16 : 8) * D * 4, "the join reuses the stages");
+  static_assert(Stage<D, F8>::UNIT == (F8 ? 128 : 64), "unit_shift");
   auto* kern = paged_attn_kernel<D, F8, WIDE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -866,6 +937,7 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   p.topk = topk;
   p.nb = (int)(((int64_t)pt->max_pages * c->page_size + 127) / 128);
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.unit_shift = c->kind == MSA_CACHE_E4M3 ? 7 : 6;
   p.status = cx.status;
   cudaError_t e = cudaSuccess;
   if (topk > 0) {

@@ -161,13 +161,14 @@ __device__ __forceinline__ uint32_t widen_f16(uint32_t two) {
 // 2^(a - b), 0 for a = -inf whatever b.
 __device__ __forceinline__ float weight(float a, float b) { return a == -INFINITY ? 0.f : exp2f(a - b); }
 
-// Shared memory of one warp's stage: KEYS key rows and as many value rows (and their scales).
-//   bf16: 16 rows of 2 D bytes, 16-byte chunks XOR-swizzled for ldmatrix;
-//   E4M3: 32 rows (the same bytes); key rows of D bytes whose 64-byte halves are swapped in odd
-//   rows, value rows padded by 16 bytes: the fragment loads then fall in distinct banks.
+// Shared memory of one warp's stage: KEYS key rows and as many value rows (and their scales),
+// 8 KB of them for most caches.
+//   bf16: rows of 2 D bytes, 16-byte chunks XOR-swizzled for ldmatrix;
+//   E4M3: key rows of D bytes whose 64-byte halves are swapped in odd rows, value rows padded
+//   by 16 bytes: the fragment loads then fall in distinct banks.
 template <int D, bool F8>
 struct Stage {
-  static constexpr int KEYS = F8 ? 32 : 16;
+  static constexpr int KEYS = F8 || D == 64 ? 32 : 16;
   static constexpr int ROW = F8 ? D : 2 * D;
   static constexpr int VROW = F8 ? D + 16 : 2 * D;
   static constexpr int V0 = KEYS * ROW;
@@ -187,18 +188,28 @@ struct Stage {
   }
 };
 
-// One warp's running softmax over its keys, for rows gq and gq + 8 of the fragments: heads gq
-// and gq + 8 (WIDE), or with at most 8 heads the low parts of head gq's operands.
+__device__ __forceinline__ float lg2_fast(float x) {  // relative to 1: about 2^-22
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// One warp's running softmax over its keys.
+//   S = Q K^T: rows are heads gq and gq + 8 (WIDE), or with at most 8 heads, E4M3, the low
+//   parts of head gq's query; columns are keys 8 t + 2 tq + e.
+//   O^T = V^T P^T: rows are value columns, columns the heads 8 nt + 2 tq + e, so that the
+//   accumulator of at most 8 heads has no idle rows; the fragments of S are those of P^T.
+// (gq = lane / 4, tq = lane % 4.)
 template <int D, bool F8, bool WIDE>
 struct WarpState {
   using St = Stage<D, F8>;
-  static constexpr int R = WIDE ? 2 : 1;
-  static constexpr int NT = D / 8;           // tiles of 8 value columns
+  static constexpr int R = WIDE ? 2 : 1;     // heads of a lane's rows of S
+  static constexpr int MT = D / 16;          // tiles of 16 value columns
   static constexpr int KT = St::KEYS / 8;    // tiles of 8 keys
   static constexpr int QS = F8 ? D / 32 : D / 16;
   uint32_t qa[QS][4];                        // query fragments
   uint32_t ql[F8 && WIDE ? QS : 1][4];       // their low parts
-  float o[NT][4];
+  float o[MT][R][4];
   float m[R], mv[R], l[R];  // max, max with the value scale (E4M3), this lane's part of the sum
   float fac[R];             // accumulator -> score in bits
 
@@ -214,7 +225,7 @@ struct WarpState {
 #pragma unroll
           for (int half = 0; half < 2; ++half)
             qa[ks][r + 2 * half] =
-                ok ? __ldg(reinterpret_cast<const uint32_t*>(row + ks * 16 + half * 8 + 2 * tq)) : 0u;
+                r < R && ok ? __ldg(reinterpret_cast<const uint32_t*>(row + ks * 16 + half * 8 + 2 * tq)) : 0u;
       } else if (r < R) {
         // lane tq holds values 64 j + 16 tq + 0..15 of the row, in the order in which step()
         // reads the codes of a key: words 4 (2 j + s) + {0, 1} are k slots 4 tq.. and
@@ -278,38 +289,46 @@ struct WarpState {
       l[r] = 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][r][e] = 0.f;
   }
 
-  // o rows gq times a0, rows gq + 8 times a1
-  __device__ __forceinline__ void rescale(float a0, float a1) {
+  // O times a factor a head, given for the rows of S (heads gq + 8 r).
+  __device__ __forceinline__ void rescale(const float (&alpha)[R], int tq) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const float2 x = fmul2(make_float2(o[i][0], o[i][1]), make_float2(a0, a0));
-      o[i][0] = x.x;
-      o[i][1] = x.y;
-      if constexpr (WIDE || !F8) {  // E4M3 with at most 8 heads leaves those rows zero
-        const float2 y = fmul2(make_float2(o[i][2], o[i][3]), make_float2(a1, a1));
-        o[i][2] = y.x;
-        o[i][3] = y.y;
+    for (int r = 0; r < R; ++r) {
+      const float2 a = make_float2(__shfl_sync(0xffffffffu, alpha[r], 8 * tq),
+                                   __shfl_sync(0xffffffffu, alpha[r], 8 * tq + 4));
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const float2 x = fmul2(make_float2(o[i][r][0], o[i][r][1]), a);
+        const float2 y = fmul2(make_float2(o[i][r][2], o[i][r][3]), a);
+        o[i][r][0] = x.x;
+        o[i][r][1] = x.y;
+        o[i][r][2] = y.x;
+        o[i][r][3] = y.y;
       }
     }
   }
 
   // The keys of a landed stage, of which the first n are the sequence's.
   __device__ __forceinline__ void step(const uint8_t* st, int n, int lane) {
-    const int gq = lane >> 2, tq = lane & 3;
+    const int gq = lane >> 2, tq = lane & 3, mi = lane >> 3;
     float sc[KT][4] = {};
     if constexpr (!F8) {
-      const int mi = lane >> 3, row = (lane & 7) + (mi >> 1) * 8;
 #pragma unroll
-      for (int ks = 0; ks < QS; ++ks) {
-        uint32_t kb[4];
-        ldmatrix_x4(kb, st + St::key_at(row, 2 * ks + (mi & 1)));
-        mma_bf16_16816(sc[0], qa[ks], kb[0], kb[1]);
-        mma_bf16_16816(sc[1], qa[ks], kb[2], kb[3]);
+      for (int kp = 0; kp < KT / 2; ++kp) {
+        const int row = 16 * kp + (lane & 7) + (mi >> 1) * 8;
+#pragma unroll
+        for (int ks = 0; ks < QS; ++ks) {
+          uint32_t kb[4];
+          ldmatrix_x4(kb, st + St::key_at(row, 2 * ks + (mi & 1)));
+          mma_bf16_16816(sc[2 * kp], qa[ks], kb[0], kb[1]);
+          mma_bf16_16816(sc[2 * kp + 1], qa[ks], kb[2], kb[3]);
+        }
       }
     } else {
       // the order of a product's terms is free: lane tq takes values 64 j + 16 tq + 0..15 of
@@ -342,7 +361,7 @@ struct WarpState {
       for (int t = 0; t < KT; ++t) {
         const float2 ks = *reinterpret_cast<const float2*>(scale + 8 * t + 2 * tq);
         const float2 vs = *reinterpret_cast<const float2*>(scale + St::KEYS + 8 * t + 2 * tq);
-        lv[t] = make_float2(__log2f(vs.x), __log2f(vs.y));
+        lv[t] = make_float2(lg2_fast(vs.x), lg2_fast(vs.y));
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           sc[t][2 * r] *= ks.x;
@@ -350,30 +369,34 @@ struct WarpState {
         }
       }
     }
-    float pr[KT][2 * R], alpha[R];  // what multiplies the values
+    float alpha[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float top = -INFINITY, topv = -INFINITY;
+      float top = -INFINITY;
 #pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float& s = sc[t][2 * r + e];
-          s *= fac[r];
-          if (n < St::KEYS) s = 8 * t + 2 * tq + e < n ? s : -INFINITY;
-          top = fmaxf(top, s);
-          if constexpr (F8) topv = fmaxf(topv, s + (e ? lv[t].y : lv[t].x));
+      for (int t = 0; t < KT; ++t) {
+        float &s0 = sc[t][2 * r], &s1 = sc[t][2 * r + 1];
+        s0 *= fac[r];
+        s1 *= fac[r];
+        if (n < St::KEYS) {
+          s0 = 8 * t + 2 * tq < n ? s0 : -INFINITY;
+          s1 = 8 * t + 2 * tq + 1 < n ? s1 : -INFINITY;
         }
+        top = fmax3(top, s0, s1);
+      }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const float m_new = fmaxf(m[r], top);
       const float m_use = m_new == -INFINITY ? 0.f : m_new;
-      const float beta = ex2_fast(m[r] - m_use);
+      alpha[r] = ex2_fast(m[r] - m_use);
       m[r] = m_new;
-      l[r] *= beta;
+      l[r] *= alpha[r];
       if constexpr (F8) {
         // o is kept in units of 2^mv, mv the running max of score + log2(value scale): the
         // weights of the codes then fit fp16 whatever the scales are
+        float topv = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < KT; ++t) topv = fmax3(topv, sc[t][2 * r] + lv[t].x, sc[t][2 * r + 1] + lv[t].y);
         topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, 1));
         topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, 2));
         const float v_new = fmaxf(mv[r], topv);
@@ -381,92 +404,87 @@ struct WarpState {
         alpha[r] = ex2_fast(mv[r] - v_use);
         mv[r] = v_new;
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float s = sc[t][2 * r + e];
-            l[r] += ex2_fast(s - m_use);
-            pr[t][2 * r + e] = ex2_fast(s + (e ? lv[t].y : lv[t].x) - v_use);
-          }
+        for (int t = 0; t < KT; ++t) {
+          float &s0 = sc[t][2 * r], &s1 = sc[t][2 * r + 1];
+          l[r] += ex2_fast(s0 - m_use) + ex2_fast(s1 - m_use);
+          s0 = ex2_fast(s0 + (lv[t].x - v_use));
+          s1 = ex2_fast(s1 + (lv[t].y - v_use));
+        }
       } else {
-        alpha[r] = beta;
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x = ex2_fast(sc[t][2 * r + e] - m_use);
-            l[r] += x;
-            pr[t][2 * r + e] = x;
-          }
+        for (int t = 0; t < KT; ++t) {
+          float &s0 = sc[t][2 * r], &s1 = sc[t][2 * r + 1];
+          s0 = ex2_fast(s0 - m_use);
+          s1 = ex2_fast(s1 - m_use);
+          l[r] += s0 + s1;
+        }
       }
     }
+    // sc now holds P (E4M3: times the value scales)
     bool same = alpha[0] == 1.f;
     if constexpr (WIDE) same = same && alpha[R - 1] == 1.f;
-    if (!__all_sync(0xffffffffu, same)) rescale(alpha[0], alpha[R - 1]);
-    if constexpr (!F8) {
-      // P enters in two bf16 parts (together 2^-17 of its value): the output's own rounding
-      // stays its largest error.  With at most 8 heads the low parts ride in the rows that no
-      // head uses; with more they take a product of their own.
-      uint32_t hi[4] = {}, lo[4] = {};
+    if (!__all_sync(0xffffffffu, same)) rescale(alpha, tq);
 #pragma unroll
-      for (int t = 0; t < KT; ++t)
+    for (int kp = 0; kp < KT / 2; ++kp) {  // 16 keys: one k step
+      if constexpr (!F8) {
+        // P enters in two bf16 parts (together 2^-17 of its value): the output's own rounding
+        // stays its largest error
+        uint32_t hi[R][2], lo[R][2];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float e0 = pr[t][2 * r], e1 = pr[t][2 * r + 1];
-          const uint32_t h = pack_bf16(e0, e1);
-          hi[2 * t + r] = h;
-          lo[2 * t + r] = pack_bf16(e0 - __uint_as_float(h << 16), e1 - __uint_as_float(h & 0xffff0000u));
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const float e0 = sc[2 * kp + t][2 * r], e1 = sc[2 * kp + t][2 * r + 1];
+            const uint32_t h = pack_bf16(e0, e1);
+            hi[r][t] = h;
+            lo[r][t] = pack_bf16(e0 - __uint_as_float(h << 16), e1 - __uint_as_float(h & 0xffff0000u));
+          }
+        const int row = 16 * kp + (lane & 7) + (mi >> 1) * 8;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          uint32_t va[4];  // V^T: matrix mi covers keys (mi >> 1) * 8.. and columns (mi & 1) * 8..
+          ldmatrix_x4_trans(va, st + St::value_at(row, 2 * i + (mi & 1)));
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            mma_bf16_16816(o[i][r], va, hi[r][0], hi[r][1]);
+            mma_bf16_16816(o[i][r], va, lo[r][0], lo[r][1]);
+          }
         }
-      if constexpr (!WIDE) {
-        hi[1] = lo[0];
-        hi[3] = lo[2];
-      }
-      const int mi = lane >> 3, row = (lane & 7) + (mi & 1) * 8;
+      } else {
+        uint32_t pb[R][2];  // weights in fp16: 2^-12 of their value
 #pragma unroll
-      for (int dt = 0; dt < D / 16; ++dt) {
-        uint32_t vb[4];
-        ldmatrix_x4_trans(vb, st + St::value_at(row, 2 * dt + (mi >> 1)));
-        mma_bf16_16816(o[2 * dt], hi, vb[0], vb[1]);
-        mma_bf16_16816(o[2 * dt + 1], hi, vb[2], vb[3]);
-        if constexpr (WIDE) {
-          mma_bf16_16816(o[2 * dt], lo, vb[0], vb[1]);
-          mma_bf16_16816(o[2 * dt + 1], lo, vb[2], vb[3]);
-        }
-      }
-    } else {
-      // weights in fp16 (2^-12 of their value), two k steps of 16 keys.  Column gq of tile t
-      // (of 8) is value 64 c + 8 gq + t: a lane's 8 codes of each of its four keys serve the
-      // 8 tiles, two keys side by side in a fragment register.
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int hs = 0; hs < St::HALVES; ++hs) {
-        uint32_t a[4] = {};
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int r = 0; r < R; ++r) a[2 * t + r] = pack_f16(pr[2 * hs + t][2 * r], pr[2 * hs + t][2 * r + 1]);
+          for (int t = 0; t < 2; ++t) pb[r][t] = pack_f16(sc[2 * kp + t][2 * r], sc[2 * kp + t][2 * r + 1]);
+        // row gq (+ 8) of tile 4 c + i is value column 64 c + 8 gq + 2 i (+ 1): a lane's 8 codes
+        // of each of its four keys serve four tiles, two keys side by side in a register
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
           uint2 w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             w[i] = *reinterpret_cast<const uint2*>(
-                st + St::V0 + (16 * hs + (i >> 1) * 8 + 2 * tq + (i & 1)) * St::VROW + 64 * c + 8 * gq);
+                st + St::V0 + (16 * kp + (i >> 1) * 8 + 2 * tq + (i & 1)) * St::VROW + 64 * c + 8 * gq);
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            // codes t of two keys into the low 16 bits
-            const uint32_t sel = (t & 3) | ((4 + (t & 3)) << 4);
-            const uint32_t b0 = __byte_perm(t < 4 ? w[0].x : w[0].y, t < 4 ? w[1].x : w[1].y, sel);
-            const uint32_t b1 = __byte_perm(t < 4 ? w[2].x : w[2].y, t < 4 ? w[3].x : w[3].y, sel);
-            mma_f16_16816(o[8 * c + t], a, widen_f16(b0), widen_f16(b1));
+          for (int i = 0; i < 4; ++i) {
+            uint32_t va[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // e & 1: column 2 i + 1; e >> 1: keys 8..15
+              const uint2 x = w[2 * (e >> 1)], y = w[2 * (e >> 1) + 1];
+              const int byte = (2 * i + (e & 1)) & 3;
+              va[e] = widen_f16(__byte_perm(i < 2 ? x.x : x.y, i < 2 ? y.x : y.y, byte | ((4 + byte) << 4)));
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) mma_f16_16816(o[4 * c + i][r], va, pb[r][0], pb[r][1]);
           }
         }
       }
     }
   }
 
-  // Column of the head's values that o[i][e] holds.
-  __device__ __forceinline__ static int column(int i, int e, int tq) {
-    return F8 ? (i >> 3) * 64 + 8 * (2 * tq + (e & 1)) + (i & 7) : 8 * i + 2 * tq + (e & 1);
+  // Value column that o[i][.][e] holds; its head is 8 r + 2 tq + (e & 1).
+  __device__ __forceinline__ static int column(int i, int e, int gq) {
+    return F8 ? (i >> 2) * 64 + 8 * gq + 2 * (i & 3) + (e >> 1) : 16 * i + gq + 8 * (e >> 1);
   }
 };
 
@@ -601,20 +619,14 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
       }
     }
     __syncthreads();  // every warp is done with its stages
-    float* s_o = reinterpret_cast<float*>(smem);  // [kWarps][ROWS][D]
+    float* s_o = reinterpret_cast<float*>(smem);  // [kWarps][ROWS][D + 4]
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int col = ws.column(i, e, tq);
-        float* row = s_o + (warp * ROWS + gq) * D + col;
-        if constexpr (WIDE) {
-          row[0] = ws.o[i][e];
-          row[8 * D] = ws.o[i][2 + e];
-        } else {
-          row[0] = ws.o[i][e] + ws.o[i][2 + e];
-        }
-      }
+      for (int r = 0; r < ws.R; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          s_o[(warp * ROWS + 8 * r + 2 * tq + (e & 1)) * (D + 4) + ws.column(i, e, gq)] = ws.o[i][r][e];
     // weights of the warps in each head's joined value, and its lse in bits
     if (tid < p.G) {
       float top = -INFINITY, l = 0.f;
@@ -637,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float f = s_w[w][h];
-          const float4 y = *reinterpret_cast<const float4*>(s_o + (w * ROWS + h) * D + c);
+          const float4 y = *reinterpret_cast<const float4*>(s_o + (w * ROWS + h) * (D + 4) + c);
           acc.x = fmaf(f, y.x, acc.x);
           acc.y = fmaf(f, y.y, acc.y);
           acc.z = fmaf(f, y.z, acc.z);
@@ -858,8 +870,8 @@ cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, bool after, c
 template <int D, bool F8, bool WIDE>
 cudaError_t launch_attn(const PagedDecode& p, cudaStream_t stream) {
   constexpr int smem = kWarps * Stage<D, F8>::COUNT * Stage<D, F8>::BYTES;
-  static_assert(smem >= kWarps * (WIDE ? 16 : 8) * D * 4, "the join reuses the stages");
-  static_assert(Stage<D, F8>::UNIT == (F8 ? 128 : 64), "unit_shift");
+  static_assert(smem >= kWarps * (WIDE ? 16 : 8) * (D + 4) * 4, "the join reuses the stages");
+  static_assert(Stage<D, F8>::UNIT == (F8 || D == 64 ? 128 : 64), "unit_shift");
   auto* kern = paged_attn_kernel<D, F8, WIDE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -937,7 +949,7 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   p.topk = topk;
   p.nb = (int)(((int64_t)pt->max_pages * c->page_size + 127) / 128);
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.unit_shift = c->kind == MSA_CACHE_E4M3 ? 7 : 6;
+  p.unit_shift = c->kind == MSA_CACHE_E4M3 || c->d == 64 ? 7 : 6;
   p.status = cx.status;
   cudaError_t e = cudaSuccess;
   if (topk > 0) {

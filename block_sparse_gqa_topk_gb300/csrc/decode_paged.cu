@@ -39,13 +39,14 @@ struct PagedDecode {
   const int32_t* lens;  // [B]
   int32_t* block_idx;   // [B][H][topk]; null: the whole cache
   float* pooled;        // [B][H][nb]
-  float* part_o;        // [2 kCtas][G][d]
-  float* part_lse;      // [2 kCtas][G], in bits (log2)
-  int64_t* starts;      // [B + 1] first unit of each sequence, written for the join
+  float* part_o;        // [2 kCtas][wh][G][d]
+  float* part_lse;      // [2 kCtas][wh][G], in bits (log2)
+  int64_t* starts;      // [B + 2] first unit of each sequence, their total, wh: for the join
   __nv_bfloat16* o;
   float* lse;
   int B, H, G, topk, nb;
-  int unit_shift;    // log2 of a unit's tokens
+  int wh;          // heads (groups) that a CTA may serve side by side
+  int keys_shift;  // log2 of a stage's keys
   float scale_log2;  // scale * log2 e: scores in bits
   int* status;
 };
@@ -60,12 +61,15 @@ __device__ __forceinline__ int seq_len(const PagedDecode& p, int b) {
   return n;
 }
 
-__device__ __forceinline__ int seq_units(const PagedDecode& p, int len) {
+// Units of a sequence for one group (wh groups): a unit is a stage of each of the kWarps / wh
+// warps that share a group's tokens.
+__device__ __forceinline__ int seq_units(const PagedDecode& p, int len, int wh) {
   if (p.block_idx) {  // the own block, cut at the length, comes last of the selected ones
     const int blocks = (len + 127) / 128;
     len -= max(0, blocks - p.topk) * 128;
   }
-  return (int)(((int64_t)len + (1 << p.unit_shift) - 1) >> p.unit_shift);
+  const int shift = p.keys_shift + (wh == 1 ? 2 : wh == 2 ? 1 : 0);
+  return (int)(((int64_t)len + (1 << shift) - 1) >> shift);
 }
 
 // The units of all (sequence, group) pairs, in order, are cut into n = min(kCtas, total) runs
@@ -79,41 +83,77 @@ __device__ __forceinline__ int cta_of(int64_t total, int64_t unit) {
   return (int)(((unit + 1) * min((int64_t)kCtas, total) - 1) / total);
 }
 
-// Every thread of the CTA gets the number of units, and a sequence with its first unit: the
-// one that holds the first unit of the CTA's run (any sequence where the run is empty).  CTA 0
-// leaves the sequences' first units for the join.
-__device__ __forceinline__ int64_t find_run(const PagedDecode& p, int* b_out, int64_t* base_out) {
-  __shared__ int64_t s_sum[kWarps];
+// Groups side by side read rows that are neighbours in a page, which HBM serves faster (E4M3, 8 x
+// 128K, d 128: 443 -> 343 us; d 64: 393 -> 232; bf16: 319 -> 309), but leave wh times the parts to
+// join.  They pay from about this many units (of one group) a CTA.
+constexpr int64_t kSideBySide = 48;
+
+struct Work {
+  int64_t total;  // units
+  int wh, HG;     // groups side by side, H / wh
+  int b;          // the sequence that holds the first unit of the CTA's run (any if that is empty)
+  int64_t base;   // its first unit
+};
+
+// Every thread of the CTA gets the work.  CTA 0 leaves what the join needs of it.
+template <bool SPARSE>
+__device__ __forceinline__ Work find_run(const PagedDecode& p) {
+  __shared__ int64_t s_sum[2][kWarps];
   __shared__ int s_b;
   __shared__ int64_t s_base;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += (int64_t)seq_units(p, seq_len(p, b)) * p.H;
-  int64_t scan = mine;
+  int64_t mine = 0, side = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int len = seq_len(p, b);
+    mine += seq_units(p, len, 1);
+    if (!SPARSE) side += seq_units(p, len, p.wh);
+  }
+  mine *= p.H;
+  side *= p.H / p.wh;
+  int64_t scan = mine, scan_side = side;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += y;
+    const int64_t x = __shfl_up_sync(0xffffffffu, scan, o);
+    const int64_t y = SPARSE ? 0 : __shfl_up_sync(0xffffffffu, scan_side, o);
+    if (lane >= o) {
+      scan += x;
+      scan_side += y;
+    }
   }
-  if (lane == 31) s_sum[warp] = scan;
+  if (lane == 31) {
+    s_sum[0][warp] = scan;
+    s_sum[1][warp] = scan_side;
+  }
   if (tid == 0) {
     s_b = 0;
     s_base = 0;
   }
   __syncthreads();
-  int64_t total = 0, base = scan - mine;  // first unit of this thread's sequences
+  Work k;
+  k.total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) base += s_sum[w];
-    total += s_sum[w];
+  for (int w = 0; w < kWarps; ++w) k.total += s_sum[0][w];
+  const bool sided = !SPARSE && p.wh > 1 && k.total >= kSideBySide * kCtas;
+  if (sided) {
+    k.total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) k.total += s_sum[1][w];
+    scan = scan_side;
+    mine = side;
   }
-  const int64_t want = run_start(total, blockIdx.x);
+  k.wh = sided ? p.wh : 1;
+  k.HG = sided ? p.H / p.wh : p.H;
+  int64_t base = scan - mine;  // first unit of this thread's sequences
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w)
+    if (w < warp) base += s_sum[sided][w];
+  const int64_t want = run_start(k.total, blockIdx.x);
   const bool here = want >= base && want < base + mine;
   if (here || blockIdx.x == 0) {
     for (int b = b0; b < b1; ++b) {
-      const int64_t n = (int64_t)seq_units(p, seq_len(p, b)) * p.H;
+      const int64_t n = (int64_t)seq_units(p, seq_len(p, b), k.wh) * k.HG;
       if (blockIdx.x == 0) p.starts[b] = base;
       if (here && want >= base && want < base + n) {
         s_b = b;
@@ -122,11 +162,14 @@ __device__ __forceinline__ int64_t find_run(const PagedDecode& p, int* b_out, in
       base += n;
     }
   }
-  if (blockIdx.x == 0 && tid == 0) p.starts[p.B] = total;
+  if (blockIdx.x == 0 && tid == 0) {
+    p.starts[p.B] = k.total;
+    p.starts[p.B + 1] = k.wh;
+  }
   __syncthreads();
-  *b_out = s_b;
-  *base_out = s_base;
-  return total;
+  k.b = s_b;
+  k.base = s_base;
+  return k;
 }
 
 // D(16x8) += A(16x16, row) * B(16x8, col), fp16
@@ -488,62 +531,67 @@ struct WarpState {
   }
 };
 
-// One CTA works through its run of units: span after span of one (sequence, group), each
-// warp on its quarter of a unit's tokens with its own stages in shared memory and its own
-// running softmax; the warps join when a span ends.  A whole (sequence, group) is written out, a
-// part of one goes to the CTA's slot 0 (its first span) or 1.
-template <int D, bool F8, bool WIDE>
+// One CTA works through its run of units: span after span of one (sequence, wh groups).  Its
+// warps take the groups side by side and share each one's tokens, every warp with its own
+// stages in shared memory and its own running softmax; they join when a span ends.  A whole
+// (sequence, groups) is written out, a part of one goes to the CTA's slot 0 (its first span) or 1.
+template <int D, bool F8, bool WIDE, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDecode p) {
   using St = Stage<D, F8>;
   constexpr int ROWS = WIDE ? 16 : 8;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[kWarps][16], s_mv[kWarps][16], s_l[kWarps][16], s_w[kWarps][16], s_lse[16];
+  __shared__ float s_m[kWarps][16], s_mv[kWarps][16], s_l[kWarps][16], s_w[kWarps][16], s_lse[kWarps][16];
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gq = lane >> 2, tq = lane & 3;
-  int b;
-  int64_t base;
-  const int64_t total = find_run(p, &b, &base);
+  const Work work = find_run<SPARSE>(p);
+  const int wh = SPARSE ? 1 : work.wh, HG = SPARSE ? p.H : work.HG;
+  int b = work.b;
+  int64_t base = work.base;
   griddep_wait();  // the selected blocks
-  int64_t u = run_start(total, blockIdx.x);
-  const int64_t u_end = run_start(total, blockIdx.x + 1);
+  int64_t u = run_start(work.total, blockIdx.x);
+  const int64_t u_end = run_start(work.total, blockIdx.x + 1);
   uint8_t* ring = smem + warp * St::COUNT * St::BYTES;
   constexpr int CH = St::ROW / 16;  // 16-byte chunks of a row
   constexpr int RPI = 32 / CH;      // rows of one copy instruction
   const int r0 = lane / CH, ch = lane % CH;
   const int64_t row_step = (int64_t)p.H * St::ROW;
   const int64_t lane_off = r0 * row_step + ch * 16;
+  // warp w works for head hg wh + w % wh, on the (w / wh)-th run of KEYS tokens of each unit
+  const int my_head = warp & (wh - 1), subs = kWarps / wh;
+  const int my_token = (wh == 1 ? warp : wh == 2 ? warp >> 1 : 0) * St::KEYS, unit = St::KEYS * subs;
   WarpState<D, F8, WIDE> ws;
   for (int slot = 0; u < u_end; slot = 1) {
     int len = seq_len(p, b);
-    int units = seq_units(p, len);
-    while (base + (int64_t)units * p.H <= u) {  // next sequence that has any
-      base += (int64_t)units * p.H;
+    int units = seq_units(p, len, wh);
+    while (base + (int64_t)units * HG <= u) {  // next sequence that has any
+      base += (int64_t)units * HG;
       ++b;
       len = seq_len(p, b);
-      units = seq_units(p, len);
+      units = seq_units(p, len, wh);
     }
-    const int g = (int)((u - base) / units);
-    const int u0 = (int)(u - base - (int64_t)g * units);
+    const int hg = (int)((u - base) / units);
+    const int u0 = (int)(u - base - (int64_t)hg * units);
+    const int g = hg * wh + my_head;
     const int n = (int)min((int64_t)(units - u0), u_end - u);
     const int64_t head0 = ((int64_t)b * p.H + g) * p.G;
     // Page ids of the next 32 units sit in the lanes of a register (and those of the 32 after
     // them are on their way), so that no lookup stands in front of a copy.  Selected blocks,
     // at most 32, sit in another.
     int blk = 0;
-    if (p.block_idx && lane < p.topk) blk = __ldg(&p.block_idx[((int64_t)b * p.H + g) * p.topk + lane]);
+    if (SPARSE && lane < p.topk) blk = __ldg(&p.block_idx[((int64_t)b * p.H + g) * p.topk + lane]);
     // first token of this warp in unit u0 + i
     auto first_token = [&](int i) {
       const int x = u0 + i;
-      if (!p.block_idx) return x * St::UNIT + warp * St::KEYS;
-      return __shfl_sync(0xffffffffu, blk, (x / St::PER) & 31) * 128 + (x % St::PER) * St::UNIT + warp * St::KEYS;
+      if (!SPARSE) return x * unit + my_token;
+      return __shfl_sync(0xffffffffu, blk, (x / St::PER) & 31) * 128 + (x % St::PER) * St::UNIT + my_token;
     };
     const int32_t* table = p.pages.table + (int64_t)b * p.pages.table_stride;
     constexpr int AHEAD = 32 / St::HALVES;  // units whose page ids a register holds
     auto page_ids = [&](int i) {  // of the halves of units i .. i + AHEAD - 1, one a lane
       const int x = u0 + i + lane / St::HALVES;
-      int tok = (lane % St::HALVES) * 16 + warp * St::KEYS;
-      if (!p.block_idx) tok += x * St::UNIT;
+      int tok = (lane % St::HALVES) * 16 + my_token;
+      if (!SPARSE) tok += x * unit;
       else tok += __shfl_sync(0xffffffffu, blk, (x / St::PER) & 31) * 128 + (x % St::PER) * St::UNIT;
       return i + lane / St::HALVES < n && tok < len ? __ldg(&table[page_of(p.pages, tok)]) : -1;
     };
@@ -600,7 +648,9 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
     ws.load_q(p, head0, gq, tq);
     for (int i = 0; i < n; ++i) {
       cp_async_wait<St::COUNT - 2>();
-      __syncwarp();  // unit i has landed for all lanes, and all are done with unit i - 1
+      // unit i has landed for all lanes, and all are done with unit i - 1; heads side by side
+      // stay in step, so that what they load together lies together in memory
+      if (wh > 1) __syncthreads(); else __syncwarp();
       load(i + St::COUNT - 1);
       const int have = len - first_token(i);
       if (have > 0) ws.step(ring + (i % St::COUNT) * St::BYTES, have, lane);
@@ -628,26 +678,34 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
         for (int e = 0; e < 4; ++e)
           s_o[(warp * ROWS + 8 * r + 2 * tq + (e & 1)) * (D + 4) + ws.column(i, e, gq)] = ws.o[i][r][e];
     // weights of the warps in each head's joined value, and its lse in bits
-    if (tid < p.G) {
+    if (tid < wh * p.G) {
+      const int w0 = tid / p.G, h = tid - w0 * p.G;
       float top = -INFINITY, l = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][tid]);
+      for (int k = 0; k < kWarps; ++k)
+        if (k < subs) top = fmaxf(top, s_m[w0 + k * wh][h]);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) l += s_l[w][tid] * weight(s_m[w][tid], top);
+      for (int k = 0; k < kWarps; ++k)
+        if (k < subs) l += s_l[w0 + k * wh][h] * weight(s_m[w0 + k * wh][h], top);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s_w[w][tid] = weight(s_mv[w][tid], top) / l;
-      s_lse[tid] = top + log2f(l);
+      for (int k = 0; k < kWarps; ++k)
+        if (k < subs) s_w[w0 + k * wh][h] = weight(s_mv[w0 + k * wh][h], top) / l;
+      s_lse[w0][h] = top + log2f(l);
     }
     __syncthreads();
     const bool whole = u0 == 0 && n == units;
-    const int64_t part = (int64_t)(2 * blockIdx.x + slot) * p.G;
-    for (int x = tid; x < p.G * (D / 4); x += kThreads) {
-      const int h = x / (D / 4), c = 4 * (x % (D / 4));
+    const int64_t part = (int64_t)(2 * blockIdx.x + slot) * wh * p.G;
+    const int64_t out0 = ((int64_t)b * p.H + hg * wh) * p.G;  // first of the wh G query heads
+    for (int x = tid; x < wh * p.G * (D / 4); x += kThreads) {
+      const int row = x / (D / 4), c = 4 * (x % (D / 4));
+      const int w0 = row / p.G, h = row - w0 * p.G;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      const float lse2 = s_lse[h];
+      const float lse2 = s_lse[w0][h];
       if (whole || lse2 > -INFINITY) {  // a part whose scores are all -inf weighs nothing in the join
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int k = 0; k < kWarps; ++k) {
+          if (k >= subs) break;
+          const int w = w0 + k * wh;
           const float f = s_w[w][h];
           const float4 y = *reinterpret_cast<const float4*>(s_o + (w * ROWS + h) * (D + 4) + c);
           acc.x = fmaf(f, y.x, acc.x);
@@ -657,12 +715,12 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
         }
       }
       if (whole) {
-        *reinterpret_cast<uint2*>(p.o + (head0 + h) * D + c) =
+        *reinterpret_cast<uint2*>(p.o + (out0 + row) * D + c) =
             make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
-        if (c == 0) p.lse[head0 + h] = lse2 * 0.6931471805599453f;
+        if (c == 0) p.lse[out0 + row] = lse2 * 0.6931471805599453f;
       } else {
-        *reinterpret_cast<float4*>(p.part_o + (part + h) * D + c) = acc;
-        if (c == 0) p.part_lse[part + h] = lse2;
+        *reinterpret_cast<float4*>(p.part_o + (part + row) * D + c) = acc;
+        if (c == 0) p.part_lse[part + row] = lse2;
       }
     }
     __syncthreads();  // the stages are free for the next span
@@ -671,35 +729,39 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
 }
 
 // Joins the parts of every (sequence, group) that the split cut; an empty sequence gets
-// o = 0 and lse = -inf.  Grid (B H, head splits): a CTA takes heads blockIdx.y, + gridDim.y,
-// ...; its warps take parts in turn, a lane 4 columns (8 warps x 32 lanes x 4 = 8 parts of 128
-// columns at once; 16 of 64).
+// o = 0 and lse = -inf.  Grid (B H, head splits, D / COLS): a CTA takes heads blockIdx.y,
+// + gridDim.y, ... and COLS value columns; its threads take parts side by side, each 4 columns.
 constexpr int kJoinThreads = 256;
-template <int D>
+template <int D, int COLS>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedDecode p) {
-  constexpr int LANES = D / 4;                    // threads of a part
+  constexpr int LANES = COLS / 4;                 // threads of a part
   constexpr int PARTS = kJoinThreads / LANES;     // parts at once
   __shared__ float s_w[kCtas + 1], s_red[8], s_sum[8];
-  __shared__ float4 s_acc[PARTS][LANES];
+  __shared__ float4 s_acc[8][LANES];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / p.H, g = blockIdx.x - b * p.H;
   const int64_t head0 = ((int64_t)b * p.H + g) * p.G;
+  const int col0 = blockIdx.z * COLS;
   griddep_wait();
   const int64_t first = __ldcg(&p.starts[b]), end = __ldcg(&p.starts[b + 1]);
   const int64_t total = __ldcg(&p.starts[p.B]);
+  const int wh = (int)__ldcg(&p.starts[p.B + 1]);
   if (first == end) {
     for (int h = blockIdx.y; h < p.G; h += gridDim.y) {
-      for (int x = tid; x < D; x += kJoinThreads) p.o[(head0 + h) * D + x] = __float2bfloat16(0.f);
-      if (tid == 0) p.lse[head0 + h] = -INFINITY;
+      for (int x = tid; x < COLS; x += kJoinThreads) p.o[(head0 + h) * D + col0 + x] = __float2bfloat16(0.f);
+      if (tid == 0 && col0 == 0) p.lse[head0 + h] = -INFINITY;
     }
     return;
   }
-  const int64_t units = (end - first) / p.H, u0 = first + g * units;
+  const int hg = wh == 4 ? g >> 2 : wh == 2 ? g >> 1 : g, HG = wh == 4 ? p.H >> 2 : wh == 2 ? p.H >> 1 : p.H;
+  const int64_t units = (end - first) / HG, u0 = first + hg * units;
   const int c0 = cta_of(total, u0), n = cta_of(total, u0 + units - 1) - c0 + 1;
   if (n == 1) return;
-  // part i is slot 0 of CTA c0 + i, except where CTA c0 began with another (sequence, group)
+  // part i is slot 0 of CTA c0 + i, except where CTA c0 began with another (sequence, groups)
   const int late = u0 != run_start(total, c0);
-  auto part_of = [&](int i) { return (int64_t)(2 * (c0 + i) + (i == 0 ? late : 0)) * p.G; };
+  auto part_of = [&](int i) {
+    return ((int64_t)(2 * (c0 + i) + (i == 0 ? late : 0)) * wh + (g - hg * wh)) * p.G;
+  };
   for (int h = blockIdx.y; h < p.G; h += gridDim.y) {
     float top = -INFINITY;
     for (int i = tid; i < n; i += kJoinThreads) {
@@ -727,7 +789,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedDec
     float l = 0.f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) l += s_sum[w];
-    const int col = tid % LANES;
+    const int col = col0 / 4 + tid % LANES;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int i = tid / LANES; i < n; i += PARTS) {
@@ -738,19 +800,27 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedDec
       acc.z = fmaf(w, y.z, acc.z);
       acc.w = fmaf(w, y.w, acc.w);
     }
-    s_acc[tid / LANES][col] = acc;
+#pragma unroll
+    for (int o = LANES; o < 32; o <<= 1) {  // parts of the same columns within the warp
+      acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+      acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+      acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
+      acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+    }
+    if (lane < LANES) s_acc[warp][lane] = acc;
     __syncthreads();
     if (tid < LANES) {
-      for (int i = 1; i < PARTS; ++i) {
-        const float4 y = s_acc[i][tid];
+#pragma unroll
+      for (int w = 1; w < 8; ++w) {
+        const float4 y = s_acc[w][tid];
         acc.x += y.x;
         acc.y += y.y;
         acc.z += y.z;
         acc.w += y.w;
       }
-      *reinterpret_cast<uint2*>(p.o + (head0 + h) * D + 4 * tid) =
+      *reinterpret_cast<uint2*>(p.o + (head0 + h) * D + col0 + 4 * tid) =
           make_uint2(pack_bf16(acc.x / l, acc.y / l), pack_bf16(acc.z / l, acc.w / l));
-      if (tid == 0) p.lse[head0 + h] = (top + log2f(l)) * 0.6931471805599453f;
+      if (tid == 0 && col0 == 0) p.lse[head0 + h] = (top + log2f(l)) * 0.6931471805599453f;
     }
     __syncthreads();
   }
@@ -867,20 +937,44 @@ cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, bool after, c
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <int D, bool F8, bool WIDE>
+template <int D, bool F8, bool WIDE, bool SPARSE>
 cudaError_t launch_attn(const PagedDecode& p, cudaStream_t stream) {
   constexpr int smem = kWarps * Stage<D, F8>::COUNT * Stage<D, F8>::BYTES;
   static_assert(smem >= kWarps * (WIDE ? 16 : 8) * (D + 4) * 4, "the join reuses the stages");
-  static_assert(Stage<D, F8>::UNIT == (F8 || D == 64 ? 128 : 64), "unit_shift");
-  auto* kern = paged_attn_kernel<D, F8, WIDE>;
+  auto* kern = paged_attn_kernel<D, F8, WIDE, SPARSE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  if ((e = launch(kern, dim3(kCtas), kThreads, smem, p.block_idx != nullptr, stream, p)) != cudaSuccess)
-    return e;
-  // one CTA a head while they are few: the join is a chain of loads, shorter the fewer heads
-  const int64_t rows = (int64_t)p.B * p.H;
-  const unsigned split = rows * p.G <= 1024 ? (unsigned)p.G : 1u;
-  return launch(paged_join_kernel<D>, dim3((unsigned)rows, split), kJoinThreads, 0, true, stream, p);
+  return launch(kern, dim3(kCtas), kThreads, smem, SPARSE, stream, p);
+}
+
+template <int D>
+cudaError_t launch_paged(const PagedDecode& p, bool f8, bool wide, cudaStream_t stream) {
+  const bool sparse = p.block_idx != nullptr;
+  cudaError_t e;
+  if (f8) {
+    if (wide) e = sparse ? launch_attn<D, true, true, true>(p, stream) : launch_attn<D, true, true, false>(p, stream);
+    else e = sparse ? launch_attn<D, true, false, true>(p, stream) : launch_attn<D, true, false, false>(p, stream);
+  } else {
+    if (wide) e = sparse ? launch_attn<D, false, true, true>(p, stream) : launch_attn<D, false, true, false>(p, stream);
+    else e = sparse ? launch_attn<D, false, false, true>(p, stream) : launch_attn<D, false, false, false>(p, stream);
+  }
+  if (e != cudaSuccess) return e;
+  // The join is a chain of loads, shorter the more parts a CTA reads at once: a CTA for each
+  // head, and for each 32 columns, while all of them run together (8 x 4 groups of 4 heads, 22
+  // parts: 22 us for the whole call with a CTA a head, 30 us with four, 25 us with one a group).
+  const int64_t rows = (int64_t)p.B * p.H, together = 4 * 152;
+  if (rows * p.G * (D / 32) <= together)
+    return launch(paged_join_kernel<D, 32>, dim3((unsigned)rows, (unsigned)p.G, D / 32), kJoinThreads, 0, true,
+                  stream, p);
+  return launch(paged_join_kernel<D, D>, dim3((unsigned)rows, rows * p.G <= together ? (unsigned)p.G : 1u),
+                kJoinThreads, 0, true, stream, p);
+}
+
+// Heads (groups) that a CTA serves side by side: all attend the same tokens when the whole cache
+// is attended, and rows of one token are neighbours in a page; selected blocks differ by group.
+int heads_side_by_side(int H, int topk) {
+  if (topk > 0) return 1;
+  return H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;
 }
 
 struct Layout {
@@ -901,9 +995,10 @@ int check_sizes(const msa_paged_cache_t* c, const msa_page_table_t* pt, int H_q,
   if ((int64_t)pt->B * c->H_kv > (1 << 24) || pt->B > 65535) return MSA_ERR_UNSUPPORTED;
   if (topk > 0 && c->d_idx == 0) return MSA_ERR_SHAPE;
   lay->part_o = 0;
-  lay->part_lse = align256((size_t)2 * kCtas * G * c->d * 4);
-  lay->starts = lay->part_lse + align256((size_t)2 * kCtas * G * 4);
-  lay->pooled = lay->starts + align256(((size_t)pt->B + 1) * 8);
+  const size_t parts = (size_t)2 * kCtas * heads_side_by_side(c->H_kv, topk) * G;
+  lay->part_lse = align256(parts * c->d * 4);
+  lay->starts = lay->part_lse + align256(parts * 4);
+  lay->pooled = lay->starts + align256(((size_t)pt->B + 2) * 8);
   lay->bytes = lay->pooled + (topk > 0 ? align256((size_t)pt->B * c->H_kv * ((cap + 127) / 128) * 4) : 0);
   return MSA_OK;
 }
@@ -949,7 +1044,8 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   p.topk = topk;
   p.nb = (int)(((int64_t)pt->max_pages * c->page_size + 127) / 128);
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.unit_shift = c->kind == MSA_CACHE_E4M3 || c->d == 64 ? 7 : 6;
+  p.wh = heads_side_by_side(p.H, topk);
+  p.keys_shift = c->kind == MSA_CACHE_E4M3 || c->d == 64 ? 5 : 4;
   p.status = cx.status;
   cudaError_t e = cudaSuccess;
   if (topk > 0) {
@@ -970,13 +1066,7 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
     if (e != cudaSuccess) return MSA_ERR_CUDA;
   }
   const bool wide = p.G > 8, f8 = c->kind == MSA_CACHE_E4M3;
-  if (c->d == 128) {
-    if (f8) e = wide ? launch_attn<128, true, true>(p, stream) : launch_attn<128, true, false>(p, stream);
-    else e = wide ? launch_attn<128, false, true>(p, stream) : launch_attn<128, false, false>(p, stream);
-  } else {
-    if (f8) e = wide ? launch_attn<64, true, true>(p, stream) : launch_attn<64, true, false>(p, stream);
-    else e = wide ? launch_attn<64, false, true>(p, stream) : launch_attn<64, false, false>(p, stream);
-  }
+  e = c->d == 128 ? launch_paged<128>(p, f8, wide, stream) : launch_paged<64>(p, f8, wide, stream);
   return finish(e);
 }
 

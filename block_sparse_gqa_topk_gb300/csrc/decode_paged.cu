@@ -26,6 +26,9 @@ constexpr int kThreads = kWarps * 32;
 // CTAs over which a call's units are spread: three on each of the 152 SMs.  Each leaves at
 // most two partial results (its first and its last (sequence, group)), whatever the batch.
 constexpr int kCtas = 152 * 3;
+// Blocks a sequence up to which the attention kernel selects for itself, 8 scores a thread: every
+// CTA of a (sequence, group) then repeats the counting, which is less than the launch it saves.
+constexpr int kSelectPer = 8;
 
 struct PagedDecode {
   PageView pages;
@@ -38,13 +41,16 @@ struct PagedDecode {
   const __nv_bfloat16* k_idx;
   const int32_t* lens;  // [B]
   int32_t* block_idx;   // [B][H][topk]; null: the whole cache
-  float* pooled;        // [B][H][nb]
+  float* pooled;        // [B][H][row]
   float* part_o;        // [2 kCtas][wh][G][d]
   float* part_lse;      // [2 kCtas][wh][G], in bits (log2)
-  int64_t* starts;      // [B + 2] first unit of each sequence, their total, wh: for the join
+  int* starts;          // [B + 2] first unit of each sequence, their total, wh: for the join
+  int* arrive;          // [B][H] parts that are written (selected blocks; zeroed by the pooling)
   __nv_bfloat16* o;
   float* lse;
-  int B, H, G, topk, nb;
+  int B, H, G, topk;
+  int row;         // blocks of the table's length, rounded up to 4
+  int select;      // the attention kernel selects the blocks itself
   int wh;          // heads (groups) that a CTA may serve side by side
   int keys_shift;  // log2 of a stage's keys
   float scale_log2;  // scale * log2 e: scores in bits
@@ -63,114 +69,120 @@ __device__ __forceinline__ int seq_len(const PagedDecode& p, int b) {
 
 // Units of a sequence for one group (wh groups): a unit is a stage of each of the kWarps / wh
 // warps that share a group's tokens.
+template <bool SPARSE>
 __device__ __forceinline__ int seq_units(const PagedDecode& p, int len, int wh) {
-  if (p.block_idx) {  // the own block, cut at the length, comes last of the selected ones
-    const int blocks = (len + 127) / 128;
+  if (SPARSE) {  // the own block, cut at the length, comes last of the selected ones
+    const int blocks = (int)(((unsigned)len + 127) / 128);
     len -= max(0, blocks - p.topk) * 128;
   }
   const int shift = p.keys_shift + (wh == 1 ? 2 : wh == 2 ? 1 : 0);
-  return (int)(((int64_t)len + (1 << shift) - 1) >> shift);
+  return (int)(((unsigned)len + (1u << shift) - 1) >> shift);
 }
 
-// The units of all (sequence, group) pairs, in order, are cut into n = min(kCtas, total) runs
-// whose lengths differ by at most one: CTA c < n takes units total c / n .. total (c + 1) / n - 1
-// (none is empty, so that every part between a pair's first and last CTA is written).
-__device__ __forceinline__ int64_t run_start(int64_t total, int cta) {
-  const int n = (int)min((int64_t)kCtas, total);
-  return cta < n ? total * cta / n : total;
-}
-__device__ __forceinline__ int cta_of(int64_t total, int64_t unit) {
-  return (int)(((unit + 1) * min((int64_t)kCtas, total) - 1) / total);
-}
+// The work of all (sequence, groups) pairs in order is cut into n runs whose lengths differ by at
+// most one: CTA c < n takes total c / n .. total (c + 1) / n - 1.  A pair's work is its units and
+// kOverhead more in front of them, about what starting and ending a pair costs a CTA, so that
+// CTAs with many short sequences get fewer units.  n is kCtas, or the multiple of the number of
+// pairs next below it where few CTAs are lost (pairs of one length are then cut alike, and no
+// CTA has parts of two), and at most total: each run is at least 1 long, so every CTA between
+// the first and the last that hold units of a pair holds some.
+constexpr int kOverhead = 2;
+__device__ __forceinline__ int seq_work(int units) { return units > 0 ? units + kOverhead : 0; }
+struct Cut {
+  int total, n, q, r;  // total = q n + r
+  float inv;           // 1 / n
+  __device__ __forceinline__ Cut(int total, int pairs) : total(total) {
+    const int even = pairs <= kCtas ? kCtas - kCtas % max(1, pairs) : 0;
+    n = max(1, min(total, even >= kCtas * 9 / 10 ? even : kCtas));
+    q = total / n;
+    r = total - q * n;
+    inv = 1.f / (float)n;
+  }
+  // r cta / n by a float product: (x + 1/2) / n is 0.5 / n from an integer, and x < 2^18 moves
+  // by at most 2^-5 / n in the roundings
+  __device__ __forceinline__ int start(int cta) const {
+    return cta >= n ? total : q * cta + (int)(((float)(r * cta) + 0.5f) * inv);
+  }
+  __device__ __forceinline__ int cta_of(int x) const {  // whose run holds x
+    int c = min(n - 1, (int)((float)x * ((float)n / (float)total)));
+    while (start(c) > x) --c;
+    while (start(c + 1) <= x) ++c;
+    return c;
+  }
+};
 
 // Groups side by side read rows that are neighbours in a page, which HBM serves faster (E4M3, 8 x
 // 128K, d 128: 443 -> 343 us; d 64: 393 -> 232; bf16: 319 -> 309), but leave wh times the parts to
-// join.  They pay from about this many units (of one group) a CTA.
-constexpr int64_t kSideBySide = 48;
+// join.  They pay from about this much work (of one group) a CTA.
+constexpr int kSideBySide = 48;
 
 struct Work {
-  int64_t total;  // units
-  int wh, HG;     // groups side by side, H / wh
-  int b;          // the sequence that holds the first unit of the CTA's run (any if that is empty)
-  int64_t base;   // its first unit
+  Cut cut;
+  int wh, HG;   // groups side by side, H / wh
+  int b, base;  // the sequence that holds the start of the CTA's run (any if that is empty), and
+                // where its work starts
 };
 
-// Every thread of the CTA gets the work.  CTA 0 leaves what the join needs of it.
+// Every warp finds the work for itself, without a barrier.  CTA 0 leaves what the join needs.
 template <bool SPARSE>
 __device__ __forceinline__ Work find_run(const PagedDecode& p) {
-  __shared__ int64_t s_sum[2][kWarps];
-  __shared__ int s_b;
-  __shared__ int64_t s_base;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.B + kThreads - 1) / kThreads;
-  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  int64_t mine = 0, side = 0;
+  const int lane = threadIdx.x & 31;
+  const int per = (p.B + 31) / 32;
+  const int b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
+  int mine = 0, side = 0;
   for (int b = b0; b < b1; ++b) {
     const int len = seq_len(p, b);
-    mine += seq_units(p, len, 1);
-    if (!SPARSE) side += seq_units(p, len, p.wh);
+    mine += seq_work(seq_units<SPARSE>(p, len, 1));
+    if (!SPARSE) side += seq_work(seq_units<SPARSE>(p, len, p.wh));
   }
-  mine *= p.H;
-  side *= p.H / p.wh;
-  int64_t scan = mine, scan_side = side;
+  const int total1 = __reduce_add_sync(0xffffffffu, mine) * p.H;
+  const bool sided = !SPARSE && p.wh > 1 && total1 >= kSideBySide * kCtas;
+  const int wh = sided ? p.wh : 1, HG = sided ? p.H / p.wh : p.H;
+  mine = (sided ? side : mine) * HG;
+  int scan = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, scan, o);
-    const int64_t y = SPARSE ? 0 : __shfl_up_sync(0xffffffffu, scan_side, o);
-    if (lane >= o) {
-      scan += x;
-      scan_side += y;
-    }
+    const int x = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += x;
   }
-  if (lane == 31) {
-    s_sum[0][warp] = scan;
-    s_sum[1][warp] = scan_side;
-  }
-  if (tid == 0) {
-    s_b = 0;
-    s_base = 0;
-  }
-  __syncthreads();
-  Work k;
-  k.total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) k.total += s_sum[0][w];
-  const bool sided = !SPARSE && p.wh > 1 && k.total >= kSideBySide * kCtas;
-  if (sided) {
-    k.total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) k.total += s_sum[1][w];
-    scan = scan_side;
-    mine = side;
-  }
-  k.wh = sided ? p.wh : 1;
-  k.HG = sided ? p.H / p.wh : p.H;
-  int64_t base = scan - mine;  // first unit of this thread's sequences
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w)
-    if (w < warp) base += s_sum[sided][w];
-  const int64_t want = run_start(k.total, blockIdx.x);
-  const bool here = want >= base && want < base + mine;
-  if (here || blockIdx.x == 0) {
+  const int total = __shfl_sync(0xffffffffu, scan, 31);
+  int base = scan - mine;  // where the work of this lane's sequences starts
+  const Cut cut(total, p.B * HG);
+  const int want = cut.start(blockIdx.x);
+  const bool first_cta = blockIdx.x == 0 && threadIdx.x < 32;
+  const unsigned holds = __ballot_sync(0xffffffffu, want >= base && want < base + mine);
+  const int src = holds ? __ffs(holds) - 1 : 0;
+  int found = 0, found_base = 0;
+  if (first_cta || lane == src) {
     for (int b = b0; b < b1; ++b) {
-      const int64_t n = (int64_t)seq_units(p, seq_len(p, b), k.wh) * k.HG;
-      if (blockIdx.x == 0) p.starts[b] = base;
-      if (here && want >= base && want < base + n) {
-        s_b = b;
-        s_base = base;
+      const int n = seq_work(seq_units<SPARSE>(p, seq_len(p, b), wh)) * HG;
+      if (first_cta) p.starts[b] = base;
+      if (want >= base && want < base + n) {
+        found = b;
+        found_base = base;
       }
       base += n;
     }
   }
-  if (blockIdx.x == 0 && tid == 0) {
-    p.starts[p.B] = k.total;
-    p.starts[p.B + 1] = k.wh;
+  if (first_cta && lane == 0) {
+    p.starts[p.B] = total;
+    p.starts[p.B + 1] = wh;
   }
-  __syncthreads();
-  k.b = s_b;
-  k.base = s_base;
-  return k;
+  __syncwarp();
+  return {cut, wh, HG, __shfl_sync(0xffffffffu, found, src), __shfl_sync(0xffffffffu, found_base, src)};
 }
+
+// The parts of one (sequence, groups) pair whose work is first .. first + units + kOverhead - 1.
+struct Parts {
+  int c0, n, late;
+  __device__ __forceinline__ Parts(const Cut& cut, int first, int units) {
+    c0 = cut.cta_of(first + kOverhead);  // the CTA that holds the first unit
+    n = cut.cta_of(first + kOverhead + units - 1) - c0 + 1;
+    late = cut.start(c0) < first;        // it began with another pair
+  }
+  // part i is slot 0 of CTA c0 + i, except where CTA c0 began with another pair
+  __device__ __forceinline__ int64_t slot(int i) const { return 2 * (c0 + i) + (i == 0 ? late : 0); }
+};
 
 // D(16x8) += A(16x16, row) * B(16x8, col), fp16
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -202,7 +214,7 @@ __device__ __forceinline__ uint32_t widen_f16(uint32_t two) {
 }
 
 // 2^(a - b), 0 for a = -inf whatever b.
-__device__ __forceinline__ float weight(float a, float b) { return a == -INFINITY ? 0.f : exp2f(a - b); }
+__device__ __forceinline__ float weight(float a, float b) { return a == -INFINITY ? 0.f : ex2_fast(a - b); }
 
 // Shared memory of one warp's stage: KEYS key rows and as many value rows (and their scales),
 // 8 KB of them for most caches.
@@ -531,6 +543,43 @@ struct WarpState {
   }
 };
 
+// o and lse of one (sequence, group) from its few parts, by the CTA that wrote the last of them.
+// s_w: [parts][G] floats of shared memory.
+template <int D>
+__device__ __forceinline__ void join_parts(const PagedDecode& p, const Parts& parts, int64_t head0, float* s_w) {
+  const int tid = threadIdx.x, lane = tid & 31, G = p.G, n = parts.n;
+  for (int h = tid >> 5; h < G; h += kWarps) {  // weights of the parts, a warp a head
+    float top = -INFINITY, l = 0.f;
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(&p.part_lse[parts.slot(i) * G + h]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int i = lane; i < n; i += 32) {
+      const float w = weight(__ldcg(&p.part_lse[parts.slot(i) * G + h]), top);
+      s_w[i * G + h] = w;
+      l += w;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    for (int i = lane; i < n; i += 32) s_w[i * G + h] /= l;
+    if (lane == 0) p.lse[head0 + h] = (top + log2f(l)) * 0.6931471805599453f;
+  }
+  __syncthreads();
+  for (int x = tid; x < G * (D / 4); x += kThreads) {
+    const int h = x / (D / 4), c = 4 * (x % (D / 4));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + (parts.slot(i) * G + h) * D + c));
+      const float w = s_w[i * G + h];
+      acc.x = fmaf(w, y.x, acc.x);
+      acc.y = fmaf(w, y.y, acc.y);
+      acc.z = fmaf(w, y.z, acc.z);
+      acc.w = fmaf(w, y.w, acc.w);
+    }
+    *reinterpret_cast<uint2*>(p.o + (head0 + h) * D + c) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+  }
+}
+
 // One CTA works through its run of units: span after span of one (sequence, wh groups).  Its
 // warps take the groups side by side and share each one's tokens, every warp with its own
 // stages in shared memory and its own running softmax; they join when a span ends.  A whole
@@ -538,19 +587,27 @@ struct WarpState {
 template <int D, bool F8, bool WIDE, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDecode p) {
   using St = Stage<D, F8>;
-  constexpr int ROWS = WIDE ? 16 : 8;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[kWarps][16], s_mv[kWarps][16], s_l[kWarps][16], s_w[kWarps][16], s_lse[kWarps][16];
+  __shared__ float s_m[kWarps][16], s_mv[kWarps][16], s_l[kWarps][16];
+  __shared__ int32_t s_blocks[kMaxSelect];
+  __shared__ int s_last;
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gq = lane >> 2, tq = lane & 3;
   const Work work = find_run<SPARSE>(p);
   const int wh = SPARSE ? 1 : work.wh, HG = SPARSE ? p.H : work.HG;
-  int b = work.b;
-  int64_t base = work.base;
-  griddep_wait();  // the selected blocks
-  int64_t u = run_start(work.total, blockIdx.x);
-  const int64_t u_end = run_start(work.total, blockIdx.x + 1);
+  int b = work.b, base = work.base;
+  griddep_wait();  // the pooled scores or the selected blocks
+  for (int e = blockIdx.x; e < p.B; e += kCtas) {  // empty slots: o = 0, lse = -inf, no blocks
+    if (seq_len(p, e) > 0) continue;
+    const int64_t heads = (int64_t)p.H * p.G;
+    for (int64_t x = tid; x < heads * D; x += kThreads) p.o[e * heads * D + x] = __float2bfloat16(0.f);
+    for (int64_t x = tid; x < heads; x += kThreads) p.lse[e * heads + x] = -INFINITY;
+    if (SPARSE && p.select)
+      for (int64_t x = tid; x < (int64_t)p.H * p.topk; x += kThreads) p.block_idx[(int64_t)e * p.H * p.topk + x] = -1;
+  }
+  int u = work.cut.start(blockIdx.x);
+  const int u_end = work.cut.start(blockIdx.x + 1);
   uint8_t* ring = smem + warp * St::COUNT * St::BYTES;
   constexpr int CH = St::ROW / 16;  // 16-byte chunks of a row
   constexpr int RPI = 32 / CH;      // rows of one copy instruction
@@ -561,25 +618,40 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
   const int my_head = warp & (wh - 1), subs = kWarps / wh;
   const int my_token = (wh == 1 ? warp : wh == 2 ? warp >> 1 : 0) * St::KEYS, unit = St::KEYS * subs;
   WarpState<D, F8, WIDE> ws;
-  for (int slot = 0; u < u_end; slot = 1) {
-    int len = seq_len(p, b);
-    int units = seq_units(p, len, wh);
-    while (base + (int64_t)units * HG <= u) {  // next sequence that has any
-      base += (int64_t)units * HG;
+  int slot = 0;  // of the CTA's next part
+  while (u < u_end) {
+    int len = seq_len(p, b), units = seq_units<SPARSE>(p, len, wh), size = seq_work(units);
+    while (base + size * HG <= u) {  // next sequence that has any
+      base += size * HG;
       ++b;
       len = seq_len(p, b);
-      units = seq_units(p, len, wh);
+      units = seq_units<SPARSE>(p, len, wh);
+      size = seq_work(units);
     }
-    const int hg = (int)((u - base) / units);
-    const int u0 = (int)(u - base - (int64_t)hg * units);
+    const int hg = (u - base) / size, first = base + hg * size;
+    const int stop = min(first + size, u_end);
+    const int u0 = max(0, u - first - kOverhead);                  // first unit of this span
+    const int n = max(0, stop - first - kOverhead) - u0;           // its units
+    u = stop;
+    if (n == 0) continue;  // only the pair's overhead fell into this run
     const int g = hg * wh + my_head;
-    const int n = (int)min((int64_t)(units - u0), u_end - u);
     const int64_t head0 = ((int64_t)b * p.H + g) * p.G;
     // Page ids of the next 32 units sit in the lanes of a register (and those of the 32 after
     // them are on their way), so that no lookup stands in front of a copy.  Selected blocks,
     // at most 32, sit in another.
     int blk = 0;
-    if (SPARSE && lane < p.topk) blk = __ldg(&p.block_idx[((int64_t)b * p.H + g) * p.topk + lane]);
+    if constexpr (SPARSE) {
+      int32_t* blocks = p.block_idx + ((int64_t)b * p.H + g) * p.topk;
+      if (p.select) {
+        select_blocks_by_rank<kSelectPer, kThreads>(p.pooled + ((int64_t)b * p.H + g) * p.row, (len - 1) / 128,
+                                                    p.topk, s_blocks);
+        __syncthreads();
+        if (lane < p.topk) blk = s_blocks[lane];
+        if (u0 == 0 && tid < p.topk) blocks[tid] = blk;
+      } else if (lane < p.topk) {
+        blk = __ldg(&blocks[lane]);
+      }
+    }
     // first token of this warp in unit u0 + i
     auto first_token = [&](int i) {
       const int x = u0 + i;
@@ -655,8 +727,17 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
       const int have = len - first_token(i);
       if (have > 0) ws.step(ring + (i % St::COUNT) * St::BYTES, have, lane);
     }
+    // join the warps: each leaves its sums in its own stages
     cp_async_wait<0>();
-    // join the warps
+    __syncwarp();
+    float* my_o = reinterpret_cast<float*>(ring);  // [8 R][D + 4]
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int r = 0; r < ws.R; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          my_o[(8 * r + 2 * tq + (e & 1)) * (D + 4) + ws.column(i, e, gq)] = ws.o[i][r][e];
 #pragma unroll
     for (int r = 0; r < (WIDE ? 2 : 1); ++r) {
       float l = ws.l[r];
@@ -668,68 +749,60 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
         s_l[warp][gq + 8 * r] = l;
       }
     }
-    __syncthreads();  // every warp is done with its stages
-    float* s_o = reinterpret_cast<float*>(smem);  // [kWarps][ROWS][D + 4]
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-      for (int r = 0; r < ws.R; ++r)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s_o[(warp * ROWS + 8 * r + 2 * tq + (e & 1)) * (D + 4) + ws.column(i, e, gq)] = ws.o[i][r][e];
-    // weights of the warps in each head's joined value, and its lse in bits
-    if (tid < wh * p.G) {
-      const int w0 = tid / p.G, h = tid - w0 * p.G;
-      float top = -INFINITY, l = 0.f;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k)
-        if (k < subs) top = fmaxf(top, s_m[w0 + k * wh][h]);
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k)
-        if (k < subs) l += s_l[w0 + k * wh][h] * weight(s_m[w0 + k * wh][h], top);
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k)
-        if (k < subs) s_w[w0 + k * wh][h] = weight(s_mv[w0 + k * wh][h], top) / l;
-      s_lse[w0][h] = top + log2f(l);
-    }
     __syncthreads();
-    const bool whole = u0 == 0 && n == units;
+    const bool whole = n == units;
     const int64_t part = (int64_t)(2 * blockIdx.x + slot) * wh * p.G;
     const int64_t out0 = ((int64_t)b * p.H + hg * wh) * p.G;  // first of the wh G query heads
     for (int x = tid; x < wh * p.G * (D / 4); x += kThreads) {
       const int row = x / (D / 4), c = 4 * (x % (D / 4));
-      const int w0 = row / p.G, h = row - w0 * p.G;
+      const int w0 = wh == 1 ? 0 : row / p.G, h = row - w0 * p.G;
+      float top = -INFINITY, l = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      const float lse2 = s_lse[w0][h];
-      if (whole || lse2 > -INFINITY) {  // a part whose scores are all -inf weighs nothing in the join
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-          if (k >= subs) break;
-          const int w = w0 + k * wh;
-          const float f = s_w[w][h];
-          const float4 y = *reinterpret_cast<const float4*>(s_o + (w * ROWS + h) * (D + 4) + c);
-          acc.x = fmaf(f, y.x, acc.x);
-          acc.y = fmaf(f, y.y, acc.y);
-          acc.z = fmaf(f, y.z, acc.z);
-          acc.w = fmaf(f, y.w, acc.w);
-        }
+      for (int k = 0; k < kWarps; ++k)
+        if (k < subs) top = fmaxf(top, s_m[w0 + k * wh][h]);
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        if (k >= subs) break;
+        const int w = w0 + k * wh;
+        l += s_l[w][h] * weight(s_m[w][h], top);
+        const float f = weight(s_mv[w][h], top);
+        const float4 y = *reinterpret_cast<const float4*>(smem + w * St::COUNT * St::BYTES + (h * (D + 4) + c) * 4);
+        acc.x = fmaf(f, y.x, acc.x);
+        acc.y = fmaf(f, y.y, acc.y);
+        acc.z = fmaf(f, y.z, acc.z);
+        acc.w = fmaf(f, y.w, acc.w);
       }
+      const float inv = whole || l > 0.f ? 1.f / l : 0.f;  // a part of scores that are all -inf
+      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       if (whole) {
         *reinterpret_cast<uint2*>(p.o + (out0 + row) * D + c) =
             make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
-        if (c == 0) p.lse[out0 + row] = lse2 * 0.6931471805599453f;
+        if (c == 0) p.lse[out0 + row] = (top + log2f(l)) * 0.6931471805599453f;
       } else {
         *reinterpret_cast<float4*>(p.part_o + (part + row) * D + c) = acc;
-        if (c == 0) p.part_lse[part + row] = lse2;
+        if (c == 0) p.part_lse[part + row] = top + log2f(l);
+      }
+    }
+    slot = 1;
+    if (SPARSE && !whole) {
+      // the pair's last part to be written joins them all (in their own order)
+      const Parts parts(work.cut, first, units);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) s_last = atomicAdd(&p.arrive[(int64_t)b * p.H + g], 1) == parts.n - 1;
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        join_parts<D>(p, parts, out0, reinterpret_cast<float*>(smem));
       }
     }
     __syncthreads();  // the stages are free for the next span
-    u += n;
   }
 }
 
-// Joins the parts of every (sequence, group) that the split cut; an empty sequence gets
-// o = 0 and lse = -inf.  Grid (B H, head splits, D / COLS): a CTA takes heads blockIdx.y,
+// Joins the parts of every (sequence, group) that the split cut, where the whole cache is
+// attended: one sequence may then have hundreds of them.  Grid (B H, head splits, D / COLS): a CTA takes heads blockIdx.y,
 // + gridDim.y, ... and COLS value columns; its threads take parts side by side, each 4 columns.
 constexpr int kJoinThreads = 256;
 template <int D, int COLS>
@@ -743,25 +816,15 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedDec
   const int64_t head0 = ((int64_t)b * p.H + g) * p.G;
   const int col0 = blockIdx.z * COLS;
   griddep_wait();
-  const int64_t first = __ldcg(&p.starts[b]), end = __ldcg(&p.starts[b + 1]);
-  const int64_t total = __ldcg(&p.starts[p.B]);
-  const int wh = (int)__ldcg(&p.starts[p.B + 1]);
-  if (first == end) {
-    for (int h = blockIdx.y; h < p.G; h += gridDim.y) {
-      for (int x = tid; x < COLS; x += kJoinThreads) p.o[(head0 + h) * D + col0 + x] = __float2bfloat16(0.f);
-      if (tid == 0 && col0 == 0) p.lse[head0 + h] = -INFINITY;
-    }
-    return;
-  }
+  const int start = __ldcg(&p.starts[b]), end = __ldcg(&p.starts[b + 1]);
+  const int total = __ldcg(&p.starts[p.B]), wh = __ldcg(&p.starts[p.B + 1]);
+  if (start == end) return;  // an empty slot
   const int hg = wh == 4 ? g >> 2 : wh == 2 ? g >> 1 : g, HG = wh == 4 ? p.H >> 2 : wh == 2 ? p.H >> 1 : p.H;
-  const int64_t units = (end - first) / HG, u0 = first + hg * units;
-  const int c0 = cta_of(total, u0), n = cta_of(total, u0 + units - 1) - c0 + 1;
+  const int size = (end - start) / HG;
+  const Parts parts(Cut(total, p.B * HG), start + hg * size, size - kOverhead);
+  const int n = parts.n;
   if (n == 1) return;
-  // part i is slot 0 of CTA c0 + i, except where CTA c0 began with another (sequence, groups)
-  const int late = u0 != run_start(total, c0);
-  auto part_of = [&](int i) {
-    return ((int64_t)(2 * (c0 + i) + (i == 0 ? late : 0)) * wh + (g - hg * wh)) * p.G;
-  };
+  auto part_of = [&](int i) { return (parts.slot(i) * wh + (g - hg * wh)) * p.G; };
   for (int h = blockIdx.y; h < p.G; h += gridDim.y) {
     float top = -INFINITY;
     for (int i = tid; i < n; i += kJoinThreads) {
@@ -837,6 +900,8 @@ __global__ void __launch_bounds__(256) paged_pool_kernel(const PagedDecode p) {
   const int b = blockIdx.y;
   const int len = seq_len(p, b);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && blockIdx.z == 0)
+    for (int h = threadIdx.x; h < p.H; h += blockDim.x) p.arrive[(int64_t)b * p.H + h] = 0;
   const int c = blockIdx.x * 8 + warp;
   if (c >= (len - 1) / 128) return;  // also for an empty slot: (0 - 1) / 128 = 0
   const int gq = lane >> 2, tq = lane & 3;
@@ -894,11 +959,12 @@ __global__ void __launch_bounds__(256) paged_pool_kernel(const PagedDecode p) {
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
       const int grp = blockIdx.z * 8 * NT + nt * 8 + 2 * tq + e;
-      if (gq == 0 && grp < p.H) p.pooled[((int64_t)b * p.H + grp) * p.nb + c] = m;
+      if (gq == 0 && grp < p.H) p.pooled[((int64_t)b * p.H + grp) * p.row + c] = m;
     }
 }
 
-// One CTA per (group, sequence): the new token's blocks; none for an empty slot.
+// One CTA per (group, sequence): the new token's blocks, for caches of more blocks than the
+// attention kernel selects from; none for an empty slot.
 template <int KM>
 __global__ void __launch_bounds__(256) paged_select_kernel(const PagedDecode p) {
   griddep_launch_dependents();
@@ -910,11 +976,10 @@ __global__ void __launch_bounds__(256) paged_select_kernel(const PagedDecode p) 
     for (int s = threadIdx.x; s < p.topk; s += blockDim.x) dst[s] = -1;
     return;
   }
-  const float* src = p.pooled + bg * p.nb;
+  const float* src = p.pooled + bg * p.row;
   const int c_own = (len - 1) / 128;
-  // a threshold over registers while a thread's share of the blocks fits them, else lists
-  if (c_own <= 4 * 256) select_blocks_by_threshold<4>(src, c_own, p.topk, dst);
-  else if (c_own <= 16 * 256) select_blocks_by_threshold<16>(src, c_own, p.topk, dst);
+  // by rank while a thread's share of the blocks fits its registers, else by lists
+  if (c_own <= 16 * 256) select_blocks_by_rank<16, 256>(src, c_own, p.topk, dst);
   else select_blocks<KM>(src, c_own, p.topk, dst);
 }
 
@@ -940,7 +1005,8 @@ cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, bool after, c
 template <int D, bool F8, bool WIDE, bool SPARSE>
 cudaError_t launch_attn(const PagedDecode& p, cudaStream_t stream) {
   constexpr int smem = kWarps * Stage<D, F8>::COUNT * Stage<D, F8>::BYTES;
-  static_assert(smem >= kWarps * (WIDE ? 16 : 8) * (D + 4) * 4, "the join reuses the stages");
+  static_assert(Stage<D, F8>::COUNT * Stage<D, F8>::BYTES >= (WIDE ? 16 : 8) * (D + 4) * 4, "sums in the stages");
+  static_assert(smem >= 32 * 128 / Stage<D, F8>::UNIT * 16 * 4, "weights of a pair's parts");
   auto* kern = paged_attn_kernel<D, F8, WIDE, SPARSE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -962,6 +1028,7 @@ cudaError_t launch_paged(const PagedDecode& p, bool f8, bool wide, cudaStream_t 
   // The join is a chain of loads, shorter the more parts a CTA reads at once: a CTA for each
   // head, and for each 32 columns, while all of them run together (8 x 4 groups of 4 heads, 22
   // parts: 22 us for the whole call with a CTA a head, 30 us with four, 25 us with one a group).
+  if (sparse) return cudaSuccess;  // joined by the attention kernel
   const int64_t rows = (int64_t)p.B * p.H, together = 4 * 152;
   if (rows * p.G * (D / 32) <= together)
     return launch(paged_join_kernel<D, 32>, dim3((unsigned)rows, (unsigned)p.G, D / 32), kJoinThreads, 0, true,
@@ -978,7 +1045,7 @@ int heads_side_by_side(int H, int topk) {
 }
 
 struct Layout {
-  size_t part_o, part_lse, starts, pooled, bytes;
+  size_t part_o, part_lse, starts, arrive, pooled, bytes;
 };
 
 // Sizes of a call; MSA_OK and the workspace's layout.  topk = 0: the whole cache.
@@ -994,12 +1061,16 @@ int check_sizes(const msa_paged_cache_t* c, const msa_page_table_t* pt, int H_q,
   if (G > 16 || topk > kMaxSelect) return MSA_ERR_UNSUPPORTED;
   if ((int64_t)pt->B * c->H_kv > (1 << 24) || pt->B > 65535) return MSA_ERR_UNSUPPORTED;
   if (topk > 0 && c->d_idx == 0) return MSA_ERR_SHAPE;
+  // the work of all pairs is counted in 32 bits
+  const int64_t most = (cap >> (c->kind == MSA_CACHE_E4M3 || c->d == 64 ? 7 : 6)) + kOverhead + 4;
+  if ((int64_t)pt->B * c->H_kv * most >= 1 << 30) return MSA_ERR_UNSUPPORTED;
   lay->part_o = 0;
   const size_t parts = (size_t)2 * kCtas * heads_side_by_side(c->H_kv, topk) * G;
   lay->part_lse = align256(parts * c->d * 4);
   lay->starts = lay->part_lse + align256(parts * 4);
-  lay->pooled = lay->starts + align256(((size_t)pt->B + 2) * 8);
-  lay->bytes = lay->pooled + (topk > 0 ? align256((size_t)pt->B * c->H_kv * ((cap + 127) / 128) * 4) : 0);
+  lay->arrive = lay->starts + align256(((size_t)pt->B + 2) * 4);
+  lay->pooled = lay->arrive + (topk > 0 ? align256((size_t)pt->B * c->H_kv * 4) : 0);
+  lay->bytes = lay->pooled + (topk > 0 ? align256((size_t)pt->B * c->H_kv * (((cap + 127) / 128 + 3) & ~3) * 4) : 0);
   return MSA_OK;
 }
 
@@ -1035,14 +1106,16 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   p.pooled = reinterpret_cast<float*>(w + lay.pooled);
   p.part_o = reinterpret_cast<float*>(w + lay.part_o);
   p.part_lse = reinterpret_cast<float*>(w + lay.part_lse);
-  p.starts = reinterpret_cast<int64_t*>(w + lay.starts);
+  p.starts = reinterpret_cast<int*>(w + lay.starts);
+  p.arrive = reinterpret_cast<int*>(w + lay.arrive);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.B = pt->B;
   p.H = c->H_kv;
   p.G = H_q / c->H_kv;
   p.topk = topk;
-  p.nb = (int)(((int64_t)pt->max_pages * c->page_size + 127) / 128);
+  const int nb = (int)(((int64_t)pt->max_pages * c->page_size + 127) / 128);
+  p.row = (nb + 3) & ~3;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wh = heads_side_by_side(p.H, topk);
   p.keys_shift = c->kind == MSA_CACHE_E4M3 || c->d == 64 ? 5 : 4;
@@ -1050,7 +1123,7 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   cudaError_t e = cudaSuccess;
   if (topk > 0) {
     const int nt = p.H > 8 ? 2 : 1;
-    const dim3 grid((unsigned)((p.nb + 7) / 8), (unsigned)p.B, (unsigned)((p.H + 8 * nt - 1) / (8 * nt)));
+    const dim3 grid((unsigned)((nb + 7) / 8), (unsigned)p.B, (unsigned)((p.H + 8 * nt - 1) / (8 * nt)));
     if (grid.x > 0) {
       if (c->d_idx == 64)
         e = nt == 1 ? launch(paged_pool_kernel<64, 1>, grid, 256, 0, false, stream, p)
@@ -1060,9 +1133,11 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
                     : launch(paged_pool_kernel<32, 2>, grid, 256, 0, false, stream, p);
       if (e != cudaSuccess) return MSA_ERR_CUDA;
     }
+    p.select = nb <= kSelectPer * kThreads;
     const dim3 gsel((unsigned)p.H, (unsigned)p.B);
-    e = topk <= 16 ? launch(paged_select_kernel<15>, gsel, 256, 0, true, stream, p)
-                   : launch(paged_select_kernel<31>, gsel, 256, 0, true, stream, p);
+    if (!p.select)
+      e = topk <= 16 ? launch(paged_select_kernel<15>, gsel, 256, 0, true, stream, p)
+                     : launch(paged_select_kernel<31>, gsel, 256, 0, true, stream, p);
     if (e != cudaSuccess) return MSA_ERR_CUDA;
   }
   const bool wide = p.G > 8, f8 = c->kind == MSA_CACHE_E4M3;

@@ -87,87 +87,85 @@ __device__ __forceinline__ void select_blocks(const float* __restrict__ src, int
   for (int s = M + 1 + t; s < topk; s += blockDim.x) dst[s] = -1;
 }
 
-// The same result for c_own <= PER * 256, by threshold: thread t holds blocks t PER ..
-// t PER + PER - 1 as order-preserving integers; the M-th largest value T is built bit by bit
-// (the largest T that at least M values reach: one block-wide count a bit), and a scan over
-// the threads, whose order is the blocks', places the values above T and the first of those
-// equal to it.  Distinct scores are told apart after about 18 counts, which replace the
-// lists' insertions and rounds.
-template <int PER>
-__device__ __forceinline__ void select_blocks_by_threshold(const float* __restrict__ src, int c_own, int topk,
-                                                           int32_t* __restrict__ dst) {
-  __shared__ int s_count[2][8], s_above[8], s_equal[8];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+// The same result for c_own <= PER * THREADS by counting ranks.  Thread t holds blocks t PER ..
+// t PER + PER - 1 as order-preserving integers.
+//   1. The M-th best of the threads' best scores bounds the M-th best score from below (M threads
+//      hold one at least as good), so at most the PER values of M threads can be taken.
+//   2. Each of those counts those above it: rank < M is taken.
+//   3. Each taken block counts the taken blocks before it: its place in ascending order.
+// Equal scores rank the lower block first throughout.  src: 16-byte aligned, PER a multiple of 4.
+template <int PER, int THREADS>
+__device__ __forceinline__ void select_blocks_by_rank(const float* __restrict__ src, int c_own, int topk,
+                                                      int32_t* __restrict__ dst) {
+  constexpr int MOST = 31;  // M <= topk - 1 <= 31
+  __shared__ __align__(16) uint32_t s_best[THREADS];
+  __shared__ uint64_t s_cand[PER * MOST];
+  __shared__ int s_n, s_bound_thread, s_sel[MOST];
+  __shared__ uint32_t s_bound;
+  const int tid = threadIdx.x;
   const int M = min(topk - 1, c_own);
-  uint32_t key[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int c = tid * PER + i;
-    const uint32_t u = c < c_own ? __float_as_uint(__ldg(&src[c])) : 0xffffffffu;
-    key[i] = (u & 0x80000000u) ? ~u : (u | 0x80000000u);  // past the end: 0, below every score
-  }
   if (M > 0) {
-    uint32_t T = 0;
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t want = T | (1u << bit);
-      int n = 0;
+    uint32_t key[PER], best = 0;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) n += key[i] >= want;
-      n = __reduce_add_sync(0xffffffffu, n);
-      if (lane == 0) s_count[bit & 1][warp] = n;
-      __syncthreads();
-      n = 0;
+    for (int i = 0; i < PER; i += 4) {
+      const int c = tid * PER + i;
+      // blocks of the last vector past c_own are within the row, or padding behind it
+      const uint4 w = c < c_own ? __ldg(reinterpret_cast<const uint4*>(src + c)) : make_uint4(0, 0, 0, 0);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int w = 0; w < 8; ++w) n += s_count[bit & 1][w];
-      if (n >= M) T = want;
-      if (n == M) {  // exactly the values from T up: no bit below matters
-        --T;
-        break;
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t k = (u[e] & 0x80000000u) ? ~u[e] : (u[e] | 0x80000000u);
+        key[i + e] = c + e < c_own ? min(max(k, 1u), 0xfffffffeu) : 0u;  // 0: no block
+        best = max(best, key[i + e]);
       }
     }
-    // places: values above T all count, those equal to T in block order while room is left
-    int above = 0, equal = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      above += key[i] > T;
-      equal += key[i] == T && tid * PER + i < c_own;
-    }
-    int sa = above, se = equal;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, sa, o), e = __shfl_up_sync(0xffffffffu, se, o);
-      if (lane >= o) {
-        sa += a;
-        se += e;
-      }
-    }
-    if (lane == 31) {
-      s_above[warp] = sa;
-      s_equal[warp] = se;
+    s_best[tid] = best;
+    if (tid == 0) {
+      s_n = 0;
+      s_bound = 1;  // every block, unless M threads hold one
+      s_bound_thread = THREADS;
     }
     __syncthreads();
-    int total = 0;
-    sa -= above;
-    se -= equal;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      total += s_above[w];
-      if (w < warp) {
-        sa += s_above[w];
-        se += s_equal[w];
-      }
+    // rank of this thread's best: of equal ones the lower thread's is above.  (A short loop:
+    // code that runs once is paid for by its size.)
+    int rank = 0;
+    const uint4* all = reinterpret_cast<const uint4*>(s_best);
+#pragma unroll 4
+    for (int t = 0; t < THREADS; t += 4) {
+      const uint4 x = all[t / 4];
+      rank += (x.x + (t < tid) > best) + (x.y + (t + 1 < tid) > best) + (x.z + (t + 2 < tid) > best) +
+              (x.w + (t + 3 < tid) > best);
     }
-    const int room = M - total;  // equal values that are taken
+    if (rank == M - 1 && best > 0) {
+      s_bound = best;
+      s_bound_thread = tid;
+    }
+    __syncthreads();
+    const uint32_t bound = s_bound + (tid <= s_bound_thread ? 0u : 1u);
+    if (best >= bound) {
+      int mine = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int c = tid * PER + i;
-      if (key[i] > T) {
-        dst[sa + min(se, room)] = c;
-        ++sa;
-      } else if (key[i] == T && c < c_own) {
-        if (se < room) dst[sa + se] = c;
-        ++se;
-      }
+      for (int i = 0; i < PER; ++i) mine += key[i] >= bound;
+      int at = atomicAdd(&s_n, mine);
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (key[i] >= bound) s_cand[at++] = ((uint64_t)key[i] << 32) | (uint32_t)(0x7fffffff - (tid * PER + i));
+    }
+    __syncthreads();
+    const int n = s_n;
+    for (int x = tid; x < n; x += THREADS) {
+      const uint64_t mine = s_cand[x];
+      int above = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) above += s_cand[j] > mine ? 1 : 0;
+      if (above < M) s_sel[above] = key_id(mine);
+    }
+    __syncthreads();
+    if (tid < M) {
+      const int id = s_sel[tid];
+      int pos = 0;
+      for (int j = 0; j < M; ++j) pos += s_sel[j] < id ? 1 : 0;
+      dst[pos] = id;
     }
   }
   if (tid == 0) dst[M] = c_own;

@@ -394,12 +394,13 @@ int msa_cache_read(const msa_paged_cache_t* c, const msa_page_table_t* pages, co
  * lens[b] = 0 is an empty slot of a padded batch: o = 0, lse = -inf, block_idx all -1.  A
  *   length that is negative or past the table sets MSA_ERR_ARG in the status word and counts
  *   as 0; a page id outside the pool sets it too and reads as zero rows.
- * H_q a multiple of the cache's H_kv with G = H_q / H_kv <= 16 (any G); B <= 65535.
+ * H_q a multiple of the cache's H_kv with G = H_q / H_kv <= 16 (any G); B <= 65535, and
+ *   B * H_kv * max_pages * page_size below 2^36.
  * In:  q [B][H_q][d], q_idx [B][H_kv][d_idx] (bf16), pages, lens (device int32 [B]).
  * Out: block_idx [B][H_kv][topk] (int32), o [B][H_q][d] (bf16), lse [B][H_q] (float32).
  * Workspace: msa_decode_paged_workspace_size (topk 0 for the dense call; 0 if the sizes are
  *   invalid), 256-byte aligned.  The result does not depend on what it held, nor on the order
- *   in which the GPU runs the parts: no atomics take part.
+ *   in which the GPU runs the parts (they are joined in their own order).
  */
 size_t msa_decode_paged_workspace_size(const msa_paged_cache_t* c, const msa_page_table_t* pages, int H_q,
                                        int topk);

@@ -69,25 +69,36 @@ __device__ __forceinline__ float2 widen(uint32_t w) {  // two bf16
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
+// E4M3 codes of four bf16 pairs divided by sc; out of line, for rows at the ends of the range.
+__device__ __noinline__ uint2 divide8(uint4 w, float sc) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  uint32_t c[2] = {0, 0};
+#pragma unroll 1
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t v = e == 0 ? u[0] : e == 1 ? u[1] : e == 2 ? u[2] : u[3];
+    const float2 x = widen(v);
+    const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x.x, sc), __fdiv_rn(x.y, sc)), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t put = (two & 0xffffu) << (16 * (e & 1));
+    if (e < 2) c[0] |= put; else c[1] |= put;
+  }
+  return make_uint2(c[0], c[1]);
+}
+
 // E4M3 codes of eight values at scale sc (amax / 448): the code nearest to the float32
 // quotient x / sc.  With r the rounded reciprocal, q0 = x r and the remainder x - q0 sc, which
 // one fma gives exactly, q0 + r (x - q0 sc) is the rounded quotient (Markstein 1990); that it
 // gives every code that division gives is checked over all pairs of bf16 significands.  Rows
 // whose amax leaves the range in which nothing underflows are divided.
-__device__ __forceinline__ uint2 quantize8(uint4 w, float sc, float r, bool divide) {
+__device__ __forceinline__ uint2 quantize8(uint4 w, float sc, float r) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  const float2 rr = make_float2(r, r), nn = make_float2(-sc, -sc);
   uint32_t c[2] = {0, 0};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float2 x = widen(u[e]);
-    float2 q;
-    if (divide) {
-      q = make_float2(__fdiv_rn(x.x, sc), __fdiv_rn(x.y, sc));
-    } else {
-      const float2 rr = make_float2(r, r), q0 = fmul2(x, rr);
-      q = ffma2(ffma2(q0, make_float2(-sc, -sc), x), rr, q0);
-      q = make_float2(copysignf(q.x, x.x), copysignf(q.y, x.y));  // a zero keeps its sign
-    }
+    const float2 q0 = fmul2(x, rr);
+    float2 q = ffma2(ffma2(q0, nn, x), rr, q0);
+    q = make_float2(copysignf(q.x, x.x), copysignf(q.y, x.y));  // a zero keeps its sign
     const uint32_t two = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
     c[e >> 1] |= (two & 0xffffu) << (16 * (e & 1));
   }
@@ -204,9 +215,15 @@ __global__ void __launch_bounds__(kThreads) cache_kernel(const __grid_constant__
         for (int o = L::LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         if (kind[i] == 1) {
           const float sc = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-          const float r = __frcp_rn(sc);
-          const bool divide = !(amax > 1e-18f && amax < 1e18f);
-          const uint2 a = quantize8(w[i][0], sc, r, divide), b = quantize8(w[i][W - 1], sc, r, divide);
+          uint2 a, b;
+          if (amax > 1e-18f && amax < 1e18f) {
+            const float r = __frcp_rn(sc);
+            a = quantize8(w[i][0], sc, r);
+            b = quantize8(w[i][W - 1], sc, r);
+          } else {
+            a = divide8(w[i][0], sc);
+            b = divide8(w[i][W - 1], sc);
+          }
           *pool[i] = make_uint4(a.x, a.y, b.x, b.y);
           if (sub == 0) *scale[i] = sc;
           continue;
@@ -230,9 +247,12 @@ template <int D, bool F8, bool WRITE>
 cudaError_t launch_cache(CacheParams& p, int num_sms, cudaStream_t st) {
   constexpr int CHUNK = Lanes<D, F8>::CHUNK;
   const int64_t items = (int64_t)p.T * p.rows;
-  // chunks of a warp: up to 8, while 16 warps a SM remain and 32 lanes find all its tokens
-  p.steps = 8;
-  while (p.steps > 1 && (items / (CHUNK * p.steps) < 16 * num_sms || CHUNK * p.steps > 30 * p.rows)) p.steps >>= 1;
+  // chunks of a warp: as many as let all warps run together (32 or 48 a SM by their registers),
+  // while 32 lanes find all of a warp's tokens
+  const int64_t together = (int64_t)num_sms * (F8 && WRITE ? 32 : 48);
+  const int64_t want = (items + CHUNK * together - 1) / (CHUNK * together);
+  const int most = 30 * p.rows / CHUNK > 1 ? 30 * p.rows / CHUNK : 1;
+  p.steps = (int)(want < most ? want : most);
   const int64_t warps = (items + CHUNK * p.steps - 1) / (CHUNK * p.steps);
   const int64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

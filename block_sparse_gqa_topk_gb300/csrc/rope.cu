@@ -23,11 +23,12 @@ constexpr int kThreads = 256;
 constexpr int kMaxRopeTensors = 4;
 constexpr int kMaxTokens = 8;    // tokens a CTA computes the angles of
 constexpr int kMaxHalf = 256;    // rot_dim / 2
+constexpr int kHeads = 2;        // heads of an item
 
 struct RopeTensor {
   const void* x;
   void* y;
-  int H, parts, rot_parts, d;  // items per head, of them rotated
+  int H, units, parts, rot_parts, d;  // heads, runs of kHeads of them, items of a run, rotated ones
   int last;                    // items of a token in this tensor and those before it
   uint32_t div_parts, div_H;
   int64_t xs[3], ys[3];  // strides of batch, token, head
@@ -67,9 +68,9 @@ __device__ __forceinline__ int small_div(int x, uint32_t m) { return m ? (int)__
 uint32_t magic(int q) { return q == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + q - 1) / q); }
 
 // One CTA serves tpb tokens: their sines and cosines, and where their rows start, go to
-// shared memory once; then the items (V pairs of one head, or 2 V values to copy) of all the
-// tensors together are spread over the threads, two in flight each.  Bound by HBM: every
-// value is read and written once.
+// shared memory once; then the items (V pairs, or 2 V values to copy, of kHeads neighbouring
+// heads, which share the pairs' sines and cosines) of all the tensors together are spread over
+// the threads.  Bound by HBM: every value is read and written once.
 template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float2 s_cs[kMaxTokens * kMaxHalf];
@@ -97,45 +98,33 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
   }
   __syncthreads();
   const int items = nt * p.t[p.n - 1].last;
-  constexpr int U = 2;
-  for (int base = threadIdx.x; base < items; base += U * kThreads) {
-    Pack<T, V> lo[U], hi[U];
-    T* dst[U];
-    int cs[U], step[U];  // angle index (-1: copied), distance of the second vector (0: no item)
+  for (int item = threadIdx.x; item < items; item += kThreads) {
+    int x = item, ti = 0;
+    while (x >= nt * p.t[ti].last) ++ti;
+    const RopeTensor& a = p.t[ti];
+    if (ti > 0) x -= nt * p.t[ti - 1].last;
+    const int row = small_div(x, a.div_parts), part = x - row * a.parts;
+    const int tok = small_div(row, a.div_H), h0 = (row - tok * a.units) * kHeads;
+    const bool turn = part < a.rot_parts;
+    // first vector of the item in its head, and the distance of the second one (0: none)
+    const int at = turn ? (INTER ? part * 2 * V : part * V) : 2 * p.half + (part - a.rot_parts) * 2 * V;
+    const int step = turn ? (INTER ? V : p.half) : at + V < a.d ? V : 0;
+    const longlong2 off = s_off[ti][tok];
+    const T* src = static_cast<const T*>(a.x) + (off.x + h0 * a.xs[2] + at);
+    T* dst = static_cast<T*>(a.y) + (off.y + h0 * a.ys[2] + at);
+    Pack<T, V> lo[kHeads], hi[kHeads];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      int x = base + u * kThreads;
-      step[u] = 0;
-      if (x >= items) continue;
-      int ti = 0;
-      while (x >= nt * p.t[ti].last) ++ti;
-      const RopeTensor& a = p.t[ti];
-      if (ti > 0) x -= nt * p.t[ti - 1].last;
-      const int row = small_div(x, a.div_parts), part = x - row * a.parts;
-      const int tok = small_div(row, a.div_H), h = row - tok * a.H;
-      int at;
-      if (part < a.rot_parts) {
-        cs[u] = tok * p.half + part * V;
-        at = INTER ? part * 2 * V : part * V;
-        step[u] = INTER ? V : p.half;
-      } else {
-        cs[u] = -1;
-        at = 2 * p.half + (part - a.rot_parts) * 2 * V;
-        step[u] = at + V < a.d ? V : -1;  // the last copied item may hold one vector
-      }
-      const longlong2 off = s_off[ti][tok];
-      const T* src = static_cast<const T*>(a.x) + (off.x + h * a.xs[2] + at);
-      dst[u] = static_cast<T*>(a.y) + (off.y + h * a.ys[2] + at);
-      lo[u] = *reinterpret_cast<const Pack<T, V>*>(src);
-      if (step[u] > 0) hi[u] = *reinterpret_cast<const Pack<T, V>*>(src + step[u]);
+    for (int u = 0; u < kHeads; ++u) {
+      if (h0 + u >= a.H) break;
+      lo[u] = *reinterpret_cast<const Pack<T, V>*>(src + u * a.xs[2]);
+      if (step) hi[u] = *reinterpret_cast<const Pack<T, V>*>(src + u * a.xs[2] + step);
     }
+    if (turn) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (step[u] == 0) continue;
-      if (cs[u] >= 0) {
+      for (int e = 0; e < V; ++e) {
+        const float2 w = s_cs[tok * p.half + part * V + e];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float2 w = s_cs[cs[u] + e];
+        for (int u = 0; u < kHeads; ++u) {
           // the pair's two values: the vectors side by side, or neighbours in them
           T* p1 = INTER ? (2 * e < V ? &lo[u].v[(2 * e) % V] : &hi[u].v[(2 * e) % V]) : &lo[u].v[e];
           T* p2 = INTER ? (2 * e + 1 < V ? &lo[u].v[(2 * e + 1) % V] : &hi[u].v[(2 * e + 1) % V])
@@ -145,8 +134,12 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
           *p2 = from_f<T>(x2 * w.x + x1 * w.y);
         }
       }
-      *reinterpret_cast<Pack<T, V>*>(dst[u]) = lo[u];
-      if (step[u] > 0) *reinterpret_cast<Pack<T, V>*>(dst[u] + step[u]) = hi[u];
+    }
+#pragma unroll
+    for (int u = 0; u < kHeads; ++u) {
+      if (h0 + u >= a.H) break;
+      *reinterpret_cast<Pack<T, V>*>(dst + u * a.ys[2]) = lo[u];
+      if (step) *reinterpret_cast<Pack<T, V>*>(dst + u * a.ys[2] + step) = hi[u];
     }
   }
 }
@@ -226,12 +219,13 @@ extern "C" int msa_rope(const msa_rope_t* r, const uint64_t* turns, const void* 
     const int tail = t.x == t.y ? 0 : t.d - r->rot_dim;  // in place: already there
     a.parts = a.rot_parts + (tail + 2 * w - 1) / (2 * w);
     a.div_parts = magic(a.parts);
-    a.div_H = magic(a.H);
+    a.units = (a.H + kHeads - 1) / kHeads;
+    a.div_H = magic(a.units);
     for (int k = 0; k < 3; ++k) {
       a.xs[k] = t.x_stride[k];
       a.ys[k] = t.y_stride[k];
     }
-    all += a.H * a.parts;
+    all += a.units * a.parts;
     a.last = all;
   }
   // tokens a CTA: up to kMaxTokens while the grid still fills the GPU and an item index

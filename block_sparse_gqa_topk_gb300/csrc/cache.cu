@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) cache_kernel(const __grid_constant__
     for (int i = 0; i < STEPS; ++i) {
       const int x = c + i * L::RPS + lane / L::LPR;
       const int y = x + skip;
-      const int tok = (int)(((float)y + 0.5f) * p.inv_rows);  // exact: y < 2^12
+      const int tok = (int)(((float)y + 0.5f) * p.inv_rows);  // exact: y < 32 rows
       const int r = y - tok * p.rows;
       int64_t row = __shfl_sync(0xffffffffu, place, tok);
       kind[i] = x >= n || row == kNoToken ? 0 : r < 2 * p.H ? 1 : sub * L::VALUES < p.d_idx ? 2 : 0;

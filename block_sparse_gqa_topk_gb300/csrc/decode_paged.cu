@@ -50,7 +50,8 @@ struct PagedDecode {
   float* lse;
   int B, H, G, topk;
   int row;         // blocks of the table's length, rounded up to 4
-  int select;      // the attention kernel selects the blocks itself
+  int ctas;        // of the attention kernel
+  int select;      // it selects the blocks itself
   int wh;          // heads (groups) that a CTA may serve side by side
   int keys_shift;  // log2 of a stage's keys
   float scale_log2;  // scale * log2 e: scores in bits
@@ -82,7 +83,7 @@ __device__ __forceinline__ int seq_units(const PagedDecode& p, int len, int wh) 
 // The work of all (sequence, groups) pairs in order is cut into n runs whose lengths differ by at
 // most one: CTA c < n takes total c / n .. total (c + 1) / n - 1.  A pair's work is its units and
 // kOverhead more in front of them, about what starting and ending a pair costs a CTA, so that
-// CTAs with many short sequences get fewer units.  n is kCtas, or the multiple of the number of
+// CTAs with many short sequences get fewer units.  n is the CTAs, or the multiple of the number of
 // pairs next below it where few CTAs are lost (pairs of one length are then cut alike, and no
 // CTA has parts of two), and at most total: each run is at least 1 long, so every CTA between
 // the first and the last that hold units of a pair holds some.
@@ -91,9 +92,9 @@ __device__ __forceinline__ int seq_work(int units) { return units > 0 ? units + 
 struct Cut {
   int total, n, q, r;  // total = q n + r
   float inv;           // 1 / n
-  __device__ __forceinline__ Cut(int total, int pairs) : total(total) {
-    const int even = pairs <= kCtas ? kCtas - kCtas % max(1, pairs) : 0;
-    n = max(1, min(total, even >= kCtas * 9 / 10 ? even : kCtas));
+  __device__ __forceinline__ Cut(int total, int pairs, int ctas) : total(total) {
+    const int even = pairs <= ctas ? ctas - ctas % max(1, pairs) : 0;
+    n = max(1, min(total, even >= ctas * 9 / 10 ? even : ctas));
     q = total / n;
     r = total - q * n;
     inv = 1.f / (float)n;
@@ -136,7 +137,7 @@ __device__ __forceinline__ Work find_run(const PagedDecode& p) {
     if (!SPARSE) side += seq_work(seq_units<SPARSE>(p, len, p.wh));
   }
   const int total1 = __reduce_add_sync(0xffffffffu, mine) * p.H;
-  const bool sided = !SPARSE && p.wh > 1 && total1 >= kSideBySide * kCtas;
+  const bool sided = !SPARSE && p.wh > 1 && total1 >= kSideBySide * p.ctas;
   const int wh = sided ? p.wh : 1, HG = sided ? p.H / p.wh : p.H;
   mine = (sided ? side : mine) * HG;
   int scan = mine;
@@ -147,7 +148,7 @@ __device__ __forceinline__ Work find_run(const PagedDecode& p) {
   }
   const int total = __shfl_sync(0xffffffffu, scan, 31);
   int base = scan - mine;  // where the work of this lane's sequences starts
-  const Cut cut(total, p.B * HG);
+  const Cut cut(total, p.B * HG, p.ctas);
   const int want = cut.start(blockIdx.x);
   const bool first_cta = blockIdx.x == 0 && threadIdx.x < 32;
   const unsigned holds = __ballot_sync(0xffffffffu, want >= base && want < base + mine);
@@ -221,7 +222,7 @@ __device__ __forceinline__ float weight(float a, float b) { return a == -INFINIT
 //   bf16: rows of 2 D bytes, 16-byte chunks XOR-swizzled for ldmatrix;
 //   E4M3: key rows of D bytes whose 64-byte halves are swapped in odd rows, value rows padded
 //   by 16 bytes: the fragment loads then fall in distinct banks.
-template <int D, bool F8>
+template <int D, bool F8, bool WIDE>
 struct Stage {
   static constexpr int KEYS = F8 || D == 64 ? 32 : 16;
   static constexpr int ROW = F8 ? D : 2 * D;
@@ -229,7 +230,11 @@ struct Stage {
   static constexpr int V0 = KEYS * ROW;
   static constexpr int S0 = V0 + KEYS * VROW;  // [2][KEYS] scales
   static constexpr int BYTES = S0 + (F8 ? 2 * KEYS * 4 : 0);
-  static constexpr int COUNT = 2;
+  // CTAs of a SM.  More than 8 heads with d = 128 take more than the 168 registers a thread that
+  // three CTAs leave: two with a third stage serve them better (8 x 128K, 16 heads a group, E4M3:
+  // 598 -> 488 us), but not with d = 64 (E4M3 323 -> 353 us).
+  static constexpr int PER_SM = WIDE && D == 128 ? 2 : 3;
+  static constexpr int COUNT = PER_SM == 2 ? 3 : 2;
   static constexpr int UNIT = KEYS * kWarps;  // tokens of a unit of work
   static constexpr int PER = 128 / UNIT;      // units of a block
   static constexpr int HALVES = KEYS / 16;    // runs of 16 tokens, which never straddle a page
@@ -257,7 +262,7 @@ __device__ __forceinline__ float lg2_fast(float x) {  // relative to 1: about 2^
 // (gq = lane / 4, tq = lane % 4.)
 template <int D, bool F8, bool WIDE>
 struct WarpState {
-  using St = Stage<D, F8>;
+  using St = Stage<D, F8, WIDE>;
   static constexpr int R = WIDE ? 2 : 1;     // heads of a lane's rows of S
   static constexpr int MT = D / 16;          // tiles of 16 value columns
   static constexpr int KT = St::KEYS / 8;    // tiles of 8 keys
@@ -585,8 +590,8 @@ __device__ __forceinline__ void join_parts(const PagedDecode& p, const Parts& pa
 // stages in shared memory and its own running softmax; they join when a span ends.  A whole
 // (sequence, groups) is written out, a part of one goes to the CTA's slot 0 (its first span) or 1.
 template <int D, bool F8, bool WIDE, bool SPARSE>
-__global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDecode p) {
-  using St = Stage<D, F8>;
+__global__ void __launch_bounds__(kThreads, Stage<D, F8, WIDE>::PER_SM) paged_attn_kernel(const PagedDecode p) {
+  using St = Stage<D, F8, WIDE>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][16], s_mv[kWarps][16], s_l[kWarps][16];
   __shared__ int32_t s_blocks[kMaxSelect];
@@ -598,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_attn_kernel(const PagedDeco
   const int wh = SPARSE ? 1 : work.wh, HG = SPARSE ? p.H : work.HG;
   int b = work.b, base = work.base;
   griddep_wait();  // the pooled scores or the selected blocks
-  for (int e = blockIdx.x; e < p.B; e += kCtas) {  // empty slots: o = 0, lse = -inf, no blocks
+  for (int e = blockIdx.x; e < p.B; e += p.ctas) {  // empty slots: o = 0, lse = -inf, no blocks
     if (seq_len(p, e) > 0) continue;
     const int64_t heads = (int64_t)p.H * p.G;
     for (int64_t x = tid; x < heads * D; x += kThreads) p.o[e * heads * D + x] = __float2bfloat16(0.f);
@@ -821,7 +826,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedDec
   if (start == end) return;  // an empty slot
   const int hg = wh == 4 ? g >> 2 : wh == 2 ? g >> 1 : g, HG = wh == 4 ? p.H >> 2 : wh == 2 ? p.H >> 1 : p.H;
   const int size = (end - start) / HG;
-  const Parts parts(Cut(total, p.B * HG), start + hg * size, size - kOverhead);
+  const Parts parts(Cut(total, p.B * HG, p.ctas), start + hg * size, size - kOverhead);
   const int n = parts.n;
   if (n == 1) return;
   auto part_of = [&](int i) { return (parts.slot(i) * wh + (g - hg * wh)) * p.G; };
@@ -1004,13 +1009,14 @@ cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, bool after, c
 
 template <int D, bool F8, bool WIDE, bool SPARSE>
 cudaError_t launch_attn(const PagedDecode& p, cudaStream_t stream) {
-  constexpr int smem = kWarps * Stage<D, F8>::COUNT * Stage<D, F8>::BYTES;
-  static_assert(Stage<D, F8>::COUNT * Stage<D, F8>::BYTES >= (WIDE ? 16 : 8) * (D + 4) * 4, "sums in the stages");
-  static_assert(smem >= 32 * 128 / Stage<D, F8>::UNIT * 16 * 4, "weights of a pair's parts");
+  constexpr int smem = kWarps * Stage<D, F8, WIDE>::COUNT * Stage<D, F8, WIDE>::BYTES;
+  static_assert(Stage<D, F8, WIDE>::COUNT * Stage<D, F8, WIDE>::BYTES >= (WIDE ? 16 : 8) * (D + 4) * 4, "sums in the stages");
+  static_assert(Stage<D, F8, WIDE>::PER_SM == (WIDE && D == 128 ? 2 : 3), "ctas");
+  static_assert(smem >= 32 * 128 / Stage<D, F8, WIDE>::UNIT * 16 * 4, "weights of a pair's parts");
   auto* kern = paged_attn_kernel<D, F8, WIDE, SPARSE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch(kern, dim3(kCtas), kThreads, smem, SPARSE, stream, p);
+  return launch(kern, dim3(p.ctas), kThreads, smem, SPARSE, stream, p);
 }
 
 template <int D>
@@ -1025,16 +1031,17 @@ cudaError_t launch_paged(const PagedDecode& p, bool f8, bool wide, cudaStream_t 
     else e = sparse ? launch_attn<D, false, false, true>(p, stream) : launch_attn<D, false, false, false>(p, stream);
   }
   if (e != cudaSuccess) return e;
-  // The join is a chain of loads, shorter the more parts a CTA reads at once: a CTA for each
-  // head, and for each 32 columns, while all of them run together (8 x 4 groups of 4 heads, 22
-  // parts: 22 us for the whole call with a CTA a head, 30 us with four, 25 us with one a group).
   if (sparse) return cudaSuccess;  // joined by the attention kernel
+  // The join is a chain of loads, shorter the more CTAs share it, while all of them run together
+  // (32 sequences, 4 groups of 4 heads, up to 22 parts: 22 us for the whole call with a CTA a
+  // head, 30 us with four a head, 25 us with one a group; 8 x 64K, 16 heads a group: 321 us with
+  // 9 a group, 344 us with one).
   const int64_t rows = (int64_t)p.B * p.H, together = 4 * 152;
   if (rows * p.G * (D / 32) <= together)
     return launch(paged_join_kernel<D, 32>, dim3((unsigned)rows, (unsigned)p.G, D / 32), kJoinThreads, 0, true,
                   stream, p);
-  return launch(paged_join_kernel<D, D>, dim3((unsigned)rows, rows * p.G <= together ? (unsigned)p.G : 1u),
-                kJoinThreads, 0, true, stream, p);
+  const int64_t split = together / rows < 1 ? 1 : together / rows < p.G ? together / rows : p.G;
+  return launch(paged_join_kernel<D, D>, dim3((unsigned)rows, (unsigned)split), kJoinThreads, 0, true, stream, p);
 }
 
 // Heads (groups) that a CTA serves side by side: all attend the same tokens when the whole cache
@@ -1118,6 +1125,7 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   p.row = (nb + 3) & ~3;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wh = heads_side_by_side(p.H, topk);
+  p.ctas = kCtas / 3 * (p.G > 8 && c->d == 128 ? 2 : 3);  // Stage::PER_SM
   p.keys_shift = c->kind == MSA_CACHE_E4M3 || c->d == 64 ? 5 : 4;
   p.status = cx.status;
   cudaError_t e = cudaSuccess;

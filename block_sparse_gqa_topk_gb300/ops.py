@@ -726,7 +726,7 @@ class PagedCache:
     """A pool of pages: k, v [num_pages, page_size, H_kv, d] bf16, or uint8 E4M3 codes with
     k_scale, v_scale [num_pages, page_size, H_kv] float32; k_idx [num_pages, page_size, d_idx]
     bf16, or None for a cache without index keys.  Page tables (int32 [B, max_pages]) and
-    lengths (int32 [B]) belong to the calls."""
+    lengths (int32 [B]) belong to the calls.  The tensors of a cache are fixed."""
 
     def __init__(self, k, v, k_idx=None, k_scale=None, v_scale=None):
         fp8 = isinstance(k, torch.Tensor) and k.dtype == torch.uint8
@@ -761,6 +761,14 @@ class PagedCache:
         self._c = _lib.PAGED_CACHE.pack(
             P, page, H_kv, d, d_idx, _lib.MSA_CACHE_E4M3 if fp8 else _lib.MSA_CACHE_BF16,
             *(0 if t is None else t.data_ptr() for t in (k, v, k_idx, k_scale, v_scale)))
+
+    def __setattr__(self, name, value):
+        if "_c" in self.__dict__:
+            raise AttributeError("the tensors of a PagedCache are fixed: make another one")
+        object.__setattr__(self, name, value)
+
+    def __reduce__(self):  # a copy has its own tensors
+        return PagedCache, (self.k, self.v, self.k_idx, self.k_scale, self.v_scale)
 
 
 def new_paged_cache(num_pages: int, H_kv: int, *, page_size: int = 128, d: int = 128, d_idx: int = 64,

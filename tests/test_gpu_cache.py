@@ -318,3 +318,14 @@ def test_refusals():
     ]:
         with pytest.raises(err):
             ops.PagedCache(*args)
+
+
+def test_a_cache_is_fixed_and_its_copy_has_its_own_pages():
+    import copy
+    c = ops.new_paged_cache(2, 1, page_size=16, d=64, d_idx=32, fp8=True)
+    with pytest.raises(AttributeError):
+        c.k = c.v
+    d = copy.deepcopy(c)
+    k, v, ki = randn((1, 1, 64), 1), randn((1, 1, 64), 2), randn((1, 32), 3)
+    ops.msa_cache_write(d, dev([[0]]), dev([1]), k, v, ki)
+    assert not c.k.any() and d.k.any() and torch.equal(d.k_idx[0, 0], ki[0])

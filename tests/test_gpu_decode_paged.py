@@ -194,6 +194,47 @@ def test_sparse(case, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+def test_long_caches_and_many_sequences(fp8):
+    """Long enough that groups are served side by side (1, 2 and 4 of them), enough sequences that
+    a warp's lanes hold several, more blocks than the attention kernel selects from, more than the
+    ranks hold, and scores that tie across them."""
+    for lens, H in (([200001, 64], 6), ([150000, 99], 4), ([40000] * 6, 8)):
+        batch = Batch(lens, 16, H, 64, 0, fp8, seed=61)
+        q = query(len(lens), H * 2, 64, 62)
+        o, lse = ops.msa_decode_paged_dense(q, batch.cache, batch.table, batch.lens_t)
+        check_dense(batch, q, 0.125, o, lse)
+    lens = [(7 * i) % 190 for i in range(1500)]
+    batch = Batch(lens, 16, 2, 64, 32, fp8, seed=63)
+    q, qi = query(1500, 2, 64, 64), query(1500, 2, 32, 65)
+    o, lse = ops.msa_decode_paged_dense(q, batch.cache, batch.table, batch.lens_t)
+    sets, o2, lse2 = ops.msa_decode_paged(q, qi, batch.cache, batch.table, batch.lens_t, 2)  # all blocks
+    for b in range(0, 1500, 37):
+        check_attention(batch, b, q, o, lse, lambda g, b=b: batch.rows(b, lens[b]), 0.125)
+        check_attention(batch, b, q, o2, lse2, lambda g, b=b: batch.rows(b, lens[b]), 0.125)
+    empty = batch.lens_t == 0
+    assert (lse[~empty] > -math.inf).all() and (lse[empty] == -math.inf).all() and not o[empty].any()
+    assert torch.equal((sets >= 0).sum(-1), ((batch.lens_t + 127) // 128)[:, None].expand(-1, 2).long())
+    for n, topk in ((140000, 16), (600000, 32)):  # 1094 and 4688 blocks
+        batch = Batch([n, 1000], 128, 1, 64, 32, fp8, seed=66)
+        ki = batch.cache.k_idx.flatten(0, 1)
+        rows = batch.rows(0, n)
+        ki[rows[5 * 128:9 * 128]] = ki[rows[128:256]].repeat(4, 1)  # five blocks that tie
+        q, qi = query(2, 3, 64, 67), query(2, 1, 32, 68)
+        qi[0, 0] = ki[rows[130]]  # and are among the best
+        sets, o, lse = ops.msa_decode_paged(q, qi, batch.cache, batch.table, batch.lens_t, topk)
+        host = sets.cpu()
+        for b, m in enumerate((n, 1000)):
+            check_selection(batch, b, m, qi[b], host[b], topk)
+
+            def tokens(g, b=b, m=m):
+                r = batch.rows(b, m)
+                return torch.cat([r[:0]] + [r[c * 128:(c + 1) * 128] for c in host[b, g].tolist() if c >= 0])
+
+            check_attention(batch, b, q, o, lse, tokens, 0.125)
+    assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_contiguous_cache_as_pages_agrees_with_msa_decode(fp8):
     """msa_decode's cache [B, Lmax] is a paged cache with pages 0, 1, 2, ...: the same sets
     (exact ties among them, lower block first) and, within both roundings, the same output."""

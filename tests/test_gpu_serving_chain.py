@@ -44,6 +44,9 @@ def training_rows(seq, rope, fp8):
 @pytest.mark.parametrize("fp8", [False, True])
 def test_prompt_then_captured_decode(fp8):
     prompts, steps, page = [300, 517, 1], 9, 16
+    # the training path takes a cached E4M3 key rounded to bf16, which moves a score by up to
+    # scale * sum |q k| 2^-9 = 64^-0.5 * 64 * E|q k| (0.64) * 2^-9 = 1e-2, and the lse with it
+    lse_tol = 2e-2 if fp8 else LSE_TOL
     seqs = sequences([n + steps for n in prompts], 1)
     rope = ops.new_rope(ROT, scaling={"type": "yarn", "factor": 4, "original_len": 256})
     want = [training_rows(s, rope, fp8) for s in seqs]
@@ -103,6 +106,6 @@ def test_prompt_then_captured_decode(fp8):
             i = n + t
             assert torch.equal(sets[r], sparse[0][:, i])
             assert (o[r].float() - sparse[1][i].float()).abs().max() <= O_TOL
-            assert (lse[r] - sparse[2][:, i]).abs().max() <= (LSE_TOL if not fp8 else 2e-2)
+            assert (lse[r] - sparse[2][:, i]).abs().max() <= lse_tol
             assert (o_dense[r].float() - dense[1][i].float()).abs().max() <= O_TOL
-            assert (lse_dense[r] - dense[2][:, i]).abs().max() <= (LSE_TOL if not fp8 else 2e-2)
+            assert (lse_dense[r] - dense[2][:, i]).abs().max() <= lse_tol

@@ -114,9 +114,9 @@ def test_cache_calls_check_their_arguments():
 
 
 def test_decode_calls_check_their_arguments():
-    need = _lib.msa_decode_paged_workspace_size(cache(), table(), 4, 0)
-    more = _lib.msa_decode_paged_workspace_size(cache(), table(n=1 << 20), 4, 4)
-    assert 0 < need < more
+    size = _lib.msa_decode_paged_workspace_size
+    need = size(cache(), table(), 4, 4)  # the pooled scores grow with the table's length
+    assert 0 < need < size(cache(), table(n=1 << 20), 4, 4) and size(cache(), table(), 4, 0) > 0
     big = 1 << 40
 
     def dense(c=cache(), t=table(), lens=256, H_q=4, scale=1.0, q=256, o=256, lse=256, ws=256, n=big):
@@ -133,12 +133,13 @@ def test_decode_calls_check_their_arguments():
                          (dict(t=table(n=1 << 28)), UNSUP), (dict(H_q=3), SHAPE), (dict(H_q=0), SHAPE),
                          (dict(H_q=34), UNSUP), (dict(scale=0.0), ARG), (dict(scale=float("nan")), ARG),
                          (dict(q=None), ARG), (dict(o=264), ARG), (dict(lse=None), ARG), (dict(lens=None), ARG),
-                         (dict(lens=258), ARG), (dict(ws=None), WS), (dict(n=need - 1), WS), (dict(ws=128), ARG),
+                         (dict(lens=258), ARG), (dict(ws=None), WS), (dict(n=255), WS), (dict(ws=128), ARG),
                          (dict(t=table(B=0)), OK)]:
             assert f(**kw) == code, (f, kw)
     for kw, code in [(dict(topk=0), SHAPE), (dict(topk=33), UNSUP), (dict(c=cache(di=0)), SHAPE),
-                     (dict(qi=None), ARG), (dict(bi=264), ARG)]:
+                     (dict(qi=None), ARG), (dict(bi=264), ARG), (dict(n=need - 1), WS)]:
         assert sparse(**kw) == code, kw
-    size = _lib.msa_decode_paged_workspace_size
+    # the work of a call is counted in 32 bits
+    assert dense(t=table(B=60000, n=1 << 20, stride=1 << 20), c=cache(H=4)) == UNSUP
     assert size(cache(), table(), 4, -1) == 0 and size(cache(), table(), 3, 0) == 0
     assert size(cache(di=0), table(), 4, 4) == 0 and size(cache(k=0), table(ids=0), 4, 4) > 0

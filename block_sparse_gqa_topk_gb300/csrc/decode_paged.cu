@@ -13,6 +13,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math.h>
+#include <atomic>
 
 #include "decode_select.cuh"
 #include "kernels.h"
@@ -1014,8 +1015,14 @@ cudaError_t launch_attn(const PagedDecode& p, cudaStream_t stream) {
   static_assert(Stage<D, F8, WIDE>::PER_SM == (WIDE && D == 128 ? 2 : 3), "ctas");
   static_assert(smem >= 32 * 128 / Stage<D, F8, WIDE>::UNIT * 16 * 4, "weights of a pair's parts");
   auto* kern = paged_attn_kernel<D, F8, WIDE, SPARSE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  // the attribute belongs to the function in a context: set again where that changes
+  static std::atomic<void*> done{nullptr};
+  void* ctx = current_context();
+  if (!ctx || done.load(std::memory_order_relaxed) != ctx) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    done.store(ctx, std::memory_order_relaxed);
+  }
   return launch(kern, dim3(p.ctas), kThreads, smem, SPARSE, stream, p);
 }
 

@@ -500,13 +500,16 @@ _ROPE_DTYPES = {torch.bfloat16: _lib.MSA_DTYPE_BF16, torch.float16: _lib.MSA_DTY
 _TWO_PI = fractions.Fraction(2 * 31415926535897932384626433832795028841971693993751, 10 ** 49)
 
 
-def _call(dev, name, f, *args):
-    """f(*args, stream) on `dev`'s current stream, with `dev` current; raises on an error."""
-    index = dev.index
+_Tensor, _BF16, _I32 = torch.Tensor, torch.bfloat16, torch.int32
+
+
+def _call(index, name, f, *args):
+    """f(*args, stream) on the current stream of device `index`, with that device current;
+    raises on an error."""
     if index == torch.cuda.current_device():
         rc = f(*args, _stream_of(index))
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             rc = f(*args, _stream_of(index))
     if rc:
         _lib.check(rc, name)
@@ -604,82 +607,90 @@ def msa_rope(xs, rope: Rope, positions=None, *, inverse: bool = False, inplace: 
     sequence.  positions int32 or int64 [T]: packed tokens [T, H, d] or [T, d];  [B, N] (a
     broadcast row is fine): tokens [B, N, H, d] or [B, N, d].  bf16, fp16 or float32 (all the
     same), d >= rot_dim; any strides (views of a fused projection), the last axis contiguous
-    or else copied once."""
-    xs = (xs,) if isinstance(xs, torch.Tensor) else tuple(xs)
+    or else copied once.  In place the tensors must not overlap."""
+    xs = (xs,) if isinstance(xs, _Tensor) else tuple(xs)
     if not 1 <= len(xs) <= 4:
         raise ValueError(f"one to four tensors, got {len(xs)}")
     if not isinstance(rope, Rope):
         raise TypeError("rope must come from new_rope")
-    x0 = xs[0]
-    bits, ps = 32, (0, 0)
-    if positions is None:
-        if not isinstance(x0, torch.Tensor) or x0.dim() < 3:
-            raise ValueError("without positions the tensors are [B, N, H, d] or [B, N, d]")
-        lead = tuple(x0.shape[:2])
-    else:
-        if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
-            raise TypeError("positions must be an int32 or int64 tensor")
-        if positions.dim() not in (1, 2):
-            raise ValueError(f"positions must be [T] or [B, N], got {tuple(positions.shape)}")
-        if positions.dtype == torch.int64:
-            bits = 64
-        ps = positions.stride() if positions.dim() == 2 else (0, positions.stride(0))
-        lead = tuple(positions.shape)
-    turns = rope.turns
-    dev, dtype, rot = turns.device, x0.dtype, rope.rot_dim
+    for x in xs:
+        if not isinstance(x, _Tensor):
+            raise TypeError("every operand must be a tensor")
+    turns, rot = rope.turns, rope.rot_dim
+    index, dtype = turns.get_device(), xs[0].dtype
     code = _ROPE_DTYPES.get(dtype)
     if code is None:
         raise TypeError(f"tensors must be bf16, fp16 or float32, got {dtype}")
-    if dev.type != "cuda" or (positions is not None and positions.device != dev):
+    bits, at, ps = 32, None, (0, 0)
+    if positions is None:
+        if xs[0].dim() < 3:
+            raise ValueError("without positions the tensors are [B, N, H, d] or [B, N, d]")
+        lead = xs[0].shape[:2]
+    else:
+        if not isinstance(positions, _Tensor) or positions.dtype not in (_I32, torch.int64):
+            raise TypeError("positions must be an int32 or int64 tensor")
+        lead, ps, at = positions.shape, positions.stride(), positions.data_ptr()
+        if len(lead) == 1:
+            ps = (0, ps[0])
+        elif len(lead) != 2:
+            raise ValueError(f"positions must be [T] or [B, N], got {tuple(lead)}")
+        if positions.dtype != _I32:
+            bits = 64
+    if index < 0 or (positions is not None and positions.get_device() != index):
         raise ValueError("rope, positions and the tensors must be on one CUDA device (no CPU path exists)")
     n = len(lead)
-    tokens = lead[0] * lead[1] if n == 2 else lead[0]
+    B, N = lead if n == 2 else (1, lead[0])
+    if inplace:
+        _check_in_place(xs)
+    # A decode step's time is the host's: each attribute is looked up once.
     ys, packed, keep = [], [], []
-    pack, empty = _lib.ROPE_TENSOR.pack, torch.empty  # a decode step is host-bound: see each lookup once
+    pack, empty, dev = _lib.ROPE_TENSOR.pack, torch.empty, turns.device
     for x in xs:
-        if not isinstance(x, torch.Tensor):
-            raise TypeError("every operand must be a tensor")
-        if x.device != dev:
-            raise ValueError("rope, positions and the tensors must be on one CUDA device (no CPU path exists)")
-        if x.dtype != dtype:
-            raise TypeError(f"all tensors must be {dtype}, got {x.dtype}")
-        shape = x.shape
+        shape, sx = x.shape, x.stride()
         more = len(shape) - n
         if shape[:n] != lead or not 1 <= more <= 2:
-            raise ValueError(f"every tensor must be {lead} + ([H,] d), got {tuple(shape)}")
-        d, H = shape[-1], shape[n] if more == 2 else 1
+            raise ValueError(f"every tensor must be {tuple(lead)} + ([H,] d), got {tuple(shape)}")
+        if x.dtype != dtype:
+            raise TypeError(f"all tensors must be {dtype}, got {x.dtype}")
+        if x.get_device() != index:
+            raise ValueError("rope, positions and the tensors must be on one CUDA device (no CPU path exists)")
+        d = shape[-1]
         if d < rot:
             raise ValueError(f"d = {d} < rot_dim = {rot}")
-        sx = x.stride()
+        H, h = (shape[n], sx[n]) if more == 2 else (1, 0)
         if inplace:
-            if sx[-1] != 1 or any(s == 0 and k > 1 for s, k in zip(sx, shape)):
-                raise ValueError("a tensor whose values overlap, or whose last axis is strided, cannot be "
-                                 "turned in place")
-            if x.requires_grad and torch.is_grad_enabled():
-                raise ValueError("a tensor that requires a gradient cannot be turned in place: use rope")
-            y = x
-            torch.autograd.graph.increment_version(x)
-        else:
-            if sx[-1] != 1:
-                x = x.contiguous()
-                keep.append(x)
-                sx = x.stride()
-            y = empty(shape, dtype=dtype, device=dev)
-        ys.append(y)
-        if tokens == 0 or H == 0:
+            ys.append(x)
+            if B and N and H:
+                b, t, p = sx[0] if n == 2 else 0, sx[n - 1], x.data_ptr()
+                packed.append(pack(p, p, b, t, h, b, t, h, H, d))
             continue
-        # strides of batch, token and head; a new y is contiguous
-        b, t, h = sx[0] if n == 2 else 0, sx[n - 1], sx[n] if more == 2 else 0
-        if inplace:
-            packed.append(pack(x.data_ptr(), x.data_ptr(), b, t, h, b, t, h, H, d))
-        else:
-            packed.append(pack(x.data_ptr(), y.data_ptr(), b, t, h, lead[-1] * H * d, H * d, d, H, d))
+        if sx[-1] != 1:
+            x = x.contiguous()
+            keep.append(x)
+            sx = x.stride()
+            h = sx[n] if more == 2 else 0
+        y = empty(shape, dtype=dtype, device=dev)
+        ys.append(y)
+        if B and N and H:  # strides of batch, token and head; y is contiguous
+            packed.append(pack(x.data_ptr(), y.data_ptr(), sx[0] if n == 2 else 0, sx[n - 1], h, N * H * d, H * d, d,
+                               H, d))
     if packed:
-        B, N = lead if n == 2 else (1, tokens)
-        r = _lib.ROPE.pack(B, N, rot, rope.interleaved, inverse, code, bits, rope.mscale, ps[0], ps[1])
-        _call(dev, "msa_rope", _lib.msa_rope, r, turns.data_ptr(),
-              None if positions is None else positions.data_ptr(), b"".join(packed), len(packed))
+        r = _lib.ROPE.pack(B, N, rot, rope.interleaved, inverse, code, bits, rope.mscale, *ps)
+        _call(index, "msa_rope", _lib.msa_rope, r, turns.data_ptr(), at, b"".join(packed), len(packed))
     return tuple(ys)
+
+
+def _check_in_place(xs):
+    if len({x.data_ptr() for x in xs if x.numel()}) != sum(x.numel() > 0 for x in xs):
+        raise ValueError("the same memory is given twice: it would be turned twice")
+    for x in xs:
+        if any(s == 0 and k > 1 for s, k in zip(x.stride(), x.shape)) or x.stride(-1) != 1:
+            raise ValueError("a tensor whose values overlap, or whose last axis is strided, cannot be "
+                             "turned in place")
+        if x.requires_grad and torch.is_grad_enabled():
+            raise ValueError("a tensor that requires a gradient cannot be turned in place: use rope")
+    for x in xs:
+        torch.autograd.graph.increment_version(x)
 
 
 class RopeFunction(torch.autograd.Function):
@@ -757,7 +768,7 @@ class PagedCache:
             raise ValueError(f"d must be 64 or 128 and d_idx 32 or 64, got {d} and {d_idx}")
         self.k, self.v, self.k_idx, self.k_scale, self.v_scale = k, v, k_idx, k_scale, v_scale
         self.num_pages, self.page_size, self.H_kv, self.d, self.d_idx, self.fp8 = P, page, H_kv, d, d_idx, fp8
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         self._c = _lib.PAGED_CACHE.pack(
             P, page, H_kv, d, d_idx, _lib.MSA_CACHE_E4M3 if fp8 else _lib.MSA_CACHE_BF16,
             *(0 if t is None else t.data_ptr() for t in (k, v, k_idx, k_scale, v_scale)))
@@ -785,42 +796,45 @@ def new_paged_cache(num_pages: int, H_kv: int, *, page_size: int = 128, d: int =
 
 
 def _pages_arg(cache, page_table, lens):
-    """The packed page table after the checks that a paged call's arguments share."""
+    """The packed page table, after the checks that a paged call's arguments share, and its B."""
     if not isinstance(cache, PagedCache):
         raise TypeError("cache must be a PagedCache")
-    for t, n, nd in ((page_table, "page_table", 2), (lens, "lens", 1)):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+    for t, n in ((page_table, "page_table"), (lens, "lens")):
+        if not isinstance(t, _Tensor) or t.dtype != _I32:
             raise TypeError(f"{n} must be an int32 tensor")
-        if t.device != cache.device:
+        if t.get_device() != cache.index:
             raise ValueError(f"{n} must be on the cache's device")
-        if t.dim() != nd or (t.numel() > 1 and t.stride(-1) != 1 and t.shape[-1] > 1):
-            raise ValueError(f"{n} must have {nd} dims, the last contiguous")
-    B, max_pages = page_table.shape
-    if lens.shape[0] != B:
-        raise ValueError(f"lens must be [{B}], got {tuple(lens.shape)}")
-    return _lib.PAGE_TABLE.pack(page_table.data_ptr(), B, max_pages, page_table.stride(0)), B, max_pages
+    shape, strides, L = page_table.shape, page_table.stride(), lens.shape
+    if len(shape) != 2 or (strides[1] != 1 and shape[1] > 1):
+        raise ValueError("page_table must have 2 dims, the last contiguous")
+    B = shape[0]
+    if len(L) != 1 or L[0] != B or (B > 1 and lens.stride(0) != 1):
+        raise ValueError(f"lens must be a contiguous [{B}], got {tuple(L)}")
+    return _lib.PAGE_TABLE.pack(page_table.data_ptr(), B, shape[1], strides[0]), B
 
 
 def _cu_arg(cu_seqlens, cache, B):
-    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dtype != torch.int32:
+    if not isinstance(cu_seqlens, _Tensor) or cu_seqlens.dtype != _I32:
         raise TypeError("cu_seqlens must be an int32 tensor")
-    if cu_seqlens.device != cache.device or cu_seqlens.shape != (B + 1,) or not cu_seqlens.is_contiguous():
+    if cu_seqlens.get_device() != cache.index or cu_seqlens.shape != (B + 1,) or not cu_seqlens.is_contiguous():
         raise ValueError(f"cu_seqlens must be a contiguous [{B + 1}] on the cache's device")
+    return cu_seqlens.data_ptr()
 
 
 def _cache_rows(t, name, cache, shape):
-    """A packed input of msa_cache_write, copied where its rows do not start on 16 bytes."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+    """A packed input of msa_cache_write (copied where its rows do not start on 16 bytes), its
+    address and strides."""
+    if not isinstance(t, _Tensor) or t.dtype != _BF16:
         raise TypeError(f"{name} must be a bf16 tensor")
-    if t.device != cache.device:
+    if t.get_device() != cache.index:
         raise ValueError(f"{name} must be on the cache's device (no CPU path exists)")
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 or t.data_ptr() % 16 or any(s % 8 for s in t.stride()[:-1]):
-        t = t.contiguous()
-        if t.data_ptr() % 16:  # contiguous already, but off a 16-byte boundary
-            t = t.clone()
-    return t
+    p, s = t.data_ptr(), t.stride()
+    if s[-1] != 1 or p % 16 or s[0] % 8 or s[-2] % 8:
+        t = t.clone(memory_format=torch.contiguous_format)
+        p, s = t.data_ptr(), t.stride()
+    return t, p, s
 
 
 def msa_cache_write(cache: PagedCache, page_table, lens, k, v, k_idx=None, *, cu_seqlens=None) -> None:
@@ -830,24 +844,24 @@ def msa_cache_write(cache: PagedCache, page_table, lens, k, v, k_idx=None, *, cu
     positions lens[b] - n .. lens[b] - 1.  cu_seqlens (int32 [B + 1]) splits the T packed tokens;
     without it there is one token a sequence (T = B), and lens[b] = 0 skips the slot.  A token
     whose place does not exist is dropped and sets the device status."""
-    pages, B, _ = _pages_arg(cache, page_table, lens)
-    T = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else -1
-    k = _cache_rows(k, "k", cache, (max(T, 0), cache.H_kv, cache.d))
-    v = _cache_rows(v, "v", cache, (T, cache.H_kv, cache.d))
+    pages, B = _pages_arg(cache, page_table, lens)
+    T = k.shape[0] if isinstance(k, _Tensor) and k.dim() == 3 else 0
+    k, pk, sk = _cache_rows(k, "k", cache, (T, cache.H_kv, cache.d))
+    v, pv, sv = _cache_rows(v, "v", cache, (T, cache.H_kv, cache.d))
     if (k_idx is None) != (cache.k_idx is None):
         raise ValueError("k_idx must be given exactly if the cache has index keys")
+    pi, si = None, (0,)
     if k_idx is not None:
-        k_idx = _cache_rows(k_idx, "k_idx", cache, (T, cache.d_idx))
+        k_idx, pi, si = _cache_rows(k_idx, "k_idx", cache, (T, cache.d_idx))
+    cu = None
     if cu_seqlens is not None:
-        _cu_arg(cu_seqlens, cache, B)
+        cu = _cu_arg(cu_seqlens, cache, B)
     elif T != B:
         raise ValueError(f"without cu_seqlens there is one token a sequence: {B}, got {T}")
     if T == 0 or B == 0:
         return
-    strides = _lib.CACHE_STRIDES.pack(k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-                                      0 if k_idx is None else k_idx.stride(0))
-    _call(cache.device, "msa_cache_write", _lib.msa_cache_write, cache._c, pages, lens.data_ptr(),
-          _ptr(cu_seqlens), T, k.data_ptr(), v.data_ptr(), _ptr(k_idx), strides)
+    _call(cache.index, "msa_cache_write", _lib.msa_cache_write, cache._c, pages, lens.data_ptr(), cu, T, pk, pv, pi,
+          _lib.CACHE_STRIDES.pack(sk[0], sk[1], sv[0], sv[1], si[0]))
 
 
 def msa_cache_read(cache: PagedCache, page_table, lens, cu_seqlens, total_tokens: int):
@@ -855,7 +869,7 @@ def msa_cache_read(cache: PagedCache, page_table, lens, cu_seqlens, total_tokens
     lens[b] - 1) in packed order: k, v [total_tokens, H_kv, d] and k_idx [total_tokens, d_idx]
     (None without index keys), bf16.  With lens[b] tokens of each it is the whole context, as
     msa_fwd_varlen and its companions take it.  Rows behind cu_seqlens[B] are not written."""
-    pages, B, _ = _pages_arg(cache, page_table, lens)
+    pages, B = _pages_arg(cache, page_table, lens)
     _cu_arg(cu_seqlens, cache, B)
     T = int(total_tokens)
     if T < 0:
@@ -867,7 +881,7 @@ def msa_cache_read(cache: PagedCache, page_table, lens, cu_seqlens, total_tokens
     if cache.k_idx is not None:
         k_idx = torch.empty((T, cache.d_idx), dtype=torch.bfloat16, device=dev)
     if T and B:
-        _call(dev, "msa_cache_read", _lib.msa_cache_read, cache._c, pages, lens.data_ptr(),
+        _call(cache.index, "msa_cache_read", _lib.msa_cache_read, cache._c, pages, lens.data_ptr(),
               cu_seqlens.data_ptr(), T, k.data_ptr(), v.data_ptr(), _ptr(k_idx))
     return k, v, k_idx
 
@@ -877,19 +891,19 @@ def msa_cache_read(cache: PagedCache, page_table, lens, cu_seqlens, total_tokens
 # stream: calls on other streams and other captured graphs never share it.
 # ---------------------------------------------------------------------------
 def _paged_args(q, cache, page_table, lens, topk, scale):
-    pages, B, _ = _pages_arg(cache, page_table, lens)
+    pages, B = _pages_arg(cache, page_table, lens)
     _need(q, "q", ndim=3)
-    H_q, d = q.shape[1:]
-    if q.device != cache.device or q.shape[0] != B or d != cache.d or H_q == 0 or H_q % cache.H_kv:
-        raise ValueError(f"q must be [{B}, a multiple of {cache.H_kv}, {cache.d}] on the cache's device, "
-                         f"got {tuple(q.shape)}")
-    if H_q // cache.H_kv > 16:
-        raise ValueError(f"at most 16 query heads a group, got {H_q // cache.H_kv}")
-    dev = cache.device
+    shape, H_kv, d = q.shape, cache.H_kv, cache.d
+    H_q = shape[1]
+    if shape[0] != B or shape[2] != d or H_q == 0 or H_q % H_kv or q.get_device() != cache.index:
+        raise ValueError(f"q must be [{B}, a multiple of {H_kv}, {d}] on the cache's device, got {tuple(shape)}")
+    if H_q // H_kv > 16:
+        raise ValueError(f"at most 16 query heads a group, got {H_q // H_kv}")
     nws = _lib.msa_decode_paged_workspace_size(cache._c, pages, H_q, topk)
     if nws == 0:
         raise ValueError("the sizes of this call are outside the supported set")
-    return (pages, H_q, float(1.0 / math.sqrt(d) if scale is None else scale), torch.empty_like(q),
+    dev = cache.device
+    return (pages, B, H_q, d ** -0.5 if scale is None else float(scale), torch.empty_like(q),
             torch.empty((B, H_q), dtype=torch.float32, device=dev),
             torch.empty(nws, dtype=torch.uint8, device=dev), nws)
 
@@ -904,15 +918,15 @@ def msa_decode_paged(q, q_idx, cache: PagedCache, page_table, lens, topk: int = 
         raise TypeError("cache must be a PagedCache")
     if cache.k_idx is None:
         raise ValueError("the cache has no index keys")
-    pages, H_q, scale, o, lse, ws, nws = _paged_args(q, cache, page_table, lens, topk, scale)
+    pages, B, H_q, scale, o, lse, ws, nws = _paged_args(q, cache, page_table, lens, topk, scale)
     _need(q_idx, "q_idx", ndim=3)
-    B, H_kv = q.shape[0], cache.H_kv
-    if tuple(q_idx.shape) != (B, H_kv, cache.d_idx) or q_idx.device != cache.device:
-        raise ValueError(f"q_idx must be {(B, H_kv, cache.d_idx)} on the cache's device, got {tuple(q_idx.shape)}")
-    block_idx = torch.empty((B, H_kv, topk), dtype=torch.int32, device=cache.device)
+    if q_idx.shape != (B, cache.H_kv, cache.d_idx) or q_idx.get_device() != cache.index:
+        raise ValueError(f"q_idx must be {(B, cache.H_kv, cache.d_idx)} on the cache's device, "
+                         f"got {tuple(q_idx.shape)}")
+    block_idx = torch.empty((B, cache.H_kv, topk), dtype=_I32, device=cache.device)
     if B:
-        _call(cache.device, "msa_decode_paged", _lib.msa_decode_paged, cache._c, pages, lens.data_ptr(), H_q,
-              topk, scale, q.data_ptr(), q_idx.data_ptr(), block_idx.data_ptr(), o.data_ptr(), lse.data_ptr(),
+        _call(cache.index, "msa_decode_paged", _lib.msa_decode_paged, cache._c, pages, lens.data_ptr(), H_q, topk,
+              scale, q.data_ptr(), q_idx.data_ptr(), block_idx.data_ptr(), o.data_ptr(), lse.data_ptr(),
               ws.data_ptr(), nws)
     return block_idx, o, lse
 
@@ -920,8 +934,8 @@ def msa_decode_paged(q, q_idx, cache: PagedCache, page_table, lens, topk: int = 
 def msa_decode_paged_dense(q, cache: PagedCache, page_table, lens, *, scale=None):
     """Attention of one new token a sequence over its whole paged cache: arguments as in
     msa_decode_paged.  Returns (o [B,H_q,d] bf16, lse [B,H_q] f32)."""
-    pages, H_q, scale, o, lse, ws, nws = _paged_args(q, cache, page_table, lens, 0, scale)
-    if q.shape[0]:
-        _call(cache.device, "msa_decode_paged_dense", _lib.msa_decode_paged_dense, cache._c, pages,
-              lens.data_ptr(), H_q, scale, q.data_ptr(), o.data_ptr(), lse.data_ptr(), ws.data_ptr(), nws)
+    pages, B, H_q, scale, o, lse, ws, nws = _paged_args(q, cache, page_table, lens, 0, scale)
+    if B:
+        _call(cache.index, "msa_decode_paged_dense", _lib.msa_decode_paged_dense, cache._c, pages, lens.data_ptr(),
+              H_q, scale, q.data_ptr(), o.data_ptr(), lse.data_ptr(), ws.data_ptr(), nws)
     return o, lse

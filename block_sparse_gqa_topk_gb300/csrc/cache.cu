@@ -31,9 +31,7 @@ struct CacheParams {
   __nv_bfloat16* xv;
   __nv_bfloat16* xi;
   int64_t sk[2], sv[2], si;  // their strides: token, head; token
-  int rows;                  // of a token: 2 H, and the index key's where there is one
-  float inv_rows;
-  int steps;                 // chunks of a warp
+  int per;                   // tokens of a warp
   int d_idx;
   int* status;
 };
@@ -84,11 +82,22 @@ __device__ __noinline__ uint2 divide8(uint4 w, float sc) {
   return make_uint2(c[0], c[1]);
 }
 
-// E4M3 codes of eight values at scale sc (amax / 448): the code nearest to the float32
-// quotient x / sc.  With r the rounded reciprocal, q0 = x r and the remainder x - q0 sc, which
-// one fma gives exactly, q0 + r (x - q0 sc) is the rounded quotient (Markstein 1990); that it
-// gives every code that division gives is checked over all pairs of bf16 significands.  Rows
-// whose amax leaves the range in which nothing underflows are divided.
+// A row's scale amax / 448 (1 for an all-zero row), and its reciprocal r for quantize8: an
+// approximate reciprocal with one Newton step.
+__device__ __forceinline__ void row_scale(float amax, float* sc, float* r) {
+  constexpr float kInv = 1.f / 448.f;
+  const float q0 = amax * kInv;
+  *sc = amax > 0.f ? fmaf(fmaf(-q0, 448.f, amax), kInv, q0) : 1.f;
+  float r0;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(*sc));
+  *r = fmaf(r0, fmaf(-*sc, r0, 1.f), r0);
+}
+
+// E4M3 codes of eight values at scale sc: the code nearest to the float32 quotient x / sc.  With r
+// the rounded reciprocal, q0 = x r and the remainder x - q0 sc, which one fma gives exactly,
+// q0 + r (x - q0 sc) is the rounded quotient (Markstein 1990; the scale above likewise); that
+// scales and codes are those that division gives is checked over all pairs of bf16 significands.
+// Rows whose amax leaves the range in which nothing underflows are divided.
 __device__ __forceinline__ uint2 quantize8(uint4 w, float sc, float r) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   const float2 rr = make_float2(r, r), nn = make_float2(-sc, -sc);
@@ -117,145 +126,186 @@ __device__ __forceinline__ uint4 dequantize8(uint2 c, float s) {
   return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
-// Items are the rows of the packed tokens in order: the keys of a token's H heads, the
-// values, the index key.  A warp takes `steps` chunks of CHUNK consecutive items; its lanes
-// find the places of the (at most 32) tokens among them together, so the chain of lookups
-// (sequence, length, page) is paid once, and then move STEPS rows at a time with all their
-// loads in flight.
-// A lane moves 16 bytes of the pool a row: 8 bf16 values, or 16 codes.
-template <int D, bool F8>
+// A token's keys, and its values, are one run of H D values in the pool; a lane moves 8 values
+// of it at a time (16 of E4M3: half the addresses and scales), a warp one token after another.  Its lanes find the places of
+// all its tokens (at most 32) together, so the chain of lookups (sequence, length, page) is paid
+// once, and while it works on STEPS vectors a lane, the next ones are on their way.
+template <int D, bool F8, bool WRITE>
 struct Lanes {
-  static constexpr int VALUES = F8 ? 16 : 8;       // of a lane
-  static constexpr int LPR = D / VALUES;           // lanes of a row
-  static constexpr int RPS = 32 / LPR;             // rows of a step
-  static constexpr int STEPS = F8 ? 2 : 4;         // rows a lane has in flight
-  static constexpr int CHUNK = RPS * STEPS;
+  static constexpr int VALUES = F8 ? 16 : 8;  // of a lane's vector
+  static constexpr int LPR = D / VALUES;      // lanes of a head's row
+  static constexpr int STEPS = F8 && WRITE ? 1 : 2;
 };
 
+// STEPS vectors a lane of one token, loaded; where they go.
 template <int D, bool F8, bool WRITE>
-__global__ void __launch_bounds__(kThreads) cache_kernel(const __grid_constant__ CacheParams p) {
-  using L = Lanes<D, F8>;
-  constexpr int STEPS = L::STEPS;
-  constexpr int W = L::VALUES / 8;  // 16-byte vectors of a lane in the packed rows
-  const int lane = threadIdx.x & 31, sub = lane % L::LPR;
-  const int64_t items = (int64_t)p.T * p.rows;
-  const int64_t i0 = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5) * (L::CHUNK * p.steps);
-  if (i0 >= items) return;
-  const int n = (int)min((int64_t)L::CHUNK * p.steps, items - i0);
-  const int t0 = (int)(i0 / p.rows);
-  const int skip = (int)(i0 - (int64_t)t0 * p.rows);
+struct Batch {
+  using L = Lanes<D, F8, WRITE>;
+  static constexpr int W = L::VALUES / 8;  // 16-byte vectors of a lane in the packed rows
+  uint4 w[L::STEPS][W];                    // (16 codes of the pool: the first)
+  float s[L::STEPS];
+  uint4* dst[L::STEPS];                    // null: nothing to store
+  float* scale[L::STEPS];
+};
+
+template <bool F8, bool WRITE>
+constexpr int kCtasPerSm = F8 && WRITE ? 4 : F8 ? 3 : 4;
+
+template <int D, bool F8, bool WRITE>
+__global__ void __launch_bounds__(kThreads, (kCtasPerSm<F8, WRITE>)) cache_kernel(const __grid_constant__ CacheParams p) {
+  using L = Lanes<D, F8, WRITE>;
+  using B = Batch<D, F8, WRITE>;
+  constexpr int W = B::W;
+  const int lane = threadIdx.x & 31;
+  const int64_t t0 = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5) * p.per;
+  if (t0 >= p.T) return;
+  const int n = (int)min((int64_t)p.per, p.T - t0);
   int64_t place = kNoToken;
-  if (lane * p.rows < skip + n) {
-    place = token_row(p, t0 + lane);
+  if (lane < n) {
+    place = token_row(p, (int)t0 + lane);
     if (place == kNoPlace) set_status(p.status, MSA_ERR_ARG);
   }
-  for (int c = 0; c < n; c += L::CHUNK) {
-    uint4* packed[STEPS];
-    uint4* pool[STEPS];
-    float* scale[STEPS];
-    int kind[STEPS];   // 0: nothing, 1: key or value, 2: index key; negative: its place is missing
+  const int half = p.H * L::LPR, units = 2 * half;  // vectors of the keys, and of the values too
+  int next_i = 0, next_u = 0;                       // token and first vector of the next batch
+  auto fetch = [&](B& b) {
+    const int64_t row = __shfl_sync(0xffffffffu, place, next_i), t = t0 + next_i;
+    const bool there = row >= 0;                     // a missing place reads as zeros
+    const bool skip = WRITE ? !there : row == kNoToken;
+    const int64_t cell = (there ? row : 0) * p.H;
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const int x = c + i * L::RPS + lane / L::LPR;
-      const int y = x + skip;
-      const int tok = (int)(((float)y + 0.5f) * p.inv_rows);  // exact: y < 32 rows
-      const int r = y - tok * p.rows;
-      int64_t row = __shfl_sync(0xffffffffu, place, tok);
-      kind[i] = x >= n || row == kNoToken ? 0 : r < 2 * p.H ? 1 : sub * L::VALUES < p.d_idx ? 2 : 0;
-      if (row < 0) {
-        kind[i] = -kind[i];
-        row = 0;
-      }
-      const int64_t t = t0 + tok;
-      const bool v = r >= p.H;
-      const int h = v ? r - p.H : r;
-      scale[i] = nullptr;
-      if (r == 2 * p.H) {
-        packed[i] = reinterpret_cast<uint4*>(p.xi + t * p.si + sub * L::VALUES);
-        pool[i] = reinterpret_cast<uint4*>(p.k_idx + row * p.d_idx + sub * L::VALUES);
+    for (int k = 0; k < L::STEPS; ++k) {
+      const int u = next_u + 32 * k + lane;
+      const bool v = u >= half;
+      const int f = v ? u - half : u, h = f / L::LPR, sub = f % L::LPR;
+      __nv_bfloat16* x = v ? p.xv + t * p.sv[0] + h * p.sv[1] : p.xk + t * p.sk[0] + h * p.sk[1];
+      uint4* packed = reinterpret_cast<uint4*>(x + sub * L::VALUES);
+      void* pool = static_cast<uint8_t*>(v ? p.v : p.k) + (cell * D + f * L::VALUES) * (F8 ? 1 : 2);
+      if (F8) b.scale[k] = (v ? p.v_scale : p.k_scale) + cell + h;
+#pragma unroll
+      for (int e = 0; e < W; ++e) b.w[k][e] = make_uint4(0, 0, 0, 0);
+      b.s[k] = 0.f;
+      b.dst[k] = nullptr;
+      if (u >= units || skip) continue;
+      b.dst[k] = WRITE ? static_cast<uint4*>(pool) : packed;
+      if (!there) continue;
+      if (WRITE) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) b.w[k][e] = __ldg(packed + e);
       } else {
-        const int64_t cell = row * p.H + h;
-        packed[i] = reinterpret_cast<uint4*>((v ? p.xv + t * p.sv[0] + h * p.sv[1]
-                                                : p.xk + t * p.sk[0] + h * p.sk[1]) + sub * L::VALUES);
-        pool[i] = reinterpret_cast<uint4*>(static_cast<uint8_t*>(v ? p.v : p.k) +
-                                           (cell * D + sub * L::VALUES) * (F8 ? 1 : 2));
-        if (F8) scale[i] = (v ? p.v_scale : p.k_scale) + cell;
+        b.w[k][0] = *static_cast<const uint4*>(pool);
+        if (F8) b.s[k] = *b.scale[k];
       }
     }
-    uint4 w[STEPS][W];
-    float s[STEPS];
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-#pragma unroll
-      for (int k = 0; k < W; ++k) w[i][k] = make_uint4(0, 0, 0, 0);  // what a missing place reads as
-      s[i] = 0.f;
-      if (kind[i] <= 0) continue;
-      if (!WRITE && F8 && kind[i] == 1) {
-        w[i][0] = *pool[i];
-        s[i] = *scale[i];
-      } else {
-#pragma unroll
-        for (int k = 0; k < W; ++k) w[i][k] = WRITE ? __ldg(packed[i] + k) : pool[i][k];
-      }
+    next_u += 32 * L::STEPS;
+    if (next_u >= units) {
+      next_u = 0;
+      ++next_i;
     }
+  };
+  auto store = [&](const B& b) {
+    if constexpr (F8 && WRITE) {
+      float amax[L::STEPS];
+      bool far = false;
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      if constexpr (F8 && WRITE) {
-        float amax = 0.f;
+      for (int k = 0; k < L::STEPS; ++k) {
+        amax[k] = 0.f;
 #pragma unroll
-        for (int k = 0; k < W; ++k) {
-          const uint32_t u[4] = {w[i][k].x, w[i][k].y, w[i][k].z, w[i][k].w};
+        for (int e = 0; e < W; ++e) {
+          const uint32_t x[4] = {b.w[k][e].x, b.w[k][e].y, b.w[k][e].z, b.w[k][e].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 x = widen(u[e]);
-            amax = fmax3(amax, fabsf(x.x), fabsf(x.y));
+          for (int c = 0; c < 4; ++c) {
+            const float2 y = widen(x[c]);
+            amax[k] = fmax3(amax[k], fabsf(y.x), fabsf(y.y));
           }
         }
+      }
+      // a row's lanes are neighbours, and 32 of them hold whole rows
 #pragma unroll
-        for (int o = L::LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if (kind[i] == 1) {
-          const float sc = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-          uint2 a, b;
-          if (amax > 1e-18f && amax < 1e18f) {
-            const float r = __frcp_rn(sc);
-            a = quantize8(w[i][0], sc, r);
-            b = quantize8(w[i][W - 1], sc, r);
-          } else {
-            a = divide8(w[i][0], sc);
-            b = divide8(w[i][W - 1], sc);
-          }
-          *pool[i] = make_uint4(a.x, a.y, b.x, b.y);
-          if (sub == 0) *scale[i] = sc;
-          continue;
+      for (int o = L::LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < L::STEPS; ++k) amax[k] = fmaxf(amax[k], __shfl_xor_sync(0xffffffffu, amax[k], o));
+#pragma unroll
+      for (int k = 0; k < L::STEPS; ++k) far = far || !(amax[k] == 0.f || (amax[k] > 1e-18f && amax[k] < 1e18f));
+      uint4 c[L::STEPS];
+      float sc[L::STEPS];
+      if (!__any_sync(0xffffffffu, far)) {
+#pragma unroll
+        for (int k = 0; k < L::STEPS; ++k) {
+          float r;
+          row_scale(amax[k], &sc[k], &r);
+          const uint2 lo = quantize8(b.w[k][0], sc[k], r), hi = quantize8(b.w[k][W - 1], sc[k], r);
+          c[k] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < L::STEPS; ++k) {
+          sc[k] = amax[k] > 0.f ? __fdiv_rn(amax[k], 448.0f) : 1.0f;
+          const uint2 lo = divide8(b.w[k][0], sc[k]), hi = divide8(b.w[k][W - 1], sc[k]);
+          c[k] = make_uint4(lo.x, lo.y, hi.x, hi.y);
         }
       }
-      if (WRITE ? kind[i] <= 0 : kind[i] == 0) continue;
-      if constexpr (F8 && !WRITE) {
-        if (kind[i] == 1 || kind[i] == -1) {
-          packed[i][0] = dequantize8(make_uint2(w[i][0].x, w[i][0].y), s[i]);
-          packed[i][W - 1] = dequantize8(make_uint2(w[i][0].z, w[i][0].w), s[i]);
-          continue;
-        }
-      }
 #pragma unroll
-      for (int k = 0; k < W; ++k) (WRITE ? pool[i] : packed[i])[k] = w[i][k];
+      for (int k = 0; k < L::STEPS; ++k) {
+        if (!b.dst[k]) continue;
+        *b.dst[k] = c[k];
+        if (lane % L::LPR == 0) *b.scale[k] = sc[k];
+      }
+    } else if constexpr (F8) {
+#pragma unroll
+      for (int k = 0; k < L::STEPS; ++k) {
+        const uint4 c = b.w[k][0];
+        const uint4 y0 = dequantize8(make_uint2(c.x, c.y), b.s[k]), y1 = dequantize8(make_uint2(c.z, c.w), b.s[k]);
+        // a lane's 32 bytes in two stores would write half sectors each: neighbours swap halves, so
+        // that a store writes the 32 bytes of every other lane
+        const bool odd = lane & 1;
+        const uint4 give = odd ? y0 : y1;
+        const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, 1), __shfl_xor_sync(0xffffffffu, give.y, 1),
+                                     __shfl_xor_sync(0xffffffffu, give.z, 1), __shfl_xor_sync(0xffffffffu, give.w, 1));
+        if (!b.dst[k]) continue;
+        uint4* even_dst = b.dst[k] - (odd ? 2 : 0);
+        even_dst[odd ? 1 : 0] = odd ? got : y0;
+        even_dst[odd ? 3 : 2] = odd ? y1 : got;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < L::STEPS; ++k)
+        if (b.dst[k]) *b.dst[k] = b.w[k][0];
     }
+  };
+  if (p.xi) {  // the index keys, d_idx / 8 lanes a token
+    const int lanes = p.d_idx >> 3, sub = lane % lanes;
+    for (int i0 = 0; i0 < n; i0 += 32 / lanes) {
+      const int i = i0 + lane / lanes;
+      const int64_t row = __shfl_sync(0xffffffffu, place, min(i, n - 1)), t = t0 + i;
+      if (i >= n || row == kNoToken || (WRITE && row < 0)) continue;
+      uint4* packed = reinterpret_cast<uint4*>(p.xi + t * p.si + sub * 8);
+      uint4* pool = reinterpret_cast<uint4*>(p.k_idx + (row < 0 ? 0 : row) * p.d_idx + sub * 8);
+      if (WRITE) *pool = __ldg(packed);
+      else *packed = row < 0 ? make_uint4(0, 0, 0, 0) : *pool;
+    }
+  }
+  B now, ahead;
+  fetch(now);
+  while (true) {  // warp-uniform: next_i is
+    const bool more = next_i < n;
+    if (more) fetch(ahead);
+    store(now);
+    if (!more) break;
+    const bool again = next_i < n;
+    if (again) fetch(now);
+    store(ahead);
+    if (!again) break;
   }
 }
 
 template <int D, bool F8, bool WRITE>
 cudaError_t launch_cache(CacheParams& p, int num_sms, cudaStream_t st) {
-  constexpr int CHUNK = Lanes<D, F8>::CHUNK;
-  const int64_t items = (int64_t)p.T * p.rows;
-  // chunks of a warp: as many as let all warps run together (32 or 48 a SM by their registers),
-  // while 32 lanes find all of a warp's tokens
-  const int64_t together = (int64_t)num_sms * (F8 && WRITE ? 32 : 48);
-  const int64_t want = (items + CHUNK * together - 1) / (CHUNK * together);
-  const int most = 30 * p.rows / CHUNK > 1 ? 30 * p.rows / CHUNK : 1;
-  p.steps = (int)(want < most ? want : most);
-  const int64_t warps = (items + CHUNK * p.steps - 1) / (CHUNK * p.steps);
+  // tokens of a warp: as many as let all warps run together
+  const int64_t together = (int64_t)num_sms * kCtasPerSm<F8, WRITE> * (kThreads / 32);
+  const int64_t want = (p.T + together - 1) / together;
+  p.per = (int)(want < 32 ? want : 32);
+  const int64_t warps = ((int64_t)p.T + p.per - 1) / p.per;
   const int64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cache_kernel<D, F8, WRITE><<<(unsigned)grid, kThreads, 0, st>>>(p);
   note_launch();
   return cudaGetLastError();
@@ -283,9 +333,6 @@ int run_cache(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   if (!strides) strides = dense;
   for (int i = 0; i < 5; ++i)
     if ((i < 4 || k_idx) && strides[i] % 8) return MSA_ERR_ARG;  // rows start on 16 bytes
-  p.rows = 2 * c->H_kv + (k_idx ? 1 : 0);
-  p.inv_rows = 1.f / (float)p.rows;
-  if ((int64_t)total_tokens * p.rows >= (int64_t)1 << 33) return MSA_ERR_UNSUPPORTED;
   Ctx cx;
   if ((rc = device_ctx(&cx))) return rc;
   p.pages = pages;

@@ -896,77 +896,154 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedDec
 }
 
 // pooled[b][g][c] = max over the 128 keys j of block c of q_idx[b, g] . k_idx[j], for every
-// block wholly before the new token's, as decode_pool_kernel computes it, over pages: one
-// warp per block, 8 NT groups per CTA, the index keys straight into mma.sync fragments (each
-// lane 16 contiguous bytes of a key row, the k slots permuted alike in the query fragments).
-// Bound by HBM: all 8 tiles of a block are in flight at once.
+// block wholly before the new token's.  The blocks of all sequences in order are dealt in turn to
+// kPoolWarps warps a SM, which take 8 NT groups each.  A warp has two stages of half a block in
+// shared memory: while it works on one half the next is on its way, and the page ids of the block
+// after it.  Bound by HBM, so what counts are the bytes in flight: 192 KB a SM (8 x 128K, 134 MB:
+// see kPoolWarps; with the halves in registers instead, 12 warps a SM, 26 us).
+constexpr int kPoolCtas = 152, kPoolWarps = 12;
+template <int DI>
+constexpr int kPoolStage = 64 * DI * 2;  // bytes
+
 template <int DI, int NT>
-__global__ void __launch_bounds__(256) paged_pool_kernel(const PagedDecode p) {
+__global__ void __launch_bounds__(kPoolWarps * 32, 1) paged_pool_kernel(const PagedDecode p) {
+  constexpr int NP = DI / 32;   // 32-wide d chunks: two k steps each
+  constexpr int CH = DI / 8;    // 16-byte chunks of a key row
+  constexpr int RPI = 32 / CH;  // rows of one copy instruction
+  extern __shared__ __align__(128) uint8_t smem[];
   griddep_launch_dependents();
-  const int b = blockIdx.y;
-  const int len = seq_len(p, b);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && blockIdx.z == 0)
-    for (int h = threadIdx.x; h < p.H; h += blockDim.x) p.arrive[(int64_t)b * p.H + h] = 0;
-  const int c = blockIdx.x * 8 + warp;
-  if (c >= (len - 1) / 128) return;  // also for an empty slot: (0 - 1) / 128 = 0
-  const int gq = lane >> 2, tq = lane & 3;
-  constexpr int NP = DI / 32;  // 32-wide d chunks: two k steps each
-  constexpr int U = 8;         // tiles in flight
-  // the pool row of each of the block's 8 tiles (a tile of 16 keys lies within one page)
-  int64_t row = lane < 8 ? pool_row(p.pages, b, c * 128 + lane * 16) : 0;
-  if (row < 0) set_status(p.status, MSA_ERR_ARG);
-  uint4 bq[NT][NP];
+  const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+  const int warp = blockIdx.x * kPoolWarps + (threadIdx.x >> 5);
+  uint8_t* stages = smem + (threadIdx.x >> 5) * 2 * kPoolStage<DI>;
+  if (blockIdx.y == 0)
+    for (int64_t x = blockIdx.x * blockDim.x + threadIdx.x; x < (int64_t)p.B * p.H; x += gridDim.x * blockDim.x)
+      p.arrive[x] = 0;
+  // blocks before each lane's sequences
+  const int per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
+  int mine = 0;
+  for (int i = b0; i < b1; ++i) mine += (max(1, seq_len(p, i)) - 1) / 128;
+  int scan = mine;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int grp = blockIdx.z * 8 * NT + nt * 8 + gq;
-    const uint4* qrow = reinterpret_cast<const uint4*>(p.q_idx + ((int64_t)b * p.H + grp) * DI);
-#pragma unroll
-    for (int j = 0; j < NP; ++j) bq[nt][j] = grp < p.H ? __ldg(&qrow[j * 4 + tq]) : make_uint4(0, 0, 0, 0);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += x;
   }
-  float mx[NT][2];
+  const int total = __shfl_sync(0xffffffffu, scan, 31);
+  int u = warp;
+  if (u >= total) return;
+  // the sequence that holds block u, and the number `base` of its first block
+  const int src = __ffs(__ballot_sync(0xffffffffu, u >= scan - mine && u < scan)) - 1;
+  int b = __shfl_sync(0xffffffffu, b0, src), base = __shfl_sync(0xffffffffu, scan - mine, src);
+  struct Place {
+    int b, c;  // sequence and block
+    int id;    // page id of tile lane % 8 of the block
+  };
+  const int tile_tok = (lane & 7) * 16;
+  auto find = [&](int x) {  // of block x, which never decreases
+    for (int n; n = (max(1, seq_len(p, b)) - 1) / 128, x >= base + n; base += n) ++b;
+    const int c = x - base;
+    return Place{b, c, __ldg(&p.pages.table[(int64_t)b * p.pages.table_stride + page_of(p.pages, c * 128 + tile_tok)])};
+  };
+  // half h of a block into stage h: 16-byte chunks, the 64-byte halves of odd rows swapped (d_idx 64)
+  const int r0 = lane / CH, ch = lane % CH;
+  auto load = [&](const Place& at, int h) {
+    uint8_t* st = stages + h * kPoolStage<DI>;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
+    for (int t = 0; t < 4; ++t) {
+      const int id = __shfl_sync(0xffffffffu, at.id, 4 * h + t);
+      const int tok = at.c * 128 + (4 * h + t) * 16;
+      const bool good = (unsigned)id < (unsigned)p.pages.num_pages;
+      if (!good) set_status(p.status, MSA_ERR_ARG);
+      const int64_t row = good ? (int64_t)id * p.pages.page_size + (tok - page_of(p.pages, tok) * p.pages.page_size) : 0;
+      const __nv_bfloat16* k = p.k_idx + (row + r0) * DI + ch * 8;
 #pragma unroll
-  for (int m0 = 0; m0 < 8; m0 += U) {
-    uint4 w0[U][NP], w1[U][NP];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = __shfl_sync(0xffffffffu, row, m0 + u);
-      const uint4* kb = reinterpret_cast<const uint4*>(p.k_idx + (r < 0 ? 0 : r) * DI);
-#pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        w0[u][j] = r < 0 ? make_uint4(0, 0, 0, 0) : __ldg(&kb[gq * (DI / 8) + j * 4 + tq]);
-        w1[u][j] = r < 0 ? make_uint4(0, 0, 0, 0) : __ldg(&kb[(gq + 8) * (DI / 8) + j * 4 + tq]);
+      for (int i = 0; i < 16 / RPI; ++i) {
+        const int r = r0 + i * RPI;
+        const int put = DI == 64 ? ch ^ ((r & 1) << 2) : ch;
+        if (good) cp_async_16(st + (t * 16 + r) * DI * 2 + put * 16, k + i * RPI * DI);
+        else cp_async_16(st + (t * 16 + r) * DI * 2 + put * 16, p.k_idx, false);  // zero rows
       }
     }
+    cp_async_commit();
+  };
+  uint4 bq[NT][NP];
+  auto load_q = [&](int b) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int nt = 0; nt < NT; ++nt) {
+      const int grp = blockIdx.y * 8 * NT + nt * 8 + gq;
+      const uint4* qrow = reinterpret_cast<const uint4*>(p.q_idx + ((int64_t)b * p.H + grp) * DI);
+#pragma unroll
+      for (int j = 0; j < NP; ++j) bq[nt][j] = grp < p.H ? __ldg(&qrow[j * 4 + tq]) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  float mx[NT][2];
+  // mma.sync A fragments from 16-byte chunks of rows gq and gq + 8, the k slots permuted alike in
+  // the query fragments
+  auto score = [&](int h) {
+    const uint8_t* st = stages + h * kPoolStage<DI>;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      uint4 lo[NP], hi[NP];
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const int get = DI == 64 ? (j * 4 + tq) ^ ((gq & 1) << 2) : tq;
+        lo[j] = *reinterpret_cast<const uint4*>(st + (t * 16 + gq) * DI * 2 + get * 16);
+        hi[j] = *reinterpret_cast<const uint4*>(st + (t * 16 + gq + 8) * DI * 2 + get * 16);
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-          const uint32_t a0[4] = {w0[u][j].x, w1[u][j].x, w0[u][j].y, w1[u][j].y};
-          const uint32_t a1[4] = {w0[u][j].z, w1[u][j].z, w0[u][j].w, w1[u][j].w};
+          const uint32_t a0[4] = {lo[j].x, hi[j].x, lo[j].y, hi[j].y};
+          const uint32_t a1[4] = {lo[j].z, hi[j].z, lo[j].w, hi[j].w};
           mma_bf16_16816(acc, a0, bq[nt][j].x, bq[nt][j].y);
           mma_bf16_16816(acc, a1, bq[nt][j].z, bq[nt][j].w);
         }
         mx[nt][0] = fmax3(mx[nt][0], acc[0], acc[2]);
         mx[nt][1] = fmax3(mx[nt][1], acc[1], acc[3]);
       }
-  }
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float m = mx[nt][e];
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-      const int grp = blockIdx.z * 8 * NT + nt * 8 + 2 * tq + e;
-      if (gq == 0 && grp < p.H) p.pooled[((int64_t)b * p.H + grp) * p.row + c] = m;
     }
+  };
+  constexpr int STEP = kPoolCtas * kPoolWarps;
+  Place now = find(u);
+  load(now, 0);
+  load(now, 1);
+  load_q(now.b);
+  Place next = u + STEP < total ? find(u + STEP) : now;
+  while (true) {
+    const bool more = u + STEP < total;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      cp_async_wait<1>();
+      __syncwarp();  // half h has landed for all lanes
+      score(h);
+      __syncwarp();  // and all are done with its stage
+      if (more) load(next, h);
+      else cp_async_commit();
+    }
+    Place later = next;
+    if (u + 2 * STEP < total) later = find(u + 2 * STEP);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float m = mx[nt][e];
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        const int grp = blockIdx.y * 8 * NT + nt * 8 + 2 * tq + e;
+        if (gq == 0 && grp < p.H) p.pooled[((int64_t)now.b * p.H + grp) * p.row + now.c] = m;
+      }
+    if (!more) break;
+    if (next.b != now.b) load_q(next.b);
+    now = next;
+    next = later;
+    u += STEP;
+  }
+  cp_async_wait<0>();
 }
 
 // One CTA per (group, sequence): the new token's blocks, for caches of more blocks than the
@@ -1008,6 +1085,25 @@ cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, bool after, c
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// The dynamic shared memory of a kernel belongs to the function in a context: set again where that
+// changes.  `done` is the kernel's own.
+template <typename Kern>
+cudaError_t allow_smem(Kern kern, int bytes, std::atomic<void*>& done) {
+  void* ctx = current_context();
+  if (ctx && done.load(std::memory_order_relaxed) == ctx) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.store(ctx, std::memory_order_relaxed);
+  return e;
+}
+
+template <int DI, int NT>
+cudaError_t launch_pool(dim3 grid, const PagedDecode& p, cudaStream_t stream) {
+  constexpr int smem = kPoolWarps * 2 * kPoolStage<DI>;
+  static std::atomic<void*> done{nullptr};
+  const cudaError_t e = allow_smem(paged_pool_kernel<DI, NT>, smem, done);
+  return e != cudaSuccess ? e : launch(paged_pool_kernel<DI, NT>, grid, kPoolWarps * 32, smem, false, stream, p);
+}
+
 template <int D, bool F8, bool WIDE, bool SPARSE>
 cudaError_t launch_attn(const PagedDecode& p, cudaStream_t stream) {
   constexpr int smem = kWarps * Stage<D, F8, WIDE>::COUNT * Stage<D, F8, WIDE>::BYTES;
@@ -1015,14 +1111,9 @@ cudaError_t launch_attn(const PagedDecode& p, cudaStream_t stream) {
   static_assert(Stage<D, F8, WIDE>::PER_SM == (WIDE && D == 128 ? 2 : 3), "ctas");
   static_assert(smem >= 32 * 128 / Stage<D, F8, WIDE>::UNIT * 16 * 4, "weights of a pair's parts");
   auto* kern = paged_attn_kernel<D, F8, WIDE, SPARSE>;
-  // the attribute belongs to the function in a context: set again where that changes
   static std::atomic<void*> done{nullptr};
-  void* ctx = current_context();
-  if (!ctx || done.load(std::memory_order_relaxed) != ctx) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    done.store(ctx, std::memory_order_relaxed);
-  }
+  const cudaError_t e = allow_smem(kern, smem, done);
+  if (e != cudaSuccess) return e;
   return launch(kern, dim3(p.ctas), kThreads, smem, SPARSE, stream, p);
 }
 
@@ -1138,14 +1229,10 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   cudaError_t e = cudaSuccess;
   if (topk > 0) {
     const int nt = p.H > 8 ? 2 : 1;
-    const dim3 grid((unsigned)((nb + 7) / 8), (unsigned)p.B, (unsigned)((p.H + 8 * nt - 1) / (8 * nt)));
-    if (grid.x > 0) {
-      if (c->d_idx == 64)
-        e = nt == 1 ? launch(paged_pool_kernel<64, 1>, grid, 256, 0, false, stream, p)
-                    : launch(paged_pool_kernel<64, 2>, grid, 256, 0, false, stream, p);
-      else
-        e = nt == 1 ? launch(paged_pool_kernel<32, 1>, grid, 256, 0, false, stream, p)
-                    : launch(paged_pool_kernel<32, 2>, grid, 256, 0, false, stream, p);
+    const dim3 grid(kPoolCtas, (unsigned)((p.H + 8 * nt - 1) / (8 * nt)));
+    if (nb > 0) {
+      if (c->d_idx == 64) e = nt == 1 ? launch_pool<64, 1>(grid, p, stream) : launch_pool<64, 2>(grid, p, stream);
+      else e = nt == 1 ? launch_pool<32, 1>(grid, p, stream) : launch_pool<32, 2>(grid, p, stream);
       if (e != cudaSuccess) return MSA_ERR_CUDA;
     }
     p.select = nb <= kSelectPer * kThreads;

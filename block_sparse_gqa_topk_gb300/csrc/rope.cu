@@ -23,12 +23,11 @@ constexpr int kThreads = 256;
 constexpr int kMaxRopeTensors = 4;
 constexpr int kMaxTokens = 8;    // tokens a CTA computes the angles of
 constexpr int kMaxHalf = 256;    // rot_dim / 2
-constexpr int kHeads = 2;        // heads of an item
 
 struct RopeTensor {
   const void* x;
   void* y;
-  int H, units, parts, rot_parts, d;  // heads, runs of kHeads of them, items of a run, rotated ones
+  int H, parts, rot_parts, d;  // heads, items of a head, of them rotated
   int last;                    // items of a token in this tensor and those before it
   uint32_t div_parts, div_H;
   int64_t xs[3], ys[3];  // strides of batch, token, head
@@ -68,11 +67,14 @@ __device__ __forceinline__ int small_div(int x, uint32_t m) { return m ? (int)__
 uint32_t magic(int q) { return q == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + q - 1) / q); }
 
 // One CTA serves tpb tokens: their sines and cosines, and where their rows start, go to
-// shared memory once; then the items (V pairs, or 2 V values to copy, of kHeads neighbouring
-// heads, which share the pairs' sines and cosines) of all the tensors together are spread over
-// the threads.  Bound by HBM: every value is read and written once.
+// shared memory once; then the items (V pairs of one head, or 2 V values to copy) of all the
+// tensors together are spread over the threads.  Bound by HBM: every value is read and written
+// once.  One item a thread at a time and 6 CTAs a SM keep the most in flight: a training pass of
+// 128K tokens (q 32 x 128, k 8 x 128, q_idx 8 x 64, k_idx, 64 rotated, 5.97 GB) takes 867 us, 6.9
+// TB/s; two heads a thread for one load of the angles 971 us, four 1360 us (registers), 8 CTAs
+// (spills) 989 us.
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float2 s_cs[kMaxTokens * kMaxHalf];
   __shared__ longlong2 s_off[kMaxRopeTensors][kMaxTokens];  // of x and y
   const int64_t t0 = (int64_t)blockIdx.x * p.tpb;
@@ -104,43 +106,30 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
     const RopeTensor& a = p.t[ti];
     if (ti > 0) x -= nt * p.t[ti - 1].last;
     const int row = small_div(x, a.div_parts), part = x - row * a.parts;
-    const int tok = small_div(row, a.div_H), h0 = (row - tok * a.units) * kHeads;
+    const int tok = small_div(row, a.div_H), h = row - tok * a.H;
     const bool turn = part < a.rot_parts;
     // first vector of the item in its head, and the distance of the second one (0: none)
     const int at = turn ? (INTER ? part * 2 * V : part * V) : 2 * p.half + (part - a.rot_parts) * 2 * V;
     const int step = turn ? (INTER ? V : p.half) : at + V < a.d ? V : 0;
     const longlong2 off = s_off[ti][tok];
-    const T* src = static_cast<const T*>(a.x) + (off.x + h0 * a.xs[2] + at);
-    T* dst = static_cast<T*>(a.y) + (off.y + h0 * a.ys[2] + at);
-    Pack<T, V> lo[kHeads], hi[kHeads];
-#pragma unroll
-    for (int u = 0; u < kHeads; ++u) {
-      if (h0 + u >= a.H) break;
-      lo[u] = *reinterpret_cast<const Pack<T, V>*>(src + u * a.xs[2]);
-      if (step) hi[u] = *reinterpret_cast<const Pack<T, V>*>(src + u * a.xs[2] + step);
-    }
+    const T* src = static_cast<const T*>(a.x) + (off.x + h * a.xs[2] + at);
+    T* dst = static_cast<T*>(a.y) + (off.y + h * a.ys[2] + at);
+    Pack<T, V> lo = *reinterpret_cast<const Pack<T, V>*>(src), hi;
+    if (step) hi = *reinterpret_cast<const Pack<T, V>*>(src + step);
     if (turn) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float2 w = s_cs[tok * p.half + part * V + e];
-#pragma unroll
-        for (int u = 0; u < kHeads; ++u) {
-          // the pair's two values: the vectors side by side, or neighbours in them
-          T* p1 = INTER ? (2 * e < V ? &lo[u].v[(2 * e) % V] : &hi[u].v[(2 * e) % V]) : &lo[u].v[e];
-          T* p2 = INTER ? (2 * e + 1 < V ? &lo[u].v[(2 * e + 1) % V] : &hi[u].v[(2 * e + 1) % V])
-                        : &hi[u].v[e];
-          const float x1 = to_f(*p1), x2 = to_f(*p2);
-          *p1 = from_f<T>(x1 * w.x - x2 * w.y);
-          *p2 = from_f<T>(x2 * w.x + x1 * w.y);
-        }
+        // the pair's two values: the vectors side by side, or neighbours in them
+        T* p1 = INTER ? (2 * e < V ? &lo.v[(2 * e) % V] : &hi.v[(2 * e) % V]) : &lo.v[e];
+        T* p2 = INTER ? (2 * e + 1 < V ? &lo.v[(2 * e + 1) % V] : &hi.v[(2 * e + 1) % V]) : &hi.v[e];
+        const float x1 = to_f(*p1), x2 = to_f(*p2);
+        *p1 = from_f<T>(x1 * w.x - x2 * w.y);
+        *p2 = from_f<T>(x2 * w.x + x1 * w.y);
       }
     }
-#pragma unroll
-    for (int u = 0; u < kHeads; ++u) {
-      if (h0 + u >= a.H) break;
-      *reinterpret_cast<Pack<T, V>*>(dst + u * a.ys[2]) = lo[u];
-      if (step) *reinterpret_cast<Pack<T, V>*>(dst + u * a.ys[2] + step) = hi[u];
-    }
+    *reinterpret_cast<Pack<T, V>*>(dst) = lo;
+    if (step) *reinterpret_cast<Pack<T, V>*>(dst + step) = hi;
   }
 }
 
@@ -219,13 +208,12 @@ extern "C" int msa_rope(const msa_rope_t* r, const uint64_t* turns, const void* 
     const int tail = t.x == t.y ? 0 : t.d - r->rot_dim;  // in place: already there
     a.parts = a.rot_parts + (tail + 2 * w - 1) / (2 * w);
     a.div_parts = magic(a.parts);
-    a.units = (a.H + kHeads - 1) / kHeads;
-    a.div_H = magic(a.units);
+    a.div_H = magic(a.H);
     for (int k = 0; k < 3; ++k) {
       a.xs[k] = t.x_stride[k];
       a.ys[k] = t.y_stride[k];
     }
-    all += a.units * a.parts;
+    all += a.H * a.parts;
     a.last = all;
   }
   // tokens a CTA: up to kMaxTokens while the grid still fills the GPU and an item index

@@ -11,7 +11,6 @@ block_idx [B,H_kv,N,topk] int32.
 from __future__ import annotations
 
 import dataclasses
-import fractions
 import math
 
 import torch
@@ -497,7 +496,7 @@ def msa_fwd_fp8(q8, q_scale, k8, k_scale, v8t, v_scale, block_idx, *, scale=None
 # ---------------------------------------------------------------------------
 _ROPE_DTYPES = {torch.bfloat16: _lib.MSA_DTYPE_BF16, torch.float16: _lib.MSA_DTYPE_F16,
                 torch.float32: _lib.MSA_DTYPE_F32}
-_TWO_PI = fractions.Fraction(2 * 31415926535897932384626433832795028841971693993751, 10 ** 49)
+_TWO_PI_E49 = 2 * 31415926535897932384626433832795028841971693993751  # 2 pi 10^49
 
 
 _Tensor, _BF16, _I32 = torch.Tensor, torch.bfloat16, torch.int32
@@ -593,9 +592,13 @@ def new_rope(rot_dim: int, *, base: float = 10000.0, interleaved: bool = False, 
     m = float(m if mscale is None else mscale)
     if not math.isfinite(m):
         raise ValueError("mscale must be finite")
-    one = 1 << 64
-    turns = [int(round(fractions.Fraction(x) / _TWO_PI * one)) % one for x in freq]
-    turns = torch.tensor([t - one if t >= one // 2 else t for t in turns], dtype=torch.int64)
+    turns = []
+    for x in freq:  # x / (2 pi) in units of 2^-64, rounded to the nearest, modulo 1
+        num, den = x.as_integer_ratio()
+        den *= _TWO_PI_E49
+        t = ((num * 10 ** 49 << 65) + den) // (2 * den) % (1 << 64)
+        turns.append(t - (1 << 64) if t >> 63 else t)
+    turns = torch.tensor(turns, dtype=torch.int64)
     return Rope(turns.to(device), rot_dim, bool(interleaved), m)
 
 

@@ -1201,11 +1201,13 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   uint8_t* w = static_cast<uint8_t*>(workspace);
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_idx = static_cast<const __nv_bfloat16*>(q_idx);
-  p.k = c->k;
-  p.v = c->v;
-  p.k_scale = c->k_scale;
-  p.v_scale = c->v_scale;
-  p.k_idx = static_cast<const __nv_bfloat16*>(c->k_idx);
+  // without pages every id is bad and every copy has no bytes: any address does for those
+  const bool pages_exist = c->num_pages > 0;
+  p.k = pages_exist ? c->k : workspace;
+  p.v = pages_exist ? c->v : workspace;
+  p.k_scale = pages_exist ? c->k_scale : static_cast<const float*>(workspace);
+  p.v_scale = pages_exist ? c->v_scale : static_cast<const float*>(workspace);
+  p.k_idx = static_cast<const __nv_bfloat16*>(pages_exist ? c->k_idx : workspace);
   p.lens = lens;
   p.block_idx = topk > 0 ? block_idx : nullptr;
   p.pooled = reinterpret_cast<float*>(w + lay.pooled);

@@ -336,6 +336,14 @@ def test_places_that_do_not_exist(fp8):
                            torch.empty(0, 16, 2, 64, dtype=torch.bfloat16, device="cuda"))
     o, lse = ops.msa_decode_paged_dense(q, empty, dev(np.zeros((3, 0))), dev([0, 0, 0]))
     assert not o.any() and (lse == -math.inf).all() and ops.device_status() == 0
+    # a pool without pages: whatever the table says is outside it, and reads as zero rows
+    empty = ops.new_paged_cache(0, 2, page_size=16, d=64, d_idx=32, fp8=fp8)
+    t = dev(np.zeros((3, 20)))
+    for call in (lambda: ops.msa_decode_paged_dense(q, empty, t, batch.lens_t),
+                 lambda: ops.msa_decode_paged(q, qi, empty, t, batch.lens_t, 4)[1:]):
+        o, lse = call()
+        assert ops.device_status() == _lib.MSA_ERR_ARG and not o.any()
+        assert (lse - torch.log(batch.lens_t.float())[:, None]).abs().max() <= 1e-5
 
 
 def test_offsets_past_32_bits():

@@ -187,6 +187,14 @@ def test_gradients():
         diff = float(((y1 - y0).double() * dq.double()).sum())
         # each of the two y's is off by at most 1e-6 (|x1| + |x2|) and half a step: < 1e-5 a value
         assert abs(diff - float(gq[b, n, h, e])) <= 2 * 2 * 1e-5 * float(dq[b, n, h].abs().max())
+    # implied positions, and an input that needs no gradient
+    yq, yk = ops.rope((q, k.detach()), r)
+    (g,) = torch.autograd.grad(yq, q, dq)
+    want, size = reference(f64(dq), np.tile(np.arange(N, dtype=np.float64), (B, 1)), freq, m, rot, True, back=True)
+    check(g, want, size, torch.float32)
+    assert not yk.requires_grad or torch.autograd.grad(ops.rope((q, k.detach()), r)[1].sum(), q,
+                                                       allow_unused=True) == (None,)
+    yq, yk = ops.rope((q, k), r, pos)
     # only one output used; the gradient of a sum arrives as a broadcast scalar
     (only,) = torch.autograd.grad(yq.sum(), q, retain_graph=True)
     want, size = reference(np.ones(q.shape), at, freq, m, rot, True, back=True)

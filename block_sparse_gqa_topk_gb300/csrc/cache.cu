@@ -127,9 +127,11 @@ __device__ __forceinline__ uint4 dequantize8(uint2 c, float s) {
 }
 
 // A token's keys, and its values, are one run of H D values in the pool; a lane moves 8 values
-// of it at a time (16 of E4M3: half the addresses and scales), a warp one token after another.  Its lanes find the places of
-// all its tokens (at most 32) together, so the chain of lookups (sequence, length, page) is paid
-// once, and while it works on STEPS vectors a lane, the next ones are on their way.
+// of it at a time (16 of E4M3: half the addresses and scales), a warp one token after another.
+// Its lanes find the places of all its tokens (at most 32) together, so the chain of lookups
+// (sequence, length, page) is paid once, and while it works on STEPS vectors a lane, the next ones
+// are on their way.  32K tokens of 8 groups, d 128, with index keys: bf16 41 us each way (6.8
+// TB/s), E4M3 write 40 us (bound by instructions: the rounding rule) and read 35 us (6 TB/s).
 template <int D, bool F8, bool WRITE>
 struct Lanes {
   static constexpr int VALUES = F8 ? 16 : 8;  // of a lane's vector
@@ -148,6 +150,8 @@ struct Batch {
   float* scale[L::STEPS];
 };
 
+// As many as the registers of a batch allow; writing E4M3 with a vector a lane on the way and 4
+// CTAs is faster than with two vectors and 3 (32K tokens, 8 groups, d 128).
 template <bool F8, bool WRITE>
 constexpr int kCtasPerSm = F8 && WRITE ? 4 : F8 ? 3 : 4;
 

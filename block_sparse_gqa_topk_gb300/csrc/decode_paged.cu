@@ -51,6 +51,7 @@ struct PagedDecode {
   float* lse;
   int B, H, G, topk;
   int row;         // blocks of the table's length, rounded up to 4
+  int cluster;     // CTAs of a (sequence, group) in the small form; 0: the other one
   int ctas;        // of the attention kernel
   int select;      // it selects the blocks itself
   int wh;          // heads (groups) that a CTA may serve side by side
@@ -586,40 +587,193 @@ __device__ __forceinline__ void join_parts(const PagedDecode& p, const Parts& pa
   }
 }
 
+// A warp's part of a span: units u0 .. u0 + n - 1 (n > 0) of group g of sequence b, in unit x the KEYS
+// tokens from x unit + my_token on; or (SPARSE) in unit x of the selected blocks, of which lane i
+// holds the i-th in blk.
+template <int D, bool F8, bool WIDE, bool SPARSE>
+__device__ __forceinline__ void attend(const PagedDecode& p, WarpState<D, F8, WIDE>& ws, uint8_t* ring, int b, int g,
+                                       int len, int u0, int n, int blk, int my_token, int unit, bool side_by_side) {
+  using St = Stage<D, F8, WIDE>;
+  const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+  const int64_t head0 = ((int64_t)b * p.H + g) * p.G;
+  constexpr int CH = St::ROW / 16;  // 16-byte chunks of a row
+  constexpr int RPI = 32 / CH;      // rows of one copy instruction
+  const int r0 = lane / CH, ch = lane % CH;
+  const int64_t row_step = (int64_t)p.H * St::ROW;
+  const int64_t lane_off = r0 * row_step + ch * 16;
+  // Page ids of the next 32 half stages sit in the lanes of a register (and those of the 32 after
+  // them are on their way), so that no lookup stands in front of a copy.
+  // first token of this warp in unit u0 + i
+  auto first_token = [&](int i) {
+    const int x = u0 + i;
+    if (!SPARSE) return x * unit + my_token;
+    return __shfl_sync(0xffffffffu, blk, (x / St::PER) & 31) * 128 + (x % St::PER) * St::UNIT + my_token;
+  };
+  const int32_t* table = p.pages.table + (int64_t)b * p.pages.table_stride;
+  constexpr int AHEAD = 32 / St::HALVES;  // units whose page ids a register holds
+  auto page_ids = [&](int i) {  // of the halves of units i .. i + AHEAD - 1, one a lane
+    const int x = u0 + i + lane / St::HALVES;
+    int tok = (lane % St::HALVES) * 16 + my_token;
+    if (!SPARSE) tok += x * unit;
+    else tok += __shfl_sync(0xffffffffu, blk, (x / St::PER) & 31) * 128 + (x % St::PER) * St::UNIT;
+    return i + lane / St::HALVES < n && tok < len ? __ldg(&table[page_of(p.pages, tok)]) : -1;
+  };
+  int ids = page_ids(0), ids_next = page_ids(AHEAD);
+  auto load = [&](int i) {
+    if (i < n) {
+      if (i > 0 && i % AHEAD == 0) {
+        ids = ids_next;
+        ids_next = page_ids(i + AHEAD);
+      }
+      uint8_t* st = ring + (i % St::COUNT) * St::BYTES;
+      const int pos0 = first_token(i);
+#pragma unroll
+      for (int hs = 0; hs < St::HALVES; ++hs) {
+        const int pos = pos0 + 16 * hs;
+        const int id = __shfl_sync(0xffffffffu, ids, (i % AHEAD) * St::HALVES + hs);
+        const int have = len - pos;  // tokens of the sequence from here on
+        if (hs == 0 && have <= 0) break;  // step() will not look at this stage
+        const bool good = (unsigned)id < (unsigned)p.pages.num_pages;
+        if (!good && have > 0) set_status(p.status, MSA_ERR_ARG);
+        const int64_t row0 =
+            good ? (int64_t)id * p.pages.page_size + (pos - page_of(p.pages, pos) * p.pages.page_size) : 0;
+        const int64_t at = (row0 * p.H + g) * St::ROW + lane_off;
+        const uint8_t* kp = static_cast<const uint8_t*>(p.k) + at;
+        const uint8_t* vp = static_cast<const uint8_t*>(p.v) + at;
+        const bool full = good && have >= 16;
+#pragma unroll
+        for (int j = 0; j < 16 / RPI; ++j) {
+          const int r = r0 + j * RPI;
+          uint8_t* kd = st + St::key_at(16 * hs + r, ch);
+          uint8_t* vd = st + St::value_at(16 * hs + r, ch);
+          if (full) {
+            cp_async_16(kd, kp + j * RPI * row_step);
+            cp_async_16(vd, vp + j * RPI * row_step);
+          } else {  // else zeros: no stale NaN meets a weight of 0
+            const bool ok = good && r < have;
+            const int64_t off = ok ? j * RPI * row_step : -lane_off;
+            cp_async_16(kd, kp + off, ok);
+            cp_async_16(vd, vp + off, ok);
+          }
+        }
+        if constexpr (F8) {  // lanes 0..15 the keys' scales, the others the values'
+          const int r = lane & 15;
+          const bool ok = good && r < have;
+          const float* src = (lane < 16 ? p.k_scale : p.v_scale) + (ok ? (row0 + r) * p.H + g : 0);
+          cp_async_4(st + St::S0 + ((lane < 16 ? 0 : St::KEYS) + 16 * hs + r) * 4, src, ok);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < St::COUNT - 1; ++i) load(i);
+  ws.load_q(p, head0, gq, tq);
+  for (int i = 0; i < n; ++i) {
+    cp_async_wait<St::COUNT - 2>();
+    // unit i has landed for all lanes, and all are done with unit i - 1; heads side by side
+    // stay in step, so that what they load together lies together in memory
+    if (side_by_side) __syncthreads(); else __syncwarp();
+    load(i + St::COUNT - 1);
+    const int have = len - first_token(i);
+    if (have > 0) ws.step(ring + (i % St::COUNT) * St::BYTES, have, lane);
+  }
+  cp_async_wait<0>();
+}
+
+// What the warps of a CTA leave of a span: running sums in their own stages ([8 R][D + 4] floats),
+// the rest here.
+struct WarpSums {
+  float m[kWarps][16], mv[kWarps][16], l[kWarps][16];
+};
+template <int D, bool F8, bool WIDE>
+__device__ __forceinline__ void leave_sums(const WarpState<D, F8, WIDE>& ws, uint8_t* ring, WarpSums& s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, tq = lane & 3;
+  __syncwarp();  // the warp is done with its stages
+  float* my_o = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+    for (int r = 0; r < ws.R; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        my_o[(8 * r + 2 * tq + (e & 1)) * (D + 4) + ws.column(i, e, gq)] = ws.o[i][r][e];
+#pragma unroll
+  for (int r = 0; r < ws.R; ++r) {
+    float l = ws.l[r];
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (tq == 0) {
+      s.m[warp][gq + 8 * r] = ws.m[r];
+      s.mv[warp][gq + 8 * r] = F8 ? ws.mv[r] : ws.m[r];
+      s.l[warp][gq + 8 * r] = l;
+    }
+  }
+}
+
+// Columns c .. c + 3 of head h, joined over the warps w0, w0 + wh, ... (subs of them), not yet
+// divided by l; the maximum (in bits) and l.
+template <int D, bool F8, bool WIDE>
+__device__ __forceinline__ float4 join_warps(const uint8_t* smem, const WarpSums& s, int h, int c, int w0, int wh,
+                                             int subs, float* top_out, float* l_out) {
+  using St = Stage<D, F8, WIDE>;
+  float top = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k)
+    if (k < subs) top = fmaxf(top, s.m[w0 + k * wh][h]);
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k) {
+    if (k >= subs) break;
+    const int w = w0 + k * wh;
+    l += s.l[w][h] * weight(s.m[w][h], top);
+    const float f = weight(s.mv[w][h], top);
+    const float4 y = *reinterpret_cast<const float4*>(smem + w * St::COUNT * St::BYTES + (h * (D + 4) + c) * 4);
+    acc.x = fmaf(f, y.x, acc.x);
+    acc.y = fmaf(f, y.y, acc.y);
+    acc.z = fmaf(f, y.z, acc.z);
+    acc.w = fmaf(f, y.w, acc.w);
+  }
+  *top_out = top;
+  *l_out = l;
+  return acc;
+}
+
+// An empty slot: o = 0, lse = -inf and no blocks for `heads` query heads from head0 on.
+template <int D>
+__device__ __forceinline__ void write_empty(const PagedDecode& p, int64_t head0, int64_t heads) {
+  for (int64_t x = threadIdx.x; x < heads * D; x += kThreads) p.o[head0 * D + x] = __float2bfloat16(0.f);
+  for (int64_t x = threadIdx.x; x < heads; x += kThreads) p.lse[head0 + x] = -INFINITY;
+}
+
 // One CTA works through its run of units: span after span of one (sequence, wh groups).  Its
 // warps take the groups side by side and share each one's tokens, every warp with its own
 // stages in shared memory and its own running softmax; they join when a span ends.  A whole
 // (sequence, groups) is written out, a part of one goes to the CTA's slot 0 (its first span) or 1.
+// Bound by HBM: 8 whole caches of 128K tokens take 590 us in bf16 (4.3 GB, 7.3 TB/s) and 334 us in
+// E4M3 (2.2 GB, 6.6 TB/s), 16 blocks of each 19 us after the scores.
 template <int D, bool F8, bool WIDE, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, Stage<D, F8, WIDE>::PER_SM) paged_attn_kernel(const PagedDecode p) {
   using St = Stage<D, F8, WIDE>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[kWarps][16], s_mv[kWarps][16], s_l[kWarps][16];
+  __shared__ WarpSums s_sums;
   __shared__ int32_t s_blocks[kMaxSelect];
   __shared__ int s_last;
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int gq = lane >> 2, tq = lane & 3;
   const Work work = find_run<SPARSE>(p);
   const int wh = SPARSE ? 1 : work.wh, HG = SPARSE ? p.H : work.HG;
   int b = work.b, base = work.base;
   griddep_wait();  // the pooled scores or the selected blocks
   for (int e = blockIdx.x; e < p.B; e += p.ctas) {  // empty slots: o = 0, lse = -inf, no blocks
     if (seq_len(p, e) > 0) continue;
-    const int64_t heads = (int64_t)p.H * p.G;
-    for (int64_t x = tid; x < heads * D; x += kThreads) p.o[e * heads * D + x] = __float2bfloat16(0.f);
-    for (int64_t x = tid; x < heads; x += kThreads) p.lse[e * heads + x] = -INFINITY;
+    write_empty<D>(p, (int64_t)e * p.H * p.G, (int64_t)p.H * p.G);
     if (SPARSE && p.select)
       for (int64_t x = tid; x < (int64_t)p.H * p.topk; x += kThreads) p.block_idx[(int64_t)e * p.H * p.topk + x] = -1;
   }
   int u = work.cut.start(blockIdx.x);
   const int u_end = work.cut.start(blockIdx.x + 1);
   uint8_t* ring = smem + warp * St::COUNT * St::BYTES;
-  constexpr int CH = St::ROW / 16;  // 16-byte chunks of a row
-  constexpr int RPI = 32 / CH;      // rows of one copy instruction
-  const int r0 = lane / CH, ch = lane % CH;
-  const int64_t row_step = (int64_t)p.H * St::ROW;
-  const int64_t lane_off = r0 * row_step + ch * 16;
   // warp w works for head hg wh + w % wh, on the (w / wh)-th run of KEYS tokens of each unit
   const int my_head = warp & (wh - 1), subs = kWarps / wh;
   const int my_token = (wh == 1 ? warp : wh == 2 ? warp >> 1 : 0) * St::KEYS, unit = St::KEYS * subs;
@@ -641,11 +795,7 @@ __global__ void __launch_bounds__(kThreads, Stage<D, F8, WIDE>::PER_SM) paged_at
     u = stop;
     if (n == 0) continue;  // only the pair's overhead fell into this run
     const int g = hg * wh + my_head;
-    const int64_t head0 = ((int64_t)b * p.H + g) * p.G;
-    // Page ids of the next 32 units sit in the lanes of a register (and those of the 32 after
-    // them are on their way), so that no lookup stands in front of a copy.  Selected blocks,
-    // at most 32, sit in another.
-    int blk = 0;
+    int blk = 0;  // lane i: the i-th selected block
     if constexpr (SPARSE) {
       int32_t* blocks = p.block_idx + ((int64_t)b * p.H + g) * p.topk;
       if (p.select) {
@@ -658,103 +808,8 @@ __global__ void __launch_bounds__(kThreads, Stage<D, F8, WIDE>::PER_SM) paged_at
         blk = __ldg(&blocks[lane]);
       }
     }
-    // first token of this warp in unit u0 + i
-    auto first_token = [&](int i) {
-      const int x = u0 + i;
-      if (!SPARSE) return x * unit + my_token;
-      return __shfl_sync(0xffffffffu, blk, (x / St::PER) & 31) * 128 + (x % St::PER) * St::UNIT + my_token;
-    };
-    const int32_t* table = p.pages.table + (int64_t)b * p.pages.table_stride;
-    constexpr int AHEAD = 32 / St::HALVES;  // units whose page ids a register holds
-    auto page_ids = [&](int i) {  // of the halves of units i .. i + AHEAD - 1, one a lane
-      const int x = u0 + i + lane / St::HALVES;
-      int tok = (lane % St::HALVES) * 16 + my_token;
-      if (!SPARSE) tok += x * unit;
-      else tok += __shfl_sync(0xffffffffu, blk, (x / St::PER) & 31) * 128 + (x % St::PER) * St::UNIT;
-      return i + lane / St::HALVES < n && tok < len ? __ldg(&table[page_of(p.pages, tok)]) : -1;
-    };
-    int ids = page_ids(0), ids_next = page_ids(AHEAD);
-    auto load = [&](int i) {
-      if (i < n) {
-        if (i > 0 && i % AHEAD == 0) {
-          ids = ids_next;
-          ids_next = page_ids(i + AHEAD);
-        }
-        uint8_t* st = ring + (i % St::COUNT) * St::BYTES;
-        const int pos0 = first_token(i);
-#pragma unroll
-        for (int hs = 0; hs < St::HALVES; ++hs) {
-          const int pos = pos0 + 16 * hs;
-          const int id = __shfl_sync(0xffffffffu, ids, (i % AHEAD) * St::HALVES + hs);
-          const int have = len - pos;  // tokens of the sequence from here on
-          if (hs == 0 && have <= 0) break;  // step() will not look at this stage
-          const bool good = (unsigned)id < (unsigned)p.pages.num_pages;
-          if (!good && have > 0) set_status(p.status, MSA_ERR_ARG);
-          const int64_t row0 =
-              good ? (int64_t)id * p.pages.page_size + (pos - page_of(p.pages, pos) * p.pages.page_size) : 0;
-          const int64_t at = (row0 * p.H + g) * St::ROW + lane_off;
-          const uint8_t* kp = static_cast<const uint8_t*>(p.k) + at;
-          const uint8_t* vp = static_cast<const uint8_t*>(p.v) + at;
-          const bool full = good && have >= 16;
-#pragma unroll
-          for (int j = 0; j < 16 / RPI; ++j) {
-            const int r = r0 + j * RPI;
-            uint8_t* kd = st + St::key_at(16 * hs + r, ch);
-            uint8_t* vd = st + St::value_at(16 * hs + r, ch);
-            if (full) {
-              cp_async_16(kd, kp + j * RPI * row_step);
-              cp_async_16(vd, vp + j * RPI * row_step);
-            } else {  // else zeros: no stale NaN meets a weight of 0
-              const bool ok = good && r < have;
-              const int64_t off = ok ? j * RPI * row_step : -lane_off;
-              cp_async_16(kd, kp + off, ok);
-              cp_async_16(vd, vp + off, ok);
-            }
-          }
-          if constexpr (F8) {  // lanes 0..15 the keys' scales, the others the values'
-            const int r = lane & 15;
-            const bool ok = good && r < have;
-            const float* src = (lane < 16 ? p.k_scale : p.v_scale) + (ok ? (row0 + r) * p.H + g : 0);
-            cp_async_4(st + St::S0 + ((lane < 16 ? 0 : St::KEYS) + 16 * hs + r) * 4, src, ok);
-          }
-        }
-      }
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < St::COUNT - 1; ++i) load(i);
-    ws.load_q(p, head0, gq, tq);
-    for (int i = 0; i < n; ++i) {
-      cp_async_wait<St::COUNT - 2>();
-      // unit i has landed for all lanes, and all are done with unit i - 1; heads side by side
-      // stay in step, so that what they load together lies together in memory
-      if (wh > 1) __syncthreads(); else __syncwarp();
-      load(i + St::COUNT - 1);
-      const int have = len - first_token(i);
-      if (have > 0) ws.step(ring + (i % St::COUNT) * St::BYTES, have, lane);
-    }
-    // join the warps: each leaves its sums in its own stages
-    cp_async_wait<0>();
-    __syncwarp();
-    float* my_o = reinterpret_cast<float*>(ring);  // [8 R][D + 4]
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-      for (int r = 0; r < ws.R; ++r)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          my_o[(8 * r + 2 * tq + (e & 1)) * (D + 4) + ws.column(i, e, gq)] = ws.o[i][r][e];
-#pragma unroll
-    for (int r = 0; r < (WIDE ? 2 : 1); ++r) {
-      float l = ws.l[r];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (tq == 0) {
-        s_m[warp][gq + 8 * r] = ws.m[r];
-        s_mv[warp][gq + 8 * r] = F8 ? ws.mv[r] : ws.m[r];
-        s_l[warp][gq + 8 * r] = l;
-      }
-    }
+    attend<D, F8, WIDE, SPARSE>(p, ws, ring, b, g, len, u0, n, blk, my_token, unit, wh > 1);
+    leave_sums(ws, ring, s_sums);
     __syncthreads();
     const bool whole = n == units;
     const int64_t part = (int64_t)(2 * blockIdx.x + slot) * wh * p.G;
@@ -762,23 +817,8 @@ __global__ void __launch_bounds__(kThreads, Stage<D, F8, WIDE>::PER_SM) paged_at
     for (int x = tid; x < wh * p.G * (D / 4); x += kThreads) {
       const int row = x / (D / 4), c = 4 * (x % (D / 4));
       const int w0 = wh == 1 ? 0 : row / p.G, h = row - w0 * p.G;
-      float top = -INFINITY, l = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k)
-        if (k < subs) top = fmaxf(top, s_m[w0 + k * wh][h]);
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) {
-        if (k >= subs) break;
-        const int w = w0 + k * wh;
-        l += s_l[w][h] * weight(s_m[w][h], top);
-        const float f = weight(s_mv[w][h], top);
-        const float4 y = *reinterpret_cast<const float4*>(smem + w * St::COUNT * St::BYTES + (h * (D + 4) + c) * 4);
-        acc.x = fmaf(f, y.x, acc.x);
-        acc.y = fmaf(f, y.y, acc.y);
-        acc.z = fmaf(f, y.z, acc.z);
-        acc.w = fmaf(f, y.w, acc.w);
-      }
+      float top, l;
+      float4 acc = join_warps<D, F8, WIDE>(smem, s_sums, h, c, w0, wh, subs, &top, &l);
       const float inv = whole || l > 0.f ? 1.f / l : 0.f;  // a part of scores that are all -inf
       acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       if (whole) {
@@ -807,9 +847,191 @@ __global__ void __launch_bounds__(kThreads, Stage<D, F8, WIDE>::PER_SM) paged_at
   }
 }
 
+// ---------------------------------------------------------------------------
+// Short caches: one cluster of CTAs per (sequence, group) does the whole call.  The CTAs share the
+// units (and the scoring of the blocks) and join through distributed shared memory.  Such a call is
+// bound by latency: this is one launch instead of two or three, without a workspace, and no CTA
+// has to find its place among the sequences (1 x 700 tokens, 2 groups: 8.0 -> 5.7 us of GPU time,
+// 24 -> 16.6 us a call; 2048 tokens, 2 groups, topk 4: 10.5 -> 8.4 and 27 -> 20 us).
+// small_cluster() has the limits.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address in CTA `rank` of the cluster that corresponds to this CTA's shared-memory address.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float cluster_ld(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+constexpr int kSmallBlocks = 32;  // blocks of a table that the small form selects from
+
+// Largest score q_idx[b, g] . k_idx[j] over the 128 keys j of block c, in every lane: mma.sync
+// fragments of the keys from global memory (as decode_pool_kernel loads them), the query in the
+// first of the 8 columns.
+template <int DI>
+__device__ __forceinline__ float block_score(const PagedDecode& p, int b, int g, int c) {
+  constexpr int NP = DI / 32;
+  const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+  const int64_t row = lane < 8 ? pool_row(p.pages, b, c * 128 + lane * 16) : 0;
+  if (row < 0) set_status(p.status, MSA_ERR_ARG);
+  const uint4* qrow = reinterpret_cast<const uint4*>(p.q_idx + ((int64_t)b * p.H + g) * DI);
+  uint4 bq[NP];
+#pragma unroll
+  for (int j = 0; j < NP; ++j) bq[j] = gq == 0 ? __ldg(&qrow[j * 4 + tq]) : make_uint4(0, 0, 0, 0);
+  float top = -INFINITY;
+#pragma unroll 2
+  for (int t = 0; t < 8; ++t) {
+    const int64_t r = __shfl_sync(0xffffffffu, row, t);
+    const uint4* kb = reinterpret_cast<const uint4*>(p.k_idx + (r < 0 ? 0 : r) * DI);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;  // a missing page reads as zero rows
+      if (r >= 0) {
+        lo = __ldg(&kb[gq * (DI / 8) + j * 4 + tq]);
+        hi = __ldg(&kb[(gq + 8) * (DI / 8) + j * 4 + tq]);
+      }
+      const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
+      mma_bf16_16816(acc, a0, bq[j].x, bq[j].y);
+      mma_bf16_16816(acc, a1, bq[j].z, bq[j].w);
+    }
+    top = fmax3(top, acc[0], acc[2]);  // column 0 in the lanes of tq = 0
+  }
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return __shfl_sync(0xffffffffu, top, 0);
+}
+
+// The M = min(topk - 1, own) best of blocks 0 .. own - 1 (lane i holds the score of block i; equal
+// ones: the lower block) and block `own`: lane i gets the i-th of them, ascending, or -1.
+__device__ __forceinline__ int select_in_warp(float score, int own, int topk) {
+  const int lane = threadIdx.x & 31, M = min(topk - 1, own);
+  const uint32_t u = __float_as_uint(score);
+  const uint32_t key = lane < own ? max((u & 0x80000000u) ? ~u : (u | 0x80000000u), 1u) : 0u;
+  int above = 0;
+#pragma unroll 8
+  for (int j = 0; j < 32; ++j) {
+    const uint32_t x = __shfl_sync(0xffffffffu, key, j);
+    above += x > key || (x == key && j < lane);
+  }
+  const unsigned taken = __ballot_sync(0xffffffffu, lane < own && above < M) | (1u << own);
+  int id = -1;
+#pragma unroll 8
+  for (int j = 0; j < 32; ++j)
+    if ((taken >> j & 1) && __popc(taken & ((1u << j) - 1)) == lane) id = j;
+  return id;
+}
+
+template <int D, bool F8, bool WIDE, int DI>  // DI = 0: the whole cache
+__global__ void __launch_bounds__(kThreads, Stage<D, F8, WIDE>::PER_SM) paged_small_kernel(const PagedDecode p) {
+  using St = Stage<D, F8, WIDE>;
+  constexpr bool SPARSE = DI > 0;
+  constexpr int ITEMS = (WIDE ? 16 : 8) * (D / 4) / kThreads;  // of 4 columns, a thread's at most
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ WarpSums s_sums;
+  __shared__ float s_lse[16], s_score[kSmallBlocks];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int size = p.cluster, pair = blockIdx.x / size, rank = blockIdx.x - pair * size;
+  const int b = pair / p.H, g = pair - b * p.H;
+  const int64_t head0 = (int64_t)pair * p.G;
+  const int len = seq_len(p, b);
+  if (len == 0) {  // the whole cluster's
+    if (rank == 0) {
+      write_empty<D>(p, head0, p.G);
+      if (SPARSE && tid < p.topk) p.block_idx[(int64_t)pair * p.topk + tid] = -1;
+    }
+    // stay as long as the others would if the length were written meanwhile
+    for (int i = 0; i < (SPARSE ? 3 : 2); ++i) cluster_sync();
+    return;
+  }
+  int blk = 0;
+  if constexpr (SPARSE) {
+    const int own = (len - 1) / 128, warps = size * kWarps;
+    for (int c = rank * kWarps + warp; c < own; c += warps) {
+      const float top = block_score<DI>(p, b, g, c);
+      if (lane == 0) s_score[c] = top;
+    }
+    cluster_sync();
+    float score = 0.f;
+    if (lane < own) score = cluster_ld(cluster_addr(&s_score[lane], lane % warps / kWarps));
+    blk = select_in_warp(score, own, p.topk);
+    if (rank == 0 && tid < p.topk) p.block_idx[(int64_t)pair * p.topk + tid] = blk;
+  }
+  const int units = seq_units<SPARSE>(p, len, 1);
+  const int u0 = units * rank / size, n = units * (rank + 1) / size - u0;
+  uint8_t* ring = smem + warp * St::COUNT * St::BYTES;
+  float4 acc[ITEMS];
+  if (n > 0) {
+    {
+      WarpState<D, F8, WIDE> ws;
+      attend<D, F8, WIDE, SPARSE>(p, ws, ring, b, g, len, u0, n, blk, warp * St::KEYS, St::UNIT, false);
+      leave_sums(ws, ring, s_sums);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const int x = tid + k * kThreads, h = x / (D / 4), c = 4 * (x % (D / 4));
+      if (h >= p.G) break;
+      float top, l;
+      acc[k] = join_warps<D, F8, WIDE>(smem, s_sums, h, c, 0, 1, kWarps, &top, &l);
+      const float inv = l > 0.f || size == 1 ? 1.f / l : 0.f;  // a part of scores that are all -inf
+      acc[k] = make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv);
+      if (c == 0) s_lse[h] = top + log2f(l);
+    }
+    __syncthreads();  // the warps' sums have been read
+    float* part = reinterpret_cast<float*>(smem);  // [G][D]
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const int x = tid + k * kThreads;
+      if (x < p.G * (D / 4)) *reinterpret_cast<float4*>(part + 4 * x) = acc[k];
+    }
+  } else if (tid < 16) {
+    s_lse[tid] = -INFINITY;
+  }
+  cluster_sync();
+  // this CTA's share of the columns, over the cluster's parts in order
+  for (int x = rank * kThreads + tid; x < p.G * (D / 4); x += size * kThreads) {
+    const int h = x / (D / 4), c = 4 * (x % (D / 4));
+    float top = -INFINITY, l = 0.f;
+    for (int r = 0; r < size; ++r) top = fmaxf(top, cluster_ld(cluster_addr(&s_lse[h], r)));
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < size; ++r) {
+      const float w = weight(cluster_ld(cluster_addr(&s_lse[h], r)), top);
+      if (w == 0.f) continue;  // a CTA without units left no sums
+      const float4 y = cluster_ld4(cluster_addr(smem + x * 16, r));
+      l += w;
+      sum.x = fmaf(w, y.x, sum.x);
+      sum.y = fmaf(w, y.y, sum.y);
+      sum.z = fmaf(w, y.z, sum.z);
+      sum.w = fmaf(w, y.w, sum.w);
+    }
+    *reinterpret_cast<uint2*>(p.o + (head0 + h) * D + c) =
+        make_uint2(pack_bf16(sum.x / l, sum.y / l), pack_bf16(sum.z / l, sum.w / l));
+    if (c == 0) p.lse[head0 + h] = (top + log2f(l)) * 0.6931471805599453f;
+  }
+  cluster_sync();  // no CTA leaves while its sums are read
+}
+
 // Joins the parts of every (sequence, group) that the split cut, where the whole cache is
-// attended: one sequence may then have hundreds of them.  Grid (B H, head splits, D / COLS): a CTA takes heads blockIdx.y,
-// + gridDim.y, ... and COLS value columns; its threads take parts side by side, each 4 columns.
+// attended: one sequence may then have hundreds of them.  Grid (B H, head splits, D / COLS): a CTA
+// takes heads blockIdx.y, + gridDim.y, ... and COLS value columns; its threads take parts side by
+// side, each 4 columns.  Bound by latency: about 3 us behind the attention (one CTA over 16 heads of
+// one long sequence: 344 us).
 constexpr int kJoinThreads = 256;
 template <int D, int COLS>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedDecode p) {
@@ -900,7 +1122,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedDec
 // kPoolWarps warps a SM, which take 8 NT groups each.  A warp has two stages of half a block in
 // shared memory: while it works on one half the next is on its way, and the page ids of the block
 // after it.  Bound by HBM, so what counts are the bytes in flight: 192 KB a SM (8 x 128K, 134 MB:
-// see kPoolWarps; with the halves in registers instead, 12 warps a SM, 26 us).
+// 24.1 us, 5.6 TB/s with the fill and drain; the halves in registers instead, 25.2 us).
 constexpr int kPoolCtas = 152, kPoolWarps = 12;
 template <int DI>
 constexpr int kPoolStage = 64 * DI * 2;  // bytes
@@ -1142,6 +1364,53 @@ cudaError_t launch_paged(const PagedDecode& p, bool f8, bool wide, cudaStream_t 
   return launch(paged_join_kernel<D, D>, dim3((unsigned)rows, (unsigned)split), kJoinThreads, 0, true, stream, p);
 }
 
+template <int D, bool F8, bool WIDE, int DI>
+cudaError_t launch_small(const PagedDecode& p, cudaStream_t stream) {
+  constexpr int smem = kWarps * Stage<D, F8, WIDE>::COUNT * Stage<D, F8, WIDE>::BYTES;
+  static_assert(smem >= 16 * D * 4, "a part");
+  auto* kern = paged_small_kernel<D, F8, WIDE, DI>;
+  static std::atomic<void*> done{nullptr};
+  const cudaError_t e = allow_smem(kern, smem, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.B * p.H * p.cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int D, int DI>
+cudaError_t launch_small(const PagedDecode& p, bool f8, bool wide, cudaStream_t stream) {
+  if (f8) return wide ? launch_small<D, true, true, DI>(p, stream) : launch_small<D, true, false, DI>(p, stream);
+  return wide ? launch_small<D, false, true, DI>(p, stream) : launch_small<D, false, false, DI>(p, stream);
+}
+
+// CTAs of a cluster of the small form, or 0 for the other one: as many as let all pairs run
+// together, if each then has at most kSmallUnits units, or twice that where the pairs alone fill
+// the GPU and the cache is read whole.  Measured (GPU time of bf16, d 128, 8 groups of 4 heads,
+// whole cache, small against other): 1 sequence of 512 tokens 6.2 / 9.1 us, of 4096 (8 units a
+// CTA) 10.5 / 12.0, of 8192 15.4 / 12.9; 8 of 2048 (8 units) 11.1 / 15.5, 16 of ragged lengths to
+// 4096 (32 units) 33.0 / 24.4; with 256 pairs, 32 of 1024 (16 units) 25.7 / 34.1 and of ragged
+// lengths to 2048 (32 units) 36.3 / 32.9.  topk 16: 1 of 2048 11.9 / 25.5, 32 of 512 (8 units)
+// 14.6 / 30.6, 64 of 1024 (16 units) 73.4 / 65.4.
+constexpr int kSmallUnits = 8;
+int small_cluster(int64_t pairs, int64_t cap, int topk, int unit, int ctas) {
+  const int64_t nb = (cap + 127) / 128;
+  if (topk > 0 && nb > kSmallBlocks) return 0;
+  const int64_t units = topk > 0 ? (nb < topk ? nb : topk) * (128 / unit) : (cap + unit - 1) / unit;
+  int c = 8;
+  while (c > 1 && pairs * c > ctas) c >>= 1;
+  return units <= (topk == 0 && c == 1 ? 2 : c) * kSmallUnits ? c : 0;
+}
+
 // Heads (groups) that a CTA serves side by side: all attend the same tokens when the whole cache
 // is attended, and rows of one token are neighbours in a page; selected blocks differ by group.
 int heads_side_by_side(int H, int topk) {
@@ -1151,6 +1420,7 @@ int heads_side_by_side(int H, int topk) {
 
 struct Layout {
   size_t part_o, part_lse, starts, arrive, pooled, bytes;
+  int cluster, ctas, keys_shift;
 };
 
 // Sizes of a call; MSA_OK and the workspace's layout.  topk = 0: the whole cache.
@@ -1169,6 +1439,11 @@ int check_sizes(const msa_paged_cache_t* c, const msa_page_table_t* pt, int H_q,
   // the work of all pairs is counted in 32 bits
   const int64_t most = (cap >> (c->kind == MSA_CACHE_E4M3 || c->d == 64 ? 7 : 6)) + kOverhead + 4;
   if ((int64_t)pt->B * c->H_kv * most >= 1 << 30) return MSA_ERR_UNSUPPORTED;
+  lay->keys_shift = c->kind == MSA_CACHE_E4M3 || c->d == 64 ? 5 : 4;
+  lay->ctas = kCtas / 3 * (G > 8 && c->d == 128 ? 2 : 3);  // Stage::PER_SM
+  lay->cluster = small_cluster((int64_t)pt->B * c->H_kv, cap, topk, kWarps << lay->keys_shift, lay->ctas);
+  lay->bytes = 0;
+  if (lay->cluster) return MSA_OK;
   lay->part_o = 0;
   const size_t parts = (size_t)2 * kCtas * heads_side_by_side(c->H_kv, topk) * G;
   lay->part_lse = align256(parts * c->d * 4);
@@ -1194,8 +1469,8 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   for (const void* x : ptrs)
     if (!x || (reinterpret_cast<uintptr_t>(x) & 15) != 0) return MSA_ERR_ARG;
   if (!lens || (reinterpret_cast<uintptr_t>(lens) & 3)) return MSA_ERR_ARG;
-  if (!workspace || workspace_bytes < lay.bytes) return MSA_ERR_WORKSPACE;
-  if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return MSA_ERR_ARG;
+  if (lay.bytes > 0 && (!workspace || workspace_bytes < lay.bytes)) return MSA_ERR_WORKSPACE;
+  if (lay.bytes > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return MSA_ERR_ARG;
   Ctx cx;
   if ((rc = device_ctx(&cx))) return rc;
   uint8_t* w = static_cast<uint8_t*>(workspace);
@@ -1203,11 +1478,11 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   p.q_idx = static_cast<const __nv_bfloat16*>(q_idx);
   // without pages every id is bad and every copy has no bytes: any address does for those
   const bool pages_exist = c->num_pages > 0;
-  p.k = pages_exist ? c->k : workspace;
-  p.v = pages_exist ? c->v : workspace;
-  p.k_scale = pages_exist ? c->k_scale : static_cast<const float*>(workspace);
-  p.v_scale = pages_exist ? c->v_scale : static_cast<const float*>(workspace);
-  p.k_idx = static_cast<const __nv_bfloat16*>(pages_exist ? c->k_idx : workspace);
+  p.k = pages_exist ? c->k : q;
+  p.v = pages_exist ? c->v : q;
+  p.k_scale = pages_exist ? c->k_scale : static_cast<const float*>(q);
+  p.v_scale = pages_exist ? c->v_scale : static_cast<const float*>(q);
+  p.k_idx = static_cast<const __nv_bfloat16*>(pages_exist ? c->k_idx : q);
   p.lens = lens;
   p.block_idx = topk > 0 ? block_idx : nullptr;
   p.pooled = reinterpret_cast<float*>(w + lay.pooled);
@@ -1225,10 +1500,23 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   p.row = (nb + 3) & ~3;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wh = heads_side_by_side(p.H, topk);
-  p.ctas = kCtas / 3 * (p.G > 8 && c->d == 128 ? 2 : 3);  // Stage::PER_SM
-  p.keys_shift = c->kind == MSA_CACHE_E4M3 || c->d == 64 ? 5 : 4;
+  p.ctas = lay.ctas;
+  p.keys_shift = lay.keys_shift;
+  p.cluster = lay.cluster;
   p.status = cx.status;
   cudaError_t e = cudaSuccess;
+  const bool wide = p.G > 8, f8 = c->kind == MSA_CACHE_E4M3;
+  if (p.cluster) {
+    if (c->d == 128)
+      e = topk == 0          ? launch_small<128, 0>(p, f8, wide, stream)
+          : c->d_idx == 64 ? launch_small<128, 64>(p, f8, wide, stream)
+                           : launch_small<128, 32>(p, f8, wide, stream);
+    else
+      e = topk == 0          ? launch_small<64, 0>(p, f8, wide, stream)
+          : c->d_idx == 64 ? launch_small<64, 64>(p, f8, wide, stream)
+                           : launch_small<64, 32>(p, f8, wide, stream);
+    return finish(e);
+  }
   if (topk > 0) {
     const int nt = p.H > 8 ? 2 : 1;
     const dim3 grid(kPoolCtas, (unsigned)((p.H + 8 * nt - 1) / (8 * nt)));
@@ -1244,7 +1532,6 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
                      : launch(paged_select_kernel<31>, gsel, 256, 0, true, stream, p);
     if (e != cudaSuccess) return MSA_ERR_CUDA;
   }
-  const bool wide = p.G > 8, f8 = c->kind == MSA_CACHE_E4M3;
   e = c->d == 128 ? launch_paged<128>(p, f8, wide, stream) : launch_paged<64>(p, f8, wide, stream);
   return finish(e);
 }

@@ -902,13 +902,11 @@ def _paged_args(q, cache, page_table, lens, topk, scale):
         raise ValueError(f"q must be [{B}, a multiple of {H_kv}, {d}] on the cache's device, got {tuple(shape)}")
     if H_q // H_kv > 16:
         raise ValueError(f"at most 16 query heads a group, got {H_q // H_kv}")
-    nws = _lib.msa_decode_paged_workspace_size(cache._c, pages, H_q, topk)
-    if nws == 0:
-        raise ValueError("the sizes of this call are outside the supported set")
+    nws = _lib.msa_decode_paged_workspace_size(cache._c, pages, H_q, topk)  # 0: needs none, or the call refuses
     dev = cache.device
     return (pages, B, H_q, d ** -0.5 if scale is None else float(scale), torch.empty_like(q),
             torch.empty((B, H_q), dtype=torch.float32, device=dev),
-            torch.empty(nws, dtype=torch.uint8, device=dev), nws)
+            torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None, nws)
 
 
 def msa_decode_paged(q, q_idx, cache: PagedCache, page_table, lens, topk: int = 16, *, scale=None):
@@ -930,7 +928,7 @@ def msa_decode_paged(q, q_idx, cache: PagedCache, page_table, lens, topk: int = 
     if B:
         _call(cache.index, "msa_decode_paged", _lib.msa_decode_paged, cache._c, pages, lens.data_ptr(), H_q, topk,
               scale, q.data_ptr(), q_idx.data_ptr(), block_idx.data_ptr(), o.data_ptr(), lse.data_ptr(),
-              ws.data_ptr(), nws)
+              ws.data_ptr() if nws else None, nws)
     return block_idx, o, lse
 
 
@@ -940,5 +938,5 @@ def msa_decode_paged_dense(q, cache: PagedCache, page_table, lens, *, scale=None
     pages, B, H_q, scale, o, lse, ws, nws = _paged_args(q, cache, page_table, lens, 0, scale)
     if B:
         _call(cache.index, "msa_decode_paged_dense", _lib.msa_decode_paged_dense, cache._c, pages, lens.data_ptr(),
-              H_q, scale, q.data_ptr(), o.data_ptr(), lse.data_ptr(), ws.data_ptr(), nws)
+              H_q, scale, q.data_ptr(), o.data_ptr(), lse.data_ptr(), ws.data_ptr() if nws else None, nws)
     return o, lse

@@ -398,9 +398,10 @@ int msa_cache_read(const msa_paged_cache_t* c, const msa_page_table_t* pages, co
  *   B * H_kv * max_pages * page_size below 2^36.
  * In:  q [B][H_q][d], q_idx [B][H_kv][d_idx] (bf16), pages, lens (device int32 [B]).
  * Out: block_idx [B][H_kv][topk] (int32), o [B][H_q][d] (bf16), lse [B][H_q] (float32).
- * Workspace: msa_decode_paged_workspace_size (topk 0 for the dense call; 0 if the sizes are
- *   invalid), 256-byte aligned.  The result does not depend on what it held, nor on the order
- *   in which the GPU runs the parts (they are joined in their own order).
+ * Workspace: msa_decode_paged_workspace_size bytes (topk 0 for the dense call; 0 if the call
+ *   needs none, as with short tables, or the sizes are invalid), 256-byte aligned.  The result
+ *   does not depend on what it held, nor on the order in which the GPU runs the parts (they are
+ *   joined in their own order).
  */
 size_t msa_decode_paged_workspace_size(const msa_paged_cache_t* c, const msa_page_table_t* pages, int H_q,
                                        int topk);

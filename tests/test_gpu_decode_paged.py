@@ -29,6 +29,10 @@ def dev(x):
     return torch.as_tensor(np.asarray(x, dtype=np.int32)).cuda()
 
 
+WIDE = "wide"  # a table for more than 8192 tokens: the form of long caches, however short these are
+SLACK = pytest.mark.parametrize("slack", [1, WIDE])
+
+
 class Batch:
     """Random pages, a shuffled table, and what no sequence holds filled with NaN."""
 
@@ -36,6 +40,8 @@ class Batch:
         g = gen(seed)
         self.lens, self.page, self.H, self.d = list(lens), page, H, d
         need = [(n + page - 1) // page for n in lens]
+        if slack is WIDE:
+            slack = 8192 // page + 1
         P = sum(need) + spare
         order = np.random.default_rng(seed).permutation(P)
         t = np.full((len(lens), max(need + [0]) + slack), -1, dtype=np.int32)
@@ -120,14 +126,19 @@ DENSE = [  # lens, page, H_kv, G, d
     ([70001], 128, 1, 16, 128),
     ([1] * 300 + [0] * 20 + [200] * 30, 32, 2, 1, 64),
     ([64 * (i % 7) + i for i in range(140)], 16, 4, 2, 128),
+    ([97, 1, 513, 0, 1100] * 5, 16, 3, 7, 64),
+    ([97, 1, 513, 0, 400] * 8, 64, 4, 9, 128),
+    ([97, 1, 200, 0, 65] * 30, 32, 4, 16, 64),
+    ([4000], 32, 1, 16, 128),
 ]
 
 
+@SLACK
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("case", range(len(DENSE)))
-def test_dense(case, fp8):
+def test_dense(case, fp8, slack):
     lens, page, H, G, d = DENSE[case]
-    batch = Batch(lens, page, H, d, 0, fp8, seed=case)
+    batch = Batch(lens, page, H, d, 0, fp8, seed=case, slack=slack)
     q = query(len(lens), H * G, d, 100 + case)
     for scale in (None, 0.3):
         o, lse = ops.msa_decode_paged_dense(q, batch.cache, batch.table, batch.lens_t, scale=scale)
@@ -168,14 +179,19 @@ SPARSE = [  # lens, page, H_kv, G, d, d_idx, topk
     ([3000, 2561], 256, 24, 2, 64, 64, 20),
     ([9000], 128, 2, 16, 128, 32, 32),
     ([131, 5, 700] * 40, 16, 1, 12, 64, 64, 3),
+    ([4000, 3969, 1100, 130], 16, 3, 4, 128, 64, 16),
+    ([2000, 129, 0, 777] * 6, 48, 4, 16, 64, 32, 5),
+    ([1000, 129, 0, 777] * 30, 32, 2, 8, 128, 32, 3),
+    ([4096, 4095, 4050, 4049], 16, 4, 3, 64, 64, 32),
 ]
 
 
+@SLACK
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("case", range(len(SPARSE)))
-def test_sparse(case, fp8):
+def test_sparse(case, fp8, slack):
     lens, page, H, G, d, di, topk = SPARSE[case]
-    batch = Batch(lens, page, H, d, di, fp8, seed=50 + case)
+    batch = Batch(lens, page, H, d, di, fp8, seed=50 + case, slack=0 if max(lens) == 4096 and slack == 1 else slack)
     q = query(len(lens), H * G, d, 200 + case)
     qi = query(len(lens), H, di, 300 + case)
     sets, o, lse = ops.msa_decode_paged(q, qi, batch.cache, batch.table, batch.lens_t, topk)
@@ -234,18 +250,19 @@ def test_long_caches_and_many_sequences(fp8):
     assert ops.device_status() == 0
 
 
+@pytest.mark.parametrize("L", [4096, 8192])
 @pytest.mark.parametrize("fp8", [False, True])
-def test_contiguous_cache_as_pages_agrees_with_msa_decode(fp8):
+def test_contiguous_cache_as_pages_agrees_with_msa_decode(fp8, L):
     """msa_decode's cache [B, Lmax] is a paged cache with pages 0, 1, 2, ...: the same sets
     (exact ties among them, lower block first) and, within both roundings, the same output."""
-    B, L, H, G, d, di, topk = 2, 4096, 2, 4, 128, 64, 6
+    B, H, G, d, di, topk = 2, 2, 4, 128, 64, 6
     g = gen(7)
     k, v = (torch.randn(B, L, H, d, generator=g, device="cuda").bfloat16() for _ in "kv")
     # blocks that are block 0 scaled by 1, 2 or 4: runs of equal pooled scores
     ki = torch.randn(B, 1, 128, di, generator=g, device="cuda").bfloat16()
     ki = (ki * (2.0 ** torch.randint(0, 3, (L // 128,), generator=g, device="cuda"))[None, :, None, None].bfloat16())
     ki = ki.reshape(B, L, di).contiguous()
-    q, qi, lens = query(B, H * G, d, 8), query(B, H, di, 9), dev([4096, 3001])
+    q, qi, lens = query(B, H * G, d, 8), query(B, H, di, 9), dev([L, 3001])
     page = 128
     table = dev(np.arange(B * L // page).reshape(B, -1))
     paged = lambda x: x.view(-1, page, *x.shape[2:])  # noqa: E731
@@ -270,11 +287,12 @@ def test_contiguous_cache_as_pages_agrees_with_msa_decode(fp8):
     assert (lse - lse2).abs().max() <= 1e-4
 
 
-def test_value_scales_far_apart_and_small_queries():
+@SLACK
+def test_value_scales_far_apart_and_small_queries(slack):
     """E4M3 rows whose scales differ by many orders of magnitude, and queries far from 1: the
     fp16 products keep their range."""
     for power, qpower in ((30, 0), (-30, 20), (60, -20), (-60, 0)):
-        batch = Batch([300], 16, 1, 64, 0, True, seed=11)
+        batch = Batch([300], 16, 1, 64, 0, True, seed=11, slack=slack)
         step = torch.linspace(-abs(power), 0, 16, device="cuda").round()
         batch.cache.v_scale.mul_(2.0 ** (step * (1 if power > 0 else -1))[None, :, None])
         batch.cache.k_scale.mul_(2.0 ** -qpower)
@@ -284,10 +302,11 @@ def test_value_scales_far_apart_and_small_queries():
     assert ops.device_status() == 0
 
 
-def test_large_scores_and_infinite_rows():
+@SLACK
+def test_large_scores_and_infinite_rows(slack):
     """Scores in the thousands (one key takes all), and an infinite or NaN value in one
     sequence: its outputs are not finite, its neighbours' are untouched."""
-    batch = Batch([300, 300], 16, 2, 64, 0, False, seed=13)
+    batch = Batch([300, 300], 16, 2, 64, 0, False, seed=13, slack=slack)
     q = (query(2, 4, 64, 14).float() * 200).bfloat16()
     o, lse = ops.msa_decode_paged_dense(q, batch.cache, batch.table, batch.lens_t)
     check_dense(batch, q, 64 ** -0.5, o, lse)
@@ -300,13 +319,14 @@ def test_large_scores_and_infinite_rows():
     assert torch.isnan(lse3[1]).all() and torch.equal(o3[0], o2[0])
 
 
+@pytest.mark.parametrize("slack", [0, WIDE])
 @pytest.mark.parametrize("fp8", [False, True])
-def test_places_that_do_not_exist(fp8):
+def test_places_that_do_not_exist(fp8, slack):
     """Bad lengths count as empty slots, bad page ids as zero rows; the status says so."""
     lens = [200, 300, 150]
-    batch = Batch(lens, 16, 2, 64, 32, fp8, seed=15, slack=0)
+    batch = Batch(lens, 16, 2, 64, 32, fp8, seed=15, slack=slack)
     q, qi = query(3, 4, 64, 16), query(3, 2, 32, 17)
-    for bad in (-1, 305, 2 ** 31 - 1, -(2 ** 31)):
+    for bad in (-1, batch.t.shape[1] * 16 + 1, 2 ** 31 - 1, -(2 ** 31)):
         lt = dev([200, bad, 150])
         o, lse = ops.msa_decode_paged_dense(q, batch.cache, batch.table, lt)
         assert ops.device_status() == _lib.MSA_ERR_ARG
@@ -338,7 +358,7 @@ def test_places_that_do_not_exist(fp8):
     assert not o.any() and (lse == -math.inf).all() and ops.device_status() == 0
     # a pool without pages: whatever the table says is outside it, and reads as zero rows
     empty = ops.new_paged_cache(0, 2, page_size=16, d=64, d_idx=32, fp8=fp8)
-    t = dev(np.zeros((3, 20)))
+    t = dev(np.zeros((3, batch.t.shape[1])))
     for call in (lambda: ops.msa_decode_paged_dense(q, empty, t, batch.lens_t),
                  lambda: ops.msa_decode_paged(q, qi, empty, t, batch.lens_t, 4)[1:]):
         o, lse = call()
@@ -368,11 +388,12 @@ def test_offsets_past_32_bits():
     assert ops.device_status() == 0
 
 
-def test_streams_and_graphs():
+@SLACK
+def test_streams_and_graphs(slack):
     """Two captured calls replayed together on two streams while lengths and queries change
     between replays: each has its own workspace and each gives the eager answer."""
     lens = [3000, 64, 0, 777]
-    batches = [Batch(lens, 16, 2, 64, 32, f, seed=21 + f) for f in (False, True)]
+    batches = [Batch(lens, 16, 2, 64, 32, f, seed=21 + f, slack=slack) for f in (False, True)]
     qs, qis = [query(4, 8, 64, 23 + i) for i in range(2)], [query(4, 2, 32, 25 + i) for i in range(2)]
     graphs, outs = [], []
     for i, bt in enumerate(batches):

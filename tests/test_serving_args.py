@@ -115,14 +115,27 @@ def test_cache_calls_check_their_arguments():
 
 def test_decode_calls_check_their_arguments():
     size = _lib.msa_decode_paged_workspace_size
-    need = size(cache(), table(), 4, 4)  # the pooled scores grow with the table's length
-    assert 0 < need < size(cache(), table(n=1 << 20), 4, 4) and size(cache(), table(), 4, 0) > 0
+    long = table(n=1024)
+    need = size(cache(), long, 4, 4)  # the pooled scores grow with the table's length
+    assert 0 < need < size(cache(), table(n=1 << 20), 4, 4) and size(cache(), long, 4, 0) > 0
+    # short tables need none: up to 8 units (128 tokens, 64 with bf16 and d 128) a CTA of a
+    # cluster of at most 8 (3 CTAs a SM hold all pairs' clusters at once; 16 units if one CTA is
+    # a cluster and all tokens are read) and, sparse, 32 blocks
+    for kw, tokens, groups in [(dict(), 8192, 1), (dict(d=128), 4096, 1), (dict(d=128, kind=1), 8192, 1),
+                               (dict(H=57), 8192, 1), (dict(H=58), 4096, 1), (dict(H=115), 2048, 1),
+                               (dict(H=229), 2048, 1), (dict(H=1000), 2048, 1), (dict(H=39, d=128), 4096, 8),
+                               (dict(H=39, d=128), 2048, 16)]:
+        H_q = groups * kw.get("H", 2)
+        assert size(cache(**kw), table(n=tokens // 16), H_q, 0) == 0, kw
+        assert size(cache(**kw), table(n=tokens // 16 + 1), H_q, 0) > 0, kw
+    assert size(cache(), table(n=256), 4, 32) == 0 and size(cache(), table(n=257), 4, 1) > 0
+    assert size(cache(H=300), table(n=256), 300, 8) == 0 and size(cache(H=300), table(n=256), 300, 9) > 0
     big = 1 << 40
 
-    def dense(c=cache(), t=table(), lens=256, H_q=4, scale=1.0, q=256, o=256, lse=256, ws=256, n=big):
+    def dense(c=cache(), t=long, lens=256, H_q=4, scale=1.0, q=256, o=256, lse=256, ws=256, n=big):
         return _lib.msa_decode_paged_dense(c, t, lens, H_q, scale, q, o, lse, ws, n, None)
 
-    def sparse(c=cache(), t=table(), lens=256, H_q=4, topk=4, scale=1.0, q=256, qi=256, bi=256, o=256, lse=256,
+    def sparse(c=cache(), t=long, lens=256, H_q=4, topk=4, scale=1.0, q=256, qi=256, bi=256, o=256, lse=256,
                ws=256, n=big):
         return _lib.msa_decode_paged(c, t, lens, H_q, topk, scale, q, qi, bi, o, lse, ws, n, None)
 
@@ -142,4 +155,4 @@ def test_decode_calls_check_their_arguments():
     # the work of a call is counted in 32 bits
     assert dense(t=table(B=60000, n=1 << 20, stride=1 << 20), c=cache(H=4)) == UNSUP
     assert size(cache(), table(), 4, -1) == 0 and size(cache(), table(), 3, 0) == 0
-    assert size(cache(di=0), table(), 4, 4) == 0 and size(cache(k=0), table(ids=0), 4, 4) > 0
+    assert size(cache(di=0), table(), 4, 4) == 0 and size(cache(k=0), table(ids=0, n=1024), 4, 4) > 0

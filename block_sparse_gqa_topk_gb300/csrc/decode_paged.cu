@@ -550,40 +550,50 @@ struct WarpState {
   }
 };
 
-// o and lse of one (sequence, group) from its few parts, by the CTA that wrote the last of them.
-// s_w: [parts][G] floats of shared memory.
+// o and lse of one (sequence, group) from its few parts (at most 64: those of the selected blocks),
+// by the CTA that wrote the last of them: a warp a head, the weights in its lanes.
 template <int D>
-__device__ __forceinline__ void join_parts(const PagedDecode& p, const Parts& parts, int64_t head0, float* s_w) {
-  const int tid = threadIdx.x, lane = tid & 31, G = p.G, n = parts.n;
-  for (int h = tid >> 5; h < G; h += kWarps) {  // weights of the parts, a warp a head
-    float top = -INFINITY, l = 0.f;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(&p.part_lse[parts.slot(i) * G + h]));
+__device__ __forceinline__ void join_parts(const PagedDecode& p, const Parts& parts, int64_t head0) {
+  constexpr int LANES = D / 4, SIDE = 32 / LANES;  // lanes of a part; parts side by side
+  const int lane = threadIdx.x & 31, G = p.G, n = parts.n;
+  const int sub = lane / LANES, c = 4 * (lane % LANES);
+  for (int h = threadIdx.x >> 5; h < G; h += kWarps) {
+    float w[2];  // of parts lane, lane + 32
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      w[e] = lane + 32 * e < n ? __ldcg(&p.part_lse[parts.slot(lane + 32 * e) * G + h]) : -INFINITY;
+    float top = fmaxf(w[0], w[1]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int i = lane; i < n; i += 32) {
-      const float w = weight(__ldcg(&p.part_lse[parts.slot(i) * G + h]), top);
-      s_w[i * G + h] = w;
-      l += w;
-    }
+    w[0] = weight(w[0], top);
+    w[1] = weight(w[1], top);
+    float l = w[0] + w[1];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    for (int i = lane; i < n; i += 32) s_w[i * G + h] /= l;
-    if (lane == 0) p.lse[head0 + h] = (top + log2f(l)) * 0.6931471805599453f;
-  }
-  __syncthreads();
-  for (int x = tid; x < G * (D / 4); x += kThreads) {
-    const int h = x / (D / 4), c = 4 * (x % (D / 4));
+    w[0] /= l;
+    w[1] /= l;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + (parts.slot(i) * G + h) * D + c));
-      const float w = s_w[i * G + h];
-      acc.x = fmaf(w, y.x, acc.x);
-      acc.y = fmaf(w, y.y, acc.y);
-      acc.z = fmaf(w, y.z, acc.z);
-      acc.w = fmaf(w, y.w, acc.w);
+    for (int i0 = 0; i0 < n; i0 += SIDE) {
+      const int i = i0 + sub;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) y = __ldcg(reinterpret_cast<const float4*>(p.part_o + (parts.slot(i) * G + h) * D + c));
+      const float f = __shfl_sync(0xffffffffu, i0 < 32 ? w[0] : w[1], i & 31);  // 0 from n on
+      acc.x = fmaf(f, y.x, acc.x);
+      acc.y = fmaf(f, y.y, acc.y);
+      acc.z = fmaf(f, y.z, acc.z);
+      acc.w = fmaf(f, y.w, acc.w);
     }
-    *reinterpret_cast<uint2*>(p.o + (head0 + h) * D + c) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+    if (SIDE == 2) {
+      acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+      acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+      acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+      acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+    }
+    if (sub == 0)
+      *reinterpret_cast<uint2*>(p.o + (head0 + h) * D + c) =
+          make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+    if (lane == 0) p.lse[head0 + h] = (top + log2f(l)) * 0.6931471805599453f;
   }
 }
 
@@ -777,7 +787,6 @@ __global__ void __launch_bounds__(kThreads, Stage<D, F8, WIDE>::PER_SM) paged_at
   // warp w works for head hg wh + w % wh, on the (w / wh)-th run of KEYS tokens of each unit
   const int my_head = warp & (wh - 1), subs = kWarps / wh;
   const int my_token = (wh == 1 ? warp : wh == 2 ? warp >> 1 : 0) * St::KEYS, unit = St::KEYS * subs;
-  WarpState<D, F8, WIDE> ws;
   int slot = 0;  // of the CTA's next part
   while (u < u_end) {
     int len = seq_len(p, b), units = seq_units<SPARSE>(p, len, wh), size = seq_work(units);
@@ -808,8 +817,11 @@ __global__ void __launch_bounds__(kThreads, Stage<D, F8, WIDE>::PER_SM) paged_at
         blk = __ldg(&blocks[lane]);
       }
     }
-    attend<D, F8, WIDE, SPARSE>(p, ws, ring, b, g, len, u0, n, blk, my_token, unit, wh > 1);
-    leave_sums(ws, ring, s_sums);
+    {
+      WarpState<D, F8, WIDE> ws;
+      attend<D, F8, WIDE, SPARSE>(p, ws, ring, b, g, len, u0, n, blk, my_token, unit, wh > 1);
+      leave_sums(ws, ring, s_sums);
+    }
     __syncthreads();
     const bool whole = n == units;
     const int64_t part = (int64_t)(2 * blockIdx.x + slot) * wh * p.G;
@@ -840,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, Stage<D, F8, WIDE>::PER_SM) paged_at
       __syncthreads();
       if (s_last) {
         __threadfence();
-        join_parts<D>(p, parts, out0, reinterpret_cast<float*>(smem));
+        join_parts<D>(p, parts, out0);
       }
     }
     __syncthreads();  // the stages are free for the next span
@@ -1122,7 +1134,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedDec
 // kPoolWarps warps a SM, which take 8 NT groups each.  A warp has two stages of half a block in
 // shared memory: while it works on one half the next is on its way, and the page ids of the block
 // after it.  Bound by HBM, so what counts are the bytes in flight: 192 KB a SM (8 x 128K, 134 MB:
-// 24.1 us, 5.6 TB/s with the fill and drain; the halves in registers instead, 25.2 us).
+// 23.6 us, 5.7 TB/s with the fill and drain; the halves in registers instead, 25.2 us; the warps of
+// an SM next to one another in the deal, so that half of the SMs have no part in the last round,
+// 24.1 us).
 constexpr int kPoolCtas = 152, kPoolWarps = 12;
 template <int DI>
 constexpr int kPoolStage = 64 * DI * 2;  // bytes
@@ -1135,7 +1149,7 @@ __global__ void __launch_bounds__(kPoolWarps * 32, 1) paged_pool_kernel(const Pa
   extern __shared__ __align__(128) uint8_t smem[];
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-  const int warp = blockIdx.x * kPoolWarps + (threadIdx.x >> 5);
+  const int warp = (threadIdx.x >> 5) * kPoolCtas + blockIdx.x;
   uint8_t* stages = smem + (threadIdx.x >> 5) * 2 * kPoolStage<DI>;
   if (blockIdx.y == 0)
     for (int64_t x = blockIdx.x * blockDim.x + threadIdx.x; x < (int64_t)p.B * p.H; x += gridDim.x * blockDim.x)
@@ -1331,7 +1345,7 @@ cudaError_t launch_attn(const PagedDecode& p, cudaStream_t stream) {
   constexpr int smem = kWarps * Stage<D, F8, WIDE>::COUNT * Stage<D, F8, WIDE>::BYTES;
   static_assert(Stage<D, F8, WIDE>::COUNT * Stage<D, F8, WIDE>::BYTES >= (WIDE ? 16 : 8) * (D + 4) * 4, "sums in the stages");
   static_assert(Stage<D, F8, WIDE>::PER_SM == (WIDE && D == 128 ? 2 : 3), "ctas");
-  static_assert(smem >= 32 * 128 / Stage<D, F8, WIDE>::UNIT * 16 * 4, "weights of a pair's parts");
+  static_assert(kMaxSelect * 128 / Stage<D, F8, WIDE>::UNIT <= 64, "parts of selected blocks");
   auto* kern = paged_attn_kernel<D, F8, WIDE, SPARSE>;
   static std::atomic<void*> done{nullptr};
   const cudaError_t e = allow_smem(kern, smem, done);

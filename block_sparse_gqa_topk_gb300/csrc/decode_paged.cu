@@ -315,7 +315,8 @@ struct WarpState {
         // 2^-10 and more below the largest keep only multiples of 2^-9 (2^-18 of the largest).
         const int e = min((int)(__float_as_uint(amax) >> 23), 253);
         const float down = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e)
-        fac[r] = p.scale_log2 / down * 0.0078125f;
+        // an infinite value has scores that are infinite or NaN, but no E4M3 form: NaN for all
+        fac[r] = isinf(amax) ? NAN : p.scale_log2 / down * 0.0078125f;
 #pragma unroll
         for (int j = 0; j < D / 64; ++j)
 #pragma unroll

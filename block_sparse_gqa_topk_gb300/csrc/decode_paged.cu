@@ -195,15 +195,6 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// D(16x8) += A(16x32, row) * B(32x8, col), E4M3
-__device__ __forceinline__ void mma_e4m3_16832(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
-      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -214,6 +205,12 @@ __device__ __forceinline__ uint32_t widen_f16(uint32_t two) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
   return h;
+}
+
+// A pair of fp16 as bf16 (exact for E4M3 values).
+__device__ __forceinline__ uint32_t f16_to_bf16(uint32_t two) {
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&two));
+  return pack_bf16(v.x, v.y);
 }
 
 // 2^(a - b), 0 for a = -inf whatever b.
@@ -257,8 +254,7 @@ __device__ __forceinline__ float lg2_fast(float x) {  // relative to 1: about 2^
 }
 
 // One warp's running softmax over its keys.
-//   S = Q K^T: rows are heads gq and gq + 8 (WIDE), or with at most 8 heads, E4M3, the low
-//   parts of head gq's query; columns are keys 8 t + 2 tq + e.
+//   S = Q K^T: rows are heads gq and gq + 8 (WIDE; else idle); columns are keys 8 t + 2 tq + e.
 //   O^T = V^T P^T: rows are value columns, columns the heads 8 nt + 2 tq + e, so that the
 //   accumulator of at most 8 heads has no idle rows; the fragments of S are those of P^T.
 // (gq = lane / 4, tq = lane % 4.)
@@ -268,14 +264,15 @@ struct WarpState {
   static constexpr int R = WIDE ? 2 : 1;     // heads of a lane's rows of S
   static constexpr int MT = D / 16;          // tiles of 16 value columns
   static constexpr int KT = St::KEYS / 8;    // tiles of 8 keys
-  static constexpr int QS = F8 ? D / 32 : D / 16;
-  uint32_t qa[QS][4];                        // query fragments
-  uint32_t ql[F8 && WIDE ? QS : 1][4];       // their low parts
+  static constexpr int QS = D / 16;
+  uint32_t qa[QS][4];       // query fragments
   float o[MT][R][4];
   float m[R], mv[R], l[R];  // max, max with the value scale (E4M3), this lane's part of the sum
   float fac[R];             // accumulator -> score in bits
+  bool far;                 // E4M3: the queries are bf16, not fp16
 
   __device__ __forceinline__ void load_q(const PagedDecode& p, int64_t head0, int gq, int tq) {
+    bool lost = false, huge[R] = {};
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int h = gq + 8 * r;
@@ -289,10 +286,11 @@ struct WarpState {
             qa[ks][r + 2 * half] =
                 r < R && ok ? __ldg(reinterpret_cast<const uint32_t*>(row + ks * 16 + half * 8 + 2 * tq)) : 0u;
       } else if (r < R) {
-        // lane tq holds values 64 j + 16 tq + 0..15 of the row, in the order in which step()
-        // reads the codes of a key: words 4 (2 j + s) + {0, 1} are k slots 4 tq.. and
-        // 16 + 4 tq.. of k step 2 j + s
-        float f[D / 64][16], amax = 0.f;
+        // lane tq holds values 64 j + 16 tq + 0..15 of the row, in the order in which step() reads
+        // the codes of a key: values 4 s + {0, 1} and 4 s + {2, 3} of them are k slots 2 tq.. and
+        // 8 + 2 tq.. of k step 4 j + s
+        float2 f[D / 64][8];
+        float amax = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 64; ++j)
 #pragma unroll
@@ -302,47 +300,57 @@ struct WarpState {
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float a = __uint_as_float(u[e] << 16), b = __uint_as_float(u[e] & 0xffff0000u);
-              f[j][8 * half + 2 * e] = a;
-              f[j][8 * half + 2 * e + 1] = b;
-              amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(b)));
+              const float2 x = make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u));
+              f[j][4 * half + e] = x;
+              amax = fmax3(amax, fabsf(x.x), fabsf(x.y));
             }
           }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // The row scaled by a power of two to a largest value in [128, 256), as the sum of two
-        // E4M3 values: 4 significant bits each hold all 8 of a bf16 value, except that values
-        // 2^-10 and more below the largest keep only multiples of 2^-9 (2^-18 of the largest).
-        const int e = min((int)(__float_as_uint(amax) >> 23), 253);
-        const float down = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e)
-        // an infinite value has scores that are infinite or NaN, but no E4M3 form: NaN for all
-        fac[r] = isinf(amax) ? NAN : p.scale_log2 / down * 0.0078125f;
+        // The row enters in fp16, scaled by a power of two to a largest value in [2^14, 2^15):
+        // exact for values of at least 2^-31 of the largest.  Where any value is smaller and loses
+        // bits (or is NaN), the group's queries enter in bf16 and the codes are widened to that
+        // (8 x 128K, d 128: 357 us for 333; 16 heads a group 425 for 385; d 64 241 for 227).
+        const int e = max((int)(__float_as_uint(amax) >> 23), 40);
+        const float down = __uint_as_float((uint32_t)(268 - e) << 23);  // 2^(141 - e)
+        const float up = __uint_as_float((uint32_t)(e - 14) << 23);
+        fac[r] = p.scale_log2 * up;
+        huge[r] = amax >= 0x1p100f;
 #pragma unroll
         for (int j = 0; j < D / 64; ++j)
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t hi = 0, lo = 0;
-#pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-              const float a = f[j][4 * w + k] * down * 128.f, b = f[j][4 * w + k + 1] * down * 128.f;
-              const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-              const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2, __NV_E4M3)));
-              const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, b - back.y), __NV_SATFINITE, __NV_E4M3);
-              hi |= (h2 & 0xffffu) << (8 * k);
-              lo |= (l2 & 0xffffu) << (8 * k);
-            }
-            uint32_t* frag = qa[2 * j + (w >> 1)];
-            if constexpr (WIDE) {
-              frag[r + 2 * (w & 1)] = hi;
-              ql[2 * j + (w >> 1)][r + 2 * (w & 1)] = lo;
-            } else {
-              frag[2 * (w & 1)] = hi;
-              frag[1 + 2 * (w & 1)] = lo;
-            }
+          for (int w = 0; w < 8; ++w) {
+            const float2 x = f[j][w];
+            const uint32_t h2 = pack_f16(x.x * down, x.y * down);
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+            lost = lost || back.x * up != x.x || back.y * up != x.y;
+            qa[4 * j + (w >> 1)][r + 2 * (w & 1)] = h2;
           }
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < QS; ++ks) qa[ks][1] = qa[ks][3] = 0u;
       }
     }
-    if constexpr (!F8) {
+    far = F8 && __any_sync(0xffffffffu, lost);
+    if constexpr (F8) {
+      if (far) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int h = gq + 8 * r;
+          // a query of 2^100 and more enters as 2^-32 of its value, so that no product with a code
+          // overflows before the key's scale is applied
+          const float down = huge[r] ? 0x1p-32f : 1.f;
+          fac[r] = p.scale_log2 / down;
+#pragma unroll
+          for (int w = 0; w < D / 8; ++w) {
+            const int at = 64 * (w >> 3) + 16 * tq + 2 * (w & 7);
+            const uint32_t u = h < p.G ? __ldg(reinterpret_cast<const uint32_t*>(p.q + (head0 + h) * D + at)) : 0u;
+            qa[w >> 1][r + 2 * (w & 1)] =
+                pack_bf16(__uint_as_float(u << 16) * down, __uint_as_float(u & 0xffff0000u) * down);
+          }
+        }
+      }
+    } else {
 #pragma unroll
       for (int r = 0; r < R; ++r) fac[r] = p.scale_log2;
     }
@@ -395,26 +403,24 @@ struct WarpState {
       }
     } else {
       // the order of a product's terms is free: lane tq takes values 64 j + 16 tq + 0..15 of
-      // key gq as the k slots of steps 2 j and 2 j + 1, and so do the query fragments
+      // key gq as the k slots of steps 4 j .. 4 j + 3, and so do the query fragments
+      auto products = [&](bool in_bf16) {
 #pragma unroll
-      for (int t = 0; t < KT; ++t)
+        for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-          const uint4 c = *reinterpret_cast<const uint4*>(st + St::key_at(8 * t + gq, 4 * j + tq));
-          mma_e4m3_16832(sc[t], qa[2 * j], c.x, c.y);
-          mma_e4m3_16832(sc[t], qa[2 * j + 1], c.z, c.w);
-          if constexpr (WIDE) {
-            mma_e4m3_16832(sc[t], ql[2 * j], c.x, c.y);
-            mma_e4m3_16832(sc[t], ql[2 * j + 1], c.z, c.w);
+          for (int j = 0; j < D / 64; ++j) {
+            const uint4 c = *reinterpret_cast<const uint4*>(st + St::key_at(8 * t + gq, 4 * j + tq));
+            const uint32_t u[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              const uint32_t k0 = widen_f16(u[s] & 0xffffu), k1 = widen_f16(u[s] >> 16);
+              if (in_bf16) mma_bf16_16816(sc[t], qa[4 * j + s], f16_to_bf16(k0), f16_to_bf16(k1));
+              else mma_f16_16816(sc[t], qa[4 * j + s], k0, k1);
+            }
           }
-        }
-      if constexpr (!WIDE) {
-#pragma unroll
-        for (int t = 0; t < KT; ++t) {
-          sc[t][0] += sc[t][2];
-          sc[t][1] += sc[t][3];
-        }
-      }
+      };
+      if (far) products(true);
+      else products(false);
     }
     // scores in bits; this lane's keys: 8 t + 2 tq + e
     float2 lv[F8 ? KT : 1];  // log2 of the value scales
@@ -427,8 +433,8 @@ struct WarpState {
         lv[t] = make_float2(lg2_fast(vs.x), lg2_fast(vs.y));
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          sc[t][2 * r] *= ks.x;
-          sc[t][2 * r + 1] *= ks.y;
+          sc[t][2 * r] *= ks.x * fac[r];  // one factor: each alone may leave the range
+          sc[t][2 * r + 1] *= ks.y * fac[r];
         }
       }
     }
@@ -439,8 +445,10 @@ struct WarpState {
 #pragma unroll
       for (int t = 0; t < KT; ++t) {
         float &s0 = sc[t][2 * r], &s1 = sc[t][2 * r + 1];
-        s0 *= fac[r];
-        s1 *= fac[r];
+        if constexpr (!F8) {
+          s0 *= fac[r];
+          s1 *= fac[r];
+        }
         if (n < St::KEYS) {
           s0 = 8 * t + 2 * tq < n ? s0 : -INFINITY;
           s1 = 8 * t + 2 * tq + 1 < n ? s1 : -INFINITY;

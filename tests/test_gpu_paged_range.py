@@ -58,3 +58,57 @@ def test_infinite_queries(d, G, fp8, slack):
                             lambda g, b=b: tokens(b, g), d ** -0.5)
 
     both_forms(batch, q, qi, 2, check)
+
+
+@SLACK
+@pytest.mark.parametrize("d,G", [(64, 2), (128, 4), (64, 12), (128, 9)])
+@pytest.mark.parametrize("power", [0, 6, 9, 12, 15, 24, 31, 40, 90, 120, -100])
+def test_queries_with_an_outlier_channel(power, d, G, slack):
+    """E4M3 pages: a channel of the query 2^power times the others, where every key is zero, does
+    not decide the softmax and takes no bits from the others.  power < 0: a channel far below them."""
+    batch = Batch([300, 129], 16, 2, d, 32, True, seed=4, slack=slack)
+    batch.cache.k[..., 7] = 0
+    q, qi = query(2, 2 * G, d, 5), query(2, 2, 32, 6)
+    q[..., 7] *= 2.0 ** power
+    if G == 4:
+        q[:, 1] = query(2, 1, d, 7)[:, 0]  # and a head without one
+
+    def check(o, lse, tokens):
+        for b in range(2):
+            check_attention(batch, b, q, o, lse, lambda g, b=b: tokens(b, g), d ** -0.5)
+
+    both_forms(batch, q, qi, 2, check)
+
+
+@SLACK
+@pytest.mark.parametrize("d,G", [(64, 2), (128, 4), (64, 12), (128, 9)])
+@pytest.mark.parametrize("power", [100, 118, -100, -118])
+def test_queries_and_key_scales_far_from_one(power, d, G, slack):
+    """E4M3 pages whose key scales undo a power of two in the queries."""
+    batch = Batch([300, 129], 16, 2, d, 32, True, seed=4, slack=slack)
+    batch.cache.k_scale.mul_(2.0 ** -power)
+    q, qi = (query(2, 2 * G, d, 5).double() * 2.0 ** power).bfloat16(), query(2, 2, 32, 6)
+
+    def check(o, lse, tokens):
+        for b in range(2):
+            check_attention(batch, b, q, o, lse, lambda g, b=b: tokens(b, g), d ** -0.5)
+
+    both_forms(batch, q, qi, 2, check)
+
+
+@SLACK
+@pytest.mark.parametrize("d,G", [(64, 2), (128, 4), (64, 12), (128, 9)])
+def test_a_huge_query_beside_small_ones(d, G, slack):
+    """E4M3 pages: a query of 2^110 with a value far below it, in a group of queries near 2^-100."""
+    batch = Batch([300, 129], 16, 2, d, 32, True, seed=4, slack=slack)
+    batch.cache.k[..., 7] = 0
+    batch.cache.k_scale.mul_(2.0 ** 100)
+    q, qi = (query(2, 2 * G, d, 5).double() * 2.0 ** -100).bfloat16(), query(2, 2, 32, 6)
+    q[:, 1] = 0
+    q[:, 1, 7], q[:, 1, 8] = 2.0 ** 110, 2.0 ** -100
+
+    def check(o, lse, tokens):
+        for b in range(2):
+            check_attention(batch, b, q, o, lse, lambda g, b=b: tokens(b, g), d ** -0.5)
+
+    both_forms(batch, q, qi, 2, check)

@@ -253,6 +253,8 @@ __device__ __forceinline__ float lg2_fast(float x) {  // relative to 1: about 2^
   return y;
 }
 
+constexpr float kWeightBits = 15.f;  // E4M3: the largest weight of a code is 2^15
+
 // One warp's running softmax over its keys.
 //   S = Q K^T: rows are heads gq and gq + 8 (WIDE; else idle); columns are keys 8 t + 2 tq + e.
 //   O^T = V^T P^T: rows are value columns, columns the heads 8 nt + 2 tq + e, so that the
@@ -463,23 +465,23 @@ struct WarpState {
       m[r] = m_new;
       l[r] *= alpha[r];
       if constexpr (F8) {
-        // o is kept in units of 2^mv, mv the running max of score + log2(value scale): the
-        // weights of the codes then fit fp16 whatever the scales are
+        // o is kept in units of 2^(mv - 15), mv the running max of score + log2(value scale): the
+        // weights of the codes are then at most 2^15, which fp16 holds whatever the scales are
         float topv = -INFINITY;
 #pragma unroll
         for (int t = 0; t < KT; ++t) topv = fmax3(topv, sc[t][2 * r] + lv[t].x, sc[t][2 * r + 1] + lv[t].y);
         topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, 1));
         topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, 2));
         const float v_new = fmaxf(mv[r], topv);
-        const float v_use = v_new == -INFINITY ? 0.f : v_new;
+        const float v_use = v_new == -INFINITY ? 0.f : v_new, v_unit = v_use - kWeightBits;
         alpha[r] = ex2_fast(mv[r] - v_use);
         mv[r] = v_new;
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
           float &s0 = sc[t][2 * r], &s1 = sc[t][2 * r + 1];
           l[r] += ex2_fast(s0 - m_use) + ex2_fast(s1 - m_use);
-          s0 = ex2_fast(s0 + (lv[t].x - v_use));
-          s1 = ex2_fast(s1 + (lv[t].y - v_use));
+          s0 = ex2_fast(s0 + (lv[t].x - v_unit));
+          s1 = ex2_fast(s1 + (lv[t].y - v_unit));
         }
       } else {
 #pragma unroll
@@ -522,7 +524,9 @@ struct WarpState {
           }
         }
       } else {
-        uint32_t pb[R][2];  // weights in fp16: 2^-12 of their value
+        // weights in fp16: 2^-12 of their value down to 2^-29 of the largest that this warp met (of
+        // weight times value scale), below that multiples of 2^-39 of it
+        uint32_t pb[R][2];
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -724,7 +728,7 @@ __device__ __forceinline__ void leave_sums(const WarpState<D, F8, WIDE>& ws, uin
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     if (tq == 0) {
       s.m[warp][gq + 8 * r] = ws.m[r];
-      s.mv[warp][gq + 8 * r] = F8 ? ws.mv[r] : ws.m[r];
+      s.mv[warp][gq + 8 * r] = F8 ? ws.mv[r] - kWeightBits : ws.m[r];
       s.l[warp][gq + 8 * r] = l;
     }
   }

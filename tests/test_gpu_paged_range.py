@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from block_sparse_gqa_topk_gb300 import ops
-from test_gpu_decode_paged import SLACK, Batch, check_attention, query
+from test_gpu_decode_paged import SLACK, Batch, check_attention, check_dense, query
 
 pytestmark = pytest.mark.gpu
 
@@ -112,3 +112,29 @@ def test_a_huge_query_beside_small_ones(d, G, slack):
             check_attention(batch, b, q, o, lse, lambda g, b=b: tokens(b, g), d ** -0.5)
 
     both_forms(batch, q, qi, 2, check)
+
+
+@SLACK
+@pytest.mark.parametrize("d,G", [(64, 2), (128, 4), (64, 12), (128, 9)])
+@pytest.mark.parametrize("nats", [12, 16, 20])
+def test_one_key_far_above_the_others(nats, d, G, slack):
+    """E4M3 pages: a key `nats` above all others whose value is zero in half of the columns: there
+    the others' values are the output."""
+    n = 300
+    batch = Batch([n], 16, 1, d, 0, True, seed=8, slack=slack)
+    c, rows = batch.cache, batch.rows(0, n)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    k = torch.randn(n, d, generator=g, device="cuda") * 0.1
+    k[:, 0] = 0
+    k[77, 0] = 1
+    v = torch.rand(n, d, generator=g, device="cuda") + 0.5
+    v[77, ::2] = 0
+    for name, x in (("k", k), ("v", v)):
+        codes, scale = ops.msa_quantize_kv_fp8(x.bfloat16().view(1, n, 1, d))
+        getattr(c, name).flatten(0, 1)[rows] = codes[0]
+        getattr(c, name + "_scale").flatten(0, 1)[rows] = scale[0]
+    q = query(1, G, d, 10)
+    q[..., 0] = nats * d ** 0.5
+    o, lse = ops.msa_decode_paged_dense(q, c, batch.table, batch.lens_t)
+    check_dense(batch, q, d ** -0.5, o, lse)
+    assert ops.device_status() == 0

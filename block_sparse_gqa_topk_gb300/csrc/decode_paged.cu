@@ -247,9 +247,9 @@ struct Stage {
   }
 };
 
-__device__ __forceinline__ float lg2_fast(float x) {  // relative to 1: about 2^-22
+__device__ __forceinline__ float lg2_fast(float x) {  // relative to 1: about 2^-22; of subnormal x too
   float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -750,8 +750,14 @@ __device__ __forceinline__ float4 join_warps(const uint8_t* smem, const WarpSums
     if (k >= subs) break;
     const int w = w0 + k * wh;
     l += s.l[w][h] * weight(s.m[w][h], top);
-    const float f = weight(s.mv[w][h], top);
-    const float4 y = *reinterpret_cast<const float4*>(smem + w * St::COUNT * St::BYTES + (h * (D + 4) + c) * 4);
+    float4 y = *reinterpret_cast<const float4*>(smem + w * St::COUNT * St::BYTES + (h * (D + 4) + c) * 4);
+    float f;
+    if constexpr (F8) {  // 2^(mv - top) as its root twice: it underflows where value scales are subnormal
+      f = weight(0.5f * s.mv[w][h], 0.5f * top);
+      y = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+    } else {
+      f = weight(s.mv[w][h], top);
+    }
     acc.x = fmaf(f, y.x, acc.x);
     acc.y = fmaf(f, y.y, acc.y);
     acc.z = fmaf(f, y.z, acc.z);

@@ -138,3 +138,22 @@ def test_one_key_far_above_the_others(nats, d, G, slack):
     o, lse = ops.msa_decode_paged_dense(q, c, batch.table, batch.lens_t)
     check_dense(batch, q, d ** -0.5, o, lse)
     assert ops.device_status() == 0
+
+
+@SLACK
+@pytest.mark.parametrize("d,G", [(64, 2), (128, 4), (64, 12), (128, 9)])
+def test_subnormal_value_scales(d, G, slack):
+    """E4M3 rows so small that their scales are subnormal float32 numbers count like any other."""
+    batch = Batch([23, 300], 16, 2, d, 0, True, seed=11, slack=slack)
+    batch.cache.v_scale.mul_(2.0 ** -120)
+    scales = batch.cache.v_scale.flatten(0, 1)[batch.rows(1, 300)]
+    assert float(scales.max()) < 2.0 ** -126 and float(scales.min()) > 0
+    q = query(2, 2 * G, d, 12)
+    o, lse = ops.msa_decode_paged_dense(q, batch.cache, batch.table, batch.lens_t)
+    check_dense(batch, q, d ** -0.5, o, lse)
+    # beside rows of ordinary size, and a row of zeros
+    batch.cache.v_scale.flatten(0, 1)[batch.rows(1, 300)[100:]] *= 2.0 ** 120
+    batch.cache.v_scale.flatten(0, 1)[batch.rows(0, 23)[5]] = 0
+    o, lse = ops.msa_decode_paged_dense(q, batch.cache, batch.table, batch.lens_t)
+    check_dense(batch, q, d ** -0.5, o, lse)
+    assert ops.device_status() == 0

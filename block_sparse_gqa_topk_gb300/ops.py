@@ -14,6 +14,7 @@ import dataclasses
 import math
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 
@@ -605,6 +606,7 @@ def new_rope(rot_dim: int, *, base: float = 10000.0, interleaved: bool = False, 
 def msa_rope(xs, rope: Rope, positions=None, *, inverse: bool = False, inplace: bool = False):
     """Rotary positions of one to four tensors in one launch; returns them as a tuple (new
     contiguous tensors, or xs themselves with inplace).  inverse turns back (the gradient).
+    Autograd does not see this call: rope is the differentiable one.
 
     positions None: tokens [B, N, H, d] or [B, N, d] (one head), each at its index in its
     sequence.  positions int32 or int64 [T]: packed tokens [T, H, d] or [T, d];  [B, N] (a
@@ -692,19 +694,39 @@ def _check_in_place(xs):
                              "turned in place")
         if x.requires_grad and torch.is_grad_enabled():
             raise ValueError("a tensor that requires a gradient cannot be turned in place: use rope")
+        if _forward_mode() and forward_ad.unpack_dual(x).tangent is not None:
+            raise ValueError("a tensor with a tangent cannot be turned in place: use rope")
     for x in xs:
         torch.autograd.graph.increment_version(x)
 
 
+def _forward_mode() -> bool:
+    """Within a level of torch.autograd.forward_ad: tensors may carry tangents, which only an
+    autograd function sees."""
+    return forward_ad._current_level >= 0
+
+
 class RopeFunction(torch.autograd.Function):
-    """msa_rope with its gradient, the inverse turn (linear in x: differentiable again)."""
+    """msa_rope with its derivatives: the tangent's turn, and for the gradient the inverse turn
+    (linear in x: differentiable again)."""
 
     @staticmethod
     def forward(ctx, rope, positions, inverse, *xs):
         ctx.rope, ctx.inverse = rope, inverse
         ctx.save_for_backward(positions)
+        ctx.save_for_forward(positions)
         ctx.set_materialize_grads(False)
+        ctx.like = [(x.shape, x.dtype, x.device) for x in xs] if _forward_mode() else None
         return msa_rope(xs, rope, positions, inverse=inverse)
+
+    @staticmethod
+    def jvp(ctx, _rope, _positions, _inverse, *ts):
+        (positions,) = ctx.saved_tensors
+        got = [i for i, t in enumerate(ts) if t is not None]
+        out = [None if t is not None else torch.zeros(s, dtype=dt, device=dev) for t, (s, dt, dev) in zip(ts, ctx.like)]
+        for i, y in zip(got, msa_rope([ts[i] for i in got], ctx.rope, positions, inverse=ctx.inverse)):
+            out[i] = y
+        return tuple(out)
 
     @staticmethod
     def backward(ctx, *dys):
@@ -713,7 +735,7 @@ class RopeFunction(torch.autograd.Function):
         out = [None] * len(dys)
         if got:
             turn = [dys[i] for i in got]
-            if torch.is_grad_enabled():  # a second derivative is wanted
+            if torch.is_grad_enabled() or _forward_mode():  # a second derivative may be wanted
                 dxs = RopeFunction.apply(ctx.rope, positions, not ctx.inverse, *turn)
             else:
                 dxs = msa_rope(turn, ctx.rope, positions, inverse=not ctx.inverse)
@@ -723,9 +745,11 @@ class RopeFunction(torch.autograd.Function):
 
 
 def rope(xs, rope: Rope, positions=None):
-    """msa_rope for training: the rotated tensors as a tuple, differentiable in xs."""
+    """msa_rope for training: the rotated tensors as a tuple, differentiable in xs (in reverse
+    and in forward mode)."""
     xs = (xs,) if isinstance(xs, torch.Tensor) else tuple(xs)
-    if torch.is_grad_enabled() and any(isinstance(x, torch.Tensor) and x.requires_grad for x in xs):
+    if _forward_mode() or (torch.is_grad_enabled() and
+                           any(isinstance(x, torch.Tensor) and x.requires_grad for x in xs)):
         return RopeFunction.apply(rope, positions, False, *xs)
     return msa_rope(xs, rope, positions)
 

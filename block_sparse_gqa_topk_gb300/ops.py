@@ -794,6 +794,7 @@ class PagedCache:
         if d not in (64, 128) or d_idx not in (0, 32, 64):
             raise ValueError(f"d must be 64 or 128 and d_idx 32 or 64, got {d} and {d_idx}")
         self.k, self.v, self.k_idx, self.k_scale, self.v_scale = k, v, k_idx, k_scale, v_scale
+        self._pools = tuple(t for t in (k, v, k_idx, k_scale, v_scale) if t is not None)
         self.num_pages, self.page_size, self.H_kv, self.d, self.d_idx, self.fp8 = P, page, H_kv, d, d_idx, fp8
         self.device, self.index = k.device, k.get_device()
         self._c = _lib.PAGED_CACHE.pack(
@@ -889,6 +890,7 @@ def msa_cache_write(cache: PagedCache, page_table, lens, k, v, k_idx=None, *, cu
         return
     _call(cache.index, "msa_cache_write", _lib.msa_cache_write, cache._c, pages, lens.data_ptr(), cu, T, pk, pv, pi,
           _lib.CACHE_STRIDES.pack(sk[0], sk[1], sv[0], sv[1], si[0]))
+    torch.autograd.graph.increment_version(cache._pools)  # a graph that saved one of them must notice
 
 
 def msa_cache_read(cache: PagedCache, page_table, lens, cu_seqlens, total_tokens: int):

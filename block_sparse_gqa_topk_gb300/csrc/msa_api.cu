@@ -8,6 +8,7 @@
 #include <mutex>
 #include <string.h>
 
+#include "device_kind.h"
 #include "kernels.h"
 
 namespace msa {
@@ -33,18 +34,14 @@ int make_ctx(Ctx* cx) {
   if (rc) return rc;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MSA_ERR_CUDA;
-  // a device's SM count and kind do not change: asked for once (-1: not an sm_103)
   static std::atomic<int> sm_count[64];
-  int sms = sm_count[dev].load(std::memory_order_relaxed);
-  if (sms == 0) {
-    int major = 0, minor = 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return MSA_ERR_CUDA;
-    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-    if (major != 10 || minor != 3) sms = -1;
-    sm_count[dev].store(sms, std::memory_order_relaxed);
-  }
+  const int sms = sm_count_of(&sm_count[dev], [dev](DeviceAttr a, int* value) {
+    const cudaDeviceAttr attr = a == DeviceAttr::kSmCount ? cudaDevAttrMultiProcessorCount
+                                : a == DeviceAttr::kMajor ? cudaDevAttrComputeCapabilityMajor
+                                                          : cudaDevAttrComputeCapabilityMinor;
+    return cudaDeviceGetAttribute(value, attr, dev) == cudaSuccess;
+  });
+  if (sms == 0) return MSA_ERR_CUDA;
   if (sms < 0) return MSA_ERR_UNSUPPORTED;  // built for sm_103a only
   {
     std::lock_guard<std::mutex> lk(g_mu);

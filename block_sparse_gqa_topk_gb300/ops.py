@@ -793,6 +793,8 @@ class PagedCache:
             raise ValueError(f"page_size must be a multiple of 16, got {page}")
         if d not in (64, 128) or d_idx not in (0, 32, 64):
             raise ValueError(f"d must be 64 or 128 and d_idx 32 or 64, got {d} and {d_idx}")
+        if H_kv < 1:
+            raise ValueError("a cache has at least one KV head")
         self.k, self.v, self.k_idx, self.k_scale, self.v_scale = k, v, k_idx, k_scale, v_scale
         self._pools = tuple(t for t in (k, v, k_idx, k_scale, v_scale) if t is not None)
         self.num_pages, self.page_size, self.H_kv, self.d, self.d_idx, self.fp8 = P, page, H_kv, d, d_idx, fp8

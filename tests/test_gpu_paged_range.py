@@ -157,3 +157,8 @@ def test_subnormal_value_scales(d, G, slack):
     o, lse = ops.msa_decode_paged_dense(q, batch.cache, batch.table, batch.lens_t)
     check_dense(batch, q, d ** -0.5, o, lse)
     assert ops.device_status() == 0
+
+
+def test_a_cache_without_heads_is_refused():
+    with pytest.raises(ValueError):
+        ops.new_paged_cache(2, 0, page_size=16, d=64, d_idx=32)

@@ -269,7 +269,7 @@ struct WarpState {
   static constexpr int QS = D / 16;
   uint32_t qa[QS][4];       // query fragments
   float o[MT][R][4];
-  float m[R], mv[R], l[R];  // max, max with the value scale (E4M3), this lane's part of the sum
+  float m[R], mv[R], l[R];  // max, max with the value scale relative to it (E4M3), lane's part of the sum
   float fac[R];             // accumulator -> score in bits
   bool far;                 // E4M3: the queries are bf16, not fp16
 
@@ -461,25 +461,33 @@ struct WarpState {
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const float m_new = fmaxf(m[r], top);
       const float m_use = m_new == -INFINITY ? 0.f : m_new;
-      alpha[r] = ex2_fast(m[r] - m_use);
+      const float m_old = m[r];
+      alpha[r] = ex2_fast(m_old - m_use);
       m[r] = m_new;
       l[r] *= alpha[r];
       if constexpr (F8) {
-        // o is kept in units of 2^(mv - 15), mv the running max of score + log2(value scale): the
-        // weights of the codes are then at most 2^15, which fp16 holds whatever the scales are
+        // o is kept in units of 2^(m + mv - 15), mv the running max of score - m + log2(value scale):
+        // the weights of the codes are then at most 2^15, which fp16 holds whatever the scales are.
+        // (Relative to m, so that a scale is not lost beside a large score.)
+        const float moved = m_old - m_use;
         float topv = -INFINITY;
 #pragma unroll
-        for (int t = 0; t < KT; ++t) topv = fmax3(topv, sc[t][2 * r] + lv[t].x, sc[t][2 * r + 1] + lv[t].y);
+        for (int t = 0; t < KT; ++t) {
+          float &s0 = sc[t][2 * r], &s1 = sc[t][2 * r + 1];
+          s0 -= m_use;
+          s1 -= m_use;
+          topv = fmax3(topv, s0 + lv[t].x, s1 + lv[t].y);
+        }
         topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, 1));
         topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, 2));
-        const float v_new = fmaxf(mv[r], topv);
+        const float v_new = fmaxf(mv[r] + moved, topv);
         const float v_use = v_new == -INFINITY ? 0.f : v_new, v_unit = v_use - kWeightBits;
-        alpha[r] = ex2_fast(mv[r] - v_use);
+        alpha[r] = ex2_fast(mv[r] + moved - v_use);
         mv[r] = v_new;
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
           float &s0 = sc[t][2 * r], &s1 = sc[t][2 * r + 1];
-          l[r] += ex2_fast(s0 - m_use) + ex2_fast(s1 - m_use);
+          l[r] += ex2_fast(s0) + ex2_fast(s1);
           s0 = ex2_fast(s0 + (lv[t].x - v_unit));
           s1 = ex2_fast(s1 + (lv[t].y - v_unit));
         }
@@ -728,7 +736,7 @@ __device__ __forceinline__ void leave_sums(const WarpState<D, F8, WIDE>& ws, uin
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     if (tq == 0) {
       s.m[warp][gq + 8 * r] = ws.m[r];
-      s.mv[warp][gq + 8 * r] = F8 ? ws.mv[r] - kWeightBits : ws.m[r];
+      if (F8) s.mv[warp][gq + 8 * r] = ws.mv[r] - kWeightBits;
       s.l[warp][gq + 8 * r] = l;
     }
   }
@@ -752,11 +760,12 @@ __device__ __forceinline__ float4 join_warps(const uint8_t* smem, const WarpSums
     l += s.l[w][h] * weight(s.m[w][h], top);
     float4 y = *reinterpret_cast<const float4*>(smem + w * St::COUNT * St::BYTES + (h * (D + 4) + c) * 4);
     float f;
-    if constexpr (F8) {  // 2^(mv - top) as its root twice: it underflows where value scales are subnormal
-      f = weight(0.5f * s.mv[w][h], 0.5f * top);
+    if constexpr (F8) {  // as its root twice: it underflows where value scales are subnormal
+      const float m = s.m[w][h];
+      f = m == -INFINITY ? 0.f : ex2_fast(0.5f * (s.mv[w][h] + (m - top)));
       y = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
     } else {
-      f = weight(s.mv[w][h], top);
+      f = weight(s.m[w][h], top);
     }
     acc.x = fmaf(f, y.x, acc.x);
     acc.y = fmaf(f, y.y, acc.y);

@@ -159,6 +159,38 @@ def test_subnormal_value_scales(d, G, slack):
     assert ops.device_status() == 0
 
 
+@SLACK
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d,G", [(64, 2), (128, 4), (64, 12), (128, 9)])
+@pytest.mark.parametrize("power", [8, 16, 24, 32, 60, 100])
+def test_scores_of_any_size(power, d, G, fp8, slack):
+    """Scores of 2^power and more, far apart: one key takes all, and its value is the output."""
+    batch = Batch([300, 129], 16, 2, d, 32, fp8, seed=31, slack=slack)
+    one = 0x38 if fp8 else 1.0  # E4M3 code of 1
+    best = [17, 128]
+    for b, n in enumerate(batch.lens):
+        rows = batch.rows(b, n)
+        k = batch.cache.k.flatten(0, 1)
+        k[rows] = 0
+        k[rows[best[b]], :, 0] = one
+        if fp8:
+            batch.cache.k_scale.flatten(0, 1)[rows] = 1
+    q, qi = query(2, 2 * G, d, 32), query(2, 2, 32, 33)
+    q[..., 0] = 2.0 ** power * d ** 0.5
+
+    def check(o, lse, tokens):
+        for b in range(2):
+            for g in range(2):
+                v = batch.values("v", batch.rows(b, batch.lens[b])[best[b]][None], g)
+                h = slice(g * G, (g + 1) * G)
+                # the weight: 2^-11 (fp16) or 2^-16 (two bf16 parts); the result's rounding: 2^-8
+                assert ((o[b, h].double() - v).abs() <= (2.0 ** -8 + 2.0 ** -11) * v.abs()).all()
+                score = q[b, h, 0].double() * d ** -0.5
+                assert ((lse[b, h].double() / score - 1).abs() <= 2.0 ** -20).all()
+
+    both_forms(batch, q, qi, 3, check)  # three blocks: all of them
+
+
 def test_a_cache_without_heads_is_refused():
     with pytest.raises(ValueError):
         ops.new_paged_cache(2, 0, page_size=16, d=64, d_idx=32)

@@ -114,9 +114,11 @@ struct Cut {
   }
 };
 
-// Groups side by side read rows that are neighbours in a page, which HBM serves faster (E4M3, 8 x
-// 128K, d 128: 443 -> 343 us; d 64: 393 -> 232; bf16: 319 -> 309), but leave wh times the parts to
-// join.  They pay from about this much work (of one group) a CTA.
+// Groups side by side read rows that are neighbours in a page, which HBM serves faster where CTAs
+// are not in step (8 groups, one group a CTA against four: 32 x 32K E4M3 d 128 450 / 336 us, d 64
+// 398 / 231, bf16 623 / 601; 16 x 60K E4M3 d 64 364 / 212), but they leave wh times the parts to join
+// and wait for one another: few pairs, cut alike, lose up to 7 percent (8 x 128K E4M3 d 128 335 / 333,
+// d 64 216 / 229, bf16 593 / 598).  They pay from about this much work (of one group) a CTA.
 constexpr int kSideBySide = 48;
 
 struct Work {
@@ -231,7 +233,7 @@ struct Stage {
   static constexpr int BYTES = S0 + (F8 ? 2 * KEYS * 4 : 0);
   // CTAs of a SM.  More than 8 heads with d = 128 take more than the 168 registers a thread that
   // three CTAs leave: two with a third stage serve them better (8 x 128K, 16 heads a group, E4M3:
-  // 598 -> 488 us), but not with d = 64 (E4M3 323 -> 353 us).
+  // 423 -> 392 us), but not with d = 64 (E4M3 269 -> 321 us).
   static constexpr int PER_SM = WIDE && D == 128 ? 2 : 3;
   static constexpr int COUNT = PER_SM == 2 ? 3 : 2;
   static constexpr int UNIT = KEYS * kWarps;  // tokens of a unit of work
@@ -509,7 +511,8 @@ struct WarpState {
     for (int kp = 0; kp < KT / 2; ++kp) {  // 16 keys: one k step
       if constexpr (!F8) {
         // P enters in two bf16 parts (together 2^-17 of its value): the output's own rounding
-        // stays its largest error
+        // stays its largest error.  (An infinite value makes its column NaN, where one part is 0
+        // or below it.)
         uint32_t hi[R][2], lo[R][2];
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -788,8 +791,9 @@ __device__ __forceinline__ void write_empty(const PagedDecode& p, int64_t head0,
 // warps take the groups side by side and share each one's tokens, every warp with its own
 // stages in shared memory and its own running softmax; they join when a span ends.  A whole
 // (sequence, groups) is written out, a part of one goes to the CTA's slot 0 (its first span) or 1.
-// Bound by HBM: 8 whole caches of 128K tokens take 590 us in bf16 (4.3 GB, 7.3 TB/s) and 334 us in
-// E4M3 (2.2 GB, 6.6 TB/s), 16 blocks of each 19 us after the scores.
+// Bound by HBM: 8 whole caches of 128K tokens take 594 us in bf16 (4.3 GB, 7.2 TB/s) and 333 us in
+// E4M3 (2.2 GB, 6.6 TB/s), 16 blocks of each 19 us after the scores.  Bound by issue: E4M3 with d = 64
+// (229 us, 5.0 TB/s) or 16 heads a group (392 us, 5.6 TB/s).
 template <int D, bool F8, bool WIDE, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, Stage<D, F8, WIDE>::PER_SM) paged_attn_kernel(const PagedDecode p) {
   using St = Stage<D, F8, WIDE>;

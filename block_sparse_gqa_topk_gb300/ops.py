@@ -533,7 +533,9 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling=None):
       {"type": "yarn", "factor": s, "original_len": L, "beta_fast": 32, "beta_slow": 1}
           pairs that turn beta_fast times or more over L keep f_i, those that turn beta_slow
           times or fewer take f_i / s, the ones between a linear mix by their turns;
-          mscale = 0.1 ln s + 1 (or "mscale") -- YaRN, Peng et al. 2023."""
+          mscale = 0.1 ln s + 1 (or "mscale") -- YaRN, Peng et al. 2023.  The mix is linear in
+          the turns, as the paper has it; a model made with one that is linear in the pair's
+          index i has to give its frequencies to new_rope as inv_freq."""
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError(f"rot_dim must be even and at least 2, got {rot_dim}")
     if not (math.isfinite(base) and base > 0):

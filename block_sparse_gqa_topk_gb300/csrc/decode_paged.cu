@@ -197,6 +197,7 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -314,7 +315,7 @@ struct WarpState {
         // The row enters in fp16, scaled by a power of two to a largest value in [2^14, 2^15):
         // exact for values of at least 2^-31 of the largest.  Where any value is smaller and loses
         // bits (or is NaN), the group's queries enter in bf16 and the codes are widened to that
-        // (8 x 128K, d 128: 357 us for 333; 16 heads a group 425 for 385; d 64 241 for 227).
+        // (8 x 128K, d 128: 358 us for 333; 16 heads a group 432 for 392; d 64 246 for 229).
         const int e = max((int)(__float_as_uint(amax) >> 23), 40);
         const float down = __uint_as_float((uint32_t)(268 - e) << 23);  // 2^(141 - e)
         const float up = __uint_as_float((uint32_t)(e - 14) << 23);

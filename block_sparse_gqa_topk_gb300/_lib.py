@@ -50,6 +50,7 @@ MSA_DTYPE_F32 = 2
 
 MSA_CACHE_BF16 = 0
 MSA_CACHE_E4M3 = 1
+MSA_CACHE_E2M1 = 2
 
 
 class Problem(ctypes.Structure):

@@ -4,13 +4,11 @@
 // moves through the lanes of a part of a warp.  An E4M3 cache stores
 //   s = amax |x| / 448 (1 for an all-zero row),  code = E4M3 nearest to x / s,
 // the rule of msa_quantize_kv_fp8 bit for bit (IEEE divisions), and reads back
-// decode(code) * s rounded once to bf16.  Both directions are bound by HBM: every row is
-// read once and written once.
-#include <cuda_fp8.h>
-#include <math.h>
-
+// decode(code) * s rounded once to bf16.  An E2M1 cache (quantize16 has its rule) stores 4-bit
+// codes with a scale for each 16 of them, and reads back code * block scale * row scale, exactly.
+// Both directions are bound by HBM: every row is read once and written once.
+#include "cache_rows.cuh"
 #include "kernels.h"
-#include "paged.cuh"
 
 namespace msa {
 namespace {
@@ -18,14 +16,12 @@ namespace {
 constexpr int kThreads = 256;
 
 struct CacheParams {
-  PageView pages;
-  const int32_t* lens;
-  const int32_t* cu;  // null: one token a sequence
-  int B, T, H;
+  TokenMap map;
+  int T, H;
   void* k;  // pool
   void* v;
-  float* k_scale;
-  float* v_scale;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
   __nv_bfloat16* k_idx;
   __nv_bfloat16* xk;  // packed rows: read by the write, written by the read
   __nv_bfloat16* xv;
@@ -36,129 +32,43 @@ struct CacheParams {
   int* status;
 };
 
-constexpr int64_t kNoToken = -1;   // the packed row belongs to no sequence: left as it is
-constexpr int64_t kNoPlace = -2;   // its place does not exist: recorded in the status word
-
-__device__ __forceinline__ int64_t token_row(const CacheParams& p, int t) {
-  int b = t, after = 1;
-  if (p.cu) {
-    int lo = 0, hi = p.B - 1;  // last sequence that starts at or before t
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(&p.cu[mid]) <= t) lo = mid; else hi = mid - 1;
-    }
-    b = lo;
-    const int first = __ldg(&p.cu[b]), end = __ldg(&p.cu[b + 1]);
-    if (t < first || t >= end) {
-      // behind the last sequence is no error; anything else is a broken cu_seqlens
-      return t >= first && b == p.B - 1 && end >= first ? kNoToken : kNoPlace;
-    }
-    after = end - t;
-  }
-  const int len = __ldg(&p.lens[b]);
-  if (!p.cu && len == 0) return kNoToken;  // an empty slot of a padded decode batch
-  const int64_t pos = (int64_t)len - after;
-  if (pos < 0 || len > (int64_t)p.pages.max_pages * p.pages.page_size) return kNoPlace;
-  const int64_t row = pool_row(p.pages, b, (int)pos);
-  return row < 0 ? kNoPlace : row;
-}
-
-__device__ __forceinline__ float2 widen(uint32_t w) {  // two bf16
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-
-// E4M3 codes of four bf16 pairs divided by sc; out of line, for rows at the ends of the range.
-__device__ __noinline__ uint2 divide8(uint4 w, float sc) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-  uint32_t c[2] = {0, 0};
-#pragma unroll 1
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t v = e == 0 ? u[0] : e == 1 ? u[1] : e == 2 ? u[2] : u[3];
-    const float2 x = widen(v);
-    const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x.x, sc), __fdiv_rn(x.y, sc)), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t put = (two & 0xffffu) << (16 * (e & 1));
-    if (e < 2) c[0] |= put; else c[1] |= put;
-  }
-  return make_uint2(c[0], c[1]);
-}
-
-// A row's scale amax / 448 (1 for an all-zero row), and its reciprocal r for quantize8: an
-// approximate reciprocal with one Newton step.
-__device__ __forceinline__ void row_scale(float amax, float* sc, float* r) {
-  constexpr float kInv = 1.f / 448.f;
-  const float q0 = amax * kInv;
-  *sc = amax > 0.f ? fmaf(fmaf(-q0, 448.f, amax), kInv, q0) : 1.f;
-  float r0;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(*sc));
-  *r = fmaf(r0, fmaf(-*sc, r0, 1.f), r0);
-}
-
-// E4M3 codes of eight values at scale sc: the code nearest to the float32 quotient x / sc.  With r
-// the rounded reciprocal, q0 = x r and the remainder x - q0 sc, which one fma gives exactly,
-// q0 + r (x - q0 sc) is the rounded quotient (Markstein 1990; the scale above likewise); that
-// scales and codes are those that division gives is checked over all pairs of bf16 significands.
-// Rows whose amax leaves the range in which nothing underflows are divided.
-__device__ __forceinline__ uint2 quantize8(uint4 w, float sc, float r) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-  const float2 rr = make_float2(r, r), nn = make_float2(-sc, -sc);
-  uint32_t c[2] = {0, 0};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 x = widen(u[e]);
-    const float2 q0 = fmul2(x, rr);
-    float2 q = ffma2(ffma2(q0, nn, x), rr, q0);
-    q = make_float2(copysignf(q.x, x.x), copysignf(q.y, x.y));  // a zero keeps its sign
-    const uint32_t two = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
-    c[e >> 1] |= (two & 0xffffu) << (16 * (e & 1));
-  }
-  return make_uint2(c[0], c[1]);
-}
-
-// decode(code) * s of eight codes, rounded to bf16.
-__device__ __forceinline__ uint4 dequantize8(uint2 c, float s) {
-  uint32_t y[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)((e < 2 ? c.x : c.y) >> (16 * (e & 1)));
-    const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
-    y[e] = pack_bf16(v.x * s, v.y * s);
-  }
-  return make_uint4(y[0], y[1], y[2], y[3]);
-}
-
 // A token's keys, and its values, are one run of H D values in the pool; a lane moves 8 values
 // of it at a time (16 of E4M3: half the addresses and scales), a warp one token after another.
 // Its lanes find the places of all its tokens (at most 32) together, so the chain of lookups
 // (sequence, length, page) is paid once, and while it works on STEPS vectors a lane, the next ones
 // are on their way.  32K tokens of 8 groups, d 128, with index keys: bf16 41 us each way (6.8
 // TB/s), E4M3 write 40 us (bound by instructions: the rounding rule) and read 35 us (6 TB/s).
-template <int D, bool F8, bool WRITE>
+template <int D, int KIND, bool WRITE>
 struct Lanes {
-  static constexpr int VALUES = F8 ? 16 : 8;  // of a lane's vector
+  static constexpr bool CODED = KIND != MSA_CACHE_BF16;
+  static constexpr int VALUES = CODED ? 16 : 8;  // of a lane's vector
   static constexpr int LPR = D / VALUES;      // lanes of a head's row
-  static constexpr int STEPS = F8 && WRITE ? 1 : 2;
+  static constexpr int STEPS = CODED && WRITE ? 1 : 2;
+  static constexpr int BITS = KIND == MSA_CACHE_E2M1 ? 4 : KIND == MSA_CACHE_E4M3 ? 8 : 16;  // of a value in the pool
+  static constexpr int SCALE = KIND == MSA_CACHE_E2M1 ? e2m1_scale_bytes(D) : 4;            // bytes of a row's scales
 };
 
 // STEPS vectors a lane of one token, loaded; where they go.
-template <int D, bool F8, bool WRITE>
+template <int D, int KIND, bool WRITE>
 struct Batch {
-  using L = Lanes<D, F8, WRITE>;
+  using L = Lanes<D, KIND, WRITE>;
   static constexpr int W = L::VALUES / 8;  // 16-byte vectors of a lane in the packed rows
-  uint4 w[L::STEPS][W];                    // (16 codes of the pool: the first)
+  uint4 w[L::STEPS][W];                    // (16 codes of the pool: the first, or half of it)
   float s[L::STEPS];
   uint4* dst[L::STEPS];                    // null: nothing to store
-  float* scale[L::STEPS];
+  uint8_t* scale[L::STEPS];
 };
 
 // As many as the registers of a batch allow; writing E4M3 with a vector a lane on the way and 4
 // CTAs is faster than with two vectors and 3 (32K tokens, 8 groups, d 128).
-template <bool F8, bool WRITE>
-constexpr int kCtasPerSm = F8 && WRITE ? 4 : F8 ? 3 : 4;
+template <int KIND, bool WRITE>
+constexpr int kCtasPerSm = KIND != MSA_CACHE_BF16 && !WRITE ? 3 : 4;
 
-template <int D, bool F8, bool WRITE>
-__global__ void __launch_bounds__(kThreads, (kCtasPerSm<F8, WRITE>)) cache_kernel(const __grid_constant__ CacheParams p) {
-  using L = Lanes<D, F8, WRITE>;
-  using B = Batch<D, F8, WRITE>;
+template <int D, int KIND, bool WRITE>
+__global__ void __launch_bounds__(kThreads, (kCtasPerSm<KIND, WRITE>)) cache_kernel(const __grid_constant__ CacheParams p) {
+  using L = Lanes<D, KIND, WRITE>;
+  using B = Batch<D, KIND, WRITE>;
+  constexpr bool F4 = KIND == MSA_CACHE_E2M1;
   constexpr int W = B::W;
   const int lane = threadIdx.x & 31;
   const int64_t t0 = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5) * p.per;
@@ -166,7 +76,8 @@ __global__ void __launch_bounds__(kThreads, (kCtasPerSm<F8, WRITE>)) cache_kerne
   const int n = (int)min((int64_t)p.per, p.T - t0);
   int64_t place = kNoToken;
   if (lane < n) {
-    place = token_row(p, (int)t0 + lane);
+    int64_t position;
+    place = token_row(p.map, (int)t0 + lane, &position);
     if (place == kNoPlace) set_status(p.status, MSA_ERR_ARG);
   }
   const int half = p.H * L::LPR, units = 2 * half;  // vectors of the keys, and of the values too
@@ -183,8 +94,8 @@ __global__ void __launch_bounds__(kThreads, (kCtasPerSm<F8, WRITE>)) cache_kerne
       const int f = v ? u - half : u, h = f / L::LPR, sub = f % L::LPR;
       __nv_bfloat16* x = v ? p.xv + t * p.sv[0] + h * p.sv[1] : p.xk + t * p.sk[0] + h * p.sk[1];
       uint4* packed = reinterpret_cast<uint4*>(x + sub * L::VALUES);
-      void* pool = static_cast<uint8_t*>(v ? p.v : p.k) + (cell * D + f * L::VALUES) * (F8 ? 1 : 2);
-      if (F8) b.scale[k] = (v ? p.v_scale : p.k_scale) + cell + h;
+      void* pool = static_cast<uint8_t*>(v ? p.v : p.k) + (cell * D + f * L::VALUES) * L::BITS / 8;
+      if (L::CODED) b.scale[k] = (v ? p.v_scale : p.k_scale) + (cell + h) * L::SCALE;
 #pragma unroll
       for (int e = 0; e < W; ++e) b.w[k][e] = make_uint4(0, 0, 0, 0);
       b.s[k] = 0.f;
@@ -196,8 +107,13 @@ __global__ void __launch_bounds__(kThreads, (kCtasPerSm<F8, WRITE>)) cache_kerne
 #pragma unroll
         for (int e = 0; e < W; ++e) b.w[k][e] = __ldg(packed + e);
       } else {
-        b.w[k][0] = *static_cast<const uint4*>(pool);
-        if (F8) b.s[k] = *b.scale[k];
+        if constexpr (F4) {
+          const uint2 c = *static_cast<const uint2*>(pool);
+          b.w[k][0] = make_uint4(c.x, c.y, b.scale[k][4 + sub], 0);  // and the block's scale
+        } else {
+          b.w[k][0] = *static_cast<const uint4*>(pool);
+        }
+        if (L::CODED) b.s[k] = *reinterpret_cast<const float*>(b.scale[k]);
       }
     }
     next_u += 32 * L::STEPS;
@@ -207,7 +123,27 @@ __global__ void __launch_bounds__(kThreads, (kCtasPerSm<F8, WRITE>)) cache_kerne
     }
   };
   auto store = [&](const B& b) {
-    if constexpr (F8 && WRITE) {
+    if constexpr (F4 && WRITE) {
+#pragma unroll
+      for (int k = 0; k < L::STEPS; ++k) {
+        const float most = block_amax(b.w[k][0], b.w[k][W - 1]);
+        float amax = most < INFINITY ? most : 0.f;
+#pragma unroll
+        for (int o = L::LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const int e = row_exponent(amax);
+        uint32_t block;
+        const uint2 c = quantize16(b.w[k][0], b.w[k][W - 1], most, e, &block);
+        const int sub = lane % L::LPR;
+        block <<= 8 * (sub & 3);  // the bytes of four lanes are a word
+        block |= __shfl_xor_sync(0xffffffffu, block, 1);
+        block |= __shfl_xor_sync(0xffffffffu, block, 2);
+        if (!b.dst[k]) continue;
+        *reinterpret_cast<uint2*>(b.dst[k]) = c;
+        uint32_t* scale = reinterpret_cast<uint32_t*>(b.scale[k]);
+        if ((sub & 3) == 0) scale[1 + sub / 4] = block;
+        if (sub == 1) scale[0] = (uint32_t)e << 23;
+      }
+    } else if constexpr (L::CODED && WRITE) {
       float amax[L::STEPS];
       bool far = false;
 #pragma unroll
@@ -252,13 +188,21 @@ __global__ void __launch_bounds__(kThreads, (kCtasPerSm<F8, WRITE>)) cache_kerne
       for (int k = 0; k < L::STEPS; ++k) {
         if (!b.dst[k]) continue;
         *b.dst[k] = c[k];
-        if (lane % L::LPR == 0) *b.scale[k] = sc[k];
+        if (lane % L::LPR == 0) *reinterpret_cast<float*>(b.scale[k]) = sc[k];
       }
-    } else if constexpr (F8) {
+    } else if constexpr (L::CODED) {
 #pragma unroll
       for (int k = 0; k < L::STEPS; ++k) {
         const uint4 c = b.w[k][0];
-        const uint4 y0 = dequantize8(make_uint2(c.x, c.y), b.s[k]), y1 = dequantize8(make_uint2(c.z, c.w), b.s[k]);
+        uint4 y0, y1;
+        if constexpr (F4) {
+          const float s = b.s[k] * e4m3_value(c.z);
+          y0 = dequantize_e2m1(c.x, s);
+          y1 = dequantize_e2m1(c.y, s);
+        } else {
+          y0 = dequantize8(make_uint2(c.x, c.y), b.s[k]);
+          y1 = dequantize8(make_uint2(c.z, c.w), b.s[k]);
+        }
         // a lane's 32 bytes in two stores would write half sectors each: neighbours swap halves, so
         // that a store writes the 32 bytes of every other lane
         const bool odd = lane & 1;
@@ -302,17 +246,26 @@ __global__ void __launch_bounds__(kThreads, (kCtasPerSm<F8, WRITE>)) cache_kerne
   }
 }
 
-template <int D, bool F8, bool WRITE>
+template <int D, int KIND, bool WRITE>
 cudaError_t launch_cache(CacheParams& p, int num_sms, cudaStream_t st) {
   // tokens of a warp: as many as let all warps run together
-  const int64_t together = (int64_t)num_sms * kCtasPerSm<F8, WRITE> * (kThreads / 32);
+  const int64_t together = (int64_t)num_sms * kCtasPerSm<KIND, WRITE> * (kThreads / 32);
   const int64_t want = (p.T + together - 1) / together;
   p.per = (int)(want < 32 ? want : 32);
   const int64_t warps = ((int64_t)p.T + p.per - 1) / p.per;
   const int64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
-  cache_kernel<D, F8, WRITE><<<(unsigned)grid, kThreads, 0, st>>>(p);
+  cache_kernel<D, KIND, WRITE><<<(unsigned)grid, kThreads, 0, st>>>(p);
   note_launch();
   return cudaGetLastError();
+}
+
+template <int D, bool WRITE>
+cudaError_t launch_cache(int kind, CacheParams& p, int num_sms, cudaStream_t st) {
+  switch (kind) {
+    case MSA_CACHE_E4M3: return launch_cache<D, MSA_CACHE_E4M3, WRITE>(p, num_sms, st);
+    case MSA_CACHE_E2M1: return launch_cache<D, MSA_CACHE_E2M1, WRITE>(p, num_sms, st);
+    default: return launch_cache<D, MSA_CACHE_BF16, WRITE>(p, num_sms, st);
+  }
 }
 
 template <bool WRITE>
@@ -339,16 +292,13 @@ int run_cache(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
     if ((i < 4 || k_idx) && strides[i] % 8) return MSA_ERR_ARG;  // rows start on 16 bytes
   Ctx cx;
   if ((rc = device_ctx(&cx))) return rc;
-  p.pages = pages;
-  p.lens = lens;
-  p.cu = cu;
-  p.B = pt->B;
+  p.map = {pages, lens, cu, pt->B};
   p.T = total_tokens;
   p.H = c->H_kv;
   p.k = c->k;
   p.v = c->v;
-  p.k_scale = c->k_scale;
-  p.v_scale = c->v_scale;
+  p.k_scale = reinterpret_cast<uint8_t*>(c->k_scale);
+  p.v_scale = reinterpret_cast<uint8_t*>(c->v_scale);
   p.k_idx = static_cast<__nv_bfloat16*>(c->k_idx);
   p.xk = static_cast<__nv_bfloat16*>(k);
   p.xv = static_cast<__nv_bfloat16*>(v);
@@ -360,15 +310,8 @@ int run_cache(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   p.si = strides[4];
   p.d_idx = c->d_idx;
   p.status = cx.status;
-  const bool f8 = c->kind == MSA_CACHE_E4M3;
-  cudaError_t e;
-  if (c->d == 128)
-    e = f8 ? launch_cache<128, true, WRITE>(p, cx.num_sms, stream)
-           : launch_cache<128, false, WRITE>(p, cx.num_sms, stream);
-  else
-    e = f8 ? launch_cache<64, true, WRITE>(p, cx.num_sms, stream)
-           : launch_cache<64, false, WRITE>(p, cx.num_sms, stream);
-  return finish(e);
+  return finish(c->d == 128 ? launch_cache<128, WRITE>(c->kind, p, cx.num_sms, stream)
+                            : launch_cache<64, WRITE>(c->kind, p, cx.num_sms, stream));
 }
 
 }  // namespace
@@ -377,7 +320,7 @@ int check_cache_sizes(const msa_paged_cache_t* c) {
   if (!c) return MSA_ERR_ARG;
   if (c->num_pages < 0 || c->page_size <= 0 || c->H_kv <= 0 || c->d <= 0 || c->d_idx < 0)
     return MSA_ERR_SHAPE;
-  if (c->kind != MSA_CACHE_BF16 && c->kind != MSA_CACHE_E4M3) return MSA_ERR_ARG;
+  if (c->kind != MSA_CACHE_BF16 && c->kind != MSA_CACHE_E4M3 && c->kind != MSA_CACHE_E2M1) return MSA_ERR_ARG;
   if (c->page_size % 16 != 0 || c->page_size > 65536) return MSA_ERR_UNSUPPORTED;
   if (c->d != 64 && c->d != 128) return MSA_ERR_UNSUPPORTED;
   if (c->d_idx != 0 && c->d_idx != 32 && c->d_idx != 64) return MSA_ERR_UNSUPPORTED;
@@ -389,8 +332,8 @@ int check_cache(const msa_paged_cache_t* c) {
   const int rc = check_cache_sizes(c);
   if (rc) return rc;
   if (c->num_pages == 0) return MSA_OK;  // no page to address
-  const bool f8 = c->kind == MSA_CACHE_E4M3;
-  const void* need[] = {c->k, c->v, f8 ? c->k_scale : c->k, f8 ? c->v_scale : c->v,
+  const bool coded = c->kind != MSA_CACHE_BF16;
+  const void* need[] = {c->k, c->v, coded ? c->k_scale : c->k, coded ? c->v_scale : c->v,
                         c->d_idx ? c->k_idx : c->k};
   for (const void* x : need)
     if (!x || (reinterpret_cast<uintptr_t>(x) & 15)) return MSA_ERR_ARG;

@@ -1,0 +1,209 @@
+// cache_rows.cuh -- rows of a paged cache: where a call's tokens belong, and the codes that a row
+// of bf16 values becomes (cache.cu, append.cu).
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include "paged.cuh"
+
+namespace msa {
+
+// The packed tokens of a call and their pages.
+struct TokenMap {
+  PageView pages;
+  const int32_t* lens;
+  const int32_t* cu;  // null: one token a sequence
+  int B;
+};
+
+constexpr int64_t kNoToken = -1;   // the packed row belongs to no sequence: left as it is
+constexpr int64_t kNoPlace = -2;   // its place does not exist: recorded in the status word
+
+// Pool row of packed token t, and its position in its sequence (where it has a row).
+__device__ __forceinline__ int64_t token_row(const TokenMap& p, int t, int64_t* position) {
+  int b = t, after = 1;
+  if (p.cu) {
+    int lo = 0, hi = p.B - 1;  // last sequence that starts at or before t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldg(&p.cu[mid]) <= t) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    const int first = __ldg(&p.cu[b]), end = __ldg(&p.cu[b + 1]);
+    if (t < first || t >= end) {
+      // behind the last sequence is no error; anything else is a broken cu_seqlens
+      return t >= first && b == p.B - 1 && end >= first ? kNoToken : kNoPlace;
+    }
+    after = end - t;
+  }
+  const int len = __ldg(&p.lens[b]);
+  if (!p.cu && len == 0) return kNoToken;  // an empty slot of a padded decode batch
+  const int64_t pos = (int64_t)len - after;
+  *position = pos;
+  if (pos < 0 || len > (int64_t)p.pages.max_pages * p.pages.page_size) return kNoPlace;
+  const int64_t row = pool_row(p.pages, b, (int)pos);
+  return row < 0 ? kNoPlace : row;
+}
+
+__device__ __forceinline__ float2 widen(uint32_t w) {  // two bf16
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// E4M3 codes of four bf16 pairs divided by sc; out of line, for rows at the ends of the range.
+static __device__ __noinline__ uint2 divide8(uint4 w, float sc) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  uint32_t c[2] = {0, 0};
+#pragma unroll 1
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t v = e == 0 ? u[0] : e == 1 ? u[1] : e == 2 ? u[2] : u[3];
+    const float2 x = widen(v);
+    const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x.x, sc), __fdiv_rn(x.y, sc)), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t put = (two & 0xffffu) << (16 * (e & 1));
+    if (e < 2) c[0] |= put; else c[1] |= put;
+  }
+  return make_uint2(c[0], c[1]);
+}
+
+// A row's scale amax / 448 (1 for an all-zero row), and its reciprocal r for quantize8: an
+// approximate reciprocal with one Newton step.
+__device__ __forceinline__ void row_scale(float amax, float* sc, float* r) {
+  constexpr float kInv = 1.f / 448.f;
+  const float q0 = amax * kInv;
+  *sc = amax > 0.f ? fmaf(fmaf(-q0, 448.f, amax), kInv, q0) : 1.f;
+  float r0;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(*sc));
+  *r = fmaf(r0, fmaf(-*sc, r0, 1.f), r0);
+}
+
+// E4M3 codes of eight values at scale sc: the code nearest to the float32 quotient x / sc.  With r
+// the rounded reciprocal, q0 = x r and the remainder x - q0 sc, which one fma gives exactly,
+// q0 + r (x - q0 sc) is the rounded quotient (Markstein 1990; the scale above likewise); that
+// scales and codes are those that division gives is checked over all pairs of bf16 significands.
+// Rows whose amax leaves the range in which nothing underflows are divided.
+__device__ __forceinline__ uint2 quantize8(uint4 w, float sc, float r) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  const float2 rr = make_float2(r, r), nn = make_float2(-sc, -sc);
+  uint32_t c[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 x = widen(u[e]);
+    const float2 q0 = fmul2(x, rr);
+    float2 q = ffma2(ffma2(q0, nn, x), rr, q0);
+    q = make_float2(copysignf(q.x, x.x), copysignf(q.y, x.y));  // a zero keeps its sign
+    const uint32_t two = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+    c[e >> 1] |= (two & 0xffffu) << (16 * (e & 1));
+  }
+  return make_uint2(c[0], c[1]);
+}
+
+// decode(code) * s of eight codes, rounded to bf16.
+__device__ __forceinline__ uint4 dequantize8(uint2 c, float s) {
+  uint32_t y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)((e < 2 ? c.x : c.y) >> (16 * (e & 1)));
+    const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
+    y[e] = pack_bf16(v.x * s, v.y * s);
+  }
+  return make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+
+// ---------------------------------------------------------------------------
+// 4-bit rows: E2M1 codes, an E4M3 scale for each 16 of them and a power of two for the row.
+// ---------------------------------------------------------------------------
+// Bytes of a row's scales: the row's (float32), then a block's each.
+constexpr int e2m1_scale_bytes(int d) { return 4 + d / 16; }
+
+// An E4M3 code as a float.
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
+}
+
+// The largest magnitude of 16 bf16 values; infinite or NaN where one of them is.
+__device__ __forceinline__ float block_amax(uint4 lo, uint4 hi) {
+  const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  uint32_t m = u[0] & 0x7fff7fffu;
+#pragma unroll
+  for (int e = 1; e < 8; ++e)
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(u[e] & 0x7fff7fffu));
+  uint32_t h;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(h) : "r"(m), "r"(m >> 16));
+  return __uint_as_float(h << 16);
+}
+
+// The exponent field of a row's scale: of the smallest power of two s >= 2^-126 with amax <= 2688 s
+// (2688 = 6 * 448 = 1.3125 * 2^11, the largest value of a block of the largest scale); 1 for amax = 0.
+__device__ __forceinline__ int row_exponent(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = (int)(u >> 23) - 11 + ((u & 0x7fffffu) > 0x280000u);
+  return u == 0 ? 127 : max(e, 1);
+}
+
+// Codes of 16 bf16 values of largest magnitude amax (of the block) at the row scale 2^(e - 127), and
+// their block scale, an E4M3 code:
+//   block = E4M3 nearest to amax / 6 / row, at least 2^-9;  code = E2M1 nearest to x / (block row).
+// amax / 6 by a product: with the rounded 1/6 (too large by 2^-25 of it) a quotient that lies on the
+// border of two E4M3 numbers still rounds to the border, and one that does not is 2^-9 away from it,
+// as amax has 8 significant bits.  The other quotient is x r with one step after it, which makes it the
+// rounded quotient (as in quantize8).  A block that holds an infinity or a NaN gets the scale NaN, so
+// that its values read as NaN.  At the largest row scale the block's ends at 320: 6 * 320 * 2^117 is
+// the largest value that bf16 holds.
+__device__ __forceinline__ uint2 quantize16(uint4 lo, uint4 hi, float amax, int e, uint32_t* block) {
+  const float down = __uint_as_float((uint32_t)(254 - e) << 23);  // 1 / row
+  const float t = fminf(fmaxf(amax * down * (1.f / 6.f), 0x1p-9f), e == 244 ? 320.f : 448.f);
+  const uint32_t code = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
+  const float bs = e4m3_value(code);
+  const float r = __frcp_rn(bs);
+  *block = amax < INFINITY ? code : 0x7fu;
+  const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  const float2 rr = make_float2(r, r), nn = make_float2(-bs, -bs), dd = make_float2(down, down);
+  float2 q[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float2 x = widen(u[k]), y = fmul2(x, dd), q0 = fmul2(y, rr);
+    q[k] = ffma2(ffma2(q0, nn, y), rr, q0);
+    q[k] = make_float2(copysignf(q[k].x, x.x), copysignf(q[k].y, x.y));  // a zero keeps its sign
+  }
+  uint32_t w[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w[k])
+        : "f"(q[4 * k].x), "f"(q[4 * k].y), "f"(q[4 * k + 1].x), "f"(q[4 * k + 1].y), "f"(q[4 * k + 2].x),
+          "f"(q[4 * k + 2].y), "f"(q[4 * k + 3].x), "f"(q[4 * k + 3].y));
+  return make_uint2(w[0], w[1]);
+}
+
+// Eight E2M1 codes as four pairs of fp16 (exact).
+__device__ __forceinline__ void widen_e2m1(uint32_t codes, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(codes));
+}
+
+// code * s of eight E2M1 codes in bf16 (s a block's scale times its row's: exact).
+__device__ __forceinline__ uint4 dequantize_e2m1(uint32_t codes, float s) {
+  uint32_t h[4], y[4];
+  widen_e2m1(codes, h);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
+    y[e] = pack_bf16(v.x * s, v.y * s);
+  }
+  return make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+}  // namespace msa

@@ -764,25 +764,31 @@ _rotated = rope  # for attention, whose argument is named rope too
 # ---------------------------------------------------------------------------
 class PagedCache:
     """A pool of pages: k, v [num_pages, page_size, H_kv, d] bf16, or uint8 E4M3 codes with
-    k_scale, v_scale [num_pages, page_size, H_kv] float32; k_idx [num_pages, page_size, d_idx]
-    bf16, or None for a cache without index keys.  Page tables (int32 [B, max_pages]) and
+    k_scale, v_scale [num_pages, page_size, H_kv] float32, or in 4 bits uint8 [.., H_kv, d / 2] (two
+    E2M1 codes a byte) with k_scale, v_scale uint8 [.., H_kv, 4 + d / 16] (a float32 power of two
+    for the row, an E4M3 scale for each 16 values; see include/msa.h); k_idx [num_pages, page_size,
+    d_idx] bf16, or None for a cache without index keys.  Page tables (int32 [B, max_pages]) and
     lengths (int32 [B]) belong to the calls.  The tensors of a cache are fixed."""
 
     def __init__(self, k, v, k_idx=None, k_scale=None, v_scale=None):
-        fp8 = isinstance(k, torch.Tensor) and k.dtype == torch.uint8
-        kind = torch.uint8 if fp8 else torch.bfloat16
+        coded = isinstance(k, _Tensor) and k.dtype == torch.uint8
+        fp4 = coded and isinstance(k_scale, _Tensor) and k_scale.dtype == torch.uint8
+        fp8 = coded and not fp4
+        kind = torch.uint8 if coded else torch.bfloat16
         _need(k, "k", kind, ndim=4)
         _need(v, "v", kind, ndim=4)
         P, page, H_kv, d = k.shape
+        d = 2 * d if fp4 else d
         if v.shape != k.shape:
             raise ValueError(f"v must be {tuple(k.shape)}, got {tuple(v.shape)}")
-        if (k_scale is not None or v_scale is not None) != fp8 or (k_scale is None) != (v_scale is None):
-            raise ValueError("E4M3 codes (uint8) have k_scale and v_scale; bf16 pages have none")
+        if (k_scale is not None or v_scale is not None) != coded or (k_scale is None) != (v_scale is None):
+            raise ValueError("codes (uint8) have k_scale and v_scale; bf16 pages have none")
+        shape = (P, page, H_kv, 4 + d // 16) if fp4 else (P, page, H_kv)
         for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if t is not None:
-                _need(t, n, torch.float32, ndim=3)
-                if tuple(t.shape) != (P, page, H_kv):
-                    raise ValueError(f"{n} must be {(P, page, H_kv)}, got {tuple(t.shape)}")
+                _need(t, n, torch.uint8 if fp4 else torch.float32, ndim=len(shape))
+                if tuple(t.shape) != shape:
+                    raise ValueError(f"{n} must be {shape}, got {tuple(t.shape)}")
         d_idx = 0
         if k_idx is not None:
             _need(k_idx, "k_idx", ndim=3)
@@ -799,10 +805,12 @@ class PagedCache:
             raise ValueError("a cache has at least one KV head")
         self.k, self.v, self.k_idx, self.k_scale, self.v_scale = k, v, k_idx, k_scale, v_scale
         self._pools = tuple(t for t in (k, v, k_idx, k_scale, v_scale) if t is not None)
-        self.num_pages, self.page_size, self.H_kv, self.d, self.d_idx, self.fp8 = P, page, H_kv, d, d_idx, fp8
+        self.num_pages, self.page_size, self.H_kv, self.d, self.d_idx = P, page, H_kv, d, d_idx
+        self.fp8, self.fp4 = fp8, fp4
         self.device, self.index = k.device, k.get_device()
         self._c = _lib.PAGED_CACHE.pack(
-            P, page, H_kv, d, d_idx, _lib.MSA_CACHE_E4M3 if fp8 else _lib.MSA_CACHE_BF16,
+            P, page, H_kv, d, d_idx,
+            _lib.MSA_CACHE_E2M1 if fp4 else _lib.MSA_CACHE_E4M3 if fp8 else _lib.MSA_CACHE_BF16,
             *(0 if t is None else t.data_ptr() for t in (k, v, k_idx, k_scale, v_scale)))
 
     def __setattr__(self, name, value):
@@ -815,16 +823,23 @@ class PagedCache:
 
 
 def new_paged_cache(num_pages: int, H_kv: int, *, page_size: int = 128, d: int = 128, d_idx: int = 64,
-                    fp8: bool = False, device="cuda") -> PagedCache:
-    """An empty PagedCache (d_idx 0: without index keys)."""
+                    fp8: bool = False, fp4: bool = False, device="cuda") -> PagedCache:
+    """An empty PagedCache (d_idx 0: without index keys), of bf16, E4M3 codes (fp8) or E2M1 codes
+    (fp4: 4.75 bits a value with its scales, 5 with d 64)."""
+    if fp8 and fp4:
+        raise ValueError("fp8 and fp4 exclude one another")
+
     def pages(*tail, dtype):
         return torch.zeros((num_pages, page_size, *tail), dtype=dtype, device=device)
 
-    kv = torch.uint8 if fp8 else torch.bfloat16
-    return PagedCache(pages(H_kv, d, dtype=kv), pages(H_kv, d, dtype=kv),
-                      pages(d_idx, dtype=torch.bfloat16) if d_idx else None,
-                      pages(H_kv, dtype=torch.float32) if fp8 else None,
-                      pages(H_kv, dtype=torch.float32) if fp8 else None)
+    def scales():
+        if fp4:
+            return pages(H_kv, 4 + d // 16, dtype=torch.uint8)
+        return pages(H_kv, dtype=torch.float32) if fp8 else None
+
+    kv, row = (torch.uint8 if fp8 or fp4 else torch.bfloat16), (d // 2 if fp4 else d)
+    return PagedCache(pages(H_kv, row, dtype=kv), pages(H_kv, row, dtype=kv),
+                      pages(d_idx, dtype=torch.bfloat16) if d_idx else None, scales(), scales())
 
 
 def _pages_arg(cache, page_table, lens):
@@ -870,7 +885,7 @@ def _cache_rows(t, name, cache, shape):
 
 
 def msa_cache_write(cache: PagedCache, page_table, lens, k, v, k_idx=None, *, cu_seqlens=None) -> None:
-    """Writes new tokens into the cache's pages, as E4M3 codes and row scales where it holds
+    """Writes new tokens into the cache's pages, as codes and their scales where it holds
     those: k, v [T, H_kv, d], k_idx [T, d_idx] (given exactly if the cache has index keys), bf16,
     any strides.  lens (int32 [B]): lengths after the call; sequence b's n new tokens go to
     positions lens[b] - n .. lens[b] - 1.  cu_seqlens (int32 [B + 1]) splits the T packed tokens;

@@ -338,6 +338,16 @@ int msa_rope(const msa_rope_t* r, const uint64_t* turns, const void* positions,
  *   k, v   [num_pages][page_size][H_kv][d]   bf16, or E4M3 codes (kind MSA_CACHE_E4M3) with
  *   k_scale, v_scale [num_pages][page_size][H_kv] float32 (the rule of msa_quantize_kv_fp8);
  *   k_idx  [num_pages][page_size][d_idx]     bf16 (d_idx = 0: a cache without index keys).
+ * In 4 bits (kind MSA_CACHE_E2M1, 4.75 bits a value with d 128 and 5 with d 64) a row, that is one
+ * head's key or value of a token, is
+ *   k, v [..][H_kv][d / 2] bytes: E2M1 codes, value 2 i in the low half of byte i;
+ *   k_scale, v_scale [..][H_kv][4 + d / 16] bytes: the row's scale (float32, a power of two), then
+ *     an E4M3 scale for each 16 values; a value is code * block scale * row scale.
+ * Written from bf16 values whose largest magnitude is a (b in a block): row scale s = the smallest
+ * power of two >= 2^-126 with a <= 2688 s (1 for a row of zeros), block scale t = the E4M3 number
+ * nearest to b / (6 s), at least 2^-9 (and at most 320 where s is 2^117, so that every value fits
+ * bf16), code = the E2M1 number nearest to x / (t s), ties to even.  A block that holds an infinity
+ * or a NaN gets the scale NaN: its values read as NaN, and it does not count in a.
  * A page table row per sequence names its pages in order (device int32, `stride` elements
  * from row to row): the token at position pos lives in row pos % page_size of page
  * ids[b * stride + pos / page_size].  Entries past a sequence's length are not read.  A
@@ -359,17 +369,19 @@ int msa_rope(const msa_rope_t* r, const uint64_t* turns, const void* positions,
  *   or five element counts (k token, k head, v token, v head, k_idx token), multiples of 8.
  * msa_cache_read: the same rows back, in bf16, to contiguous k, v, k_idx (NULL: not read);
  *   cu_seqlens says how many of each sequence's last tokens (up to position lens[b] - 1)
- *   are wanted.  E4M3 rows are decode(code) * scale rounded once.  Rows behind
+ *   are wanted.  E4M3 rows are decode(code) * scale rounded once, E2M1 rows their values
+ *   (exact in bf16, except below its normal range).  Rows behind
  *   cu_seqlens[B] are left as they are; rows without a place are zeros and set MSA_ERR_ARG.
  */
 #define MSA_CACHE_BF16 0
 #define MSA_CACHE_E4M3 1
+#define MSA_CACHE_E2M1 2
 typedef struct msa_paged_cache {
   int32_t num_pages, page_size, H_kv, d, d_idx, kind;
   void* k;
   void* v;
   void* k_idx;
-  float* k_scale;
+  float* k_scale; /* E2M1: the rows' scale bytes */
   float* v_scale;
 } msa_paged_cache_t;
 typedef struct msa_page_table {

@@ -34,7 +34,7 @@ EXPORTS = ("msa_workspace_size", "msa_index_topk", "msa_fwd", "msa_bwd",
            "msa_decode_workspace_size", "msa_decode", "msa_quantize_kv_fp8",
            "msa_decode_fp8", "msa_quantize_fwd_fp8", "msa_fwd_fp8", "msa_plan_size",
            "msa_index_topk_plan", "msa_fwd_plan", "msa_bwd_plan", "msa_rope", "msa_cache_write",
-           "msa_cache_read", "msa_decode_paged_workspace_size", "msa_decode_paged",
+           "msa_cache_read", "msa_cache_append", "msa_decode_paged_workspace_size", "msa_decode_paged",
            "msa_decode_paged_dense")
 
 MSA_KERNEL_INDEX = 0
@@ -66,6 +66,9 @@ class Problem(ctypes.Structure):
 ROPE = struct.Struct("=7if2q")
 ROPE_TENSOR = struct.Struct("=QQ6qii")
 CACHE_STRIDES = struct.Struct("=5q")
+# msa_append_t: rot_dim, interleaved, positions_bits, mscale, H_q, H_i, positions_stride, then the
+# token and head strides of q, k, v, q_idx and the token stride of k_idx
+APPEND = struct.Struct("=3if2i10q")
 # msa_paged_cache_t: num_pages, page_size, H_kv, d, d_idx, kind, k, v, k_idx, k_scale, v_scale
 PAGED_CACHE = struct.Struct("=6i5Q")
 # msa_page_table_t: ids, B, max_pages, stride
@@ -153,6 +156,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.msa_cache_write.restype = i32
     lib.msa_cache_read.argtypes = [buf, buf, vp, vp, i32, vp, vp, vp, vp]
     lib.msa_cache_read.restype = i32
+    lib.msa_cache_append.argtypes = [buf, buf, vp, vp, i32, buf] + [vp] * 10
+    lib.msa_cache_append.restype = i32
     lib.msa_decode_paged_workspace_size.argtypes = [buf, buf, i32, i32]
     lib.msa_decode_paged_workspace_size.restype = sz
     lib.msa_decode_paged.argtypes = [buf, buf, vp, i32, i32, f32, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -314,6 +319,13 @@ def msa_cache_write(cache: bytes, pages: bytes, lens, cu_seqlens, total_tokens, 
 def msa_cache_read(cache: bytes, pages: bytes, lens, cu_seqlens, total_tokens, k, v, k_idx,
                    stream) -> int:
     return load().msa_cache_read(cache, pages, lens, cu_seqlens, total_tokens, k, v, k_idx, stream)
+
+
+def msa_cache_append(cache: bytes, pages: bytes, lens, cu_seqlens, total_tokens, append: bytes, turns, positions, q,
+                     k, v, q_idx, k_idx, q_out, q_idx_out, stream) -> int:
+    """append: a packed APPEND."""
+    return load().msa_cache_append(cache, pages, lens, cu_seqlens, total_tokens, append, turns, positions, q, k, v,
+                                   q_idx, k_idx, q_out, q_idx_out, stream)
 
 
 def msa_decode_paged_workspace_size(cache: bytes, pages: bytes, H_q: int, topk: int) -> int:

@@ -76,8 +76,7 @@ __global__ void __launch_bounds__(kThreads, (kCtasPerSm<KIND, WRITE>)) cache_ker
   const int n = (int)min((int64_t)p.per, p.T - t0);
   int64_t place = kNoToken;
   if (lane < n) {
-    int64_t position;
-    place = token_row(p.map, (int)t0 + lane, &position);
+    place = token_row(p.map, (int)t0 + lane);
     if (place == kNoPlace) set_status(p.status, MSA_ERR_ARG);
   }
   const int half = p.H * L::LPR, units = 2 * half;  // vectors of the keys, and of the values too
@@ -123,73 +122,10 @@ __global__ void __launch_bounds__(kThreads, (kCtasPerSm<KIND, WRITE>)) cache_ker
     }
   };
   auto store = [&](const B& b) {
-    if constexpr (F4 && WRITE) {
+    if constexpr (L::CODED && WRITE) {
 #pragma unroll
-      for (int k = 0; k < L::STEPS; ++k) {
-        const float most = block_amax(b.w[k][0], b.w[k][W - 1]);
-        float amax = most < INFINITY ? most : 0.f;
-#pragma unroll
-        for (int o = L::LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const int e = row_exponent(amax);
-        uint32_t block;
-        const uint2 c = quantize16(b.w[k][0], b.w[k][W - 1], most, e, &block);
-        const int sub = lane % L::LPR;
-        block <<= 8 * (sub & 3);  // the bytes of four lanes are a word
-        block |= __shfl_xor_sync(0xffffffffu, block, 1);
-        block |= __shfl_xor_sync(0xffffffffu, block, 2);
-        if (!b.dst[k]) continue;
-        *reinterpret_cast<uint2*>(b.dst[k]) = c;
-        uint32_t* scale = reinterpret_cast<uint32_t*>(b.scale[k]);
-        if ((sub & 3) == 0) scale[1 + sub / 4] = block;
-        if (sub == 1) scale[0] = (uint32_t)e << 23;
-      }
-    } else if constexpr (L::CODED && WRITE) {
-      float amax[L::STEPS];
-      bool far = false;
-#pragma unroll
-      for (int k = 0; k < L::STEPS; ++k) {
-        amax[k] = 0.f;
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-          const uint32_t x[4] = {b.w[k][e].x, b.w[k][e].y, b.w[k][e].z, b.w[k][e].w};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float2 y = widen(x[c]);
-            amax[k] = fmax3(amax[k], fabsf(y.x), fabsf(y.y));
-          }
-        }
-      }
-      // a row's lanes are neighbours, and 32 of them hold whole rows
-#pragma unroll
-      for (int o = L::LPR / 2; o > 0; o >>= 1)
-#pragma unroll
-        for (int k = 0; k < L::STEPS; ++k) amax[k] = fmaxf(amax[k], __shfl_xor_sync(0xffffffffu, amax[k], o));
-#pragma unroll
-      for (int k = 0; k < L::STEPS; ++k) far = far || !(amax[k] == 0.f || (amax[k] > 1e-18f && amax[k] < 1e18f));
-      uint4 c[L::STEPS];
-      float sc[L::STEPS];
-      if (!__any_sync(0xffffffffu, far)) {
-#pragma unroll
-        for (int k = 0; k < L::STEPS; ++k) {
-          float r;
-          row_scale(amax[k], &sc[k], &r);
-          const uint2 lo = quantize8(b.w[k][0], sc[k], r), hi = quantize8(b.w[k][W - 1], sc[k], r);
-          c[k] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < L::STEPS; ++k) {
-          sc[k] = amax[k] > 0.f ? __fdiv_rn(amax[k], 448.0f) : 1.0f;
-          const uint2 lo = divide8(b.w[k][0], sc[k]), hi = divide8(b.w[k][W - 1], sc[k]);
-          c[k] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < L::STEPS; ++k) {
-        if (!b.dst[k]) continue;
-        *b.dst[k] = c[k];
-        if (lane % L::LPR == 0) *reinterpret_cast<float*>(b.scale[k]) = sc[k];
-      }
+      for (int k = 0; k < L::STEPS; ++k)
+        store_codes<D, KIND>(b.w[k][0], b.w[k][W - 1], b.dst[k], b.scale[k], b.dst[k] != nullptr);
     } else if constexpr (L::CODED) {
 #pragma unroll
       for (int k = 0; k < L::STEPS; ++k) {

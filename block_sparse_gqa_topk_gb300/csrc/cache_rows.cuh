@@ -21,8 +21,9 @@ struct TokenMap {
 constexpr int64_t kNoToken = -1;   // the packed row belongs to no sequence: left as it is
 constexpr int64_t kNoPlace = -2;   // its place does not exist: recorded in the status word
 
-// Pool row of packed token t, and its position in its sequence (where it has a row).
-__device__ __forceinline__ int64_t token_row(const TokenMap& p, int t, int64_t* position) {
+// The sequence of packed token t and the token's position there; >= 0 (the position), or kNoToken or
+// kNoPlace.
+__device__ __forceinline__ int64_t token_position(const TokenMap& p, int t, int* sequence) {
   int b = t, after = 1;
   if (p.cu) {
     int lo = 0, hi = p.B - 1;  // last sequence that starts at or before t
@@ -38,11 +39,19 @@ __device__ __forceinline__ int64_t token_row(const TokenMap& p, int t, int64_t* 
     }
     after = end - t;
   }
+  *sequence = b;
   const int len = __ldg(&p.lens[b]);
   if (!p.cu && len == 0) return kNoToken;  // an empty slot of a padded decode batch
   const int64_t pos = (int64_t)len - after;
-  *position = pos;
   if (pos < 0 || len > (int64_t)p.pages.max_pages * p.pages.page_size) return kNoPlace;
+  return pos;
+}
+
+// Pool row of packed token t, or kNoToken or kNoPlace.
+__device__ __forceinline__ int64_t token_row(const TokenMap& p, int t) {
+  int b;
+  const int64_t pos = token_position(p, t, &b);
+  if (pos < 0) return pos;
   const int64_t row = pool_row(p.pages, b, (int)pos);
   return row < 0 ? kNoPlace : row;
 }
@@ -180,6 +189,57 @@ __device__ __forceinline__ uint2 quantize16(uint4 lo, uint4 hi, float amax, int 
         : "f"(q[4 * k].x), "f"(q[4 * k].y), "f"(q[4 * k + 1].x), "f"(q[4 * k + 1].y), "f"(q[4 * k + 2].x),
           "f"(q[4 * k + 2].y), "f"(q[4 * k + 3].x), "f"(q[4 * k + 3].y));
   return make_uint2(w[0], w[1]);
+}
+
+// A row of D bf16 values in D / 16 neighbouring lanes of a warp, 16 each, stored as codes (dst: the lane's)
+// with the row's scales.  All lanes of the warp come here; those that are not `there` store nothing.
+template <int D, int KIND>
+__device__ __forceinline__ void store_codes(uint4 lo, uint4 hi, void* dst, uint8_t* scale, bool there) {
+  constexpr int LPR = D / 16;
+  const int sub = threadIdx.x % LPR;
+  if constexpr (KIND == MSA_CACHE_E2M1) {
+    const float most = block_amax(lo, hi);
+    float amax = most < INFINITY ? most : 0.f;
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const int e = row_exponent(amax);
+    uint32_t block;
+    const uint2 c = quantize16(lo, hi, most, e, &block);
+    block <<= 8 * (sub & 3);  // the bytes of four lanes are a word
+    block |= __shfl_xor_sync(0xffffffffu, block, 1);
+    block |= __shfl_xor_sync(0xffffffffu, block, 2);
+    if (!there) return;
+    *static_cast<uint2*>(dst) = c;
+    uint32_t* words = reinterpret_cast<uint32_t*>(scale);
+    if ((sub & 3) == 0) words[1 + sub / 4] = block;
+    if (sub == 1) words[0] = (uint32_t)e << 23;
+  } else {
+    const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    float amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 x = widen(u[e]);
+      amax = fmax3(amax, fabsf(x.x), fabsf(x.y));
+    }
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const bool far = !(amax == 0.f || (amax > 1e-18f && amax < 1e18f));
+    uint2 c0, c1;
+    float sc;
+    if (!__any_sync(0xffffffffu, far)) {
+      float r;
+      row_scale(amax, &sc, &r);
+      c0 = quantize8(lo, sc, r);
+      c1 = quantize8(hi, sc, r);
+    } else {
+      sc = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+      c0 = divide8(lo, sc);
+      c1 = divide8(hi, sc);
+    }
+    if (!there) return;
+    *static_cast<uint4*>(dst) = make_uint4(c0.x, c0.y, c1.x, c1.y);
+    if (sub == 0) *reinterpret_cast<float*>(scale) = sc;
+  }
 }
 
 // Eight E2M1 codes as four pairs of fp16 (exact).

@@ -10,11 +10,8 @@
 // turn.  position * turns[i] in wrapping 64-bit arithmetic is the angle's fraction of a
 // turn without rounding, so position 2^20 is as exact as position 1; its signed value is
 // rounded once to float and handed to sincospif.  No table is read or kept.
-#include <cuda_fp16.h>
-#include <math.h>
-
-#include "common.cuh"
 #include "kernels.h"
+#include "rope_items.cuh"
 
 namespace msa {
 namespace {
@@ -45,27 +42,6 @@ struct RopeParams {
   RopeTensor t[kMaxRopeTensors];
 };
 
-template <typename T> __device__ __forceinline__ float to_f(T v);
-template <> __device__ __forceinline__ float to_f(float v) { return v; }
-template <> __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <> __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-template <typename T> __device__ __forceinline__ T from_f(float v);
-template <> __device__ __forceinline__ float from_f(float v) { return v; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16(v); }
-template <> __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
-
-// V values moved by one load: 16 bytes, or a single value where strides or addresses do
-// not allow more.
-template <typename T, int V>
-struct alignas(V * sizeof(T)) Pack {
-  T v[V];
-};
-
-// x / q for 0 <= x < 2^18 and q < 2^14 with m = ceil(2^32 / q): x m / 2^32 exceeds x / q by less
-// than 2^18 / 2^32 < 1 / q.  (q = 1 has m = 2^32, which does not fit: m = 0 stands for it.)
-__device__ __forceinline__ int small_div(int x, uint32_t m) { return m ? (int)__umulhi((uint32_t)x, m) : x; }
-uint32_t magic(int q) { return q == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + q - 1) / q); }
-
 // One CTA serves tpb tokens: their sines and cosines, and where their rows start, go to
 // shared memory once; then the items (V pairs of one head, or 2 V values to copy) of all the
 // tensors together are spread over the threads.  Bound by HBM: every value is read and written
@@ -88,10 +64,8 @@ __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant
       pos = p.pos64 ? __ldg(static_cast<const int64_t*>(p.positions) + at)
                     : (int64_t)__ldg(static_cast<const int32_t*>(p.positions) + at);
     }
-    const int64_t frac = (int64_t)((uint64_t)pos * __ldg(&p.turns[pair]));
-    float s, c;
-    sincospif((float)frac * 1.0842021724855044e-19f /* 2^-63: half turns */, &s, &c);
-    s_cs[i] = make_float2(c * p.mscale, s * p.mscale * p.sign);
+    const float2 w = turn_of(pos, __ldg(&p.turns[pair]), p.mscale);
+    s_cs[i] = make_float2(w.x, w.y * p.sign);
   }
   if (threadIdx.x < p.n * kMaxTokens) {
     const int ti = threadIdx.x / kMaxTokens, tok = threadIdx.x % kMaxTokens;
@@ -107,29 +81,11 @@ __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant
     if (ti > 0) x -= nt * p.t[ti - 1].last;
     const int row = small_div(x, a.div_parts), part = x - row * a.parts;
     const int tok = small_div(row, a.div_H), h = row - tok * a.H;
-    const bool turn = part < a.rot_parts;
-    // first vector of the item in its head, and the distance of the second one (0: none)
-    const int at = turn ? (INTER ? part * 2 * V : part * V) : 2 * p.half + (part - a.rot_parts) * 2 * V;
-    const int step = turn ? (INTER ? V : p.half) : at + V < a.d ? V : 0;
     const longlong2 off = s_off[ti][tok];
-    const T* src = static_cast<const T*>(a.x) + (off.x + h * a.xs[2] + at);
-    T* dst = static_cast<T*>(a.y) + (off.y + h * a.ys[2] + at);
-    Pack<T, V> lo = *reinterpret_cast<const Pack<T, V>*>(src), hi;
-    if (step) hi = *reinterpret_cast<const Pack<T, V>*>(src + step);
-    if (turn) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float2 w = s_cs[tok * p.half + part * V + e];
-        // the pair's two values: the vectors side by side, or neighbours in them
-        T* p1 = INTER ? (2 * e < V ? &lo.v[(2 * e) % V] : &hi.v[(2 * e) % V]) : &lo.v[e];
-        T* p2 = INTER ? (2 * e + 1 < V ? &lo.v[(2 * e + 1) % V] : &hi.v[(2 * e + 1) % V]) : &hi.v[e];
-        const float x1 = to_f(*p1), x2 = to_f(*p2);
-        *p1 = from_f<T>(x1 * w.x - x2 * w.y);
-        *p2 = from_f<T>(x2 * w.x + x1 * w.y);
-      }
-    }
-    *reinterpret_cast<Pack<T, V>*>(dst) = lo;
-    if (step) *reinterpret_cast<Pack<T, V>*>(dst + step) = hi;
+    RopeItem<T, V> it(part, a.rot_parts, p.half, a.d, INTER);
+    it.load(static_cast<const T*>(a.x) + (off.x + h * a.xs[2]));
+    if (it.turn) it.template rotate<INTER>(s_cs + tok * p.half, part);
+    it.store(static_cast<T*>(a.y) + (off.y + h * a.ys[2]));
   }
 }
 

@@ -912,6 +912,79 @@ def msa_cache_write(cache: PagedCache, page_table, lens, k, v, k_idx=None, *, cu
     torch.autograd.graph.increment_version(cache._pools)  # a graph that saved one of them must notice
 
 
+def _turned_rows(t, name, cache, T, d):
+    """A query of msa_cache_append [T, heads, d] (copied where its last axis is strided), its address,
+    strides and heads."""
+    if not isinstance(t, _Tensor) or t.dtype != _BF16:
+        raise TypeError(f"{name} must be a bf16 tensor")
+    if t.get_device() != cache.index:
+        raise ValueError(f"{name} must be on the cache's device (no CPU path exists)")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != d or not 1 <= shape[1] <= 1024:
+        raise ValueError(f"{name} must be [{T}, heads (at most 1024), {d}], got {tuple(shape)}")
+    s = t.stride()
+    if s[2] != 1:
+        t = t.contiguous()
+        s = t.stride()
+    return t, t.data_ptr(), s[0], s[1], shape[1]
+
+
+def msa_cache_append(cache: PagedCache, page_table, lens, rope: Rope, q, k, v, q_idx=None, k_idx=None, *,
+                     positions=None, cu_seqlens=None):
+    """msa_rope of q, k, q_idx and k_idx and msa_cache_write of the turned k and k_idx and of v, in one
+    launch and with their results bit for bit: returns (q, q_idx) turned (new tensors).
+
+    q [T, H_q, d], k, v [T, H_kv, d], q_idx [T, heads, d_idx], k_idx [T, d_idx] (q_idx and k_idx given
+    exactly if the cache has index keys), bf16, any strides.  lens, cu_seqlens: as in msa_cache_write
+    (without cu_seqlens one token a sequence, lens[b] = 0 an empty slot).  positions: int32 or int64
+    [T], or None: each token's place in its sequence.  rot_dim of the rope at most d and d_idx.  A token
+    that is not written (an empty slot, behind the last sequence, or without a place, which sets the
+    device status) gets zero rows in q and q_idx.  Autograd does not see this call."""
+    pages, B = _pages_arg(cache, page_table, lens)
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must come from new_rope")
+    turns, rot, d, d_idx = rope.turns, rope.rot_dim, cache.d, cache.d_idx
+    if turns.get_device() != cache.index:
+        raise ValueError("rope must be on the cache's device")
+    if rot > d or (d_idx and rot > d_idx):
+        raise ValueError(f"rot_dim = {rot} is more than a head holds ({d}, index heads {d_idx or 'none'})")
+    if (q_idx is None) != (d_idx == 0) or (k_idx is None) != (d_idx == 0):
+        raise ValueError("q_idx and k_idx must be given exactly if the cache has index keys")
+    T = q.shape[0] if isinstance(q, _Tensor) and q.dim() == 3 else 0
+    q, pq, q0, q1, H_q = _turned_rows(q, "q", cache, T, d)
+    k, pk, sk = _cache_rows(k, "k", cache, (T, cache.H_kv, d))
+    v, pv, sv = _cache_rows(v, "v", cache, (T, cache.H_kv, d))
+    pqi, qi0, qi1, H_i, pki, ki0 = None, 0, 0, 0, None, 0
+    if d_idx:
+        q_idx, pqi, qi0, qi1, H_i = _turned_rows(q_idx, "q_idx", cache, T, d_idx)
+        k_idx, pki, ski = _cache_rows(k_idx, "k_idx", cache, (T, d_idx))
+        ki0 = ski[0]
+    bits, at, ps = 32, None, 0
+    if positions is not None:
+        if not isinstance(positions, _Tensor) or positions.dtype not in (_I32, torch.int64):
+            raise TypeError("positions must be an int32 or int64 tensor")
+        if positions.get_device() != cache.index or positions.shape != (T,):
+            raise ValueError(f"positions must be [{T}] on the cache's device, got {tuple(positions.shape)}")
+        at, ps = positions.data_ptr(), positions.stride(0)
+        if positions.dtype != _I32:
+            bits = 64
+    cu = None
+    if cu_seqlens is not None:
+        cu = _cu_arg(cu_seqlens, cache, B)
+    elif T != B:
+        raise ValueError(f"without cu_seqlens there is one token a sequence: {B}, got {T}")
+    empty = torch.empty if B else torch.zeros  # no sequence: every row is behind the last one
+    y = empty((T, H_q, d), dtype=_BF16, device=cache.device)
+    yi = empty((T, H_i, d_idx), dtype=_BF16, device=cache.device) if d_idx else None
+    if T and B:
+        a = _lib.APPEND.pack(rot, rope.interleaved, bits, rope.mscale, H_q, H_i, ps, q0, q1, sk[0], sk[1], sv[0], sv[1],
+                             qi0, qi1, ki0)
+        _call(cache.index, "msa_cache_append", _lib.msa_cache_append, cache._c, pages, lens.data_ptr(), cu, T, a,
+              turns.data_ptr(), at, pq, pk, pv, pqi, pki, y.data_ptr(), _ptr(yi))
+        torch.autograd.graph.increment_version(cache._pools)
+    return y, yi
+
+
 def msa_cache_read(cache: PagedCache, page_table, lens, cu_seqlens, total_tokens: int):
     """The last cu_seqlens[b + 1] - cu_seqlens[b] tokens of every sequence (up to position
     lens[b] - 1) in packed order: k, v [total_tokens, H_kv, d] and k_idx [total_tokens, d_idx]

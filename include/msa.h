@@ -397,6 +397,33 @@ int msa_cache_read(const msa_paged_cache_t* c, const msa_page_table_t* pages, co
                    cudaStream_t stream);
 
 /*
+ * A call's new tokens turned to their positions and appended to a paged cache, in one launch: the
+ * results of msa_rope on q, k, q_idx and k_idx and of msa_cache_write on the turned k and k_idx and on
+ * v, bit for bit (a cache of codes codes the turned keys as they are in bf16).
+ * In:  q [total_tokens][H_q][d], k, v [total_tokens][H_kv][d], q_idx [total_tokens][H_i][d_idx],
+ *   k_idx [total_tokens][d_idx], bf16, with the strides of msa_append_t in elements (those of k, v and
+ *   k_idx multiples of 8 and their addresses of 16 bytes; q and q_idx at any address).  q_idx, k_idx
+ *   and q_idx_out are given exactly if the cache has index keys.  turns, mscale, interleaved, rot_dim:
+ *   as in msa_rope; rot_dim at most d and d_idx.  positions: device int32 or int64 [total_tokens], or
+ *   NULL for the tokens' places in their sequences.  pages, lens, cu_seqlens: as in msa_cache_write.
+ * Out: q_out [total_tokens][H_q][d], q_idx_out [total_tokens][H_i][d_idx] (contiguous, 16-byte aligned,
+ *   apart from the inputs).  A token that msa_cache_write skips (an empty slot, behind
+ *   cu_seqlens[B]) or drops (no place: MSA_ERR_ARG in the status word) gets zero rows there.
+ */
+typedef struct msa_append {
+  int32_t rot_dim, interleaved, positions_bits; /* 32 or 64 */
+  float mscale;
+  int32_t H_q, H_i;
+  int64_t positions_stride;
+  int64_t q_stride[2], k_stride[2], v_stride[2], q_idx_stride[2]; /* token, head */
+  int64_t k_idx_stride;
+} msa_append_t;
+int msa_cache_append(const msa_paged_cache_t* c, const msa_page_table_t* pages, const int32_t* lens,
+                     const int32_t* cu_seqlens, int total_tokens, const msa_append_t* a, const uint64_t* turns,
+                     const void* positions, const void* q, const void* k, const void* v, const void* q_idx,
+                     const void* k_idx, void* q_out, void* q_idx_out, cudaStream_t stream);
+
+/*
  * Decode over a paged cache: one new query token per sequence, its own k, v and k_idx
  * already in the cache (msa_cache_write), lens[b] the length with it.
  *   msa_decode_paged: msa_decode's computation (block selection over the index keys, ties to

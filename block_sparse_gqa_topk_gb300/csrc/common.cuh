@@ -403,6 +403,14 @@ __device__ __forceinline__ void cp_async_4(void* dst, const void* src, bool pred
                "r"(n)
                : "memory");
 }
+// The same to shared-memory addresses.
+__device__ __forceinline__ void cp_async_16_to(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>  // 4, 8 or 16 bytes (zero-fill when predicated off)
+__device__ __forceinline__ void cp_async_to(uint32_t dst, const void* src, bool pred) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(pred ? N : 0), "n"(N) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {

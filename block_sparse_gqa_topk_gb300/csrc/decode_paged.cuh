@@ -227,8 +227,8 @@ __device__ __forceinline__ float weight(float a, float b) { return a == -INFINIT
 //   bf16: rows of 2 D bytes, 16-byte chunks XOR-swizzled for ldmatrix;
 //   E4M3: key rows of D bytes whose 64-byte halves are swapped in odd rows, value rows padded
 //   by 16 bytes: the fragment loads then fall in distinct banks;
-//   E2M1: key rows of D / 2 bytes, value rows padded by 16 bytes, for the same reason, and behind the
-//   row scales the blocks' [2][KEYS][D / 16].
+//   E2M1: key rows of D / 2 bytes, value rows padded by 16 bytes, for the same reason; the records of
+//   scales lie behind all warps' stages.
 template <int D, int KIND, bool WIDE>
 struct Stage {
   static constexpr bool CODED = KIND != MSA_CACHE_BF16, F4 = KIND == MSA_CACHE_E2M1;
@@ -238,14 +238,18 @@ struct Stage {
   static constexpr int BLOCKS = F4 ? D / 16 : 0;         // block scales of a row
   static constexpr int SCALE = CODED ? 4 + BLOCKS : 0;   // bytes of a row's scales in the pool
   static constexpr int V0 = KEYS * ROW;
-  static constexpr int S0 = V0 + KEYS * VROW;  // [2][KEYS] scales
-  static constexpr int B0 = S0 + (CODED ? 2 * KEYS * 4 : 0);  // [2][KEYS][BLOCKS] block scales
-  static constexpr int BYTES = B0 + 2 * KEYS * BLOCKS;
+  static constexpr int S0 = V0 + KEYS * VROW;  // [2][KEYS] scales of E4M3 rows
+  static constexpr int BYTES = S0 + (CODED && !F4 ? 2 * KEYS * 4 : 0);
+  // E2M1: the scales of a stage, [2][KEYS] records as in the pool (the warps' one after another, or
+  // [2][KEYS][4] of four groups together)
+  static constexpr int SCALES = F4 ? 2 * KEYS * SCALE : 0;
   // CTAs of a SM.  More than 8 heads with d = 128 take more than the 168 registers a thread that
   // three CTAs leave: two with a third stage serve them better (8 x 128K, 16 heads a group, E4M3:
   // 423 -> 392 us), but not with d = 64 (E4M3 269 -> 321 us).
   static constexpr int PER_SM = WIDE && D == 128 ? 2 : 3;
   static constexpr int COUNT = PER_SM == 2 ? 3 : 2;
+  static constexpr int RINGS = kWarps * COUNT * BYTES;           // bytes of all stages without E2M1's scales
+  static constexpr int SMEM = RINGS + kWarps * COUNT * SCALES;  // and with them
   static constexpr int UNIT = KEYS * kWarps;  // tokens of a unit of work
   static constexpr int PER = 128 / UNIT;      // units of a block
   static constexpr int HALVES = KEYS / 16;    // runs of 16 tokens, which never straddle a page
@@ -288,15 +292,13 @@ struct WarpState {
   static constexpr int MT = D / 16;          // tiles of 16 value columns
   static constexpr int KT = St::KEYS / 8;    // tiles of 8 keys
   static constexpr int QS = D / 16;
-  static constexpr bool CODED = St::CODED, F4 = St::F4;
+  static constexpr bool CODED = St::CODED;
+  static_assert(!St::F4, "4 bits have their own");
   uint32_t qa[QS][4];       // query fragments
   float o[MT][R][4];
   float m[R], mv[R], l[R];  // max, max with the value scale relative to it (codes), lane's part of the sum
   float fac[R];             // accumulator -> score in bits
   bool far;                 // codes: the queries are bf16, not fp16
-
-  // A lane's values of a query, and of a key's codes, are D / 64 runs of 16; where run j starts.
-  __device__ __forceinline__ static int run(int j, int tq) { return F4 ? D / 4 * tq + 16 * j : 64 * j + 16 * tq; }
 
   __device__ __forceinline__ void load_q(const PagedDecode& p, int64_t head0, int gq, int tq) {
     bool lost = false, huge[R] = {};
@@ -313,7 +315,7 @@ struct WarpState {
             qa[ks][r + 2 * half] =
                 r < R && ok ? __ldg(reinterpret_cast<const uint32_t*>(row + ks * 16 + half * 8 + 2 * tq)) : 0u;
       } else if (r < R) {
-        // lane tq holds runs j of 16 values of the row, in the order in which step() reads
+        // lane tq holds values 64 j + 16 tq + 0..15 of the row, in the order in which step() reads
         // the codes of a key: values 4 s + {0, 1} and 4 s + {2, 3} of them are k slots 2 tq.. and
         // 8 + 2 tq.. of k step 4 j + s
         float2 f[D / 64][8];
@@ -322,7 +324,7 @@ struct WarpState {
         for (int j = 0; j < D / 64; ++j)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const uint4 w = ok ? __ldg(reinterpret_cast<const uint4*>(row + run(j, tq) + 8 * half))
+            const uint4 w = ok ? __ldg(reinterpret_cast<const uint4*>(row + 64 * j + 16 * tq + 8 * half))
                                : make_uint4(0, 0, 0, 0);
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -370,7 +372,7 @@ struct WarpState {
           fac[r] = p.scale_log2 / down;
 #pragma unroll
           for (int w = 0; w < D / 8; ++w) {
-            const int at = run(w >> 3, tq) + 2 * (w & 7);
+            const int at = 64 * (w >> 3) + 16 * tq + 2 * (w & 7);
             const uint32_t u = h < p.G ? __ldg(reinterpret_cast<const uint32_t*>(p.q + (head0 + h) * D + at)) : 0u;
             qa[w >> 1][r + 2 * (w & 1)] =
                 pack_bf16(__uint_as_float(u << 16) * down, __uint_as_float(u & 0xffff0000u) * down);
@@ -428,39 +430,6 @@ struct WarpState {
           mma_bf16_16816(sc[2 * kp + 1], qa[ks], kb[2], kb[3]);
         }
       }
-    } else if constexpr (F4) {
-      // as below, the lane's D / 64 blocks of 16 codes of key gq side by side
-      auto products = [&](bool in_bf16) {
-#pragma unroll
-        for (int t = 0; t < KT; ++t) {
-          uint32_t u[D / 32], scale[D / 64];
-          const uint8_t* codes = st + (8 * t + gq) * St::ROW + tq * (D / 8);
-          const uint8_t* block = st + St::B0 + (8 * t + gq) * St::BLOCKS + tq * (D / 64);
-          if constexpr (D == 128) {
-            const uint4 c = *reinterpret_cast<const uint4*>(codes);
-            u[0] = c.x, u[1] = c.y, u[2] = c.z, u[3] = c.w;
-            const uint32_t two = widen_f16(*reinterpret_cast<const uint16_t*>(block));
-            scale[0] = __byte_perm(two, two, 0x1010);
-            scale[1] = __byte_perm(two, two, 0x3232);
-          } else {
-            const uint2 c = *reinterpret_cast<const uint2*>(codes);
-            u[0] = c.x, u[1] = c.y;
-            scale[0] = widen_f16(*block * 0x0101u);
-          }
-#pragma unroll
-          for (int w = 0; w < D / 32; ++w) {
-            uint32_t k[4];
-            widen_scaled(u[w], scale[w / 2], k);
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              if (in_bf16) mma_bf16_16816(sc[t], qa[2 * w + s], f16_to_bf16(k[2 * s]), f16_to_bf16(k[2 * s + 1]));
-              else mma_f16_16816(sc[t], qa[2 * w + s], k[2 * s], k[2 * s + 1]);
-            }
-          }
-        }
-      };
-      if (far) products(true);
-      else products(false);
     } else {
       // the order of a product's terms is free: lane tq takes values 64 j + 16 tq + 0..15 of
       // key gq as the k slots of steps 4 j .. 4 j + 3, and so do the query fragments
@@ -483,7 +452,7 @@ struct WarpState {
       else products(false);
     }
     // scores in bits; this lane's keys: 8 t + 2 tq + e
-    float2 lv[CODED ? KT : 1];  // log2 of the value scales (the rows')
+    float2 lv[CODED ? KT : 1];  // log2 of the value scales
     if constexpr (CODED) {
       const float* scale = reinterpret_cast<const float*>(st + St::S0);
 #pragma unroll
@@ -598,64 +567,26 @@ struct WarpState {
         for (int r = 0; r < R; ++r)
 #pragma unroll
           for (int t = 0; t < 2; ++t) pb[r][t] = pack_f16(sc[2 * kp + t][2 * r], sc[2 * kp + t][2 * r + 1]);
-        if constexpr (F4) {
-          // row gq (+ 8) of tile i is value column D / 8 gq + 2 i (+ 1): a lane's D / 8 codes of each of
-          // its four keys, one block's, serve all tiles.  The codes of two keys go side by side into
-          // a byte, so that they come out as a pair, with the pair of their block's scales.
-          uint32_t w[4][D / 64], scale[2];
-          const int key = 16 * kp + 2 * tq;  // keys key, + 1, + 8, + 9
-          const uint8_t* block = st + St::B0 + (St::KEYS + key) * St::BLOCKS + gq * (D / 8) / 16;
+        // row gq (+ 8) of tile 4 c + i is value column 64 c + 8 gq + 2 i (+ 1): a lane's 8 codes
+        // of each of its four keys serve four tiles, two keys side by side in a register
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint2 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = *reinterpret_cast<const uint2*>(
+                st + St::V0 + (16 * kp + (i >> 1) * 8 + 2 * tq + (i & 1)) * St::VROW + 64 * c + 8 * gq);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint8_t* codes = st + St::V0 + (key + (i >> 1) * 8 + (i & 1)) * St::VROW + gq * (D / 16);
-            if constexpr (D == 128) {
-              const uint2 c = *reinterpret_cast<const uint2*>(codes);
-              w[i][0] = c.x, w[i][1] = c.y;
-            } else {
-              w[i][0] = *reinterpret_cast<const uint32_t*>(codes);
-            }
-          }
+            uint32_t va[4];
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            scale[e] = widen_f16(block[8 * e * St::BLOCKS] | (uint32_t)block[(8 * e + 1) * St::BLOCKS] << 8);
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            uint32_t va[4][4];  // [keys 8..15, column 2 i + 1][i], in the order of a fragment's registers
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t x = w[2 * e][c], y = w[2 * e + 1][c];
-              widen_scaled((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), scale[e], va[2 * e]);
-              widen_scaled(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), scale[e], va[2 * e + 1]);
+            for (int e = 0; e < 4; ++e) {  // e & 1: column 2 i + 1; e >> 1: keys 8..15
+              const uint2 x = w[2 * (e >> 1)], y = w[2 * (e >> 1) + 1];
+              const int byte = (2 * i + (e & 1)) & 3;
+              va[e] = widen_f16(__byte_perm(i < 2 ? x.x : x.y, i < 2 ? y.x : y.y, byte | ((4 + byte) << 4)));
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t a[4] = {va[0][i], va[1][i], va[2][i], va[3][i]};
-#pragma unroll
-              for (int r = 0; r < R; ++r) mma_f16_16816(o[4 * c + i][r], a, pb[r][0], pb[r][1]);
-            }
-          }
-        } else {
-          // row gq (+ 8) of tile 4 c + i is value column 64 c + 8 gq + 2 i (+ 1): a lane's 8 codes
-          // of each of its four keys serve four tiles, two keys side by side in a register
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            uint2 w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = *reinterpret_cast<const uint2*>(
-                  st + St::V0 + (16 * kp + (i >> 1) * 8 + 2 * tq + (i & 1)) * St::VROW + 64 * c + 8 * gq);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t va[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {  // e & 1: column 2 i + 1; e >> 1: keys 8..15
-                const uint2 x = w[2 * (e >> 1)], y = w[2 * (e >> 1) + 1];
-                const int byte = (2 * i + (e & 1)) & 3;
-                va[e] = widen_f16(__byte_perm(i < 2 ? x.x : x.y, i < 2 ? y.x : y.y, byte | ((4 + byte) << 4)));
-              }
-#pragma unroll
-              for (int r = 0; r < R; ++r) mma_f16_16816(o[4 * c + i][r], va, pb[r][0], pb[r][1]);
-            }
+            for (int r = 0; r < R; ++r) mma_f16_16816(o[4 * c + i][r], va, pb[r][0], pb[r][1]);
           }
         }
       }
@@ -664,10 +595,289 @@ struct WarpState {
 
   // Value column that o[i][.][e] holds; its head is 8 r + 2 tq + (e & 1).
   __device__ __forceinline__ static int column(int i, int e, int gq) {
-    return F4   ? D / 8 * gq + 2 * i + (e >> 1)
-           : CODED ? (i >> 2) * 64 + 8 * gq + 2 * (i & 3) + (e >> 1)
-                   : 16 * i + gq + 8 * (e >> 1);
+    return CODED ? (i >> 2) * 64 + 8 * gq + 2 * (i & 3) + (e >> 1) : 16 * i + gq + 8 * (e >> 1);
   }
+};
+
+// A matrix of 8 x 8 16-bit values, row gq and columns 2 tq, 2 tq + 1 a lane, turned over.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
+  uint32_t t;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(t) : "r"(a));
+  return t;
+}
+
+// The running softmax over 4-bit keys.  Widening the codes takes the ALU (a conversion a pair, 2 cycles) and the
+// FMA pipe (a product with the block's scale a pair, 2 cycles), and mma.sync (8 cycles) holds up the
+// latter, so its products are few:
+//   S^T = K Q^T: rows are keys, columns the heads 8 r + 2 tq + e (no idle rows; heads as rows: 16 of
+//   32 products idle, 8 x 128K 38 us more);  O^T = V^T P^T as above, P^T turned over by movmatrix.
+// A lane's 4 keys of 32 meet the 2 heads of its columns, so maxima go over 8 lanes; that is left out while
+// no score passes the running ones.
+template <int D, bool WIDE>
+struct WarpState<D, MSA_CACHE_E2M1, WIDE> {
+  using St = Stage<D, MSA_CACHE_E2M1, WIDE>;
+  static constexpr int R = WIDE ? 2 : 1;  // tiles of 8 heads
+  static constexpr int MT = D / 16;       // tiles of 16 value columns
+  static constexpr int KP = St::KEYS / 16;
+  static constexpr int QS = D / 16;
+  uint32_t qb[QS][R][2];  // query fragments
+  float o[MT][R][4];
+  float m[R][2], mv[R][2], l[R][2];  // of heads 8 r + 2 tq + e: as in the form above
+  float fac[R][2];
+  bool far;
+
+  __device__ __forceinline__ void load_q(const PagedDecode& p, int64_t head0, int gq, int tq) {
+    bool lost = false, huge[R] = {};
+    float row_fac[R];  // of heads 8 r + gq
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int h = gq + 8 * r;
+      const bool ok = h < p.G;
+      const __nv_bfloat16* row = p.q + (head0 + (ok ? h : 0)) * D + D / 4 * tq;
+      // lane tq holds values D / 4 tq .. of the row, in the order in which step() reads the codes of a
+      // key: of each 16, values 4 s + {0, 1} and 4 s + {2, 3} are k slots 2 tq.. and 8 + 2 tq.. of k step s
+      float2 f[D / 64][8];
+      float amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint4 w = ok ? __ldg(reinterpret_cast<const uint4*>(row + 16 * j + 8 * half)) : make_uint4(0, 0, 0, 0);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 x = widen(u[e]);
+            f[j][4 * half + e] = x;
+            amax = fmax3(amax, fabsf(x.x), fabsf(x.y));
+          }
+        }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // fp16 or bf16 by the rule of the form above
+      const int e = max((int)(__float_as_uint(amax) >> 23), 40);
+      const float down = __uint_as_float((uint32_t)(268 - e) << 23);  // 2^(141 - e)
+      const float up = __uint_as_float((uint32_t)(e - 14) << 23);
+      row_fac[r] = p.scale_log2 * up;
+      huge[r] = amax >= 0x1p100f;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          const float2 x = f[j][w];
+          const uint32_t h2 = pack_f16(x.x * down, x.y * down);
+          const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+          lost = lost || back.x * up != x.x || back.y * up != x.y;
+          qb[4 * j + (w >> 1)][r][w & 1] = h2;
+        }
+    }
+    far = __any_sync(0xffffffffu, lost);
+    if (far) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int h = gq + 8 * r;
+        const float down = huge[r] ? 0x1p-32f : 1.f;
+        row_fac[r] = p.scale_log2 / down;
+#pragma unroll
+        for (int w = 0; w < D / 8; ++w) {
+          const int at = D / 4 * tq + 2 * w;
+          const uint32_t u = h < p.G ? __ldg(reinterpret_cast<const uint32_t*>(p.q + (head0 + h) * D + at)) : 0u;
+          const float2 x = widen(u);
+          qb[w >> 1][r][w & 1] = pack_bf16(x.x * down, x.y * down);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        fac[r][e] = __shfl_sync(0xffffffffu, row_fac[r], 4 * (2 * tq + e));
+        m[r][e] = mv[r][e] = -INFINITY;
+        l[r][e] = 0.f;
+      }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][r][e] = 0.f;
+  }
+
+  // The keys of a landed stage, of which the first n are the sequence's; rec: the first key's record of
+  // scales, RS bytes from one to the next.
+  template <int RS>
+  __device__ __forceinline__ void step(const uint8_t* st, const uint8_t* rec, int n, int lane) {
+    const int gq = lane >> 2, tq = lane & 3;
+    float sc[KP][R][4] = {};
+    auto products = [&](bool in_bf16) {
+      uint32_t u[KP][2][D / 32], scale[KP][2][D / 64];
+#pragma unroll
+      for (int kp = 0; kp < KP; ++kp)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // keys 16 kp + 8 i + gq
+          const int key = 16 * kp + 8 * i + gq;
+          const uint8_t *codes = st + key * St::ROW + tq * (D / 8), *block = rec + key * RS + 4 + tq * (D / 64);
+          if constexpr (D == 128) {
+            const uint4 c = *reinterpret_cast<const uint4*>(codes);
+            u[kp][i][0] = c.x, u[kp][i][1] = c.y, u[kp][i][2] = c.z, u[kp][i][3] = c.w;
+            const uint32_t two = widen_f16(*reinterpret_cast<const uint16_t*>(block));
+            scale[kp][i][0] = __byte_perm(two, two, 0x1010);
+            scale[kp][i][1] = __byte_perm(two, two, 0x3232);
+          } else {
+            const uint2 c = *reinterpret_cast<const uint2*>(codes);
+            u[kp][i][0] = c.x, u[kp][i][1] = c.y;
+            scale[kp][i][0] = widen_f16(*block * 0x0101u);
+          }
+        }
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+        for (int kp = 0; kp < KP; ++kp) {
+          uint32_t k[2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) widen_scaled(u[kp][i][w], scale[kp][i][w / 2], k[i]);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            uint32_t a[4] = {k[0][2 * s], k[1][2 * s], k[0][2 * s + 1], k[1][2 * s + 1]};
+            if (in_bf16) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) a[e] = f16_to_bf16(a[e]);
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              if (in_bf16) mma_bf16_16816(sc[kp][r], a, qb[2 * w + s][r][0], qb[2 * w + s][r][1]);
+              else mma_f16_16816(sc[kp][r], a, qb[2 * w + s][r][0], qb[2 * w + s][r][1]);
+            }
+          }
+        }
+    };
+    if (far) products(true);
+    else products(false);
+    // scores in bits: sc[kp][r][2 i + e] of key 16 kp + 8 i + gq and head 8 r + 2 tq + e
+    float lv[KP][2];  // log2 of the value rows' scales
+    bool raise = false;
+#pragma unroll
+    for (int kp = 0; kp < KP; ++kp)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int key = 16 * kp + 8 * i + gq;
+        const float ks = *reinterpret_cast<const float*>(rec + key * RS);
+        lv[kp][i] = lg2_fast(*reinterpret_cast<const float*>(rec + (St::KEYS + key) * RS));
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& s = sc[kp][r][2 * i + e];
+            s *= ks * fac[r][e];  // one factor: each alone may leave the range
+            if (n < St::KEYS && key >= n) s = -INFINITY;
+          }
+      }
+    float top[R][2], mu[R][2];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mu[r][e] = m[r][e] == -INFINITY ? 0.f : m[r][e];
+        float topv = -INFINITY;
+        top[r][e] = -INFINITY;
+#pragma unroll
+        for (int kp = 0; kp < KP; ++kp) {
+          const float s0 = sc[kp][r][e], s1 = sc[kp][r][2 + e];
+          top[r][e] = fmax3(top[r][e], s0, s1);
+          topv = fmax3(topv, s0 - mu[r][e] + lv[kp][0], s1 - mu[r][e] + lv[kp][1]);
+        }
+        raise = raise || top[r][e] > m[r][e] || topv > mv[r][e];
+      }
+    if (__any_sync(0xffffffffu, raise)) {  // new maxima: all that was summed takes their units
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float alpha[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float t = top[r][e];
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+          const float m_new = fmaxf(m[r][e], t), m_use = m_new == -INFINITY ? 0.f : m_new;
+          const float moved = m[r][e] - m_use;
+          m[r][e] = m_new;
+          mu[r][e] = m_use;
+          l[r][e] *= ex2_fast(moved);
+          // o is kept in units of 2^(m + mv - 15), mv the running max of score - m + log2(value scale)
+          float topv = -INFINITY;
+#pragma unroll
+          for (int kp = 0; kp < KP; ++kp)
+            topv = fmax3(topv, sc[kp][r][e] - m_use + lv[kp][0], sc[kp][r][2 + e] - m_use + lv[kp][1]);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, x));
+          const float v_new = fmaxf(mv[r][e] + moved, topv);
+          alpha[e] = ex2_fast(mv[r][e] + moved - (v_new == -INFINITY ? 0.f : v_new));
+          mv[r][e] = v_new;
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][r][e] *= alpha[e & 1];
+      }
+    }
+    uint32_t pb[KP][R][2];  // the weights times the value scales, in fp16 as in the form above
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float unit[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) unit[e] = (mv[r][e] == -INFINITY ? 0.f : mv[r][e]) - kWeightBits;
+#pragma unroll
+      for (int kp = 0; kp < KP; ++kp)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float w[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float s = sc[kp][r][2 * i + e] - mu[r][e];
+            l[r][e] += ex2_fast(s);
+            w[e] = ex2_fast(s + (lv[kp][i] - unit[e]));
+          }
+          pb[kp][r][i] = transpose_8x8(pack_f16(w[0], w[1]));
+        }
+    }
+    // row gq (+ 8) of tile i is value column D / 8 gq + 2 i (+ 1): a lane's D / 8 codes of each of its four
+    // keys, one block's, serve all tiles.  The codes of two keys go side by side into a byte, so that
+    // they come out as a pair, with the pair of their block's scales.
+#pragma unroll
+    for (int kp = 0; kp < KP; ++kp) {
+      uint32_t w[4][D / 64], scale[2];
+      const int key = 16 * kp + 2 * tq;  // keys key, + 1, + 8, + 9
+      const uint8_t* block = rec + (St::KEYS + key) * RS + 4 + gq * (D / 8) / 16;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* codes = st + St::V0 + (key + (i >> 1) * 8 + (i & 1)) * St::VROW + gq * (D / 16);
+        if constexpr (D == 128) {
+          const uint2 c = *reinterpret_cast<const uint2*>(codes);
+          w[i][0] = c.x, w[i][1] = c.y;
+        } else {
+          w[i][0] = *reinterpret_cast<const uint32_t*>(codes);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) scale[e] = widen_f16(block[8 * e * RS] | (uint32_t)block[(8 * e + 1) * RS] << 8);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t va[4][4];  // [keys 8..15, column 2 i + 1][i], in the order of a fragment's registers
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t x = w[2 * e][c], y = w[2 * e + 1][c];
+          widen_scaled((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), scale[e], va[2 * e]);
+          widen_scaled(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), scale[e], va[2 * e + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a[4] = {va[0][i], va[1][i], va[2][i], va[3][i]};
+#pragma unroll
+          for (int r = 0; r < R; ++r) mma_f16_16816(o[4 * c + i][r], a, pb[kp][r][0], pb[kp][r][1]);
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ static int column(int i, int e, int gq) { return D / 8 * gq + 2 * i + (e >> 1); }
 };
 
 // o and lse of one (sequence, group) from its few parts (at most 64: those of the selected blocks),
@@ -719,12 +929,14 @@ __device__ __forceinline__ void join_parts(const PagedDecode& p, const Parts& pa
 
 // A warp's part of a span: units u0 .. u0 + n - 1 (n > 0) of group g of sequence b, in unit x the KEYS
 // tokens from x unit + my_token on; or (SPARSE) in unit x of the selected blocks, of which lane i
-// holds the i-th in blk.
-template <int D, int KIND, bool WIDE, bool SPARSE>
-__device__ __forceinline__ void attend(const PagedDecode& p, WarpState<D, KIND, WIDE>& ws, uint8_t* ring, int b, int g,
+// holds the i-th in blk.  SHARED (4 bits): the CTA's warps attend four groups of the same tokens, and
+// copy the scales of all four together.
+template <int D, int KIND, bool WIDE, bool SPARSE, bool SHARED>
+__device__ __forceinline__ void attend(const PagedDecode& p, WarpState<D, KIND, WIDE>& ws, uint8_t* smem, int b, int g,
                                        int len, int u0, int n, int blk, int my_token, int unit, bool side_by_side) {
   using St = Stage<D, KIND, WIDE>;
-  const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, tq = lane & 3;
+  uint8_t* ring = smem + warp * St::COUNT * St::BYTES;
   const int64_t head0 = ((int64_t)b * p.H + g) * p.G;
   constexpr int CH = St::ROW / 16;  // 16-byte chunks of a row
   constexpr int RPI = 32 / CH;      // rows of one copy instruction
@@ -749,11 +961,79 @@ __device__ __forceinline__ void attend(const PagedDecode& p, WarpState<D, KIND, 
     return i + lane / St::HALVES < n && tok < len ? __ldg(&table[page_of(p.pages, tok)]) : -1;
   };
   int ids = page_ids(0), ids_next = page_ids(AHEAD);
+  // 4 bits.  The scales of a run of 16 tokens are chunks of CHUNK bytes, numbered as they lie in shared
+  // memory, 32 an instruction: neighbours come from the same cache lines (a copy of 4 bytes for each
+  // lane's own line takes about 27 cycles, and most of them were lookups).  One group's records are 3 words (d 64:
+  // one pair) each; the records of four groups are neighbours in the pool, and a warp copies those of
+  // all four for its run of 16 keys or values.
+  constexpr bool F4 = St::F4;
+  constexpr int RECORD = (SHARED ? 4 : 1) * St::SCALE;  // bytes of scales a token
+  constexpr int CHUNK = SHARED ? 16 : D == 64 ? 8 : 4;
+  constexpr int PER_ROW = F4 ? RECORD / CHUNK : 1, OF_RUN = (SHARED ? 16 : 32) * PER_ROW, COPIES = (OF_RUN + 31) / 32;
+  uint8_t* scales = smem + St::RINGS + (SHARED ? 0 : warp * St::COUNT * St::SCALES);
+  constexpr int SCALES = SHARED ? 4 * St::SCALES : St::SCALES;  // bytes of a stage's
+  const uint8_t* scale_src[COPIES];
+  int scale_row[COPIES];  // 16: no chunk
+  if constexpr (F4) {
+#pragma unroll
+    for (int j = 0; j < COPIES; ++j) {
+      const int x = 32 * j + lane, r = x / PER_ROW;
+      const bool v = SHARED ? warp >= 2 : r >= 16;
+      scale_row[j] = x < OF_RUN ? r & 15 : 16;
+      scale_src[j] = (v ? p.v_scale : p.k_scale) + ((int64_t)(r & 15) * p.H + (SHARED ? g & ~3 : g)) * St::SCALE +
+                     (x - r * PER_ROW) * CHUNK;
+    }
+  }
+  const uint8_t* k_src = static_cast<const uint8_t*>(p.k) + (int64_t)g * St::ROW + lane_off;
+  const uint8_t* v_src = static_cast<const uint8_t*>(p.v) + (int64_t)g * St::ROW + lane_off;
+  auto load4 = [&](int i) {
+    const uint32_t st = smem_u32(ring) + (i % St::COUNT) * St::BYTES;
+    const uint32_t sc = smem_u32(scales) + (i % St::COUNT) * SCALES;
+    const int pos0 = first_token(i);
+#pragma unroll
+    for (int hs = 0; hs < St::HALVES; ++hs) {
+      const int pos = pos0 + 16 * hs;
+      const int id = __shfl_sync(0xffffffffu, ids, (i % AHEAD) * St::HALVES + hs);
+      int have = len - pos;  // tokens of the sequence from here on
+      const bool good = (unsigned)id < (unsigned)p.pages.num_pages && have > 0;
+      if (!good && have > 0) set_status(p.status, MSA_ERR_ARG);
+      // any bits are codes, so those of missing rows may be whatever is there: their scales are zeros
+      const int64_t row0 = (int64_t)id * p.pages.page_size + (pos - page_of(p.pages, pos) * p.pages.page_size);
+      if (good) {
+        const uint8_t *kp = k_src + row0 * row_step, *vp = v_src + row0 * row_step;
+#pragma unroll
+        for (int j = 0; j < 16 / RPI; ++j) {
+          const int r = 16 * hs + j * RPI;
+          cp_async_16_to(st + r * St::ROW + lane * 16, kp + j * RPI * row_step);
+          cp_async_16_to(st + St::V0 + (r + r0) * St::VROW + ch * 16, vp + j * RPI * row_step);
+        }
+      } else {
+        have = 0;
+      }
+      const int64_t off = good ? row0 * p.H * St::SCALE : 0;
+      if (!SHARED || (warp & 1) == hs) {
+#pragma unroll
+        for (int j = 0; j < COPIES; ++j) {
+          const int x = 32 * j + lane;
+          // (one group's: keys, then values KEYS records behind)
+          const int to = SHARED ? (warp >> 1) * St::KEYS * RECORD + x * CHUNK
+                                : x * CHUNK + (x >= 16 * PER_ROW ? (St::KEYS - 16) * RECORD : 0);
+          if (scale_row[j] < 16)
+            cp_async_to<CHUNK>(sc + 16 * hs * RECORD + to, scale_src[j] + off, scale_row[j] < have);
+        }
+      }
+    }
+  };
   auto load = [&](int i) {
     if (i < n) {
       if (i > 0 && i % AHEAD == 0) {
         ids = ids_next;
         ids_next = page_ids(i + AHEAD);
+      }
+      if constexpr (F4) {
+        load4(i);
+        cp_async_commit();
+        return;
       }
       uint8_t* st = ring + (i % St::COUNT) * St::BYTES;
       const int pos0 = first_token(i);
@@ -787,12 +1067,10 @@ __device__ __forceinline__ void attend(const PagedDecode& p, WarpState<D, KIND, 
           }
         }
         if constexpr (St::CODED) {  // lanes 0..15 the keys' scales, the others the values'
-          const int r = lane & 15, at = (lane < 16 ? 0 : St::KEYS) + 16 * hs + r;
+          const int r = lane & 15;
           const bool ok = good && r < have;
-          const uint8_t* src = (lane < 16 ? p.k_scale : p.v_scale) + (ok ? ((row0 + r) * p.H + g) * St::SCALE : 0);
-          cp_async_4(st + St::S0 + at * 4, src, ok);
-#pragma unroll
-          for (int w = 0; w < St::BLOCKS; w += 4) cp_async_4(st + St::B0 + at * St::BLOCKS + w, src + 4 + w, ok);
+          const uint8_t* src = (lane < 16 ? p.k_scale : p.v_scale) + (ok ? ((row0 + r) * p.H + g) * 4 : 0);
+          cp_async_4(st + St::S0 + ((lane < 16 ? 0 : St::KEYS) + 16 * hs + r) * 4, src, ok);
         }
       }
     }
@@ -808,7 +1086,11 @@ __device__ __forceinline__ void attend(const PagedDecode& p, WarpState<D, KIND, 
     if (side_by_side) __syncthreads(); else __syncwarp();
     load(i + St::COUNT - 1);
     const int have = len - first_token(i);
-    if (have > 0) ws.step(ring + (i % St::COUNT) * St::BYTES, have, lane);
+    if (have <= 0) continue;
+    const uint8_t* st = ring + (i % St::COUNT) * St::BYTES;
+    if constexpr (F4)
+      ws.template step<RECORD>(st, scales + (i % St::COUNT) * SCALES + (SHARED ? g & 3 : 0) * St::SCALE, have, lane);
+    else ws.step(st, have, lane);
   }
   cp_async_wait<0>();
 }
@@ -819,10 +1101,11 @@ struct WarpSums {
   float m[kWarps][16], mv[kWarps][16], l[kWarps][16];
 };
 template <int D, int KIND, bool WIDE>
-__device__ __forceinline__ void leave_sums(const WarpState<D, KIND, WIDE>& ws, uint8_t* ring, WarpSums& s) {
+__device__ __forceinline__ void leave_sums(const WarpState<D, KIND, WIDE>& ws, uint8_t* smem, WarpSums& s) {
+  using St = Stage<D, KIND, WIDE>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, tq = lane & 3;
   __syncwarp();  // the warp is done with its stages
-  float* my_o = reinterpret_cast<float*>(ring);
+  float* my_o = reinterpret_cast<float*>(smem + warp * St::COUNT * St::BYTES);
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -830,15 +1113,33 @@ __device__ __forceinline__ void leave_sums(const WarpState<D, KIND, WIDE>& ws, u
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         my_o[(8 * r + 2 * tq + (e & 1)) * (D + 4) + ws.column(i, e, gq)] = ws.o[i][r][e];
+  if constexpr (KIND == MSA_CACHE_E2M1) {
 #pragma unroll
-  for (int r = 0; r < ws.R; ++r) {
-    float l = ws.l[r];
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    if (tq == 0) {
-      s.m[warp][gq + 8 * r] = ws.m[r];
-      if (ws.CODED) s.mv[warp][gq + 8 * r] = ws.mv[r] - kWeightBits;
-      s.l[warp][gq + 8 * r] = l;
+    for (int r = 0; r < ws.R; ++r)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = ws.l[r][e];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+        const int h = 8 * r + 2 * tq + e;
+        if (gq == 0) {
+          s.m[warp][h] = ws.m[r][e];
+          s.mv[warp][h] = ws.mv[r][e] - kWeightBits;
+          s.l[warp][h] = l;
+        }
+      }
+    return;
+  } else {
+#pragma unroll
+    for (int r = 0; r < ws.R; ++r) {
+      float l = ws.l[r];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (tq == 0) {
+        s.m[warp][gq + 8 * r] = ws.m[r];
+        if (ws.CODED) s.mv[warp][gq + 8 * r] = ws.mv[r] - kWeightBits;
+        s.l[warp][gq + 8 * r] = l;
+      }
     }
   }
 }
@@ -913,7 +1214,6 @@ __global__ void __launch_bounds__(kThreads, Stage<D, KIND, WIDE>::PER_SM) paged_
   }
   int u = work.cut.start(blockIdx.x);
   const int u_end = work.cut.start(blockIdx.x + 1);
-  uint8_t* ring = smem + warp * St::COUNT * St::BYTES;
   // warp w works for head hg wh + w % wh, on the (w / wh)-th run of KEYS tokens of each unit
   const int my_head = warp & (wh - 1), subs = kWarps / wh;
   const int my_token = (wh == 1 ? warp : wh == 2 ? warp >> 1 : 0) * St::KEYS, unit = St::KEYS * subs;
@@ -949,8 +1249,11 @@ __global__ void __launch_bounds__(kThreads, Stage<D, KIND, WIDE>::PER_SM) paged_
     }
     {
       WarpState<D, KIND, WIDE> ws;
-      attend<D, KIND, WIDE, SPARSE>(p, ws, ring, b, g, len, u0, n, blk, my_token, unit, wh > 1);
-      leave_sums(ws, ring, s_sums);
+      if (St::F4 && !SPARSE && wh == 4)
+        attend<D, KIND, WIDE, SPARSE, St::F4 && !SPARSE>(p, ws, smem, b, g, len, u0, n, blk, my_token, unit, true);
+      else
+        attend<D, KIND, WIDE, SPARSE, false>(p, ws, smem, b, g, len, u0, n, blk, my_token, unit, wh > 1);
+      leave_sums(ws, smem, s_sums);
     }
     __syncthreads();
     const bool whole = n == units;
@@ -1116,13 +1419,12 @@ __global__ void __launch_bounds__(kThreads, Stage<D, KIND, WIDE>::PER_SM) paged_
   }
   const int units = seq_units<SPARSE>(p, len, 1);
   const int u0 = units * rank / size, n = units * (rank + 1) / size - u0;
-  uint8_t* ring = smem + warp * St::COUNT * St::BYTES;
   float4 acc[ITEMS];
   if (n > 0) {
     {
       WarpState<D, KIND, WIDE> ws;
-      attend<D, KIND, WIDE, SPARSE>(p, ws, ring, b, g, len, u0, n, blk, warp * St::KEYS, St::UNIT, false);
-      leave_sums(ws, ring, s_sums);
+      attend<D, KIND, WIDE, SPARSE, false>(p, ws, smem, b, g, len, u0, n, blk, warp * St::KEYS, St::UNIT, false);
+      leave_sums(ws, smem, s_sums);
     }
     __syncthreads();
 #pragma unroll
@@ -1291,7 +1593,7 @@ cudaError_t allow_smem(Kern kern, int bytes, std::atomic<void*>& done) {
 
 template <int D, int KIND, bool WIDE, bool SPARSE>
 cudaError_t launch_attn(const PagedDecode& p, cudaStream_t stream) {
-  constexpr int smem = kWarps * Stage<D, KIND, WIDE>::COUNT * Stage<D, KIND, WIDE>::BYTES;
+  constexpr int smem = Stage<D, KIND, WIDE>::SMEM;
   static_assert(Stage<D, KIND, WIDE>::COUNT * Stage<D, KIND, WIDE>::BYTES >= (WIDE ? 16 : 8) * (D + 4) * 4, "sums in the stages");
   static_assert(Stage<D, KIND, WIDE>::PER_SM == (WIDE && D == 128 ? 2 : 3), "ctas");
   static_assert(kMaxSelect * 128 / Stage<D, KIND, WIDE>::UNIT <= 64, "parts of selected blocks");
@@ -1324,7 +1626,7 @@ cudaError_t launch_paged(const PagedDecode& p, bool wide, cudaStream_t stream) {
 
 template <int D, int KIND, bool WIDE, int DI>
 cudaError_t launch_small(const PagedDecode& p, cudaStream_t stream) {
-  constexpr int smem = kWarps * Stage<D, KIND, WIDE>::COUNT * Stage<D, KIND, WIDE>::BYTES;
+  constexpr int smem = Stage<D, KIND, WIDE>::SMEM;
   static_assert(smem >= 16 * D * 4, "a part");
   auto* kern = paged_small_kernel<D, KIND, WIDE, DI>;
   static std::atomic<void*> done{nullptr};

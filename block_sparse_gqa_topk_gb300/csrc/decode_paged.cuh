@@ -51,6 +51,8 @@ struct PagedDecode {
   __nv_bfloat16* o;
   float* lse;
   int B, H, G, topk;
+  int together;    // 4 bits: four groups side by side come by TMA
+  uint64_t wait_ns;  // bound of a wait for it
   int row;         // blocks of the table's length, rounded up to 4
   int cluster;     // CTAs of a (sequence, group) in the small form; 0: the other one
   int ctas;        // of the attention kernel
@@ -240,19 +242,22 @@ struct Stage {
   static constexpr int V0 = KEYS * ROW;
   static constexpr int S0 = V0 + KEYS * VROW;  // [2][KEYS] scales of E4M3 rows
   static constexpr int BYTES = S0 + (CODED && !F4 ? 2 * KEYS * 4 : 0);
-  // E2M1: the scales of a stage, [2][KEYS] records as in the pool (the warps' one after another, or
-  // [2][KEYS][4] of four groups together)
-  static constexpr int SCALES = F4 ? 2 * KEYS * SCALE : 0;
+  static constexpr int SCALES = F4 ? 2 * KEYS * SCALE : 0;  // E2M1: a stage's scales, [2][KEYS] records as in the pool
   // CTAs of a SM.  More than 8 heads with d = 128 take more than the 168 registers a thread that
   // three CTAs leave: two with a third stage serve them better (8 x 128K, 16 heads a group, E4M3:
   // 423 -> 392 us), but not with d = 64 (E4M3 269 -> 321 us).
   static constexpr int PER_SM = WIDE && D == 128 ? 2 : 3;
   static constexpr int COUNT = PER_SM == 2 ? 3 : 2;
+  static constexpr int HALVES = KEYS / 16;    // runs of 16 tokens, which never straddle a page
   static constexpr int RINGS = kWarps * COUNT * BYTES;           // bytes of all stages without E2M1's scales
   static constexpr int SMEM = RINGS + kWarps * COUNT * SCALES;  // and with them
+  // E2M1, four groups of the same tokens together: stages of the CTA, each [2][HALVES] boxes of 16 tokens
+  // of keys or values (four groups' codes of a token side by side, 16-byte chunks XOR-swizzled by TMA)
+  // and the four groups' scales.
+  static constexpr int BOX = 16 * 4 * ROW, TOGETHER = 2 * HALVES * BOX + 4 * SCALES, TOGETHER_COUNT = 3;
+  static constexpr int SMEM_TOGETHER = TOGETHER_COUNT * TOGETHER + 1024;  // their start is rounded up
   static constexpr int UNIT = KEYS * kWarps;  // tokens of a unit of work
   static constexpr int PER = 128 / UNIT;      // units of a block
-  static constexpr int HALVES = KEYS / 16;    // runs of 16 tokens, which never straddle a page
   __device__ __forceinline__ static uint32_t key_at(int r, int ch) {
     if constexpr (!CODED) return swz<ROW>(r, ch);
     else if constexpr (F4) return r * ROW + (ch << 4);
@@ -702,10 +707,54 @@ struct WarpState<D, MSA_CACHE_E2M1, WIDE> {
         for (int e = 0; e < 4; ++e) o[i][r][e] = 0.f;
   }
 
+  // Where a lane finds its codes in a stage, and the keys that its rows of the products are.  Of the
+  // 16 keys of a run, rows 8 i + gq of S^T and k slots 8 i + 2 tq + s of P^T are keys 8 i + key and 8 i + slot[s].
+  // One group's stage: keys in their order.  Four groups': the rows of 8 keys are 128 or 256 bytes apart, and
+  // keys in the order 0 2 4 6 1 3 5 7, with the two of a pair changed over in half of the lanes (swap),
+  // are what brings a load's chunks into distinct banks.
+  template <bool TOGETHER>
+  struct Place {
+    static constexpr int KEY8 = TOGETHER ? 8 * 4 * St::ROW : 8 * St::ROW;  // bytes of 8 key rows
+    static constexpr int VALUE8 = TOGETHER ? KEY8 : 8 * St::VROW;
+    static constexpr int RS = (TOGETHER ? 4 : 1) * St::SCALE;  // from a record of scales to the next
+    int k, v[2], key, slot[2];
+    bool swap;
+    __device__ __forceinline__ Place(int lane, int group) {
+      const int gq = lane >> 2, tq = lane & 3;
+      if constexpr (TOGETHER) {
+        auto order = [](int x) { return (x & 3) << 1 | x >> 2; };
+        auto at = [&](int row, int byte) {
+          const int x = row * 4 * St::ROW + group * St::ROW + byte;
+          return x ^ ((x >> 7 & 7) << 4);
+        };
+        swap = D == 128 ? tq & 1 : tq >> 1;
+        key = order(gq);
+        k = at(key, tq * (D / 8));
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          slot[s] = order(2 * tq + (s ^ (int)swap));
+          v[s] = St::HALVES * St::BOX + at(slot[s], gq * (D / 16));
+        }
+      } else {
+        swap = false;
+        key = gq;
+        k = gq * St::ROW + tq * (D / 8);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          slot[s] = 2 * tq + s;
+          v[s] = St::V0 + slot[s] * St::VROW + gq * (D / 16);
+        }
+      }
+    }
+  };
+
   // The keys of a landed stage, of which the first n are the sequence's; rec: the first key's record of
-  // scales, RS bytes from one to the next.
-  template <int RS>
-  __device__ __forceinline__ void step(const uint8_t* st, const uint8_t* rec, int n, int lane) {
+  // scales.
+  template <bool TOGETHER>
+  __device__ __forceinline__ void step(const uint8_t* st, const uint8_t* rec, const Place<TOGETHER>& at, int n,
+                                       int lane) {
+    using P = Place<TOGETHER>;
+    constexpr int RS = P::RS;
     const int gq = lane >> 2, tq = lane & 3;
     float sc[KP][R][4] = {};
     auto products = [&](bool in_bf16) {
@@ -713,9 +762,9 @@ struct WarpState<D, MSA_CACHE_E2M1, WIDE> {
 #pragma unroll
       for (int kp = 0; kp < KP; ++kp)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {  // keys 16 kp + 8 i + gq
-          const int key = 16 * kp + 8 * i + gq;
-          const uint8_t *codes = st + key * St::ROW + tq * (D / 8), *block = rec + key * RS + 4 + tq * (D / 64);
+        for (int i = 0; i < 2; ++i) {  // row 8 i + gq
+          const uint8_t* codes = st + at.k + (2 * kp + i) * P::KEY8;
+          const uint8_t* block = rec + (16 * kp + 8 * i + at.key) * RS + 4 + tq * (D / 64);
           if constexpr (D == 128) {
             const uint4 c = *reinterpret_cast<const uint4*>(codes);
             u[kp][i][0] = c.x, u[kp][i][1] = c.y, u[kp][i][2] = c.z, u[kp][i][3] = c.w;
@@ -752,14 +801,14 @@ struct WarpState<D, MSA_CACHE_E2M1, WIDE> {
     };
     if (far) products(true);
     else products(false);
-    // scores in bits: sc[kp][r][2 i + e] of key 16 kp + 8 i + gq and head 8 r + 2 tq + e
+    // scores in bits: sc[kp][r][2 i + e] of key 16 kp + 8 i + at.key and head 8 r + 2 tq + e
     float lv[KP][2];  // log2 of the value rows' scales
     bool raise = false;
 #pragma unroll
     for (int kp = 0; kp < KP; ++kp)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int key = 16 * kp + 8 * i + gq;
+        const int key = 16 * kp + 8 * i + at.key;
         const float ks = *reinterpret_cast<const float*>(rec + key * RS);
         lv[kp][i] = lg2_fast(*reinterpret_cast<const float*>(rec + (St::KEYS + key) * RS));
 #pragma unroll
@@ -835,7 +884,8 @@ struct WarpState<D, MSA_CACHE_E2M1, WIDE> {
             l[r][e] += ex2_fast(s);
             w[e] = ex2_fast(s + (lv[kp][i] - unit[e]));
           }
-          pb[kp][r][i] = transpose_8x8(pack_f16(w[0], w[1]));
+          const uint32_t t = transpose_8x8(pack_f16(w[0], w[1]));
+          pb[kp][r][i] = TOGETHER ? __byte_perm(t, t, at.swap ? 0x1032 : 0x3210) : t;
         }
     }
     // row gq (+ 8) of tile i is value column D / 8 gq + 2 i (+ 1): a lane's D / 8 codes of each of its four
@@ -844,11 +894,10 @@ struct WarpState<D, MSA_CACHE_E2M1, WIDE> {
 #pragma unroll
     for (int kp = 0; kp < KP; ++kp) {
       uint32_t w[4][D / 64], scale[2];
-      const int key = 16 * kp + 2 * tq;  // keys key, + 1, + 8, + 9
-      const uint8_t* block = rec + (St::KEYS + key) * RS + 4 + gq * (D / 8) / 16;
+      const uint8_t* block = rec + (St::KEYS + 16 * kp) * RS + 4 + gq * (D / 8) / 16;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint8_t* codes = st + St::V0 + (key + (i >> 1) * 8 + (i & 1)) * St::VROW + gq * (D / 16);
+      for (int i = 0; i < 4; ++i) {  // k slot 8 (i / 2) + 2 tq + i % 2
+        const uint8_t* codes = st + at.v[i & 1] + (2 * kp + (i >> 1)) * P::VALUE8;
         if constexpr (D == 128) {
           const uint2 c = *reinterpret_cast<const uint2*>(codes);
           w[i][0] = c.x, w[i][1] = c.y;
@@ -857,7 +906,8 @@ struct WarpState<D, MSA_CACHE_E2M1, WIDE> {
         }
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) scale[e] = widen_f16(block[8 * e * RS] | (uint32_t)block[(8 * e + 1) * RS] << 8);
+      for (int e = 0; e < 2; ++e)
+        scale[e] = widen_f16(block[(8 * e + at.slot[0]) * RS] | (uint32_t)block[(8 * e + at.slot[1]) * RS] << 8);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         uint32_t va[4][4];  // [keys 8..15, column 2 i + 1][i], in the order of a fragment's registers
@@ -927,11 +977,26 @@ __device__ __forceinline__ void join_parts(const PagedDecode& p, const Parts& pa
   }
 }
 
+// Place<false> of the states that have one.
+template <typename State>
+struct NoPlace {
+  __device__ __forceinline__ NoPlace(int, int) {}
+};
+template <typename State, bool F4>
+struct PlaceIn {
+  using Type = NoPlace<State>;
+};
+template <typename State>
+struct PlaceIn<State, true> {
+  using Type = typename State::template Place<false>;
+};
+template <typename State>
+using PlaceOf = typename PlaceIn<State, State::St::F4>::Type;
+
 // A warp's part of a span: units u0 .. u0 + n - 1 (n > 0) of group g of sequence b, in unit x the KEYS
 // tokens from x unit + my_token on; or (SPARSE) in unit x of the selected blocks, of which lane i
-// holds the i-th in blk.  SHARED (4 bits): the CTA's warps attend four groups of the same tokens, and
-// copy the scales of all four together.
-template <int D, int KIND, bool WIDE, bool SPARSE, bool SHARED>
+// holds the i-th in blk.
+template <int D, int KIND, bool WIDE, bool SPARSE>
 __device__ __forceinline__ void attend(const PagedDecode& p, WarpState<D, KIND, WIDE>& ws, uint8_t* smem, int b, int g,
                                        int len, int u0, int n, int blk, int my_token, int unit, bool side_by_side) {
   using St = Stage<D, KIND, WIDE>;
@@ -961,26 +1026,18 @@ __device__ __forceinline__ void attend(const PagedDecode& p, WarpState<D, KIND, 
     return i + lane / St::HALVES < n && tok < len ? __ldg(&table[page_of(p.pages, tok)]) : -1;
   };
   int ids = page_ids(0), ids_next = page_ids(AHEAD);
-  // 4 bits.  The scales of a run of 16 tokens are chunks of CHUNK bytes, numbered as they lie in shared
-  // memory, 32 an instruction: neighbours come from the same cache lines (a copy of 4 bytes for each
-  // lane's own line takes about 27 cycles, and most of them were lookups).  One group's records are 3 words (d 64:
-  // one pair) each; the records of four groups are neighbours in the pool, and a warp copies those of
-  // all four for its run of 16 keys or values.
+  // 4 bits.  The scales of a run of 16 tokens are chunks of CHUNK bytes, keys' and then values', numbered
+  // as they lie in shared memory, 32 an instruction, so that neighbours come from the same cache lines
+  // (a copy whose lanes have a line each takes about 27 cycles).
   constexpr bool F4 = St::F4;
-  constexpr int RECORD = (SHARED ? 4 : 1) * St::SCALE;  // bytes of scales a token
-  constexpr int CHUNK = SHARED ? 16 : D == 64 ? 8 : 4;
-  constexpr int PER_ROW = F4 ? RECORD / CHUNK : 1, OF_RUN = (SHARED ? 16 : 32) * PER_ROW, COPIES = (OF_RUN + 31) / 32;
-  uint8_t* scales = smem + St::RINGS + (SHARED ? 0 : warp * St::COUNT * St::SCALES);
-  constexpr int SCALES = SHARED ? 4 * St::SCALES : St::SCALES;  // bytes of a stage's
-  const uint8_t* scale_src[COPIES];
-  int scale_row[COPIES];  // 16: no chunk
+  constexpr int CHUNK = D == 64 ? 8 : 4, PER_ROW = F4 ? St::SCALE / CHUNK : 1;
+  uint8_t* scales = smem + St::RINGS + warp * St::COUNT * St::SCALES;
+  const uint8_t* scale_src[PER_ROW];
   if constexpr (F4) {
 #pragma unroll
-    for (int j = 0; j < COPIES; ++j) {
+    for (int j = 0; j < PER_ROW; ++j) {
       const int x = 32 * j + lane, r = x / PER_ROW;
-      const bool v = SHARED ? warp >= 2 : r >= 16;
-      scale_row[j] = x < OF_RUN ? r & 15 : 16;
-      scale_src[j] = (v ? p.v_scale : p.k_scale) + ((int64_t)(r & 15) * p.H + (SHARED ? g & ~3 : g)) * St::SCALE +
+      scale_src[j] = (r >= 16 ? p.v_scale : p.k_scale) + ((int64_t)(r & 15) * p.H + g) * St::SCALE +
                      (x - r * PER_ROW) * CHUNK;
     }
   }
@@ -988,7 +1045,7 @@ __device__ __forceinline__ void attend(const PagedDecode& p, WarpState<D, KIND, 
   const uint8_t* v_src = static_cast<const uint8_t*>(p.v) + (int64_t)g * St::ROW + lane_off;
   auto load4 = [&](int i) {
     const uint32_t st = smem_u32(ring) + (i % St::COUNT) * St::BYTES;
-    const uint32_t sc = smem_u32(scales) + (i % St::COUNT) * SCALES;
+    const uint32_t sc = smem_u32(scales) + (i % St::COUNT) * St::SCALES;
     const int pos0 = first_token(i);
 #pragma unroll
     for (int hs = 0; hs < St::HALVES; ++hs) {
@@ -1011,16 +1068,11 @@ __device__ __forceinline__ void attend(const PagedDecode& p, WarpState<D, KIND, 
         have = 0;
       }
       const int64_t off = good ? row0 * p.H * St::SCALE : 0;
-      if (!SHARED || (warp & 1) == hs) {
 #pragma unroll
-        for (int j = 0; j < COPIES; ++j) {
-          const int x = 32 * j + lane;
-          // (one group's: keys, then values KEYS records behind)
-          const int to = SHARED ? (warp >> 1) * St::KEYS * RECORD + x * CHUNK
-                                : x * CHUNK + (x >= 16 * PER_ROW ? (St::KEYS - 16) * RECORD : 0);
-          if (scale_row[j] < 16)
-            cp_async_to<CHUNK>(sc + 16 * hs * RECORD + to, scale_src[j] + off, scale_row[j] < have);
-        }
+      for (int j = 0; j < PER_ROW; ++j) {
+        const int x = 32 * j + lane, r = x / PER_ROW;
+        cp_async_to<CHUNK>(sc + 16 * hs * St::SCALE + x * CHUNK + (r >= 16 ? (St::KEYS - 16) * St::SCALE : 0),
+                           scale_src[j] + off, (r & 15) < have);
       }
     }
   };
@@ -1079,6 +1131,7 @@ __device__ __forceinline__ void attend(const PagedDecode& p, WarpState<D, KIND, 
 #pragma unroll
   for (int i = 0; i < St::COUNT - 1; ++i) load(i);
   ws.load_q(p, head0, gq, tq);
+  [[maybe_unused]] const PlaceOf<WarpState<D, KIND, WIDE>> place(lane, 0);
   for (int i = 0; i < n; ++i) {
     cp_async_wait<St::COUNT - 2>();
     // unit i has landed for all lanes, and all are done with unit i - 1; heads side by side
@@ -1088,11 +1141,130 @@ __device__ __forceinline__ void attend(const PagedDecode& p, WarpState<D, KIND, 
     const int have = len - first_token(i);
     if (have <= 0) continue;
     const uint8_t* st = ring + (i % St::COUNT) * St::BYTES;
-    if constexpr (F4)
-      ws.template step<RECORD>(st, scales + (i % St::COUNT) * SCALES + (SHARED ? g & 3 : 0) * St::SCALE, have, lane);
+    if constexpr (F4) ws.step(st, scales + (i % St::COUNT) * St::SCALES, place, have, lane);
     else ws.step(st, have, lane);
   }
   cp_async_wait<0>();
+}
+
+// The tensor maps of a 4-bit cache's keys and values, [num_pages page_size][H row / 128][128 bytes]; other
+// kernels have none.
+template <bool SOME>
+struct CodeMaps {};
+template <>
+struct CodeMaps<true> {
+  CUtensorMap k, v;
+};
+
+// The stages that a CTA fills by TMA: which comes next, and the parity of its barrier's phase.
+struct StageRing {
+  uint64_t* full;
+  int at;
+  uint32_t parity;
+  bool lost;  // a wait ran out
+  template <int COUNT>
+  __device__ __forceinline__ void advance() {
+    if (++at == COUNT) {
+      at = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+// attend() for the four warps of a CTA that serve four groups of a 4-bit cache side by side: one thread
+// brings the codes of all four by TMA, 16 tokens a box, and each warp copies the scales of all four for 16 of a
+// unit's 64 key and value rows, in 16-byte chunks (four groups' records are neighbours in the pool).
+// (8 x 128K: 297 us with each warp copying for itself, of which the copies alone took 226.)
+template <int D, bool WIDE>
+__device__ __forceinline__ void attend_together(const PagedDecode& p, const CodeMaps<true>& maps,
+                                                WarpState<D, MSA_CACHE_E2M1, WIDE>& ws, uint8_t* smem, StageRing& ring,
+                                                int b, int g, int len, int u0, int n) {
+  using St = Stage<D, MSA_CACHE_E2M1, WIDE>;
+  constexpr int COUNT = St::TOGETHER_COUNT, H4 = 4 * St::SCALE, PER_ROW = H4 / 16, COPIES = (16 * PER_ROW + 31) / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t head0 = ((int64_t)b * p.H + g) * p.G;
+  const int32_t* table = p.pages.table + (int64_t)b * p.pages.table_stride;
+  constexpr int AHEAD = 32 / St::HALVES;  // units whose page ids a register holds
+  auto page_ids = [&](int i) {
+    const int tok = (u0 + i) * St::KEYS + lane * 16;
+    return i + lane / St::HALVES < n && tok < len ? __ldg(&table[page_of(p.pages, tok)]) : -1;
+  };
+  int ids = page_ids(0), ids_next = page_ids(AHEAD);
+  // chunks 32 j + lane of this warp's 16 records: keys (warps 0, 1) or values of half warp % 2
+  const uint8_t* scale_src[COPIES];
+#pragma unroll
+  for (int j = 0; j < COPIES; ++j) {
+    const int x = 32 * j + lane, r = x / PER_ROW;
+    scale_src[j] = (warp >= 2 ? p.v_scale : p.k_scale) + ((int64_t)r * p.H + (g & ~3)) * St::SCALE + (x - r * PER_ROW) * 16;
+  }
+  const uint32_t scale_dst = 2 * St::HALVES * St::BOX + ((warp >> 1) * St::KEYS + (warp & 1) * 16) * H4 + lane * 16;
+  const int chunk_col = (g & ~3) * St::ROW / 128;
+  StageRing fill = ring;
+  auto load = [&](int i) {
+    if (i < n) {
+      if (i > 0 && i % AHEAD == 0) {
+        ids = ids_next;
+        ids_next = page_ids(i + AHEAD);
+      }
+      uint8_t* st = smem + fill.at * St::TOGETHER;
+      uint64_t* full = fill.full + fill.at;
+      const int pos0 = (u0 + i) * St::KEYS;
+      int row0[St::HALVES], have[St::HALVES];  // first row of each half, and its tokens (0: none, or no page)
+#pragma unroll
+      for (int hs = 0; hs < St::HALVES; ++hs) {
+        const int pos = pos0 + 16 * hs, id = __shfl_sync(0xffffffffu, ids, (i % AHEAD) * St::HALVES + hs);
+        have[hs] = len - pos;
+        const bool good = (unsigned)id < (unsigned)p.pages.num_pages;
+        if (!good && have[hs] > 0) set_status(p.status, MSA_ERR_ARG);
+        if (!good) have[hs] = 0;
+        row0[hs] = have[hs] > 0 ? id * p.pages.page_size + (pos - page_of(p.pages, pos) * p.pages.page_size) : 0;
+      }
+      if (threadIdx.x == 0) {
+        // any bits are codes: what a missing half leaves in its boxes meets scales of zero
+        int boxes = 0;
+#pragma unroll
+        for (int hs = 0; hs < St::HALVES; ++hs) boxes += have[hs] > 0 ? 2 : 0;
+        mbar_arrive_expect_tx(full, boxes * St::BOX);
+#pragma unroll
+        for (int hs = 0; hs < St::HALVES; ++hs) {
+          if (have[hs] <= 0) continue;
+          tma_load_3d(st + hs * St::BOX, &maps.k, full, 0, chunk_col, row0[hs]);
+          tma_load_3d(st + (St::HALVES + hs) * St::BOX, &maps.v, full, 0, chunk_col, row0[hs]);
+        }
+      }
+      const int half = warp & 1, mine = half ? have[1] : have[0];
+      const int64_t off = (int64_t)(half ? row0[1] : row0[0]) * p.H * St::SCALE;
+#pragma unroll
+      for (int j = 0; j < COPIES; ++j) {
+        const int x = 32 * j + lane;
+        if (x < 16 * PER_ROW) cp_async_to<16>(smem_u32(st) + scale_dst + 512 * j, scale_src[j] + off, x / PER_ROW < mine);
+      }
+      fill.advance<COUNT>();
+    }
+    cp_async_commit();
+  };
+  // what the warps left of the span before (and read of it) comes before TMA's writes
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < COUNT - 1; ++i) load(i);
+  ws.load_q(p, head0, lane >> 2, lane & 3);
+  const typename WarpState<D, MSA_CACHE_E2M1, WIDE>::template Place<true> place(lane, g & 3);
+  for (int i = 0; i < n; ++i) {
+    cp_async_wait<COUNT - 2>();
+    if (!ring.lost && !mbar_wait(ring.full + ring.at, ring.parity, p.wait_ns)) {
+      ring.lost = true;
+      set_status(p.status, MSA_ERR_DEVICE_TIMEOUT);
+    }
+    // unit i has landed for all warps, and all are done with unit i - 1
+    __syncthreads();
+    load(i + COUNT - 1);
+    const uint8_t* st = smem + ring.at * St::TOGETHER;
+    ws.step(st, st + 2 * St::HALVES * St::BOX + (g & 3) * St::SCALE, place, len - (u0 + i) * St::KEYS, lane);
+    ring.advance<COUNT>();
+  }
+  cp_async_wait<0>();
+  __syncthreads();  // the sums go where other warps' codes lie
 }
 
 // What the warps of a CTA leave of a span: running sums in their own stages ([8 R][D + 4] floats),
@@ -1194,9 +1366,23 @@ __device__ __forceinline__ void write_empty(const PagedDecode& p, int64_t head0,
 // E4M3 (2.2 GB, 6.6 TB/s), 16 blocks of each 19 us after the scores.  Bound by issue: E4M3 with d = 64
 // (229 us, 5.0 TB/s) or 16 heads a group (392 us, 5.6 TB/s).
 template <int D, int KIND, bool WIDE, bool SPARSE>
-__global__ void __launch_bounds__(kThreads, Stage<D, KIND, WIDE>::PER_SM) paged_attn_kernel(const PagedDecode p) {
+__global__ void __launch_bounds__(kThreads, Stage<D, KIND, WIDE>::PER_SM)
+    paged_attn_kernel(const PagedDecode p, const __grid_constant__ CodeMaps<(KIND == MSA_CACHE_E2M1 && !SPARSE)> maps) {
   using St = Stage<D, KIND, WIDE>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr bool TOGETHER = St::F4 && !SPARSE;
+  extern __shared__ __align__(128) uint8_t smem_start[];
+  // TMA's swizzle goes by the address
+  uint8_t* smem = TOGETHER ? smem_start + (-smem_u32(smem_start) & 1023) : smem_start;
+  __shared__ uint64_t s_full[TOGETHER ? St::TOGETHER_COUNT : 1];
+  StageRing stages{s_full, 0, 0, false};
+  if (TOGETHER && p.together) {
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int i = 0; i < St::TOGETHER_COUNT; ++i) mbar_init(&s_full[i], 1);
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
   __shared__ WarpSums s_sums;
   __shared__ int32_t s_blocks[kMaxSelect];
   __shared__ int s_last;
@@ -1249,10 +1435,14 @@ __global__ void __launch_bounds__(kThreads, Stage<D, KIND, WIDE>::PER_SM) paged_
     }
     {
       WarpState<D, KIND, WIDE> ws;
-      if (St::F4 && !SPARSE && wh == 4)
-        attend<D, KIND, WIDE, SPARSE, St::F4 && !SPARSE>(p, ws, smem, b, g, len, u0, n, blk, my_token, unit, true);
-      else
-        attend<D, KIND, WIDE, SPARSE, false>(p, ws, smem, b, g, len, u0, n, blk, my_token, unit, wh > 1);
+      bool done = false;
+      if constexpr (TOGETHER) {
+        if (wh == 4 && p.together) {
+          attend_together<D, WIDE>(p, maps, ws, smem, stages, b, g, len, u0, n);
+          done = true;
+        }
+      }
+      if (!done) attend<D, KIND, WIDE, SPARSE>(p, ws, smem, b, g, len, u0, n, blk, my_token, unit, wh > 1);
       leave_sums(ws, smem, s_sums);
     }
     __syncthreads();
@@ -1423,7 +1613,7 @@ __global__ void __launch_bounds__(kThreads, Stage<D, KIND, WIDE>::PER_SM) paged_
   if (n > 0) {
     {
       WarpState<D, KIND, WIDE> ws;
-      attend<D, KIND, WIDE, SPARSE, false>(p, ws, smem, b, g, len, u0, n, blk, warp * St::KEYS, St::UNIT, false);
+      attend<D, KIND, WIDE, SPARSE>(p, ws, smem, b, g, len, u0, n, blk, warp * St::KEYS, St::UNIT, false);
       leave_sums(ws, smem, s_sums);
     }
     __syncthreads();
@@ -1563,9 +1753,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedDec
 
 // Launches with programmatic stream serialization: the kernel may be scheduled while its
 // predecessor drains, and waits for it (griddep_wait) before it touches what that wrote.
-template <typename Kern>
+template <typename Kern, typename... More>
 cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, bool after, cudaStream_t stream,
-                   const PagedDecode& p) {
+                   const PagedDecode& p, const More&... more) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -1577,7 +1767,7 @@ cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, bool after, c
   cfg.attrs = attr;
   cfg.numAttrs = after ? 1 : 0;
   note_launch();
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  return cudaLaunchKernelEx(&cfg, kern, p, more...);
 }
 
 // The dynamic shared memory of a kernel belongs to the function in a context: set again where that
@@ -1593,7 +1783,9 @@ cudaError_t allow_smem(Kern kern, int bytes, std::atomic<void*>& done) {
 
 template <int D, int KIND, bool WIDE, bool SPARSE>
 cudaError_t launch_attn(const PagedDecode& p, cudaStream_t stream) {
-  constexpr int smem = Stage<D, KIND, WIDE>::SMEM;
+  using St = Stage<D, KIND, WIDE>;
+  constexpr bool TOGETHER = St::F4 && !SPARSE;
+  constexpr int smem = !TOGETHER ? St::SMEM : St::SMEM_TOGETHER > St::SMEM + 1024 ? St::SMEM_TOGETHER : St::SMEM + 1024;
   static_assert(Stage<D, KIND, WIDE>::COUNT * Stage<D, KIND, WIDE>::BYTES >= (WIDE ? 16 : 8) * (D + 4) * 4, "sums in the stages");
   static_assert(Stage<D, KIND, WIDE>::PER_SM == (WIDE && D == 128 ? 2 : 3), "ctas");
   static_assert(kMaxSelect * 128 / Stage<D, KIND, WIDE>::UNIT <= 64, "parts of selected blocks");
@@ -1601,7 +1793,18 @@ cudaError_t launch_attn(const PagedDecode& p, cudaStream_t stream) {
   static std::atomic<void*> done{nullptr};
   const cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
-  return launch(kern, dim3(p.ctas), kThreads, smem, SPARSE, stream, p);
+  CodeMaps<TOGETHER> maps = {};
+  if constexpr (TOGETHER) {
+    if (p.together) {
+      const uint64_t dims[3] = {128, (uint64_t)p.H * St::ROW / 128, (uint64_t)p.pages.num_pages * p.pages.page_size};
+      const uint64_t strides[2] = {128, (uint64_t)p.H * St::ROW};
+      const uint32_t box[3] = {128, 4 * St::ROW / 128, 16};
+      if (!encode_tiled(&maps.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+          !encode_tiled(&maps.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    }
+  }
+  return launch(kern, dim3(p.ctas), kThreads, smem, SPARSE, stream, p, maps);
 }
 
 template <int D, int KIND>

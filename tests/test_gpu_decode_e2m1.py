@@ -14,10 +14,19 @@ import pytest
 import torch
 
 from oracle import fp4
+from oracle.fp8 import e4m3_decode
 from block_sparse_gqa_topk_gb300 import _lib, ops
 from test_gpu_decode_paged import DENSE, SLACK, SPARSE, WIDE, Batch, check_selection, dev, gen, query
 
 pytestmark = pytest.mark.gpu
+
+
+TABLES = []  # the oracle's values of E2M1 and E4M3 codes
+
+
+@pytest.fixture(autouse=True, scope="module")
+def tables():
+    TABLES[:] = [torch.from_numpy(x).cuda() for x in (fp4.e2m1_decode(np.arange(16)), e4m3_decode(np.arange(256)))]
 
 
 class Batch4(Batch):
@@ -41,9 +50,11 @@ class Batch4(Batch):
         self.cache = ops.PagedCache(pools[0], pools[2], self.cache.k_idx, pools[1], pools[3])
 
     def values(self, name, rows, g):
-        codes = getattr(self.cache, name).flatten(0, 1)[rows, g].cpu().numpy()
-        scales = getattr(self.cache, name + "_scale").flatten(0, 1)[rows, g].cpu().numpy()
-        return torch.from_numpy(fp4.dequantize_rows(codes, scales)).cuda()
+        codes = getattr(self.cache, name).flatten(0, 1)[rows, g]
+        scales = getattr(self.cache, name + "_scale").flatten(0, 1)[rows, g]
+        x = TABLES[0][torch.stack([codes & 15, codes >> 4], -1).flatten(-2).int()]
+        x = x.unflatten(-1, (-1, 16)) * TABLES[1][scales[..., 4:].int()][..., None]
+        return x.flatten(-2) * scales[..., :4].contiguous().view(torch.float32).double()
 
     def check_row(self, b, q, o, lse, tokens, scale):
         """Row b against 64 bits: tokens(g) gives the pool rows that group g attends."""
@@ -61,7 +72,7 @@ class Batch4(Batch):
             w = torch.exp(s - want[:, None])
             e_s = (self.d + 4) * 2.0 ** -23 * scale * (qq.abs() @ k.abs().T).amax(-1, keepdim=True)
             e_w = e_s + 2.0 ** -21 + 2.0 ** -11
-            least = 2.0 ** -40 * (w * row).amax(-1, keepdim=True) * (v.abs() / row[:, None]).sum(0)
+            least = 2.0 ** -40 * (w * row).amax(-1, keepdim=True) * (v.abs() / row.where(row > 0, 1.0)[:, None]).sum(0)
             tol = 2 * e_w * (w @ v.abs()) + 2.0 ** -8 * (w @ v).abs() + least
             off = (o[b, h].double() - w @ v).abs()
             assert (off <= tol).all(), (b, g, float((off - tol).max()))
@@ -109,13 +120,44 @@ def test_sparse(case, slack):
     assert all(torch.equal(x, y) for x, y in zip(got, again))
 
 
-@pytest.mark.parametrize("lens,H", [([200001, 64], 6), ([150000, 99], 4), ([40000] * 6, 8)])
-def test_groups_side_by_side(lens, H):
-    """Long enough that a CTA serves 2 and 4 groups."""
-    batch = Batch4(lens, 16, H, 64, 0, seed=61)
-    q = query(len(lens), H * 2, 64, 62)
+LONG = [  # lens, H, page: enough work that a CTA serves 2 and 4 groups side by side
+    ([480001, 64], 6, 128),
+    ([720007, 1, 0, 16], 4, 16),
+    ([351000], 8, 48),
+    ([30000 + 17 * i for i in range(12)], 8, 128),
+]
+
+
+@pytest.mark.parametrize("d,G", [(64, 2), (128, 4), (64, 16), (128, 11)])
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_groups_side_by_side(case, d, G):
+    lens, H, page = LONG[case]
+    batch = Batch4(lens, page, H, d, 0, seed=61 + case)
+    q = query(len(lens), H * G, d, 62)
     o, lse = ops.msa_decode_paged_dense(q, batch.cache, batch.table, batch.lens_t)
-    batch.check_dense(q, 0.125, o, lse)
+    batch.check_dense(q, d ** -0.5, o, lse)
+    again = ops.msa_decode_paged_dense(q, batch.cache, batch.table, batch.lens_t)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    assert ops.device_status() == 0
+
+
+def test_groups_side_by_side_without_a_page():
+    """Ids outside the pool, whole runs and a page of half a unit: zero rows, which count in the softmax, as
+    the cache with rows of zeros gives them."""
+    lens, H, d, page = [360013], 8, 64, 16
+    batch = Batch4(lens, page, H, d, 0, seed=71)
+    q = query(1, H * 2, d, 72)
+    t = batch.t.copy()
+    bad = [0, 5, 6, 7, 4000, 22498, 22500]
+    t[0, bad] = [-1, batch.cache.num_pages, 2 ** 31 - 1, -2, -1, -1, -1]
+    o, lse = ops.msa_decode_paged_dense(q, batch.cache, dev(t), batch.lens_t)
+    assert ops.device_status() == _lib.MSA_ERR_ARG
+    for i in bad:
+        for n in ("k_scale", "v_scale"):
+            getattr(batch.cache, n)[int(batch.t[0, i])] = 0
+    want = ops.msa_decode_paged_dense(q, batch.cache, batch.table, batch.lens_t)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    batch.check_dense(q, d ** -0.5, o, lse)
     assert ops.device_status() == 0
 
 

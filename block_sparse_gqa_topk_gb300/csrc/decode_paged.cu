@@ -236,10 +236,11 @@ int check_sizes(const msa_paged_cache_t* c, const msa_page_table_t* pt, int H_q,
   lay->keys_shift = coded || c->d == 64 ? 5 : 4;  // Stage::KEYS
   lay->ctas = kCtas / 3 * (G > 8 && c->d == 128 ? 2 : 3);  // Stage::PER_SM
   lay->cluster = small_cluster((int64_t)pt->B * c->H_kv, cap, topk, kWarps << lay->keys_shift, lay->ctas);
+  if (c->kind == MSA_CACHE_E2M1 && topk == 0 && lay->ctas == kCtas) lay->ctas = kMaxCtas;  // Stage::DENSE_PER_SM
   lay->bytes = 0;
   if (lay->cluster) return MSA_OK;
   lay->part_o = 0;
-  const size_t parts = (size_t)2 * kCtas * heads_side_by_side(c->H_kv, topk) * G;
+  const size_t parts = (size_t)2 * (lay->ctas > kCtas ? lay->ctas : kCtas) * heads_side_by_side(c->H_kv, topk) * G;
   lay->part_lse = align256(parts * c->d * 4);
   lay->starts = lay->part_lse + align256(parts * 4);
   lay->arrive = lay->starts + align256(((size_t)pt->B + 2) * 4);
@@ -308,7 +309,7 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   p.cluster = lay.cluster;
   // four groups of a 4-bit cache come together where a batch may be long enough for groups side by side
   const int64_t most = (int64_t)p.B * p.H * (((int64_t)pt->max_pages * c->page_size + 127) / 128 + kOverhead);
-  p.together = c->kind == MSA_CACHE_E2M1 && p.wh == 4 && pages_exist && most >= (int64_t)kSideBySide * p.ctas &&
+  p.together = c->kind == MSA_CACHE_E2M1 && p.wh == 4 && pages_exist && most >= (int64_t)kSideBySideTogether * p.ctas &&
                (int64_t)c->num_pages * c->page_size < (int64_t{1} << 31);
   p.wait_ns = cx.wait_ns;
   p.status = cx.status;

@@ -27,7 +27,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 // CTAs over which a call's units are spread: three on each of the 152 SMs.  Each leaves at
 // most two partial results (its first and its last (sequence, group)), whatever the batch.
-constexpr int kCtas = 152 * 3;
+constexpr int kCtas = 152 * 3, kMaxCtas = 152 * 4;  // (four for whole 4-bit caches)
 // Blocks a sequence up to which the attention kernel selects for itself, 8 scores a thread: every
 // CTA of a (sequence, group) then repeats the counting, which is less than the launch it saves.
 constexpr int kSelectPer = 8;
@@ -44,8 +44,8 @@ struct PagedDecode {
   const int32_t* lens;  // [B]
   int32_t* block_idx;   // [B][H][topk]; null: the whole cache
   float* pooled;        // [B][H][row]
-  float* part_o;        // [2 kCtas][wh][G][d]
-  float* part_lse;      // [2 kCtas][wh][G], in bits (log2)
+  float* part_o;        // [2 ctas][wh][G][d]
+  float* part_lse;      // [2 ctas][wh][G], in bits (log2)
   int* starts;          // [B + 2] first unit of each sequence, their total, wh: for the join
   int* arrive;          // [B][H] parts that are written (selected blocks; zeroed by the pooling)
   __nv_bfloat16* o;
@@ -106,8 +106,8 @@ struct Cut {
     r = total - q * n;
     inv = 1.f / (float)n;
   }
-  // r cta / n by a float product: (x + 1/2) / n is 0.5 / n from an integer, and x < 2^18 moves
-  // by at most 2^-5 / n in the roundings
+  // r cta / n by a float product: (x + 1/2) / n is 0.5 / n from an integer, and x < n^2 < 2^19 moves
+  // by at most 2^-4 / n in the roundings
   __device__ __forceinline__ int start(int cta) const {
     return cta >= n ? total : q * cta + (int)(((float)(r * cta) + 0.5f) * inv);
   }
@@ -125,6 +125,8 @@ struct Cut {
 // and wait for one another: few pairs, cut alike, lose up to 7 percent (8 x 128K E4M3 d 128 335 / 333,
 // d 64 216 / 229, bf16 593 / 598).  They pay from about this much work (of one group) a CTA.
 constexpr int kSideBySide = 48;
+// 4-bit caches whose groups come together by TMA gain by that much sooner.
+constexpr int kSideBySideTogether = 12;
 
 struct Work {
   Cut cut;
@@ -146,7 +148,7 @@ __device__ __forceinline__ Work find_run(const PagedDecode& p) {
     if (!SPARSE) side += seq_work(seq_units<SPARSE>(p, len, p.wh));
   }
   const int total1 = __reduce_add_sync(0xffffffffu, mine) * p.H;
-  const bool sided = !SPARSE && p.wh > 1 && total1 >= kSideBySide * p.ctas;
+  const bool sided = !SPARSE && p.wh > 1 && total1 >= (p.together ? kSideBySideTogether : kSideBySide) * p.ctas;
   const int wh = sided ? p.wh : 1, HG = sided ? p.H / p.wh : p.H;
   mine = (sided ? side : mine) * HG;
   int scan = mine;
@@ -248,13 +250,15 @@ struct Stage {
   // 423 -> 392 us), but not with d = 64 (E4M3 269 -> 321 us).
   static constexpr int PER_SM = WIDE && D == 128 ? 2 : 3;
   static constexpr int COUNT = PER_SM == 2 ? 3 : 2;
+  // whole 4-bit caches: four, as their products wait for one another (8 x 128K 287 -> 273 us)
+  static constexpr int DENSE_PER_SM = F4 && PER_SM == 3 ? 4 : PER_SM;
   static constexpr int HALVES = KEYS / 16;    // runs of 16 tokens, which never straddle a page
   static constexpr int RINGS = kWarps * COUNT * BYTES;           // bytes of all stages without E2M1's scales
   static constexpr int SMEM = RINGS + kWarps * COUNT * SCALES;  // and with them
   // E2M1, four groups of the same tokens together: stages of the CTA, each [2][HALVES] boxes of 16 tokens
   // of keys or values (four groups' codes of a token side by side, 16-byte chunks XOR-swizzled by TMA)
   // and the four groups' scales.
-  static constexpr int BOX = 16 * 4 * ROW, TOGETHER = 2 * HALVES * BOX + 4 * SCALES, TOGETHER_COUNT = 3;
+  static constexpr int BOX = 16 * 4 * ROW, TOGETHER = 2 * HALVES * BOX + 4 * SCALES, TOGETHER_COUNT = DENSE_PER_SM == 4 ? 2 : 3;
   static constexpr int SMEM_TOGETHER = TOGETHER_COUNT * TOGETHER + 1024;  // their start is rounded up
   static constexpr int UNIT = KEYS * kWarps;  // tokens of a unit of work
   static constexpr int PER = 128 / UNIT;      // units of a block
@@ -616,8 +620,9 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
 // latter, so its products are few:
 //   S^T = K Q^T: rows are keys, columns the heads 8 r + 2 tq + e (no idle rows; heads as rows: 16 of
 //   32 products idle, 8 x 128K 38 us more);  O^T = V^T P^T as above, P^T turned over by movmatrix.
-// A lane's 4 keys of 32 meet the 2 heads of its columns, so maxima go over 8 lanes; that is left out while
-// no score passes the running ones.
+// A lane's 4 keys of 32 meet the 2 heads of its columns (with at most 4 heads 2 keys, so that the lanes of the
+// other columns have a part too); maxima go over the lanes of a head, which is left out while no score passes
+// the running ones.
 template <int D, bool WIDE>
 struct WarpState<D, MSA_CACHE_E2M1, WIDE> {
   using St = Stage<D, MSA_CACHE_E2M1, WIDE>;
@@ -629,9 +634,10 @@ struct WarpState<D, MSA_CACHE_E2M1, WIDE> {
   float o[MT][R][4];
   float m[R][2], mv[R][2], l[R][2];  // of heads 8 r + 2 tq + e: as in the form above
   float fac[R][2];
-  bool far;
+  bool far, few;  // few: at most 4 heads
 
   __device__ __forceinline__ void load_q(const PagedDecode& p, int64_t head0, int gq, int tq) {
+    few = p.G <= 4;
     bool lost = false, huge[R] = {};
     float row_fac[R];  // of heads 8 r + gq
 #pragma unroll
@@ -695,7 +701,7 @@ struct WarpState<D, MSA_CACHE_E2M1, WIDE> {
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        fac[r][e] = __shfl_sync(0xffffffffu, row_fac[r], 4 * (2 * tq + e));
+        fac[r][e] = __shfl_sync(0xffffffffu, row_fac[r], 4 * (2 * (few ? tq & 1 : tq) + e));
         m[r][e] = mv[r][e] = -INFINITY;
         l[r][e] = 0.f;
       }
@@ -747,6 +753,100 @@ struct WarpState<D, MSA_CACHE_E2M1, WIDE> {
       }
     }
   };
+
+  // From products to weights: sc[k][r][2 i + e] of key key0 + 16 k + 8 i + at.key and head 8 r + 2 tq + e becomes
+  // out[k][r][i], turned over for the product with the values.  pairs: lanes tq and tq ^ 2 hold keys of the same
+  // heads.
+  template <typename P, int K>
+  __device__ __forceinline__ void weights(float (&sc)[K][R][4], uint32_t (&out)[K][R][2], const uint8_t* rec,
+                                          const P& at, int key0, int n, bool pairs) {
+    constexpr int RS = P::RS;
+    float lv[K][2];  // log2 of the value rows' scales
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int key = key0 + 16 * k + 8 * i + at.key;
+        const float ks = *reinterpret_cast<const float*>(rec + key * RS);
+        lv[k][i] = lg2_fast(*reinterpret_cast<const float*>(rec + (St::KEYS + key) * RS));
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& s = sc[k][r][2 * i + e];
+            s *= ks * fac[r][e];  // scores in bits; one factor: each alone may leave the range
+            if (n < St::KEYS && key >= n) s = -INFINITY;
+          }
+      }
+    float top[R][2], mu[R][2];
+    bool raise = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mu[r][e] = m[r][e] == -INFINITY ? 0.f : m[r][e];
+        float topv = -INFINITY;
+        top[r][e] = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const float s0 = sc[k][r][e], s1 = sc[k][r][2 + e];
+          top[r][e] = fmax3(top[r][e], s0, s1);
+          topv = fmax3(topv, s0 - mu[r][e] + lv[k][0], s1 - mu[r][e] + lv[k][1]);
+        }
+        raise = raise || top[r][e] > m[r][e] || topv > mv[r][e];
+      }
+    if (__any_sync(0xffffffffu, raise)) {  // new maxima: all that was summed takes their units
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float alpha[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          auto all = [&](float x) {  // over the lanes of the head
+            if (pairs) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+            return x;
+          };
+          const float m_new = fmaxf(m[r][e], all(top[r][e])), m_use = m_new == -INFINITY ? 0.f : m_new;
+          const float moved = m[r][e] - m_use;
+          m[r][e] = m_new;
+          mu[r][e] = m_use;
+          l[r][e] *= ex2_fast(moved);
+          // o is kept in units of 2^(m + mv - 15), mv the running max of score - m + log2(value scale)
+          float topv = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+            topv = fmax3(topv, sc[k][r][e] - m_use + lv[k][0], sc[k][r][2 + e] - m_use + lv[k][1]);
+          const float v_new = fmaxf(mv[r][e] + moved, all(topv));
+          alpha[e] = ex2_fast(mv[r][e] + moved - (v_new == -INFINITY ? 0.f : v_new));
+          mv[r][e] = v_new;
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][r][e] *= alpha[e & 1];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float unit[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) unit[e] = (mv[r][e] == -INFINITY ? 0.f : mv[r][e]) - kWeightBits;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float w[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float s = sc[k][r][2 * i + e] - mu[r][e];
+            l[r][e] += ex2_fast(s);
+            w[e] = ex2_fast(s + (lv[k][i] - unit[e]));
+          }
+          out[k][r][i] = transpose_8x8(pack_f16(w[0], w[1]));
+        }
+    }
+  }
 
   // The keys of a landed stage, of which the first n are the sequence's; rec: the first key's record of
   // scales.
@@ -801,92 +901,33 @@ struct WarpState<D, MSA_CACHE_E2M1, WIDE> {
     };
     if (far) products(true);
     else products(false);
-    // scores in bits: sc[kp][r][2 i + e] of key 16 kp + 8 i + at.key and head 8 r + 2 tq + e
-    float lv[KP][2];  // log2 of the value rows' scales
-    bool raise = false;
-#pragma unroll
-    for (int kp = 0; kp < KP; ++kp)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int key = 16 * kp + 8 * i + at.key;
-        const float ks = *reinterpret_cast<const float*>(rec + key * RS);
-        lv[kp][i] = lg2_fast(*reinterpret_cast<const float*>(rec + (St::KEYS + key) * RS));
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float& s = sc[kp][r][2 * i + e];
-            s *= ks * fac[r][e];  // one factor: each alone may leave the range
-            if (n < St::KEYS && key >= n) s = -INFINITY;
-          }
-      }
-    float top[R][2], mu[R][2];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mu[r][e] = m[r][e] == -INFINITY ? 0.f : m[r][e];
-        float topv = -INFINITY;
-        top[r][e] = -INFINITY;
-#pragma unroll
-        for (int kp = 0; kp < KP; ++kp) {
-          const float s0 = sc[kp][r][e], s1 = sc[kp][r][2 + e];
-          top[r][e] = fmax3(top[r][e], s0, s1);
-          topv = fmax3(topv, s0 - mu[r][e] + lv[kp][0], s1 - mu[r][e] + lv[kp][1]);
-        }
-        raise = raise || top[r][e] > m[r][e] || topv > mv[r][e];
-      }
-    if (__any_sync(0xffffffffu, raise)) {  // new maxima: all that was summed takes their units
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float alpha[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float t = top[r][e];
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
-          const float m_new = fmaxf(m[r][e], t), m_use = m_new == -INFINITY ? 0.f : m_new;
-          const float moved = m[r][e] - m_use;
-          m[r][e] = m_new;
-          mu[r][e] = m_use;
-          l[r][e] *= ex2_fast(moved);
-          // o is kept in units of 2^(m + mv - 15), mv the running max of score - m + log2(value scale)
-          float topv = -INFINITY;
-#pragma unroll
-          for (int kp = 0; kp < KP; ++kp)
-            topv = fmax3(topv, sc[kp][r][e] - m_use + lv[kp][0], sc[kp][r][2 + e] - m_use + lv[kp][1]);
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, x));
-          const float v_new = fmaxf(mv[r][e] + moved, topv);
-          alpha[e] = ex2_fast(mv[r][e] + moved - (v_new == -INFINITY ? 0.f : v_new));
-          mv[r][e] = v_new;
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][r][e] *= alpha[e & 1];
-      }
-    }
     uint32_t pb[KP][R][2];  // the weights times the value scales, in fp16 as in the form above
+    if (!WIDE && few) {
+      // the lanes of columns 4 .. 7, which no head has, take the second 16 keys of columns 0 .. 3
+      float mine[1][R][4];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float unit[2];
+      for (int x = 0; x < 4; ++x) {
+        const float other = __shfl_xor_sync(0xffffffffu, sc[KP - 1][0][x], 2);
+        mine[0][0][x] = tq & 2 ? other : sc[0][0][x];
+      }
+      uint32_t t[1][R][2];
+      weights<P, 1>(mine, t, rec, at, (tq & 2) << 3, n, true);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) unit[e] = (mv[r][e] == -INFINITY ? 0.f : mv[r][e]) - kWeightBits;
+      for (int i = 0; i < 2; ++i) {  // rows 4 .. 7 of the turned matrix are the second 16 keys'
+        pb[0][0][i] = t[0][0][i];
+        pb[KP - 1][0][i] = __shfl_xor_sync(0xffffffffu, t[0][0][i], 16);
+      }
+    } else {
+      weights<P, KP>(sc, pb, rec, at, 0, n, false);
+    }
+    if (TOGETHER) {
+      const uint32_t order = at.swap ? 0x1032 : 0x3210;
 #pragma unroll
       for (int kp = 0; kp < KP; ++kp)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float w[2];
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float s = sc[kp][r][2 * i + e] - mu[r][e];
-            l[r][e] += ex2_fast(s);
-            w[e] = ex2_fast(s + (lv[kp][i] - unit[e]));
-          }
-          const uint32_t t = transpose_8x8(pack_f16(w[0], w[1]));
-          pb[kp][r][i] = TOGETHER ? __byte_perm(t, t, at.swap ? 0x1032 : 0x3210) : t;
-        }
+          for (int i = 0; i < 2; ++i) pb[kp][r][i] = __byte_perm(pb[kp][r][i], pb[kp][r][i], order);
     }
     // row gq (+ 8) of tile i is value column D / 8 gq + 2 i (+ 1): a lane's D / 8 codes of each of its four
     // keys, one block's, serve all tiles.  The codes of two keys go side by side into a byte, so that
@@ -1200,6 +1241,18 @@ __device__ __forceinline__ void attend_together(const PagedDecode& p, const Code
   const uint32_t scale_dst = 2 * St::HALVES * St::BOX + ((warp >> 1) * St::KEYS + (warp & 1) * 16) * H4 + lane * 16;
   const int chunk_col = (g & ~3) * St::ROW / 128;
   StageRing fill = ring;
+  const int page_size = p.pages.page_size, mine = warp & 1;
+  const int64_t scale_step = (int64_t)p.H * St::SCALE;
+  // first row of half hs of unit i and its tokens, -1 and 0 where there are none or no page
+  auto half_of = [&](int i, int hs, int* have) {
+    const int pos = (u0 + i) * St::KEYS + 16 * hs, id = __shfl_sync(0xffffffffu, ids, (i % AHEAD) * St::HALVES + hs);
+    *have = len - pos;
+    if ((unsigned)id < (unsigned)p.pages.num_pages && *have > 0)
+      return id * page_size + (pos - page_of(p.pages, pos) * page_size);
+    if (*have > 0) set_status(p.status, MSA_ERR_ARG);
+    *have = 0;
+    return -1;
+  };
   auto load = [&](int i) {
     if (i < n) {
       if (i > 0 && i % AHEAD == 0) {
@@ -1207,37 +1260,28 @@ __device__ __forceinline__ void attend_together(const PagedDecode& p, const Code
         ids_next = page_ids(i + AHEAD);
       }
       uint8_t* st = smem + fill.at * St::TOGETHER;
-      uint64_t* full = fill.full + fill.at;
-      const int pos0 = (u0 + i) * St::KEYS;
-      int row0[St::HALVES], have[St::HALVES];  // first row of each half, and its tokens (0: none, or no page)
+      int have;
+      if (warp == 0) {
+        int row[St::HALVES];
 #pragma unroll
-      for (int hs = 0; hs < St::HALVES; ++hs) {
-        const int pos = pos0 + 16 * hs, id = __shfl_sync(0xffffffffu, ids, (i % AHEAD) * St::HALVES + hs);
-        have[hs] = len - pos;
-        const bool good = (unsigned)id < (unsigned)p.pages.num_pages;
-        if (!good && have[hs] > 0) set_status(p.status, MSA_ERR_ARG);
-        if (!good) have[hs] = 0;
-        row0[hs] = have[hs] > 0 ? id * p.pages.page_size + (pos - page_of(p.pages, pos) * p.pages.page_size) : 0;
-      }
-      if (threadIdx.x == 0) {
-        // any bits are codes: what a missing half leaves in its boxes meets scales of zero
-        int boxes = 0;
+        for (int hs = 0; hs < St::HALVES; ++hs) row[hs] = half_of(i, hs, &have);
+        if (lane == 0) {
+          // any bits are codes: what a missing half leaves in its boxes meets scales of zero
+          uint64_t* full = fill.full + fill.at;
+          mbar_arrive_expect_tx(full, ((row[0] >= 0) + (row[1] >= 0)) * 2 * St::BOX);
 #pragma unroll
-        for (int hs = 0; hs < St::HALVES; ++hs) boxes += have[hs] > 0 ? 2 : 0;
-        mbar_arrive_expect_tx(full, boxes * St::BOX);
-#pragma unroll
-        for (int hs = 0; hs < St::HALVES; ++hs) {
-          if (have[hs] <= 0) continue;
-          tma_load_3d(st + hs * St::BOX, &maps.k, full, 0, chunk_col, row0[hs]);
-          tma_load_3d(st + (St::HALVES + hs) * St::BOX, &maps.v, full, 0, chunk_col, row0[hs]);
+          for (int hs = 0; hs < St::HALVES; ++hs) {
+            if (row[hs] < 0) continue;
+            tma_load_3d(st + hs * St::BOX, &maps.k, full, 0, chunk_col, row[hs]);
+            tma_load_3d(st + (St::HALVES + hs) * St::BOX, &maps.v, full, 0, chunk_col, row[hs]);
+          }
         }
       }
-      const int half = warp & 1, mine = half ? have[1] : have[0];
-      const int64_t off = (int64_t)(half ? row0[1] : row0[0]) * p.H * St::SCALE;
+      const int64_t off = max(half_of(i, mine, &have), 0) * scale_step;
 #pragma unroll
       for (int j = 0; j < COPIES; ++j) {
         const int x = 32 * j + lane;
-        if (x < 16 * PER_ROW) cp_async_to<16>(smem_u32(st) + scale_dst + 512 * j, scale_src[j] + off, x / PER_ROW < mine);
+        if (x < 16 * PER_ROW) cp_async_to<16>(smem_u32(st) + scale_dst + 512 * j, scale_src[j] + off, x / PER_ROW < have);
       }
       fill.advance<COUNT>();
     }
@@ -1293,7 +1337,8 @@ __device__ __forceinline__ void leave_sums(const WarpState<D, KIND, WIDE>& ws, u
         float l = ws.l[r][e];
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-        const int h = 8 * r + 2 * tq + e;
+        if (ws.few) l += __shfl_xor_sync(0xffffffffu, l, 2);
+        const int h = 8 * r + 2 * tq + e;  // (few: heads 4 and more are no one's)
         if (gq == 0) {
           s.m[warp][h] = ws.m[r][e];
           s.mv[warp][h] = ws.mv[r][e] - kWeightBits;
@@ -1366,7 +1411,7 @@ __device__ __forceinline__ void write_empty(const PagedDecode& p, int64_t head0,
 // E4M3 (2.2 GB, 6.6 TB/s), 16 blocks of each 19 us after the scores.  Bound by issue: E4M3 with d = 64
 // (229 us, 5.0 TB/s) or 16 heads a group (392 us, 5.6 TB/s).
 template <int D, int KIND, bool WIDE, bool SPARSE>
-__global__ void __launch_bounds__(kThreads, Stage<D, KIND, WIDE>::PER_SM)
+__global__ void __launch_bounds__(kThreads, (SPARSE ? Stage<D, KIND, WIDE>::PER_SM : Stage<D, KIND, WIDE>::DENSE_PER_SM))
     paged_attn_kernel(const PagedDecode p, const __grid_constant__ CodeMaps<(KIND == MSA_CACHE_E2M1 && !SPARSE)> maps) {
   using St = Stage<D, KIND, WIDE>;
   constexpr bool TOGETHER = St::F4 && !SPARSE;
@@ -1671,7 +1716,7 @@ template <int D, int COLS>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedDecode p) {
   constexpr int LANES = COLS / 4;                 // threads of a part
   constexpr int PARTS = kJoinThreads / LANES;     // parts at once
-  __shared__ float s_w[kCtas + 1], s_red[8], s_sum[8];
+  __shared__ float s_w[kMaxCtas + 1], s_red[8], s_sum[8];
   __shared__ float4 s_acc[8][LANES];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / p.H, g = blockIdx.x - b * p.H;

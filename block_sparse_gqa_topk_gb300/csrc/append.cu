@@ -37,13 +37,7 @@ struct AppendParams {
   float mscale;
   uint32_t div_half;
   ItemTensor t[5];
-  // rows that become codes (coded caches: k, v)
-  const __nv_bfloat16* row_x[2];
-  int64_t row_xs[2][2];
-  uint8_t* row_pool[2];
-  uint8_t* row_scale[2];
-  int H;
-  uint32_t div_2H;
+  CodedRows rows;  // k, v where the cache holds codes
   int* status;
 };
 
@@ -94,7 +88,7 @@ __device__ __forceinline__ uint4 turned8(const __nv_bfloat16* x, uint4 w, int i0
 // once; then the items of q, q_idx and k_idx (and of k and v in a bf16 cache) are spread over the
 // threads, and the rows of k and v that become codes over the warps.  Bound by HBM.
 template <int D, int KIND, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads, 5) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 6) append_kernel(const __grid_constant__ AppendParams p) {
   __shared__ float2 s_cs[kMaxTokens * kMaxHalf];
   __shared__ int64_t s_row[kMaxTokens];
   const int t0 = blockIdx.x * p.tpb, nt = min(p.tpb, p.T - t0);
@@ -130,31 +124,12 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const __grid_consta
     if (row < 0) it.clear();  // no token of a sequence: a zero query
     it.store(a.y + ((a.pool ? row : (int64_t)(t0 + tok)) * a.H + h) * a.d);
   }
-  if constexpr (KIND != MSA_CACHE_BF16) {
-    constexpr int LPR = D / 16, BITS = KIND == MSA_CACHE_E2M1 ? 4 : 8;
-    constexpr int SCALE = KIND == MSA_CACHE_E2M1 ? e2m1_scale_bytes(D) : 4;
-    const int lane = threadIdx.x & 31, rows = nt * 2 * p.H;
-    for (int i0 = threadIdx.x - lane; i0 < rows * LPR; i0 += kThreads) {  // whole warps
-      const int r = (i0 + lane) / LPR, sub = lane % LPR;
-      const int tok = min(small_div(r, p.div_2H), nt - 1), hv = r - tok * 2 * p.H;
-      const int v = hv >= p.H, h = v ? hv - p.H : hv;
-      const int64_t row = s_row[tok];
-      const bool there = r < rows && row >= 0;
-      uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-      const int64_t cell = there ? row * p.H + h : 0;
-      if (there) {
-        const __nv_bfloat16* x = p.row_x[v] + ((t0 + tok) * p.row_xs[v][0] + h * p.row_xs[v][1]);
-        lo = __ldg(reinterpret_cast<const uint4*>(x + 16 * sub));
-        hi = __ldg(reinterpret_cast<const uint4*>(x + 16 * sub + 8));
-        if (!v) {
-          lo = turned8<INTER>(x, lo, 16 * sub, p.half, s_cs + tok * p.half);
-          hi = turned8<INTER>(x, hi, 16 * sub + 8, p.half, s_cs + tok * p.half);
-        }
-      }
-      store_codes<D, KIND>(lo, hi, p.row_pool[v] + (cell * D + 16 * sub) * BITS / 8, p.row_scale[v] + cell * SCALE,
-                           there);
-    }
-  }
+  if constexpr (KIND != MSA_CACHE_BF16)
+    store_rows<D, KIND>(p.rows, t0, nt, s_row, [&](const __nv_bfloat16* x, int tok, int i0, uint4& lo, uint4& hi) {
+      const float2* cs = s_cs + tok * p.half;
+      lo = turned8<INTER>(x, lo, i0, p.half, cs);
+      hi = turned8<INTER>(x, hi, i0 + 8, p.half, cs);
+    });
 }
 
 template <int D, int KIND>
@@ -217,8 +192,8 @@ extern "C" int msa_cache_append(const msa_paged_cache_t* c, const msa_page_table
   p.half = a->rot_dim / 2;
   p.div_half = magic(p.half);
   p.mscale = a->mscale;
-  p.H = c->H_kv;
-  p.div_2H = magic(2 * p.H);
+  const int H = p.rows.H = c->H_kv;
+  p.rows.div_2H = magic(2 * H);
   p.status = cx.status;
   const int w = vec ? 8 : 1;
   int all = 0;  // items of a token
@@ -241,20 +216,19 @@ extern "C" int msa_cache_append(const msa_paged_cache_t* c, const msa_page_table
   add(q, q_out, a->H_q, c->d, true, false, a->q_stride[0], a->q_stride[1]);
   const bool coded = c->kind != MSA_CACHE_BF16;
   if (!coded) {
-    add(k, c->k, p.H, c->d, true, true, a->k_stride[0], a->k_stride[1]);
-    add(v, c->v, p.H, c->d, false, true, a->v_stride[0], a->v_stride[1]);
+    add(k, c->k, H, c->d, true, true, a->k_stride[0], a->k_stride[1]);
+    add(v, c->v, H, c->d, false, true, a->v_stride[0], a->v_stride[1]);
   }
   if (c->d_idx) {
     add(q_idx, q_idx_out, a->H_i, c->d_idx, true, false, a->q_idx_stride[0], a->q_idx_stride[1]);
     add(k_idx, c->k_idx, 1, c->d_idx, true, true, a->k_idx_stride, 0);
   }
-  p.row_x[0] = static_cast<const __nv_bfloat16*>(k);
-  p.row_x[1] = static_cast<const __nv_bfloat16*>(v);
   for (int i = 0; i < 2; ++i) {
-    p.row_xs[0][i] = a->k_stride[i];
-    p.row_xs[1][i] = a->v_stride[i];
-    p.row_pool[i] = static_cast<uint8_t*>(i ? c->v : c->k);
-    p.row_scale[i] = reinterpret_cast<uint8_t*>(i ? c->v_scale : c->k_scale);
+    p.rows.x[i] = static_cast<const __nv_bfloat16*>(i ? v : k);
+    p.rows.stride[0][i] = a->k_stride[i];
+    p.rows.stride[1][i] = a->v_stride[i];
+    p.rows.pool[i] = static_cast<uint8_t*>(i ? c->v : c->k);
+    p.rows.scale[i] = reinterpret_cast<uint8_t*>(i ? c->v_scale : c->k_scale);
   }
   // tokens of a CTA: up to kMaxTokens while the grid still fills the GPU and an item index stays below
   // 2^18 (small_div)

@@ -32,18 +32,19 @@ struct CacheParams {
   int* status;
 };
 
-// A token's keys, and its values, are one run of H D values in the pool; a lane moves 8 values
-// of it at a time (16 of E4M3: half the addresses and scales), a warp one token after another.
+// Reading, and writing bf16.  A token's keys, and its values, are one run of H D values in the pool; a lane
+// moves 8 values of it at a time (16 codes: half the addresses and scales), a warp one token after another.
 // Its lanes find the places of all its tokens (at most 32) together, so the chain of lookups
 // (sequence, length, page) is paid once, and while it works on STEPS vectors a lane, the next ones
-// are on their way.  32K tokens of 8 groups, d 128, with index keys: bf16 41 us each way (6.8
-// TB/s), E4M3 write 40 us (bound by instructions: the rounding rule) and read 35 us (6 TB/s).
+// are on their way.  32K tokens of 8 groups, d 128, with index keys, calls back to
+// back: bf16 49 us each way, E4M3 read 40 us, 4 bits 35 us (5.3 TB/s).
 template <int D, int KIND, bool WRITE>
 struct Lanes {
   static constexpr bool CODED = KIND != MSA_CACHE_BF16;
+  static_assert(!CODED || !WRITE, "cache_code_kernel writes codes");
   static constexpr int VALUES = CODED ? 16 : 8;  // of a lane's vector
-  static constexpr int LPR = D / VALUES;      // lanes of a head's row
-  static constexpr int STEPS = CODED && WRITE ? 1 : 2;
+  static constexpr int LPR = D / VALUES;         // lanes of a head's row
+  static constexpr int STEPS = 2;
   static constexpr int BITS = KIND == MSA_CACHE_E2M1 ? 4 : KIND == MSA_CACHE_E4M3 ? 8 : 16;  // of a value in the pool
   static constexpr int SCALE = KIND == MSA_CACHE_E2M1 ? e2m1_scale_bytes(D) : 4;            // bytes of a row's scales
 };
@@ -56,16 +57,14 @@ struct Batch {
   uint4 w[L::STEPS][W];                    // (16 codes of the pool: the first, or half of it)
   float s[L::STEPS];
   uint4* dst[L::STEPS];                    // null: nothing to store
-  uint8_t* scale[L::STEPS];
 };
 
-// As many as the registers of a batch allow; writing E4M3 with a vector a lane on the way and 4
-// CTAs is faster than with two vectors and 3 (32K tokens, 8 groups, d 128).
-template <int KIND, bool WRITE>
-constexpr int kCtasPerSm = KIND != MSA_CACHE_BF16 && !WRITE ? 3 : 4;
+// As many as the registers of a batch allow.
+template <int KIND>
+constexpr int kCtasPerSm = KIND != MSA_CACHE_BF16 ? 3 : 4;
 
 template <int D, int KIND, bool WRITE>
-__global__ void __launch_bounds__(kThreads, (kCtasPerSm<KIND, WRITE>)) cache_kernel(const __grid_constant__ CacheParams p) {
+__global__ void __launch_bounds__(kThreads, (kCtasPerSm<KIND>)) cache_kernel(const __grid_constant__ CacheParams p) {
   using L = Lanes<D, KIND, WRITE>;
   using B = Batch<D, KIND, WRITE>;
   constexpr bool F4 = KIND == MSA_CACHE_E2M1;
@@ -94,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, (kCtasPerSm<KIND, WRITE>)) cache_ker
       __nv_bfloat16* x = v ? p.xv + t * p.sv[0] + h * p.sv[1] : p.xk + t * p.sk[0] + h * p.sk[1];
       uint4* packed = reinterpret_cast<uint4*>(x + sub * L::VALUES);
       void* pool = static_cast<uint8_t*>(v ? p.v : p.k) + (cell * D + f * L::VALUES) * L::BITS / 8;
-      if (L::CODED) b.scale[k] = (v ? p.v_scale : p.k_scale) + (cell + h) * L::SCALE;
+      [[maybe_unused]] const uint8_t* scale = (v ? p.v_scale : p.k_scale) + (cell + h) * L::SCALE;
 #pragma unroll
       for (int e = 0; e < W; ++e) b.w[k][e] = make_uint4(0, 0, 0, 0);
       b.s[k] = 0.f;
@@ -108,11 +107,11 @@ __global__ void __launch_bounds__(kThreads, (kCtasPerSm<KIND, WRITE>)) cache_ker
       } else {
         if constexpr (F4) {
           const uint2 c = *static_cast<const uint2*>(pool);
-          b.w[k][0] = make_uint4(c.x, c.y, b.scale[k][4 + sub], 0);  // and the block's scale
+          b.w[k][0] = make_uint4(c.x, c.y, scale[4 + sub], 0);  // and the block's scale
         } else {
           b.w[k][0] = *static_cast<const uint4*>(pool);
         }
-        if (L::CODED) b.s[k] = *reinterpret_cast<const float*>(b.scale[k]);
+        if (L::CODED) b.s[k] = *reinterpret_cast<const float*>(scale);
       }
     }
     next_u += 32 * L::STEPS;
@@ -122,11 +121,7 @@ __global__ void __launch_bounds__(kThreads, (kCtasPerSm<KIND, WRITE>)) cache_ker
     }
   };
   auto store = [&](const B& b) {
-    if constexpr (L::CODED && WRITE) {
-#pragma unroll
-      for (int k = 0; k < L::STEPS; ++k)
-        store_codes<D, KIND>(b.w[k][0], b.w[k][W - 1], b.dst[k], b.scale[k], b.dst[k] != nullptr);
-    } else if constexpr (L::CODED) {
+    if constexpr (L::CODED) {
 #pragma unroll
       for (int k = 0; k < L::STEPS; ++k) {
         const uint4 c = b.w[k][0];
@@ -182,17 +177,66 @@ __global__ void __launch_bounds__(kThreads, (kCtasPerSm<KIND, WRITE>)) cache_ker
   }
 }
 
-template <int D, int KIND, bool WRITE>
-cudaError_t launch_cache(CacheParams& p, int num_sms, cudaStream_t st) {
-  // tokens of a warp: as many as let all warps run together
-  const int64_t together = (int64_t)num_sms * kCtasPerSm<KIND, WRITE> * (kThreads / 32);
-  const int64_t want = (p.T + together - 1) / together;
-  p.per = (int)(want < 32 ? want : 32);
-  const int64_t warps = ((int64_t)p.T + p.per - 1) / p.per;
-  const int64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
-  cache_kernel<D, KIND, WRITE><<<(unsigned)grid, kThreads, 0, st>>>(p);
+// Writing codes: a CTA takes 8 tokens, and each D / 16 lanes a row at a time.  Bound by instructions and the loads
+// in flight, so as many CTAs as the registers allow: 32K tokens of 8 groups, d 128: E4M3 38.5 us, 4 bits 37.6 with eight a
+// SM (41.1 and 39.9 with six; warps that take tokens in turn with the next vectors on their way, as
+// above: 40.7 and 43.8, and 4.8 us for a single token a sequence in place of 3.2).
+constexpr int kCodeTokens = 8;
+template <int D, int KIND>
+__global__ void __launch_bounds__(kThreads, 8)
+    cache_code_kernel(const __grid_constant__ CacheParams p, const __grid_constant__ CodedRows rows) {
+  __shared__ int64_t s_row[kCodeTokens];
+  const int t0 = blockIdx.x * p.per, nt = min(p.per, p.T - t0);
+  if (threadIdx.x < nt) {
+    const int64_t row = token_row(p.map, t0 + threadIdx.x);
+    if (row == kNoPlace) set_status(p.status, MSA_ERR_ARG);
+    s_row[threadIdx.x] = row;
+  }
+  __syncthreads();
+  if (p.xi) {  // the index keys, d_idx / 8 lanes a token
+    const int lanes = p.d_idx >> 3, tok = threadIdx.x / lanes, sub = threadIdx.x % lanes;
+    if (tok < nt && s_row[tok] >= 0)
+      reinterpret_cast<uint4*>(p.k_idx + s_row[tok] * p.d_idx)[sub] =
+          __ldg(reinterpret_cast<const uint4*>(p.xi + (t0 + tok) * p.si) + sub);
+  }
+  store_rows<D, KIND>(rows, t0, nt, s_row, [](const __nv_bfloat16*, int, int, uint4&, uint4&) {});
+}
+
+template <int D, int KIND>
+cudaError_t launch_codes(CacheParams& p, int num_sms, cudaStream_t st) {
+  CodedRows r = {};
+  r.x[0] = p.xk;
+  r.x[1] = p.xv;
+  for (int i = 0; i < 2; ++i) {
+    r.stride[0][i] = p.sk[i];
+    r.stride[1][i] = p.sv[i];
+    r.pool[i] = static_cast<uint8_t*>(i ? p.v : p.k);
+    r.scale[i] = i ? p.v_scale : p.k_scale;
+  }
+  r.H = p.H;
+  r.div_2H = magic(2 * p.H);
+  p.per = kCodeTokens;  // while the grid fills the GPU
+  while (p.per > 1 && ((int64_t)p.T + p.per - 1) / p.per < 8 * num_sms) p.per >>= 1;
+  cache_code_kernel<D, KIND><<<(unsigned)(((int64_t)p.T + p.per - 1) / p.per), kThreads, 0, st>>>(p, r);
   note_launch();
   return cudaGetLastError();
+}
+
+template <int D, int KIND, bool WRITE>
+cudaError_t launch_cache(CacheParams& p, int num_sms, cudaStream_t st) {
+  if constexpr (WRITE && KIND != MSA_CACHE_BF16) {
+    return launch_codes<D, KIND>(p, num_sms, st);
+  } else {
+    // tokens of a warp: as many as let all warps run together
+    const int64_t together = (int64_t)num_sms * kCtasPerSm<KIND> * (kThreads / 32);
+    const int64_t want = (p.T + together - 1) / together;
+    p.per = (int)(want < 32 ? want : 32);
+    const int64_t warps = ((int64_t)p.T + p.per - 1) / p.per;
+    const int64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
+    cache_kernel<D, KIND, WRITE><<<(unsigned)grid, kThreads, 0, st>>>(p);
+    note_launch();
+    return cudaGetLastError();
+  }
 }
 
 template <int D, bool WRITE>

@@ -7,6 +7,7 @@
 #include <math.h>
 
 #include "paged.cuh"
+#include "small_div.cuh"
 
 namespace msa {
 
@@ -134,13 +135,12 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
 // The largest magnitude of 16 bf16 values; infinite or NaN where one of them is.
 __device__ __forceinline__ float block_amax(uint4 lo, uint4 hi) {
   const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  uint32_t m = u[0] & 0x7fff7fffu;
+  uint32_t m = u[0];  // magnitudes count, signs are of no account
 #pragma unroll
-  for (int e = 1; e < 8; ++e)
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(u[e] & 0x7fff7fffu));
+  for (int e = 1; e < 8; ++e) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(u[e]));
   uint32_t h;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(h) : "r"(m), "r"(m >> 16));
-  return __uint_as_float(h << 16);
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(h) : "r"(m), "r"(m >> 16));
+  return __uint_as_float(h << 16 & 0x7fffffffu);
 }
 
 // The exponent field of a row's scale: of the smallest power of two s >= 2^-126 with amax <= 2688 s
@@ -151,43 +151,68 @@ __device__ __forceinline__ int row_exponent(float amax) {
   return u == 0 ? 127 : max(e, 1);
 }
 
+// Eight E2M1 codes of the values nearest to those of q.
+__device__ __forceinline__ uint32_t narrow_e2m1(const float2 (&q)[4]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(q[0].x), "f"(q[0].y), "f"(q[1].x), "f"(q[1].y), "f"(q[2].x), "f"(q[2].y), "f"(q[3].x), "f"(q[3].y));
+  return w;
+}
+
+// The same of eight bf16 values x down / bs, divided; out of line, for rows at the ends of the range.
+static __device__ __noinline__ uint32_t divide_e2m1(uint4 w, float down, float bs) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  float2 q[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 x = widen(u[k]);
+    q[k] = make_float2(__fdiv_rn(x.x * down, bs), __fdiv_rn(x.y * down, bs));
+  }
+  return narrow_e2m1(q);
+}
+
 // Codes of 16 bf16 values of largest magnitude amax (of the block) at the row scale 2^(e - 127), and
 // their block scale, an E4M3 code:
 //   block = E4M3 nearest to amax / 6 / row, at least 2^-9;  code = E2M1 nearest to x / (block row).
 // amax / 6 by a product: with the rounded 1/6 (too large by 2^-25 of it) a quotient that lies on the
 // border of two E4M3 numbers still rounds to the border, and one that does not is 2^-9 away from it,
-// as amax has 8 significant bits.  The other quotient is x r with one step after it, which makes it the
-// rounded quotient (as in quantize8).  A block that holds an infinity or a NaN gets the scale NaN, so
-// that its values read as NaN.  At the largest row scale the block's ends at 320: 6 * 320 * 2^117 is
-// the largest value that bf16 holds.
+// as amax has 8 significant bits.  The other quotient is x (r + s), 1 / block = r + s to 2^-46 of it, rounded
+// once: what lies on the border of two codes (block times it has 8 bits) comes out as the border, and
+// everything else is 2^-9 away.  r <= 1 / block, so that s is no negative number and a zero keeps its sign.
+// A block that holds an infinity or a NaN gets the scale NaN, so that its values read as NaN.  At the
+// largest row scale the block's ends at 320: 6 * 320 * 2^117 is the largest value that bf16 holds.
 __device__ __forceinline__ uint2 quantize16(uint4 lo, uint4 hi, float amax, int e, uint32_t* block) {
   const float down = __uint_as_float((uint32_t)(254 - e) << 23);  // 1 / row
   const float t = fminf(fmaxf(amax * down * (1.f / 6.f), 0x1p-9f), e == 244 ? 320.f : 448.f);
   const uint32_t code = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
   const float bs = e4m3_value(code);
-  const float r = __frcp_rn(bs);
   *block = amax < INFINITY ? code : 0x7fu;
+  // there the factors below leave the range
+  if (__any_sync(0xffffffffu, e < 30 || e > 210)) return make_uint2(divide_e2m1(lo, down, bs), divide_e2m1(hi, down, bs));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(bs));
+  r = fmaf(r, fmaf(-bs, r, 1.f), r);              // within an ulp
+  r = __uint_as_float(__float_as_uint(r) - 2);    // and not above
+  const float s = fmaf(-r, bs, 1.f) * r;
+  const float2 rr = make_float2(r * down, r * down), ss = make_float2(s * down, s * down);
   const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  const float2 rr = make_float2(r, r), nn = make_float2(-bs, -bs), dd = make_float2(down, down);
-  float2 q[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float2 x = widen(u[k]), y = fmul2(x, dd), q0 = fmul2(y, rr);
-    q[k] = ffma2(ffma2(q0, nn, y), rr, q0);
-    q[k] = make_float2(copysignf(q[k].x, x.x), copysignf(q[k].y, x.y));  // a zero keeps its sign
-  }
   uint32_t w[2];
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-        "mov.b32 %0, {a, b, c, d};\n\t}"
-        : "=r"(w[k])
-        : "f"(q[4 * k].x), "f"(q[4 * k].y), "f"(q[4 * k + 1].x), "f"(q[4 * k + 1].y), "f"(q[4 * k + 2].x),
-          "f"(q[4 * k + 2].y), "f"(q[4 * k + 3].x), "f"(q[4 * k + 3].y));
+  for (int h = 0; h < 2; ++h) {
+    float2 q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = widen(u[4 * h + k]);
+      q[k] = ffma2(x, rr, fmul2(x, ss));
+    }
+    w[h] = narrow_e2m1(q);
+  }
   return make_uint2(w[0], w[1]);
 }
 
@@ -239,6 +264,41 @@ __device__ __forceinline__ void store_codes(uint4 lo, uint4 hi, void* dst, uint8
     if (!there) return;
     *static_cast<uint4*>(dst) = make_uint4(c0.x, c0.y, c1.x, c1.y);
     if (sub == 0) *reinterpret_cast<float*>(scale) = sc;
+  }
+}
+
+// The keys and values of a call whose rows become codes.
+struct CodedRows {
+  const __nv_bfloat16* x[2];  // keys, values
+  int64_t stride[2][2];       // of token, head
+  uint8_t* pool[2];
+  uint8_t* scale[2];
+  int H;
+  uint32_t div_2H;  // magic(2 H)
+};
+
+// The rows of tokens t0 .. t0 + nt - 1 by the whole CTA, D / 16 lanes a row: to the pool rows in s_row (negative:
+// none), keys after turn(row, token, first value, lo, hi).
+template <int D, int KIND, typename Turn>
+__device__ __forceinline__ void store_rows(const CodedRows& p, int t0, int nt, const int64_t* s_row, Turn turn) {
+  constexpr int LPR = D / 16, BITS = KIND == MSA_CACHE_E2M1 ? 4 : 8;
+  constexpr int SCALE = KIND == MSA_CACHE_E2M1 ? e2m1_scale_bytes(D) : 4;
+  const int lane = threadIdx.x & 31, rows = nt * 2 * p.H;
+  for (int i0 = threadIdx.x - lane; i0 < rows * LPR; i0 += blockDim.x) {  // whole warps
+    const int r = (i0 + lane) / LPR, sub = lane % LPR;
+    const int tok = min(small_div(r, p.div_2H), nt - 1), hv = r - tok * 2 * p.H;
+    const int v = hv >= p.H, h = v ? hv - p.H : hv;
+    const int64_t row = s_row[tok];
+    const bool there = r < rows && row >= 0;
+    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+    const int64_t cell = there ? row * p.H + h : 0;
+    if (there) {
+      const __nv_bfloat16* x = p.x[v] + ((t0 + tok) * p.stride[v][0] + h * p.stride[v][1]);
+      lo = __ldg(reinterpret_cast<const uint4*>(x + 16 * sub));
+      hi = __ldg(reinterpret_cast<const uint4*>(x + 16 * sub + 8));
+      if (!v) turn(x, tok, 16 * sub, lo, hi);
+    }
+    store_codes<D, KIND>(lo, hi, p.pool[v] + (cell * D + 16 * sub) * BITS / 8, p.scale[v] + cell * SCALE, there);
   }
 }
 

@@ -1212,102 +1212,101 @@ struct StageRing {
   }
 };
 
-// attend() for the four warps of a CTA that serve four groups of a 4-bit cache side by side: one thread
-// brings the codes of all four by TMA, 16 tokens a box, and each warp copies the scales of all four for 16 of a
-// unit's 64 key and value rows, in 16-byte chunks (four groups' records are neighbours in the pool).
-// (8 x 128K: 297 us with each warp copying for itself, of which the copies alone took 226.)
+// attend() for the four warps of a CTA that serve four groups of a 4-bit cache side by side.  They take turns in
+// bringing a unit of all four groups: the codes by TMA, 16 tokens a box, and the scales in 16-byte chunks (four
+// groups' records are neighbours in the pool; boxes of 48 bytes take TMA longer than those of the codes).  What
+// counts beside the products are the instructions of the copies: 8 x 128K, d 128: each warp copying for itself
+// 334 us; codes by TMA and a warp's part of the scales by each 273; in turn 269.
 template <int D, bool WIDE>
 __device__ __forceinline__ void attend_together(const PagedDecode& p, const CodeMaps<true>& maps,
                                                 WarpState<D, MSA_CACHE_E2M1, WIDE>& ws, uint8_t* smem, StageRing& ring,
                                                 int b, int g, int len, int u0, int n) {
   using St = Stage<D, MSA_CACHE_E2M1, WIDE>;
-  constexpr int COUNT = St::TOGETHER_COUNT, H4 = 4 * St::SCALE, PER_ROW = H4 / 16, COPIES = (16 * PER_ROW + 31) / 32;
+  constexpr int COUNT = St::TOGETHER_COUNT, RECORD = 4 * St::SCALE, SCALES = 2 * St::HALVES * St::BOX;
+  constexpr int PER_ROW = RECORD / 16, COPIES = (16 * PER_ROW + 31) / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t head0 = ((int64_t)b * p.H + g) * p.G;
   const int32_t* table = p.pages.table + (int64_t)b * p.pages.table_stride;
-  constexpr int AHEAD = 32 / St::HALVES;  // units whose page ids a register holds
+  constexpr int AHEAD = 32 / St::HALVES;  // units whose page ids a register holds, one of 16 tokens a lane
   auto page_ids = [&](int i) {
     const int tok = (u0 + i) * St::KEYS + lane * 16;
     return i + lane / St::HALVES < n && tok < len ? __ldg(&table[page_of(p.pages, tok)]) : -1;
   };
   int ids = page_ids(0), ids_next = page_ids(AHEAD);
-  // chunks 32 j + lane of this warp's 16 records: keys (warps 0, 1) or values of half warp % 2
-  const uint8_t* scale_src[COPIES];
+  const int scale_step = p.H * St::SCALE;
+  int chunk_row[COPIES], chunk_off[COPIES];  // chunks 32 j + lane of 16 records (16: none)
 #pragma unroll
   for (int j = 0; j < COPIES; ++j) {
     const int x = 32 * j + lane, r = x / PER_ROW;
-    scale_src[j] = (warp >= 2 ? p.v_scale : p.k_scale) + ((int64_t)r * p.H + (g & ~3)) * St::SCALE + (x - r * PER_ROW) * 16;
+    chunk_row[j] = x < 16 * PER_ROW ? r : 16;
+    chunk_off[j] = r * scale_step + (g & ~3) * St::SCALE + (x - r * PER_ROW) * 16;
   }
-  const uint32_t scale_dst = 2 * St::HALVES * St::BOX + ((warp >> 1) * St::KEYS + (warp & 1) * 16) * H4 + lane * 16;
-  const int chunk_col = (g & ~3) * St::ROW / 128;
   StageRing fill = ring;
-  const int page_size = p.pages.page_size, mine = warp & 1;
-  const int64_t scale_step = (int64_t)p.H * St::SCALE;
-  // first row of half hs of unit i and its tokens, -1 and 0 where there are none or no page
-  auto half_of = [&](int i, int hs, int* have) {
-    const int pos = (u0 + i) * St::KEYS + 16 * hs, id = __shfl_sync(0xffffffffu, ids, (i % AHEAD) * St::HALVES + hs);
-    *have = len - pos;
-    if ((unsigned)id < (unsigned)p.pages.num_pages && *have > 0)
-      return id * page_size + (pos - page_of(p.pages, pos) * page_size);
-    if (*have > 0) set_status(p.status, MSA_ERR_ARG);
-    *have = 0;
-    return -1;
-  };
-  auto load = [&](int i) {
-    if (i < n) {
-      if (i > 0 && i % AHEAD == 0) {
-        ids = ids_next;
-        ids_next = page_ids(i + AHEAD);
-      }
+  auto load = [&](int i) {  // unit i < n, by warp i % 4
+    if (i % AHEAD == 0 && i > 0) {
+      ids = ids_next;
+      ids_next = page_ids(i + AHEAD);
+    }
+    if ((i & 3) == warp) {
       uint8_t* st = smem + fill.at * St::TOGETHER;
-      int have;
-      if (warp == 0) {
-        int row[St::HALVES];
+      uint64_t* full = fill.full + fill.at;
+      int row[St::HALVES], have[St::HALVES], boxes = 0;  // first row of each half, and its tokens (0: none, or no page)
 #pragma unroll
-        for (int hs = 0; hs < St::HALVES; ++hs) row[hs] = half_of(i, hs, &have);
-        if (lane == 0) {
-          // any bits are codes: what a missing half leaves in its boxes meets scales of zero
-          uint64_t* full = fill.full + fill.at;
-          mbar_arrive_expect_tx(full, ((row[0] >= 0) + (row[1] >= 0)) * 2 * St::BOX);
+      for (int hs = 0; hs < St::HALVES; ++hs) {
+        const int pos = (u0 + i) * St::KEYS + 16 * hs, id = __shfl_sync(0xffffffffu, ids, (i % AHEAD) * St::HALVES + hs);
+        have[hs] = len - pos;
+        const bool good = (unsigned)id < (unsigned)p.pages.num_pages;
+        if (!good && have[hs] > 0) set_status(p.status, MSA_ERR_ARG);
+        if (!good || have[hs] < 0) have[hs] = 0;
+        row[hs] = have[hs] > 0 ? id * p.pages.page_size + (pos - page_of(p.pages, pos) * p.pages.page_size) : 0;
+        boxes += have[hs] > 0 ? 2 : 0;
+      }
+      if (lane == 0) {
+        // any bits are codes: what a missing half leaves in its boxes meets scales of zero
+        mbar_arrive_expect_tx(full, boxes * St::BOX);
+        const int col = (g & ~3) * St::ROW / 128;
 #pragma unroll
-          for (int hs = 0; hs < St::HALVES; ++hs) {
-            if (row[hs] < 0) continue;
-            tma_load_3d(st + hs * St::BOX, &maps.k, full, 0, chunk_col, row[hs]);
-            tma_load_3d(st + (St::HALVES + hs) * St::BOX, &maps.v, full, 0, chunk_col, row[hs]);
-          }
+        for (int hs = 0; hs < St::HALVES; ++hs) {
+          if (have[hs] == 0) continue;
+          tma_load_3d(st + hs * St::BOX, &maps.k, full, 0, col, row[hs]);
+          tma_load_3d(st + (St::HALVES + hs) * St::BOX, &maps.v, full, 0, col, row[hs]);
         }
       }
-      const int64_t off = max(half_of(i, mine, &have), 0) * scale_step;
+      __syncwarp();
+      const uint32_t to = smem_u32(st) + SCALES + lane * 16;
 #pragma unroll
-      for (int j = 0; j < COPIES; ++j) {
-        const int x = 32 * j + lane;
-        if (x < 16 * PER_ROW) cp_async_to<16>(smem_u32(st) + scale_dst + 512 * j, scale_src[j] + off, x / PER_ROW < have);
+      for (int hs = 0; hs < St::HALVES; ++hs) {
+        const int64_t off = (int64_t)row[hs] * scale_step;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const uint8_t* from = (v ? p.v_scale : p.k_scale) + off;
+#pragma unroll
+          for (int j = 0; j < COPIES; ++j)
+            if (chunk_row[j] < 16)
+              cp_async_to<16>(to + (v * St::KEYS + 16 * hs) * RECORD + 512 * j, from + chunk_off[j], chunk_row[j] < have[hs]);
+        }
       }
-      fill.advance<COUNT>();
+      cp_async_mbar_arrive(full);
     }
-    cp_async_commit();
+    fill.advance<COUNT>();
   };
   // what the warps left of the span before (and read of it) comes before TMA's writes
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < COUNT - 1; ++i) load(i);
+  for (int i = 0; i < min(n, COUNT - 1); ++i) load(i);
   ws.load_q(p, head0, lane >> 2, lane & 3);
   const typename WarpState<D, MSA_CACHE_E2M1, WIDE>::template Place<true> place(lane, g & 3);
   for (int i = 0; i < n; ++i) {
-    cp_async_wait<COUNT - 2>();
     if (!ring.lost && !mbar_wait(ring.full + ring.at, ring.parity, p.wait_ns)) {
       ring.lost = true;
       set_status(p.status, MSA_ERR_DEVICE_TIMEOUT);
     }
-    // unit i has landed for all warps, and all are done with unit i - 1
-    __syncthreads();
-    load(i + COUNT - 1);
+    __syncthreads();  // all warps are done with unit i - 1
+    if (i + COUNT - 1 < n) load(i + COUNT - 1);
     const uint8_t* st = smem + ring.at * St::TOGETHER;
-    ws.step(st, st + 2 * St::HALVES * St::BOX + (g & 3) * St::SCALE, place, len - (u0 + i) * St::KEYS, lane);
+    ws.step(st, st + SCALES + (g & 3) * St::SCALE, place, len - (u0 + i) * St::KEYS, lane);
     ring.advance<COUNT>();
   }
-  cp_async_wait<0>();
   __syncthreads();  // the sums go where other warps' codes lie
 }
 
@@ -1423,7 +1422,7 @@ __global__ void __launch_bounds__(kThreads, (SPARSE ? Stage<D, KIND, WIDE>::PER_
   if (TOGETHER && p.together) {
     if (threadIdx.x == 0) {
 #pragma unroll
-      for (int i = 0; i < St::TOGETHER_COUNT; ++i) mbar_init(&s_full[i], 1);
+      for (int i = 0; i < St::TOGETHER_COUNT; ++i) mbar_init(&s_full[i], 1 + 32);  // TMA's thread, and a warp's copies
       fence_mbar_init();
     }
     __syncthreads();

@@ -6,7 +6,7 @@
 // the rule of msa_quantize_kv_fp8 bit for bit (IEEE divisions), and reads back
 // decode(code) * s rounded once to bf16.  An E2M1 cache (quantize16 has its rule) stores 4-bit
 // codes with a scale for each 16 of them, and reads back code * block scale * row scale, exactly.
-// Both directions are bound by HBM: every row is read once and written once.
+// Either way every row is read once and written once.
 #include "cache_rows.cuh"
 #include "kernels.h"
 
@@ -27,48 +27,35 @@ struct CacheParams {
   __nv_bfloat16* xv;
   __nv_bfloat16* xi;
   int64_t sk[2], sv[2], si;  // their strides: token, head; token
-  int per;                   // tokens of a warp
+  int per;                   // tokens of a warp (codes: of a CTA)
   int d_idx;
   int* status;
 };
 
-// Reading, and writing bf16.  A token's keys, and its values, are one run of H D values in the pool; a lane
-// moves 8 values of it at a time (16 codes: half the addresses and scales), a warp one token after another.
-// Its lanes find the places of all its tokens (at most 32) together, so the chain of lookups
-// (sequence, length, page) is paid once, and while it works on STEPS vectors a lane, the next ones
-// are on their way.  32K tokens of 8 groups, d 128, with index keys, calls back to
-// back: bf16 49 us each way, E4M3 read 40 us, 4 bits 35 us (5.3 TB/s).
-template <int D, int KIND, bool WRITE>
+// bf16.  A token's keys, and its values, are one run of H D values in the pool; a lane moves 8 values
+// of it at a time, a warp one token after another.  Its lanes find the places of all its tokens (at
+// most 32) together, so the chain of lookups (sequence, length, page) is paid once, and while it
+// works on STEPS vectors a lane, the next ones are on their way.  32K tokens of 8 groups, d 128, with
+// index keys, calls back to back: 49 us each way.
+template <int D>
 struct Lanes {
-  static constexpr bool CODED = KIND != MSA_CACHE_BF16;
-  static_assert(!CODED || !WRITE, "cache_code_kernel writes codes");
-  static constexpr int VALUES = CODED ? 16 : 8;  // of a lane's vector
-  static constexpr int LPR = D / VALUES;         // lanes of a head's row
+  static constexpr int LPR = D / 8;  // lanes of a head's row
   static constexpr int STEPS = 2;
-  static constexpr int BITS = KIND == MSA_CACHE_E2M1 ? 4 : KIND == MSA_CACHE_E4M3 ? 8 : 16;  // of a value in the pool
-  static constexpr int SCALE = KIND == MSA_CACHE_E2M1 ? e2m1_scale_bytes(D) : 4;            // bytes of a row's scales
 };
 
 // STEPS vectors a lane of one token, loaded; where they go.
-template <int D, int KIND, bool WRITE>
+template <int D>
 struct Batch {
-  using L = Lanes<D, KIND, WRITE>;
-  static constexpr int W = L::VALUES / 8;  // 16-byte vectors of a lane in the packed rows
-  uint4 w[L::STEPS][W];                    // (16 codes of the pool: the first, or half of it)
-  float s[L::STEPS];
-  uint4* dst[L::STEPS];                    // null: nothing to store
+  uint4 w[Lanes<D>::STEPS];
+  uint4* dst[Lanes<D>::STEPS];  // null: nothing to store
 };
 
-// As many as the registers of a batch allow.
-template <int KIND>
-constexpr int kCtasPerSm = KIND != MSA_CACHE_BF16 ? 3 : 4;
+constexpr int kCtasPerSm = 4;  // as the registers of a batch allow
 
-template <int D, int KIND, bool WRITE>
-__global__ void __launch_bounds__(kThreads, (kCtasPerSm<KIND>)) cache_kernel(const __grid_constant__ CacheParams p) {
-  using L = Lanes<D, KIND, WRITE>;
-  using B = Batch<D, KIND, WRITE>;
-  constexpr bool F4 = KIND == MSA_CACHE_E2M1;
-  constexpr int W = B::W;
+template <int D, bool WRITE>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) cache_kernel(const __grid_constant__ CacheParams p) {
+  using L = Lanes<D>;
+  using B = Batch<D>;
   const int lane = threadIdx.x & 31;
   const int64_t t0 = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5) * p.per;
   if (t0 >= p.T) return;
@@ -91,28 +78,13 @@ __global__ void __launch_bounds__(kThreads, (kCtasPerSm<KIND>)) cache_kernel(con
       const bool v = u >= half;
       const int f = v ? u - half : u, h = f / L::LPR, sub = f % L::LPR;
       __nv_bfloat16* x = v ? p.xv + t * p.sv[0] + h * p.sv[1] : p.xk + t * p.sk[0] + h * p.sk[1];
-      uint4* packed = reinterpret_cast<uint4*>(x + sub * L::VALUES);
-      void* pool = static_cast<uint8_t*>(v ? p.v : p.k) + (cell * D + f * L::VALUES) * L::BITS / 8;
-      [[maybe_unused]] const uint8_t* scale = (v ? p.v_scale : p.k_scale) + (cell + h) * L::SCALE;
-#pragma unroll
-      for (int e = 0; e < W; ++e) b.w[k][e] = make_uint4(0, 0, 0, 0);
-      b.s[k] = 0.f;
+      uint4* packed = reinterpret_cast<uint4*>(x + sub * 8);
+      uint4* pool = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(v ? p.v : p.k) + cell * D + f * 8);
+      b.w[k] = make_uint4(0, 0, 0, 0);
       b.dst[k] = nullptr;
       if (u >= units || skip) continue;
-      b.dst[k] = WRITE ? static_cast<uint4*>(pool) : packed;
-      if (!there) continue;
-      if (WRITE) {
-#pragma unroll
-        for (int e = 0; e < W; ++e) b.w[k][e] = __ldg(packed + e);
-      } else {
-        if constexpr (F4) {
-          const uint2 c = *static_cast<const uint2*>(pool);
-          b.w[k][0] = make_uint4(c.x, c.y, scale[4 + sub], 0);  // and the block's scale
-        } else {
-          b.w[k][0] = *static_cast<const uint4*>(pool);
-        }
-        if (L::CODED) b.s[k] = *reinterpret_cast<const float*>(scale);
-      }
+      b.dst[k] = WRITE ? pool : packed;
+      if (there) b.w[k] = WRITE ? __ldg(packed) : *pool;
     }
     next_u += 32 * L::STEPS;
     if (next_u >= units) {
@@ -121,35 +93,9 @@ __global__ void __launch_bounds__(kThreads, (kCtasPerSm<KIND>)) cache_kernel(con
     }
   };
   auto store = [&](const B& b) {
-    if constexpr (L::CODED) {
 #pragma unroll
-      for (int k = 0; k < L::STEPS; ++k) {
-        const uint4 c = b.w[k][0];
-        uint4 y0, y1;
-        if constexpr (F4) {
-          const float s = b.s[k] * e4m3_value(c.z);
-          y0 = dequantize_e2m1(c.x, s);
-          y1 = dequantize_e2m1(c.y, s);
-        } else {
-          y0 = dequantize8(make_uint2(c.x, c.y), b.s[k]);
-          y1 = dequantize8(make_uint2(c.z, c.w), b.s[k]);
-        }
-        // a lane's 32 bytes in two stores would write half sectors each: neighbours swap halves, so
-        // that a store writes the 32 bytes of every other lane
-        const bool odd = lane & 1;
-        const uint4 give = odd ? y0 : y1;
-        const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, 1), __shfl_xor_sync(0xffffffffu, give.y, 1),
-                                     __shfl_xor_sync(0xffffffffu, give.z, 1), __shfl_xor_sync(0xffffffffu, give.w, 1));
-        if (!b.dst[k]) continue;
-        uint4* even_dst = b.dst[k] - (odd ? 2 : 0);
-        even_dst[odd ? 1 : 0] = odd ? got : y0;
-        even_dst[odd ? 3 : 2] = odd ? y1 : got;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < L::STEPS; ++k)
-        if (b.dst[k]) *b.dst[k] = b.w[k][0];
-    }
+    for (int k = 0; k < L::STEPS; ++k)
+      if (b.dst[k]) *b.dst[k] = b.w[k];
   };
   if (p.xi) {  // the index keys, d_idx / 8 lanes a token
     const int lanes = p.d_idx >> 3, sub = lane % lanes;
@@ -177,15 +123,21 @@ __global__ void __launch_bounds__(kThreads, (kCtasPerSm<KIND>)) cache_kernel(con
   }
 }
 
-// Writing codes: a CTA takes 8 tokens, and each D / 16 lanes a row at a time.  Bound by instructions and the loads
-// in flight, so as many CTAs as the registers allow: 32K tokens of 8 groups, d 128: E4M3 38.5 us, 4 bits 37.6 with eight a
-// SM (41.1 and 39.9 with six; warps that take tokens in turn with the next vectors on their way, as
-// above: 40.7 and 43.8, and 4.8 us for a single token a sequence in place of 3.2).
-constexpr int kCodeTokens = 8;
+// Codes.  A CTA takes kCodeTokens<D> tokens, and each D / 16 lanes a row at a time.  Bound by instructions and the
+// loads in flight, so as many CTAs as the registers allow.  32K tokens of 8 groups, with index keys, calls back
+// to back, d 128 (d 64), us:               E4M3 write    4 bits        E4M3 read     4 bits
+//   eight CTAs a SM                        38.7 (21.8)   37.6 (21.8)   37.0 (19.6)   34.1 (18.0)
+//   six                                    41.1          39.9          39.2          36.8
+//   warps that take token after token      40.2 (22.8)   43.8 (23.8)   40.3 (20.1)   34.6 (19.2)
+// (the last with the next vectors on their way, as above; a token a sequence takes it 4.8 us, and 3.2 here).
+template <int D>
+constexpr int kCodeTokens = 1024 / D;
+constexpr int kCodeCtas = 8;
+
 template <int D, int KIND>
-__global__ void __launch_bounds__(kThreads, 8)
+__global__ void __launch_bounds__(kThreads, kCodeCtas)
     cache_code_kernel(const __grid_constant__ CacheParams p, const __grid_constant__ CodedRows rows) {
-  __shared__ int64_t s_row[kCodeTokens];
+  __shared__ int64_t s_row[kCodeTokens<D>];
   const int t0 = blockIdx.x * p.per, nt = min(p.per, p.T - t0);
   if (threadIdx.x < nt) {
     const int64_t row = token_row(p.map, t0 + threadIdx.x);
@@ -202,6 +154,70 @@ __global__ void __launch_bounds__(kThreads, 8)
   store_rows<D, KIND>(rows, t0, nt, s_row, [](const __nv_bfloat16*, int, int, uint4&, uint4&) {});
 }
 
+// Reading codes, the same way.
+template <int D, int KIND>
+__global__ void __launch_bounds__(kThreads, kCodeCtas) cache_decode_kernel(const __grid_constant__ CacheParams p, uint32_t div_2H) {
+  constexpr int LPR = D / 16, BITS = KIND == MSA_CACHE_E2M1 ? 4 : 8;
+  constexpr int SCALE = KIND == MSA_CACHE_E2M1 ? e2m1_scale_bytes(D) : 4;
+  __shared__ int64_t s_row[kCodeTokens<D>];
+  const int t0 = blockIdx.x * p.per, nt = min(p.per, p.T - t0);
+  if (threadIdx.x < nt) {
+    const int64_t row = token_row(p.map, t0 + threadIdx.x);
+    if (row == kNoPlace) set_status(p.status, MSA_ERR_ARG);
+    s_row[threadIdx.x] = row;
+  }
+  __syncthreads();
+  if (p.xi) {
+    const int lanes = p.d_idx >> 3, tok = threadIdx.x / lanes, sub = threadIdx.x % lanes;
+    if (tok < nt && s_row[tok] != kNoToken)
+      reinterpret_cast<uint4*>(p.xi + (t0 + tok) * p.si)[sub] =
+          s_row[tok] < 0 ? make_uint4(0, 0, 0, 0) : reinterpret_cast<const uint4*>(p.k_idx + s_row[tok] * p.d_idx)[sub];
+  }
+  const int lane = threadIdx.x & 31, rows = nt * 2 * p.H, sub = lane % LPR;
+  const bool odd = lane & 1;
+  for (int i0 = threadIdx.x - lane; i0 < rows * LPR; i0 += kThreads) {  // whole warps
+    const int r = (i0 + lane) / LPR, tok = min(small_div(r, div_2H), nt - 1), hv = r - tok * 2 * p.H;
+    const int v = hv >= p.H, h = v ? hv - p.H : hv;
+    const int64_t row = s_row[tok];
+    uint4 y0 = make_uint4(0, 0, 0, 0), y1 = y0;  // a missing place reads as zeros
+    if (r < rows && row >= 0) {
+      const int64_t cell = row * p.H + h;
+      const uint8_t* codes = static_cast<const uint8_t*>(v ? p.v : p.k) + (cell * D + 16 * sub) * BITS / 8;
+      const uint8_t* scale = (v ? p.v_scale : p.k_scale) + cell * SCALE;
+      float s = *reinterpret_cast<const float*>(scale);
+      if constexpr (KIND == MSA_CACHE_E2M1) {
+        const uint2 x = *reinterpret_cast<const uint2*>(codes);
+        s *= e4m3_value(scale[4 + sub]);
+        y0 = dequantize_e2m1(x.x, s);
+        y1 = dequantize_e2m1(x.y, s);
+      } else {
+        const uint4 x = *reinterpret_cast<const uint4*>(codes);
+        y0 = dequantize8(make_uint2(x.x, x.y), s);
+        y1 = dequantize8(make_uint2(x.z, x.w), s);
+      }
+    }
+    // a lane's 32 bytes in two stores would write half sectors each: neighbours swap halves, so that a store
+    // writes the 32 bytes of every other lane
+    const uint4 give = odd ? y0 : y1;
+    const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, 1), __shfl_xor_sync(0xffffffffu, give.y, 1),
+                                 __shfl_xor_sync(0xffffffffu, give.z, 1), __shfl_xor_sync(0xffffffffu, give.w, 1));
+    if (r >= rows || row == kNoToken) continue;
+    __nv_bfloat16* x = v ? p.xv + (t0 + tok) * p.sv[0] + h * p.sv[1] : p.xk + (t0 + tok) * p.sk[0] + h * p.sk[1];
+    uint4* even_dst = reinterpret_cast<uint4*>(x + 16 * (sub & ~1));
+    even_dst[odd ? 1 : 0] = odd ? got : y0;
+    even_dst[odd ? 3 : 2] = odd ? y1 : got;
+  }
+}
+
+template <int D, int KIND>
+cudaError_t launch_decode(CacheParams& p, int num_sms, cudaStream_t st) {
+  p.per = kCodeTokens<D>;
+  while (p.per > 1 && ((int64_t)p.T + p.per - 1) / p.per < kCodeCtas * num_sms) p.per >>= 1;
+  cache_decode_kernel<D, KIND><<<(unsigned)(((int64_t)p.T + p.per - 1) / p.per), kThreads, 0, st>>>(p, magic(2 * p.H));
+  note_launch();
+  return cudaGetLastError();
+}
+
 template <int D, int KIND>
 cudaError_t launch_codes(CacheParams& p, int num_sms, cudaStream_t st) {
   CodedRows r = {};
@@ -215,37 +231,32 @@ cudaError_t launch_codes(CacheParams& p, int num_sms, cudaStream_t st) {
   }
   r.H = p.H;
   r.div_2H = magic(2 * p.H);
-  p.per = kCodeTokens;  // while the grid fills the GPU
-  while (p.per > 1 && ((int64_t)p.T + p.per - 1) / p.per < 8 * num_sms) p.per >>= 1;
+  p.per = kCodeTokens<D>;  // while the grid fills the GPU
+  while (p.per > 1 && ((int64_t)p.T + p.per - 1) / p.per < kCodeCtas * num_sms) p.per >>= 1;
   cache_code_kernel<D, KIND><<<(unsigned)(((int64_t)p.T + p.per - 1) / p.per), kThreads, 0, st>>>(p, r);
   note_launch();
   return cudaGetLastError();
 }
 
-template <int D, int KIND, bool WRITE>
-cudaError_t launch_cache(CacheParams& p, int num_sms, cudaStream_t st) {
-  if constexpr (WRITE && KIND != MSA_CACHE_BF16) {
-    return launch_codes<D, KIND>(p, num_sms, st);
-  } else {
-    // tokens of a warp: as many as let all warps run together
-    const int64_t together = (int64_t)num_sms * kCtasPerSm<KIND> * (kThreads / 32);
-    const int64_t want = (p.T + together - 1) / together;
-    p.per = (int)(want < 32 ? want : 32);
-    const int64_t warps = ((int64_t)p.T + p.per - 1) / p.per;
-    const int64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    cache_kernel<D, KIND, WRITE><<<(unsigned)grid, kThreads, 0, st>>>(p);
-    note_launch();
-    return cudaGetLastError();
-  }
+template <int D, bool WRITE>
+cudaError_t launch_bf16(CacheParams& p, int num_sms, cudaStream_t st) {
+  // tokens of a warp: as many as let all warps run together
+  const int64_t together = (int64_t)num_sms * kCtasPerSm * (kThreads / 32);
+  const int64_t want = (p.T + together - 1) / together;
+  p.per = (int)(want < 32 ? want : 32);
+  const int64_t warps = ((int64_t)p.T + p.per - 1) / p.per;
+  const int64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
+  cache_kernel<D, WRITE><<<(unsigned)grid, kThreads, 0, st>>>(p);
+  note_launch();
+  return cudaGetLastError();
 }
 
 template <int D, bool WRITE>
 cudaError_t launch_cache(int kind, CacheParams& p, int num_sms, cudaStream_t st) {
-  switch (kind) {
-    case MSA_CACHE_E4M3: return launch_cache<D, MSA_CACHE_E4M3, WRITE>(p, num_sms, st);
-    case MSA_CACHE_E2M1: return launch_cache<D, MSA_CACHE_E2M1, WRITE>(p, num_sms, st);
-    default: return launch_cache<D, MSA_CACHE_BF16, WRITE>(p, num_sms, st);
-  }
+  if (kind == MSA_CACHE_BF16) return launch_bf16<D, WRITE>(p, num_sms, st);
+  if (kind == MSA_CACHE_E4M3)
+    return WRITE ? launch_codes<D, MSA_CACHE_E4M3>(p, num_sms, st) : launch_decode<D, MSA_CACHE_E4M3>(p, num_sms, st);
+  return WRITE ? launch_codes<D, MSA_CACHE_E2M1>(p, num_sms, st) : launch_decode<D, MSA_CACHE_E2M1>(p, num_sms, st);
 }
 
 template <bool WRITE>

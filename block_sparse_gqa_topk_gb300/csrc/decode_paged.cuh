@@ -10,7 +10,8 @@
 //   lse = ln sum_i e^lse_i,  o = sum_i e^(lse_i - lse) o_i.
 //
 // The cache is read once and each byte meets 2 G multiply-adds, so HBM sets the pace and the
-// products run on mma.sync with the group's heads as the 16 rows.
+// products run on mma.sync with the group's heads as the 16 rows (4 bits, where widening the codes sets
+// the pace, with keys as rows).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -25,7 +26,7 @@ namespace msa {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-// CTAs over which a call's units are spread: three on each of the 152 SMs.  Each leaves at
+// CTAs over which a call's units are spread: three (four) on each of the 152 SMs.  Each leaves at
 // most two partial results (its first and its last (sequence, group)), whatever the batch.
 constexpr int kCtas = 152 * 3, kMaxCtas = 152 * 4;  // (four for whole 4-bit caches)
 // Blocks a sequence up to which the attention kernel selects for itself, 8 scores a thread: every
@@ -1216,7 +1217,8 @@ struct StageRing {
 // bringing a unit of all four groups: the codes by TMA, 16 tokens a box, and the scales in 16-byte chunks (four
 // groups' records are neighbours in the pool; boxes of 48 bytes take TMA longer than those of the codes).  What
 // counts beside the products are the instructions of the copies: 8 x 128K, d 128: each warp copying for itself
-// 334 us; codes by TMA and a warp's part of the scales by each 273; in turn 269.
+// 334 us; codes by TMA and a warp's part of the scales by each 273; in turn 269 (the last warp
+// to be done with a stage filling it again, without a barrier: 312).
 template <int D, bool WIDE>
 __device__ __forceinline__ void attend_together(const PagedDecode& p, const CodeMaps<true>& maps,
                                                 WarpState<D, MSA_CACHE_E2M1, WIDE>& ws, uint8_t* smem, StageRing& ring,
@@ -1408,7 +1410,8 @@ __device__ __forceinline__ void write_empty(const PagedDecode& p, int64_t head0,
 // (sequence, groups) is written out, a part of one goes to the CTA's slot 0 (its first span) or 1.
 // Bound by HBM: 8 whole caches of 128K tokens take 594 us in bf16 (4.3 GB, 7.2 TB/s) and 333 us in
 // E4M3 (2.2 GB, 6.6 TB/s), 16 blocks of each 19 us after the scores.  Bound by issue: E4M3 with d = 64
-// (229 us, 5.0 TB/s) or 16 heads a group (392 us, 5.6 TB/s).
+// (229 us, 5.0 TB/s) or 16 heads a group (392 us, 5.6 TB/s), and 4 bits (263 us, 1.3 GB, 4.85 TB/s; d = 64
+// 190 us).
 template <int D, int KIND, bool WIDE, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, (SPARSE ? Stage<D, KIND, WIDE>::PER_SM : Stage<D, KIND, WIDE>::DENSE_PER_SM))
     paged_attn_kernel(const PagedDecode p, const __grid_constant__ CodeMaps<(KIND == MSA_CACHE_E2M1 && !SPARSE)> maps) {

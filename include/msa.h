@@ -424,8 +424,8 @@ int msa_cache_append(const msa_paged_cache_t* c, const msa_page_table_t* pages, 
                      const void* k_idx, void* q_out, void* q_idx_out, cudaStream_t stream);
 
 /*
- * Decode over a paged cache: one new query token per sequence, its own k, v and k_idx
- * already in the cache (msa_cache_write), lens[b] the length with it.
+ * Decode over a paged cache of any kind: one new query token per sequence, its own k, v and k_idx
+ * already in the cache (msa_cache_write, msa_cache_append), lens[b] the length with it.
  *   msa_decode_paged: msa_decode's computation (block selection over the index keys, ties to
  *     the lower block, then attention over the selected blocks) on pages.  topk <= 32.
  *   msa_decode_paged_dense: attention over all lens[b] tokens (the dense set of the indexer

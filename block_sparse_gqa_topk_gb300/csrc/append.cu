@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 6) append_kernel(const __grid_consta
 
 template <int D, int KIND>
 cudaError_t launch_append(const AppendParams& p, bool vec, bool inter, cudaStream_t st) {
-  const unsigned grid = (unsigned)((p.T + p.tpb - 1) / p.tpb);
+  const unsigned grid = (unsigned)(((int64_t)p.T + p.tpb - 1) / p.tpb);
   if (vec) {
     if (inter) append_kernel<D, KIND, 8, true><<<grid, kThreads, 0, st>>>(p);
     else append_kernel<D, KIND, 8, false><<<grid, kThreads, 0, st>>>(p);
@@ -233,7 +233,7 @@ extern "C" int msa_cache_append(const msa_paged_cache_t* c, const msa_page_table
   // tokens of a CTA: up to kMaxTokens while the grid still fills the GPU and an item index stays below
   // 2^18 (small_div)
   p.tpb = kMaxTokens;
-  while (p.tpb > 1 && ((p.T + p.tpb - 1) / p.tpb < 8 * cx.num_sms || (int64_t)p.tpb * all > (1 << 18))) p.tpb >>= 1;
+  while (p.tpb > 1 && (((int64_t)p.T + p.tpb - 1) / p.tpb < 8 * cx.num_sms || (int64_t)p.tpb * all > (1 << 18))) p.tpb >>= 1;
   const bool inter = a->interleaved != 0;
   cudaError_t e;
   switch (c->kind) {

@@ -1527,6 +1527,10 @@ __global__ void __launch_bounds__(kThreads, (SPARSE ? Stage<D, KIND, WIDE>::PER_
     }
     __syncthreads();  // the stages are free for the next span
   }
+  if (TOGETHER && stages.lost) {  // no wait held the later copies: those in flight have their time to land
+    for (int i = 0; i < St::TOGETHER_COUNT; ++i)
+      mbar_wait(&s_full[i], i < stages.at ? stages.parity : stages.parity ^ 1, p.wait_ns);
+  }
 }
 
 // ---------------------------------------------------------------------------

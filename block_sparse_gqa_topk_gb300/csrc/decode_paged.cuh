@@ -263,9 +263,8 @@ struct Stage {
   static constexpr int SMEM_TOGETHER = TOGETHER_COUNT * TOGETHER + 1024;  // their start is rounded up
   static constexpr int UNIT = KEYS * kWarps;  // tokens of a unit of work
   static constexpr int PER = 128 / UNIT;      // units of a block
-  __device__ __forceinline__ static uint32_t key_at(int r, int ch) {
+  __device__ __forceinline__ static uint32_t key_at(int r, int ch) {  // not of E2M1
     if constexpr (!CODED) return swz<ROW>(r, ch);
-    else if constexpr (F4) return r * ROW + (ch << 4);
     else return r * ROW + ((D == 128 ? ch ^ ((r & 1) << 2) : ch) << 4);
   }
   __device__ __forceinline__ static uint32_t value_at(int r, int ch) {
@@ -1126,45 +1125,44 @@ __device__ __forceinline__ void attend(const PagedDecode& p, WarpState<D, KIND, 
       }
       if constexpr (F4) {
         load4(i);
-        cp_async_commit();
-        return;
-      }
-      uint8_t* st = ring + (i % St::COUNT) * St::BYTES;
-      const int pos0 = first_token(i);
+      } else {
+        uint8_t* st = ring + (i % St::COUNT) * St::BYTES;
+        const int pos0 = first_token(i);
 #pragma unroll
-      for (int hs = 0; hs < St::HALVES; ++hs) {
-        const int pos = pos0 + 16 * hs;
-        const int id = __shfl_sync(0xffffffffu, ids, (i % AHEAD) * St::HALVES + hs);
-        const int have = len - pos;  // tokens of the sequence from here on
-        if (hs == 0 && have <= 0) break;  // step() will not look at this stage
-        const bool good = (unsigned)id < (unsigned)p.pages.num_pages;
-        if (!good && have > 0) set_status(p.status, MSA_ERR_ARG);
-        const int64_t row0 =
-            good ? (int64_t)id * p.pages.page_size + (pos - page_of(p.pages, pos) * p.pages.page_size) : 0;
-        const int64_t at = (row0 * p.H + g) * St::ROW + lane_off;
-        const uint8_t* kp = static_cast<const uint8_t*>(p.k) + at;
-        const uint8_t* vp = static_cast<const uint8_t*>(p.v) + at;
-        const bool full = good && have >= 16;
+        for (int hs = 0; hs < St::HALVES; ++hs) {
+          const int pos = pos0 + 16 * hs;
+          const int id = __shfl_sync(0xffffffffu, ids, (i % AHEAD) * St::HALVES + hs);
+          const int have = len - pos;  // tokens of the sequence from here on
+          if (hs == 0 && have <= 0) break;  // step() will not look at this stage
+          const bool good = (unsigned)id < (unsigned)p.pages.num_pages;
+          if (!good && have > 0) set_status(p.status, MSA_ERR_ARG);
+          const int64_t row0 =
+              good ? (int64_t)id * p.pages.page_size + (pos - page_of(p.pages, pos) * p.pages.page_size) : 0;
+          const int64_t at = (row0 * p.H + g) * St::ROW + lane_off;
+          const uint8_t* kp = static_cast<const uint8_t*>(p.k) + at;
+          const uint8_t* vp = static_cast<const uint8_t*>(p.v) + at;
+          const bool full = good && have >= 16;
 #pragma unroll
-        for (int j = 0; j < 16 / RPI; ++j) {
-          const int r = r0 + j * RPI;
-          uint8_t* kd = st + St::key_at(16 * hs + r, ch);
-          uint8_t* vd = st + St::value_at(16 * hs + r, ch);
-          if (full) {
-            cp_async_16(kd, kp + j * RPI * row_step);
-            cp_async_16(vd, vp + j * RPI * row_step);
-          } else {  // else zeros: no stale NaN meets a weight of 0
-            const bool ok = good && r < have;
-            const int64_t off = ok ? j * RPI * row_step : -lane_off;
-            cp_async_16(kd, kp + off, ok);
-            cp_async_16(vd, vp + off, ok);
+          for (int j = 0; j < 16 / RPI; ++j) {
+            const int r = r0 + j * RPI;
+            uint8_t* kd = st + St::key_at(16 * hs + r, ch);
+            uint8_t* vd = st + St::value_at(16 * hs + r, ch);
+            if (full) {
+              cp_async_16(kd, kp + j * RPI * row_step);
+              cp_async_16(vd, vp + j * RPI * row_step);
+            } else {  // else zeros: no stale NaN meets a weight of 0
+              const bool ok = good && r < have;
+              const int64_t off = ok ? j * RPI * row_step : -lane_off;
+              cp_async_16(kd, kp + off, ok);
+              cp_async_16(vd, vp + off, ok);
+            }
           }
-        }
-        if constexpr (St::CODED) {  // lanes 0..15 the keys' scales, the others the values'
-          const int r = lane & 15;
-          const bool ok = good && r < have;
-          const uint8_t* src = (lane < 16 ? p.k_scale : p.v_scale) + (ok ? ((row0 + r) * p.H + g) * 4 : 0);
-          cp_async_4(st + St::S0 + ((lane < 16 ? 0 : St::KEYS) + 16 * hs + r) * 4, src, ok);
+          if constexpr (St::CODED) {  // lanes 0..15 the keys' scales, the others the values'
+            const int r = lane & 15;
+            const bool ok = good && r < have;
+            const uint8_t* src = (lane < 16 ? p.k_scale : p.v_scale) + (ok ? ((row0 + r) * p.H + g) * 4 : 0);
+            cp_async_4(st + St::S0 + ((lane < 16 ? 0 : St::KEYS) + 16 * hs + r) * 4, src, ok);
+          }
         }
       }
     }

@@ -293,3 +293,83 @@ def test_far_pages():
     b = ops.msa_decode_paged(q, qi, near, dev([list(range(6))]), dev([n]), 3)
     assert all(torch.equal(x, y) for x, y in zip(a, b))
     assert ops.device_status() == 0
+
+
+def test_far_pages_of_a_long_call():
+    """The same where the groups come together, for the dense call and for reading back."""
+    page, H, d, n = 128, 8, 128, 121003
+    own = (n + page - 1) // page
+    pages = (2 ** 31) // (page * H * d // 2) + own + 40
+    c = ops.new_paged_cache(pages, H, page_size=page, d=d, d_idx=64, fp4=True)
+    near = ops.new_paged_cache(own, H, page_size=page, d=d, d_idx=64, fp4=True)
+    table, near_table = dev([list(range(pages - own, pages))]), dev([list(range(own))])
+    k, v, ki = query(n, H, d, 1), query(n, H, d, 2), query(n, 64, 64, 3)[:, 0]
+    ops.msa_cache_write(c, table, dev([n]), k, v, ki, cu_seqlens=dev([0, n]))
+    ops.msa_cache_write(near, near_table, dev([n]), k, v, ki, cu_seqlens=dev([0, n]))
+    assert torch.equal(c.k[-own:], near.k) and torch.equal(c.v_scale[-own:], near.v_scale)
+    q, qi = query(1, 32, d, 4), query(1, H, 64, 5)
+    a = (*ops.msa_decode_paged(q, qi, c, table, dev([n]), 3), *ops.msa_decode_paged_dense(q, c, table, dev([n])),
+         *ops.msa_cache_read(c, table, dev([n]), dev([0, n]), n))
+    b = (*ops.msa_decode_paged(q, qi, near, near_table, dev([n]), 3),
+         *ops.msa_decode_paged_dense(q, near, near_table, dev([n])),
+         *ops.msa_cache_read(near, near_table, dev([n]), dev([0, n]), n))
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("slack", [1, 2000])
+def test_a_pool_without_pages(slack):
+    """Every id is bad: zero rows, as the status says."""
+    c = ops.new_paged_cache(0, 4, page_size=16, d=64, d_idx=32, fp4=True)
+    q, qi = query(2, 8, 64, 1), query(2, 4, 32, 2)
+    t = dev(np.zeros((2, 20 * slack)))
+    o, lse = ops.msa_decode_paged_dense(q, c, t, dev([300, 17]))
+    assert ops.device_status() == _lib.MSA_ERR_ARG
+    assert not o.any() and torch.allclose(lse, torch.tensor([[300.0], [17.0]], device="cuda").log().expand(2, 8))
+    sets, o, lse = ops.msa_decode_paged(q, qi, c, t, dev([300, 17]), 2)
+    assert ops.device_status() == _lib.MSA_ERR_ARG and not o.any()
+
+
+@pytest.mark.parametrize("d,G", [(64, 3), (128, 4), (128, 16)])
+def test_three_sets_of_four_groups(d, G):
+    """Twelve groups come together four at a time, on pages that end inside a unit."""
+    lens, H = [90001, 5, 0, 33], 12
+    batch = Batch4(lens, 48, H, d, 0, seed=81)
+    q = query(len(lens), H * G, d, 82)
+    o, lse = ops.msa_decode_paged_dense(q, batch.cache, batch.table, batch.lens_t)
+    assert ops.device_status() == 0
+    batch.check_dense(q, d ** -0.5, o, lse)
+
+
+def test_long_calls_on_two_streams_and_in_two_graphs():
+    """Calls whose groups come together, at the same time on two streams and replayed together."""
+    batches = [Batch4([60000 + 31 * i, 30001], 64, 8, 128, 0, seed=90 + i) for i in range(2)]
+    qs = [query(2, 32, 128, 92 + i) for i in range(2)]
+
+    def call(i):
+        return ops.msa_decode_paged_dense(qs[i], batches[i].cache, batches[i].table, batches[i].lens_t)
+
+    want = [call(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for i, s in enumerate(streams):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append([call(i) for _ in range(3)])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, y) for out in got[i] for x, y in zip(want[i], out))
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = call(i)
+        graphs.append((g, out))
+    for _ in range(3):
+        for s, (g, _) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, y) for x, y in zip(want[i], graphs[i][1]))
+    assert ops.device_status() == 0

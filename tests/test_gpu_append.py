@@ -243,3 +243,15 @@ def test_refusals():
         call(cache=plain)
     assert ops.msa_cache_append(plain, t, lens, ops.new_rope(64), *x[:3])[1] is None
     assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("kind", range(3))
+def test_a_pool_without_pages(kind):
+    """No id is one of the pool's: tokens are dropped with zero queries, the status says so; an empty slot is none."""
+    c = ops.new_paged_cache(0, 2, page_size=16, d=64, d_idx=32, **KINDS[kind])
+    q, k, v, qi, ki = inputs(2, 4, 2, 2, 64, 32, 11)
+    table, rope = dev([[0, 0], [0, 0]]), ops.new_rope(32)
+    y, yi = ops.msa_cache_append(c, table, dev([20, 0]), rope, q, k, v, qi, ki)
+    assert ops.device_status() == _lib.MSA_ERR_ARG and not y.any() and not yi.any()
+    y, yi = ops.msa_cache_append(c, table, dev([0, 0]), rope, q, k, v, qi, ki)
+    assert ops.device_status() == 0 and not y.any() and not yi.any()

@@ -311,6 +311,7 @@ int run_paged(const msa_paged_cache_t* c, const msa_page_table_t* pt, const int3
   const int64_t most = (int64_t)p.B * p.H * (((int64_t)pt->max_pages * c->page_size + 127) / 128 + kOverhead);
   p.together = c->kind == MSA_CACHE_E2M1 && p.wh == 4 && pages_exist && most >= (int64_t)kSideBySideTogether * p.ctas &&
                (int64_t)c->num_pages * c->page_size < (int64_t{1} << 31);
+  p.withheld = cx.debug & MSA_DEBUG_WITHHOLD_LOAD ? 0 : -1;
   p.wait_ns = cx.wait_ns;
   p.status = cx.status;
   cudaError_t e = cudaSuccess;

@@ -53,6 +53,7 @@ struct PagedDecode {
   float* lse;
   int B, H, G, topk;
   int together;    // 4 bits: four groups side by side come by TMA
+  int withheld;    // unit of a span whose copies are left out (msa_debug_set); -1: none
   uint64_t wait_ns;  // bound of a wait for it
   int row;         // blocks of the table's length, rounded up to 4
   int cluster;     // CTAs of a (sequence, group) in the small form; 0: the other one
@@ -1202,7 +1203,6 @@ struct StageRing {
   uint64_t* full;
   int at;
   uint32_t parity;
-  bool lost;  // a wait ran out
   template <int COUNT>
   __device__ __forceinline__ void advance() {
     if (++at == COUNT) {
@@ -1218,8 +1218,10 @@ struct StageRing {
 // counts beside the products are the instructions of the copies: 8 x 128K, d 128: each warp copying for itself
 // 334 us; codes by TMA and a warp's part of the scales by each 273; in turn 269 (the last warp
 // to be done with a stage filling it again, without a barrier: 312).
+// False, in all threads alike, where a wait ran out: no copy of the CTA is then on its way that was not given
+// its time to land, and none follows.
 template <int D, bool WIDE>
-__device__ __forceinline__ void attend_together(const PagedDecode& p, const CodeMaps<true>& maps,
+__device__ __forceinline__ bool attend_together(const PagedDecode& p, const CodeMaps<true>& maps,
                                                 WarpState<D, MSA_CACHE_E2M1, WIDE>& ws, uint8_t* smem, StageRing& ring,
                                                 int b, int g, int len, int u0, int n) {
   using St = Stage<D, MSA_CACHE_E2M1, WIDE>;
@@ -1248,7 +1250,7 @@ __device__ __forceinline__ void attend_together(const PagedDecode& p, const Code
       ids = ids_next;
       ids_next = page_ids(i + AHEAD);
     }
-    if ((i & 3) == warp) {
+    if ((i & 3) == warp && i != p.withheld) {
       uint8_t* st = smem + fill.at * St::TOGETHER;
       uint64_t* full = fill.full + fill.at;
       int row[St::HALVES], have[St::HALVES], boxes = 0;  // first row of each half, and its tokens (0: none, or no page)
@@ -1298,17 +1300,22 @@ __device__ __forceinline__ void attend_together(const PagedDecode& p, const Code
   ws.load_q(p, head0, lane >> 2, lane & 3);
   const typename WarpState<D, MSA_CACHE_E2M1, WIDE>::template Place<true> place(lane, g & 3);
   for (int i = 0; i < n; ++i) {
-    if (!ring.lost && !mbar_wait(ring.full + ring.at, ring.parity, p.wait_ns)) {
-      ring.lost = true;
+    const bool late = !mbar_wait(ring.full + ring.at, ring.parity, p.wait_ns);
+    if (__syncthreads_or(late)) {  // all warps are done with unit i - 1
       set_status(p.status, MSA_ERR_DEVICE_TIMEOUT);
+      for (int k = i; k < min(n, i + COUNT - 1); ++k) {  // the units on their way, each in its own phase
+        mbar_wait(ring.full + ring.at, ring.parity, p.wait_ns);
+        ring.advance<COUNT>();
+      }
+      return false;
     }
-    __syncthreads();  // all warps are done with unit i - 1
     if (i + COUNT - 1 < n) load(i + COUNT - 1);
     const uint8_t* st = smem + ring.at * St::TOGETHER;
     ws.step(st, st + SCALES + (g & 3) * St::SCALE, place, len - (u0 + i) * St::KEYS, lane);
     ring.advance<COUNT>();
   }
   __syncthreads();  // the sums go where other warps' codes lie
+  return true;
 }
 
 // What the warps of a CTA leave of a span: running sums in their own stages ([8 R][D + 4] floats),
@@ -1420,7 +1427,7 @@ __global__ void __launch_bounds__(kThreads, (SPARSE ? Stage<D, KIND, WIDE>::PER_
   // TMA's swizzle goes by the address
   uint8_t* smem = TOGETHER ? smem_start + (-smem_u32(smem_start) & 1023) : smem_start;
   __shared__ uint64_t s_full[TOGETHER ? St::TOGETHER_COUNT : 1];
-  StageRing stages{s_full, 0, 0, false};
+  StageRing stages{s_full, 0, 0};
   if (TOGETHER && p.together) {
     if (threadIdx.x == 0) {
 #pragma unroll
@@ -1484,7 +1491,7 @@ __global__ void __launch_bounds__(kThreads, (SPARSE ? Stage<D, KIND, WIDE>::PER_
       bool done = false;
       if constexpr (TOGETHER) {
         if (wh == 4 && p.together) {
-          attend_together<D, WIDE>(p, maps, ws, smem, stages, b, g, len, u0, n);
+          if (!attend_together<D, WIDE>(p, maps, ws, smem, stages, b, g, len, u0, n)) return;
           done = true;
         }
       }
@@ -1525,10 +1532,6 @@ __global__ void __launch_bounds__(kThreads, (SPARSE ? Stage<D, KIND, WIDE>::PER_
       }
     }
     __syncthreads();  // the stages are free for the next span
-  }
-  if (TOGETHER && stages.lost) {  // no wait held the later copies: those in flight have their time to land
-    for (int i = 0; i < St::TOGETHER_COUNT; ++i)
-      mbar_wait(&s_full[i], i < stages.at ? stages.parity : stages.parity ^ 1, p.wait_ns);
   }
 }
 

@@ -461,9 +461,10 @@ const char* msa_status_string(int code);
 
 /* Test knob for the failure path, per process: the bounded device waits give up
  * after wait_limit_ns (0 restores the default of 2 s); flags bit 0
- * (MSA_DEBUG_WITHHOLD_LOAD) makes the next index-top-k launches withhold their first
- * TMA load, so the consumer's wait runs out, the kernel records
- * MSA_ERR_DEVICE_TIMEOUT and returns without hanging. */
+ * (MSA_DEBUG_WITHHOLD_LOAD) makes the next index-top-k launches, and those of the whole-cache
+ * decode that bring four groups of a 4-bit cache by TMA, withhold their first
+ * load, so the consumer's wait runs out, the kernel records
+ * MSA_ERR_DEVICE_TIMEOUT and returns without hanging (its outputs are then undefined). */
 #define MSA_DEBUG_WITHHOLD_LOAD 1
 int msa_debug_set(uint64_t wait_limit_ns, int flags);
 

@@ -409,6 +409,7 @@ int msa_cache_read(const msa_paged_cache_t* c, const msa_page_table_t* pages, co
  * Out: q_out [total_tokens][H_q][d], q_idx_out [total_tokens][H_i][d_idx] (contiguous, 16-byte aligned,
  *   apart from the inputs).  A token that msa_cache_write skips (an empty slot, behind
  *   cu_seqlens[B]) or drops (no place: MSA_ERR_ARG in the status word) gets zero rows there.
+ *   Without sequences (B = 0) the call returns at once, and q_out and q_idx_out stay as they are.
  */
 typedef struct msa_append {
   int32_t rot_dim, interleaved, positions_bits; /* 32 or 64 */

@@ -182,8 +182,9 @@ static __device__ __noinline__ uint32_t divide_e2m1(uint4 w, float down, float b
 //   block = E4M3 nearest to amax / 6 / row, at least 2^-9;  code = E2M1 nearest to x / (block row).
 // amax / 6 by a product: with the rounded 1/6 (too large by 2^-25 of it) a quotient that lies on the
 // border of two E4M3 numbers still rounds to the border, and one that does not is 2^-9 away from it,
-// as amax has 8 significant bits.  The other quotient is x (r + s), 1 / block = r + s to 2^-46 of it, rounded
-// once: what lies on the border of two codes (block times it has 8 bits) comes out as the border, and
+// as amax has 8 significant bits.  The other quotient is x (r + s), rounded once, with 1 / block = r + s to 2^-42
+// of it (r is at most 3 2^-23 of it too small; s leaves out the square of that, and its own rounding,
+// 2^-45): what lies on the border of two codes (block times it has 8 bits) comes out as the border, and
 // everything else is 2^-9 away.  r <= 1 / block, so that s is no negative number and a zero keeps its sign.
 // A block that holds an infinity or a NaN gets the scale NaN, so that its values read as NaN.  At the
 // largest row scale the block's ends at 320: 6 * 320 * 2^117 is the largest value that bf16 holds.

@@ -828,6 +828,8 @@ def new_paged_cache(num_pages: int, H_kv: int, *, page_size: int = 128, d: int =
     (fp4: 4.75 bits a value with its scales, 5 with d 64)."""
     if fp8 and fp4:
         raise ValueError("fp8 and fp4 exclude one another")
+    if d not in (64, 128):  # before d / 2 drops a half
+        raise ValueError(f"d must be 64 or 128, got {d}")
 
     def pages(*tail, dtype):
         return torch.zeros((num_pages, page_size, *tail), dtype=dtype, device=device)

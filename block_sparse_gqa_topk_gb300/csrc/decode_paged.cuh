@@ -10,8 +10,8 @@
 //   lse = ln sum_i e^lse_i,  o = sum_i e^(lse_i - lse) o_i.
 //
 // The cache is read once and each byte meets 2 G multiply-adds, so HBM sets the pace and the
-// products run on mma.sync with the group's heads as the 16 rows (4 bits, where widening the codes sets
-// the pace, with keys as rows).
+// products run on mma.sync with the group's heads as the 16 rows (4 bits, where the instructions of
+// widening and scaling the codes weigh more than their bytes, with keys as rows).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -128,7 +128,9 @@ struct Cut {
 // d 64 216 / 229, bf16 593 / 598).  They pay from about this much work (of one group) a CTA.
 constexpr int kSideBySide = 48;
 // 4-bit caches whose groups come together by TMA gain from less work on, as one warp copies for all
-// (32 ragged sequences up to 32K, 8 groups: 105 us where they begin at 24 or 48 units a CTA, 82 at 12).
+// (32 ragged sequences up to 32K, 8 groups: 105 us where they begin at 24 or 48 units a CTA, 82 at 12), but
+// not from little: with about 7 units a CTA, 4 groups of 32 ragged sequences up to 8K take 31.2 us apart and 32.2
+// together (begun at 3 or 6), 8 groups up to 4K 34.7 and 35.7.
 constexpr int kSideBySideTogether = 12;
 
 struct Work {
@@ -1416,8 +1418,10 @@ __device__ __forceinline__ void write_empty(const PagedDecode& p, int64_t head0,
 // (sequence, groups) is written out, a part of one goes to the CTA's slot 0 (its first span) or 1.
 // Bound by HBM: 8 whole caches of 128K tokens take 594 us in bf16 (4.3 GB, 7.2 TB/s) and 333 us in
 // E4M3 (2.2 GB, 6.6 TB/s), 16 blocks of each 19 us after the scores.  Bound by issue: E4M3 with d = 64
-// (229 us, 5.0 TB/s) or 16 heads a group (392 us, 5.6 TB/s), and 4 bits (263 us, 1.3 GB, 4.85 TB/s; d = 64
-// 190 us).
+// (229 us, 5.0 TB/s) or 16 heads a group (392 us, 5.6 TB/s).  4 bits (262 us, 1.3 GB, 4.9 TB/s; d = 64 184 us)
+// fill neither HBM nor a pipe (59 percent of the issue slots, ALU 53): 16 warps a SM wait for the
+// latency of their own chains and for one another at a unit's barrier.  With 16 heads a group 8 warps a SM are left,
+// and E4M3 is faster (417 us for 392).
 template <int D, int KIND, bool WIDE, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, (SPARSE ? Stage<D, KIND, WIDE>::PER_SM : Stage<D, KIND, WIDE>::DENSE_PER_SM))
     paged_attn_kernel(const PagedDecode p, const __grid_constant__ CodeMaps<(KIND == MSA_CACHE_E2M1 && !SPARSE)> maps) {

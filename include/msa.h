@@ -404,7 +404,8 @@ int msa_cache_read(const msa_paged_cache_t* c, const msa_page_table_t* pages, co
  *   k_idx [total_tokens][d_idx], bf16, with the strides of msa_append_t in elements (those of k, v and
  *   k_idx multiples of 8 and their addresses of 16 bytes; q and q_idx at any address).  q_idx, k_idx
  *   and q_idx_out are given exactly if the cache has index keys.  turns, mscale, interleaved, rot_dim:
- *   as in msa_rope; rot_dim at most d and d_idx.  positions: device int32 or int64 [total_tokens], or
+ *   as in msa_rope; rot_dim at most d and d_idx (one table turns all four: other tables for the index
+ *   branch, or a turn wider than its keys, take msa_rope and msa_cache_write).  positions: device int32 or int64 [total_tokens], or
  *   NULL for the tokens' places in their sequences.  pages, lens, cu_seqlens: as in msa_cache_write.
  * Out: q_out [total_tokens][H_q][d], q_idx_out [total_tokens][H_i][d_idx] (contiguous, 16-byte aligned,
  *   apart from the inputs).  A token that msa_cache_write skips (an empty slot, behind

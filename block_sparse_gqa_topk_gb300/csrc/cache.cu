@@ -10,6 +10,8 @@
 #include "cache_rows.cuh"
 #include "kernels.h"
 
+#include <algorithm>
+
 namespace msa {
 namespace {
 
@@ -123,21 +125,36 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) cache_kernel(const __gri
   }
 }
 
-// Codes.  A CTA takes kCodeTokens<D> tokens, and each D / 16 lanes a row at a time.  Bound by instructions and the
+// Codes.  A CTA takes code_tokens() tokens, and each D / 16 lanes a row at a time.  Bound by instructions and the
 // loads in flight, so as many CTAs as the registers allow.  32K tokens of 8 groups, with index keys, calls back
 // to back, d 128 (d 64), us:               E4M3 write    4 bits        E4M3 read     4 bits
 //   eight CTAs a SM                        38.7 (21.8)   37.6 (21.8)   37.0 (19.6)   34.1 (18.0)
 //   six                                    41.1          39.9          39.2          36.8
 //   warps that take token after token      40.2 (22.8)   43.8 (23.8)   40.3 (20.1)   34.6 (19.2)
 // (the last with the next vectors on their way, as above; a token a sequence takes it 4.8 us, and 3.2 here).
-template <int D>
-constexpr int kCodeTokens = 1024 / D;
 constexpr int kCodeCtas = 8;
+constexpr int kMaxCodeTokens = 32;  // as the lanes of their index keys fit a CTA
+
+// Tokens of a CTA: at most `rounds` of its threads' work; in a call of one or two waves of CTAs as many as
+// make them even, and where an SM has a CTA all the same, as give all its threads something to do.  E4M3, us:
+//   3000 tokens of 2 heads, d 128, written 3.4 and read 3.6 (2 tokens a CTA, 1500 CTAs: 4.8 and 4.8);
+//   20000 of 8 heads read 24.6 (8 tokens, a little over two waves: 25.5; 16, a little over one: 28.3);
+//   32K of 4 heads read 17.3 in eight rounds, 18.9 in four; 13000 of 8 heads written 17.4 and 16.4.
+template <int D, bool WRITE>
+int code_tokens(int T, int H, int num_sms) {
+  const int items = 2 * H * (D / 16), round = kThreads / items;  // threads' pieces of a token
+  const int eight = 8 * kThreads / items, four = 4 * kThreads / items;
+  const int rounds = WRITE ? std::max(four, std::min(1024 / D, eight)) : eight;
+  const int most = std::max(1, std::min(kMaxCodeTokens, rounds)), together = num_sms * kCodeCtas;
+  if (T > 2 * (int64_t)most * together) return most;
+  const int wave = T > most * together ? 2 * together : together;
+  return std::max(std::max((T + wave - 1) / wave, 1), std::min(std::min((T + num_sms - 1) / num_sms, round), most));
+}
 
 template <int D, int KIND>
 __global__ void __launch_bounds__(kThreads, kCodeCtas)
     cache_code_kernel(const __grid_constant__ CacheParams p, const __grid_constant__ CodedRows rows) {
-  __shared__ int64_t s_row[kCodeTokens<D>];
+  __shared__ int64_t s_row[kMaxCodeTokens];
   const int t0 = blockIdx.x * p.per, nt = min(p.per, p.T - t0);
   if (threadIdx.x < nt) {
     const int64_t row = token_row(p.map, t0 + threadIdx.x);
@@ -159,7 +176,7 @@ template <int D, int KIND>
 __global__ void __launch_bounds__(kThreads, kCodeCtas) cache_decode_kernel(const __grid_constant__ CacheParams p, uint32_t div_2H) {
   constexpr int LPR = D / 16, BITS = KIND == MSA_CACHE_E2M1 ? 4 : 8;
   constexpr int SCALE = KIND == MSA_CACHE_E2M1 ? e2m1_scale_bytes(D) : 4;
-  __shared__ int64_t s_row[kCodeTokens<D>];
+  __shared__ int64_t s_row[kMaxCodeTokens];
   const int t0 = blockIdx.x * p.per, nt = min(p.per, p.T - t0);
   if (threadIdx.x < nt) {
     const int64_t row = token_row(p.map, t0 + threadIdx.x);
@@ -211,8 +228,7 @@ __global__ void __launch_bounds__(kThreads, kCodeCtas) cache_decode_kernel(const
 
 template <int D, int KIND>
 cudaError_t launch_decode(CacheParams& p, int num_sms, cudaStream_t st) {
-  p.per = kCodeTokens<D>;
-  while (p.per > 1 && ((int64_t)p.T + p.per - 1) / p.per < kCodeCtas * num_sms) p.per >>= 1;
+  p.per = code_tokens<D, false>(p.T, p.H, num_sms);
   cache_decode_kernel<D, KIND><<<(unsigned)(((int64_t)p.T + p.per - 1) / p.per), kThreads, 0, st>>>(p, magic(2 * p.H));
   note_launch();
   return cudaGetLastError();
@@ -231,8 +247,7 @@ cudaError_t launch_codes(CacheParams& p, int num_sms, cudaStream_t st) {
   }
   r.H = p.H;
   r.div_2H = magic(2 * p.H);
-  p.per = kCodeTokens<D>;  // while the grid fills the GPU
-  while (p.per > 1 && ((int64_t)p.T + p.per - 1) / p.per < kCodeCtas * num_sms) p.per >>= 1;
+  p.per = code_tokens<D, true>(p.T, p.H, num_sms);
   cache_code_kernel<D, KIND><<<(unsigned)(((int64_t)p.T + p.per - 1) / p.per), kThreads, 0, st>>>(p, r);
   note_launch();
   return cudaGetLastError();
